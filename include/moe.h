@@ -430,6 +430,181 @@ int moe_create_streaming_store(const moe_desc *desc, const moe_store *store,
                                const moe_weights *slot_w, int32_t n_slots, void *state,
                                moe_handle **out);
 
+/* ---------------------------------------------------------------------------
+ * Scored routing: the selection by a score of the logits plus a balance bias,
+ * optionally within the best groups of experts, and weights from the scores.
+ *   softmax  p_e = exp(l_e - max l) / sum, 1 for exp(0) also at l = max = +-inf;
+ *            the sum of the fp32 exponentials is rounded once to fp32, so the
+ *            scores do not depend on an order of summation
+ *   sigmoid  p_e = 1 / (1 + exp(-l_e))
+ *   select   s_e = p_e + bias_e (fp32). With n_groups > 1 the experts form
+ *            n_groups consecutive groups of equal size; a group's score is the
+ *            sum of its group_top largest s_e, and only experts of the
+ *            topk_groups best groups (ties to the lower group) can be chosen
+ *   topk_idx the top_k largest s_e, descending, ties to the lower index
+ *            (+0 == -0)
+ *   topk_w   p_e of the chosen (without the bias), divided by their sum when
+ *            renormalise is set (all 0 when that sum is 0), times scale
+ * A bias of -inf takes an expert out as long as top_k others are left. NaN
+ * logits count as -inf and are reported as for moe_plan; a NaN s_e (a NaN or
+ * +inf bias) counts as -inf and is reported the same way.
+ * ------------------------------------------------------------------------- */
+enum moe_score {
+    MOE_SCORE_SOFTMAX = 0,
+    MOE_SCORE_SIGMOID = 1
+};
+
+typedef struct moe_route_desc {
+    int32_t score;        /* enum moe_score */
+    int32_t n_groups;     /* 1..32, divides n_experts; 1: no groups */
+    int32_t topk_groups;  /* 1..n_groups; topk_groups * group size >= top_k */
+    int32_t group_top;    /* 1 or 2, at most the group size */
+    int32_t renormalise;  /* 0 or 1 */
+    float scale;          /* finite */
+} moe_route_desc;
+
+/* moe_plan with scored routing: same logits / x rules, plan layout, workspace
+ * (MOE_OP_PLAN) and errors. bias: fp32 [n_experts] (NULL: none).
+ * MOE_ERR_INVALID_ARG for a route field outside the ranges above. */
+int moe_plan_scored(moe_handle *h, int32_t T, const float *logits, const uint16_t *x,
+                    const moe_route_desc *route, const float *bias, const moe_plan_buf *plan,
+                    void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The attention half of a decoder layer: norm and rotation of the queries and
+ * keys, a paged key/value cache held in MXFP4, and attention over it.
+ *
+ * Layouts (bf16 as uint16 bit patterns; token rows may be strided, e.g. slices
+ * of one fused projection; strides in elements, multiples of 8; base pointers
+ * 16-byte aligned):
+ *   q, out   bf16 [T][n_heads][head_dim]
+ *   k, v     bf16 [T][n_kv_heads][head_dim]; query head h reads key/value head
+ *            h / (n_heads / n_kv_heads)
+ * The cache, per page p and key/value head h (token o of the page, dimension
+ * x; 16-byte aligned arrays). Each 32 dimensions of a token are one MXFP4
+ * block of 16 code bytes; the blocks of 8 consecutive tokens lie together:
+ *   k_q, v_q  uint8 [n_pages][n_kv_heads][page_size/8][head_dim/32][8][16]
+ *             element x in byte (x % 32) / 2 of block [o/8][x/32][o%8], even x
+ *             in the low nibble (E2M1 codes)
+ *   k_s       uint8 [n_pages][n_kv_heads][page_size][head_dim/32]   (E8M0)
+ *   v_s       uint8 [n_pages][n_kv_heads][page_size/2][head_dim/32][2]: the
+ *             scales of tokens o and o + 1 (o even) side by side
+ * A token's slot is page * page_size + o.
+ * ------------------------------------------------------------------------- */
+
+/* Supported: head_dim 64 or 128; n_kv_heads divides n_heads, n_heads <= 1024;
+ * page_size 16, 32, 64, 128 or 256; n_pages * page_size <= 2^31 - 1. */
+typedef struct moe_attn_desc {
+    int32_t n_heads;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    int32_t page_size;
+    int32_t n_pages;
+} moe_attn_desc;
+
+typedef struct moe_kv_cache {
+    uint8_t *k_q, *k_s, *v_q, *v_s;
+} moe_kv_cache;
+
+typedef struct moe_attn moe_attn;
+
+/* Host. Bytes of one code array (k_q or v_q) and of one scale array of a
+ * cache; -1 for an unsupported shape. */
+int64_t moe_kv_code_bytes(const moe_attn_desc *desc);
+int64_t moe_kv_scale_bytes(const moe_attn_desc *desc);
+
+/* Host. Validates the shape and the device as moe_create does, records the
+ * cache pointers (caller-owned, they must outlive the handle) and allocates
+ * the 4-byte device status word. *out is NULL on failure. */
+int moe_attn_create(const moe_attn_desc *desc, const moe_kv_cache *cache, moe_attn **out);
+
+/* Host. Frees the status word and the handle. NULL is a no-op. */
+void moe_attn_destroy(moe_attn *a);
+
+/* Norm and rotation parameters. Each head row x of q and k becomes
+ * y = x / sqrt(mean(x^2) + eps) * weight (no norm where the weight is NULL),
+ * of which the first rope_dim elements turn by the token's position: pairs
+ * (i, i + rope_dim/2) or, interleaved, (2i, 2i + 1):
+ *   (a, b) -> (a cos_i - b sin_i, b cos_i + a sin_i)
+ * in fp32, rounded once to bf16. */
+typedef struct moe_rope_desc {
+    int32_t rope_dim;          /* 0 (no rotation) or a multiple of 16, <= head_dim */
+    int32_t interleaved;       /* 0 or 1 */
+    int32_t n_pos;             /* rows of cos_sin */
+    float eps;                 /* >= 0, finite */
+    const float *cos_sin;      /* [n_pos][rope_dim]: rope_dim/2 cosines, then the sines;
+                                  16-byte aligned; may be NULL when rope_dim is 0 */
+    const uint16_t *q_weight;  /* bf16 [head_dim], 16-byte aligned, or NULL */
+    const uint16_t *k_weight;
+} moe_rope_desc;
+
+/* Norm and rotation of T tokens' queries and keys in one pass. positions:
+ * int32 [T] (ignored, may be NULL, when rope_dim is 0); a position outside
+ * [0, n_pos) is reported as MOE_ERR_BAD_INDEX and its rows are not written.
+ * An output may be its own input (same pointer and stride) but must not
+ * overlap one otherwise. q or k may be NULL with its output: that part is
+ * left out. */
+int moe_qk_norm_rope(moe_attn *a, int32_t T, const moe_rope_desc *rope, const int32_t *positions,
+                     const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                     uint16_t *q_out, int64_t q_out_stride, uint16_t *k_out, int64_t k_out_stride,
+                     void *stream);
+
+/* Writes T tokens' keys and values into the cache slots slots[t] (int32 [T])
+ * in MXFP4: per 32 elements the scale 2^(floor(log2 max|x|) - 2), at least
+ * 2^-127, elements rounded to the nearest E2M1 value, ties to even, magnitudes
+ * above 6 clamped to 6; a block of zeros gets scale byte 0. A block holding an
+ * infinity or NaN gets scale byte 255: all of it reads as NaN. A slot of -1
+ * skips the token; any other slot outside the cache is reported as
+ * MOE_ERR_BAD_INDEX and skipped. Slots must be distinct. */
+int moe_kv_append(moe_attn *a, int32_t T, const uint16_t *k, int64_t k_stride, const uint16_t *v,
+                  int64_t v_stride, const int32_t *slots, void *stream);
+
+/* Reads n slots back: k and v rows (bf16, exact; either may be NULL) of
+ * slots[i]. Slots -1 and outside the cache as for moe_kv_append: their rows
+ * are not written. */
+int moe_kv_read(moe_attn *a, int32_t n, const int32_t *slots, uint16_t *k, int64_t k_stride,
+                uint16_t *v, int64_t v_stride, void *stream);
+
+/* A batch of sequences. Sequence b has the query rows cu_q[b] .. cu_q[b+1]-1
+ * and kv_len[b] cached tokens, of which its queries are the last: query i of n
+ * sits at position p = kv_len[b] - n + i and sees the keys j <= p, with
+ * window > 0 only those with j > p - window. A query that sees no key (an
+ * empty sequence, or p < 0) gets out = 0 and lse = -inf. Token j of sequence b
+ * is token j % page_size of page page_table[b][j / page_size]. */
+typedef struct moe_attn_batch {
+    int32_t n_seqs;             /* >= 0 */
+    int32_t n_tokens;           /* query rows in all, cu_q[n_seqs] */
+    int32_t max_q;              /* bounds on a sequence's query rows and cached tokens: */
+    int32_t max_kv;             /* they size the launch and the workspace */
+    int32_t table_stride;       /* entries of a page_table row, >= ceil(max_kv / page_size) */
+    int32_t window;             /* 0: none */
+    float scale;                /* of the products q . k, finite */
+    const int32_t *cu_q;        /* [n_seqs + 1], or NULL: one query row per sequence */
+    const int32_t *kv_len;      /* [n_seqs] */
+    const int32_t *page_table;  /* [n_seqs][table_stride] */
+} moe_attn_batch;
+
+/* Host. Scratch bytes of moe_attn_forward for a batch within these bounds. */
+size_t moe_attn_workspace_bytes(const moe_attn *a, int32_t n_seqs, int32_t n_tokens, int32_t max_q,
+                                int32_t max_kv);
+
+/* Attention of a batch over the cache: out = softmax(scale q . k) v in bf16
+ * and, when lse is not NULL, lse fp32 [n_tokens][n_heads] = log(sum(exp(scale
+ * q . k))). The products of the codes are exact; sums and the softmax are fp32, the
+ * weights of v are rounded to fp16 or bf16. Within one sequence, head and block of 32 dimensions,
+ * values whose scale is over 2^29 below the largest count as zero. An infinity or NaN in a query, a key or a
+ * value reaches the rows that see it and no others. Lengths outside the
+ * bounds, cu_q that does not ascend from 0 to at most n_tokens and pages outside the
+ * cache are reported as MOE_ERR_BAD_INDEX; lengths are clamped and tokens of
+ * such pages left out. ws: >= moe_attn_workspace_bytes, 256-byte aligned when
+ * that is non-zero; calls that overlap on the GPU need their own. */
+int moe_attn_forward(moe_attn *a, const moe_attn_batch *batch, const uint16_t *q, int64_t q_stride,
+                     uint16_t *out, int64_t out_stride, float *lse, void *ws, size_t ws_bytes,
+                     void *stream);
+
+/* Host. As moe_status, for an attention handle. */
+int moe_attn_status(moe_attn *a, void *stream);
+
 /* Host. Instrumentation for timing one kernel on the library's own stream:
  * while `which` names a kernel (enum moe_prof_kernel), every later call that
  * launches it records ev_start (a cudaEvent_t) immediately before that launch

@@ -39,7 +39,10 @@ EXPORTS = ("moe_create", "moe_destroy", "moe_expert_bytes", "moe_prepared_bytes"
            "moe_decode_noalloc", "moe_stream_state_bytes", "moe_create_streaming",
            "moe_stream_stats", "moe_store_tiles_per_expert", "moe_store_blob_bound",
            "moe_store_encode", "moe_store_decode", "moe_create_streaming_store",
-           "moe_profile_kernel", "moe_set_fault_injection", "moe_status", "moe_strerror")
+           "moe_profile_kernel", "moe_set_fault_injection", "moe_status", "moe_strerror",
+           "moe_plan_scored", "moe_kv_code_bytes", "moe_kv_scale_bytes", "moe_attn_create",
+           "moe_attn_destroy", "moe_qk_norm_rope", "moe_kv_append", "moe_kv_read",
+           "moe_attn_workspace_bytes", "moe_attn_forward", "moe_attn_status")
 
 MOE_INJECT_NONE = 0
 MOE_INJECT_GEMM_STALL = 1
@@ -60,6 +63,9 @@ MOE_ACT_MXFP4 = 1
 
 MOE_W_MXFP4 = 0
 MOE_W_FP8 = 1
+
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
 
 
 class moe_desc(ctypes.Structure):
@@ -90,6 +96,35 @@ class moe_weights(ctypes.Structure):
 class moe_plan_buf(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("topk_idx", "topk_w", "counts", "offsets", "perm",
                                                 "inv", "active")]
+
+
+class moe_route_desc(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("n_groups", ctypes.c_int32),
+                ("topk_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class moe_attn_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_heads", "n_kv_heads", "head_dim", "page_size",
+                                               "n_pages")]
+
+
+class moe_kv_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_q", "k_s", "v_q", "v_s")]
+
+
+class moe_rope_desc(ctypes.Structure):
+    _fields_ = [("rope_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("n_pos", ctypes.c_int32), ("eps", ctypes.c_float), ("cos_sin", ctypes.c_void_p),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p)]
+
+
+class moe_attn_batch(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("n_tokens", ctypes.c_int32),
+                ("max_q", ctypes.c_int32), ("max_kv", ctypes.c_int32),
+                ("table_stride", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p)]
 
 
 class MoeError(RuntimeError):
@@ -163,6 +198,30 @@ def lib() -> ctypes.CDLL:
                                                  ctypes.POINTER(moe_weights), i32, p,
                                                  ctypes.POINTER(p)]
         L.moe_create_streaming_store.restype = ctypes.c_int
+        L.moe_plan_scored.argtypes = [p, i32, p, p, ctypes.POINTER(moe_route_desc), p,
+                                      ctypes.POINTER(moe_plan_buf), p, sz, p]
+        L.moe_plan_scored.restype = ctypes.c_int
+        for fn in (L.moe_kv_code_bytes, L.moe_kv_scale_bytes):
+            fn.argtypes = [ctypes.POINTER(moe_attn_desc)]
+            fn.restype = i64
+        L.moe_attn_create.argtypes = [ctypes.POINTER(moe_attn_desc), ctypes.POINTER(moe_kv_cache),
+                                      ctypes.POINTER(p)]
+        L.moe_attn_create.restype = ctypes.c_int
+        L.moe_attn_destroy.argtypes = [p]
+        L.moe_attn_destroy.restype = None
+        L.moe_qk_norm_rope.argtypes = [p, i32, ctypes.POINTER(moe_rope_desc), p, p, i64, p, i64, p,
+                                       i64, p, i64, p]
+        L.moe_qk_norm_rope.restype = ctypes.c_int
+        L.moe_kv_append.argtypes = [p, i32, p, i64, p, i64, p, p]
+        L.moe_kv_append.restype = ctypes.c_int
+        L.moe_kv_read.argtypes = [p, i32, p, p, i64, p, i64, p]
+        L.moe_kv_read.restype = ctypes.c_int
+        L.moe_attn_workspace_bytes.argtypes = [p, i32, i32, i32, i32]
+        L.moe_attn_workspace_bytes.restype = sz
+        L.moe_attn_forward.argtypes = [p, ctypes.POINTER(moe_attn_batch), p, i64, p, i64, p, p, sz, p]
+        L.moe_attn_forward.restype = ctypes.c_int
+        L.moe_attn_status.argtypes = [p, p]
+        L.moe_attn_status.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -323,6 +382,63 @@ def moe_set_fault_injection(h, mode: int, timeout_cycles: int = 0) -> int:
 
 def moe_status(h, stream=None) -> int:
     return lib().moe_status(h, _stream(stream))
+
+
+def moe_plan_scored(h, T, logits, x, route: moe_route_desc, bias, plan: moe_plan_buf, ws, ws_bytes,
+                    stream=None) -> int:
+    return lib().moe_plan_scored(h, T, _ptr(logits), _ptr(x), ctypes.byref(route), _ptr(bias),
+                                 ctypes.byref(plan), _ptr(ws), ws_bytes, _stream(stream))
+
+
+def moe_kv_code_bytes(desc: moe_attn_desc) -> int:
+    return lib().moe_kv_code_bytes(ctypes.byref(desc))
+
+
+def moe_kv_scale_bytes(desc: moe_attn_desc) -> int:
+    return lib().moe_kv_scale_bytes(ctypes.byref(desc))
+
+
+def moe_attn_create(desc: moe_attn_desc, cache: moe_kv_cache) -> int:
+    h = ctypes.c_void_p()
+    rc = lib().moe_attn_create(ctypes.byref(desc), ctypes.byref(cache), ctypes.byref(h))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_attn_create")
+    return h.value
+
+
+def moe_attn_destroy(a: int) -> None:
+    lib().moe_attn_destroy(a)
+
+
+def moe_qk_norm_rope(a, T, rope: moe_rope_desc, positions, q, q_stride, k, k_stride, q_out,
+                     q_out_stride, k_out, k_out_stride, stream=None) -> int:
+    return lib().moe_qk_norm_rope(a, T, ctypes.byref(rope), _ptr(positions), _ptr(q), q_stride,
+                                  _ptr(k), k_stride, _ptr(q_out), q_out_stride, _ptr(k_out),
+                                  k_out_stride, _stream(stream))
+
+
+def moe_kv_append(a, T, k, k_stride, v, v_stride, slots, stream=None) -> int:
+    return lib().moe_kv_append(a, T, _ptr(k), k_stride, _ptr(v), v_stride, _ptr(slots),
+                               _stream(stream))
+
+
+def moe_kv_read(a, n, slots, k, k_stride, v, v_stride, stream=None) -> int:
+    return lib().moe_kv_read(a, n, _ptr(slots), _ptr(k), k_stride, _ptr(v), v_stride,
+                             _stream(stream))
+
+
+def moe_attn_workspace_bytes(a, n_seqs: int, n_tokens: int, max_q: int, max_kv: int) -> int:
+    return lib().moe_attn_workspace_bytes(a, n_seqs, n_tokens, max_q, max_kv)
+
+
+def moe_attn_forward(a, batch: moe_attn_batch, q, q_stride, out, out_stride, lse, ws, ws_bytes,
+                     stream=None) -> int:
+    return lib().moe_attn_forward(a, ctypes.byref(batch), _ptr(q), q_stride, _ptr(out), out_stride,
+                                  _ptr(lse), _ptr(ws), ws_bytes, _stream(stream))
+
+
+def moe_attn_status(a, stream=None) -> int:
+    return lib().moe_attn_status(a, _stream(stream))
 
 
 def check(rc: int, where: str = "") -> None:

@@ -3,21 +3,9 @@
 #include <stdlib.h>
 #include <string.h>
 
-#include <nvtx3/nvToolsExt.h>
-
+#include "api_util.h"
 #include "common.cuh"
 #include "kernels.h"
-
-#define MOE_API extern "C" __attribute__((visibility("default")))
-
-// NVTX range over one entry point (host side; shows each call in profiler
-// timelines, does nothing when no profiling tool is attached).
-struct NvtxRange {
-    explicit NvtxRange(const char *name) { nvtxRangePushA(name); }
-    ~NvtxRange() { nvtxRangePop(); }
-    NvtxRange(const NvtxRange &) = delete;
-    NvtxRange &operator=(const NvtxRange &) = delete;
-};
 
 struct moe_handle {
     moe_desc desc;
@@ -43,9 +31,6 @@ struct moe_handle {
     long long timeout;     // limit of every device-side wait (SM clock cycles)
     int inject;            // enum moe_inject (test hook; MOE_INJECT_NONE by default)
 };
-
-// Device-side waits give up after this many SM clocks (about one second).
-static const long long kTimeoutCycles = 2000000000LL;
 
 // cuTensorMapEncodeTiled, looked up through the runtime so the library does
 // not link the driver library directly (it must load on hosts without a GPU).
@@ -154,10 +139,6 @@ static bool make_map_bf16(CUtensorMap *m, const void *base, uint64_t cols, uint6
     return make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, cols, rows, cols * 2, 64,
                        box_rows);
 }
-
-static bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-
-static size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 // prepared weight scales of the wE experts in the weight arrays: gate/up
 // tiles (64 + 64 rows), then down tiles (128 rows)
@@ -585,9 +566,10 @@ static bool plan_ok(const moe_plan_buf *p) {
            p->active;
 }
 
-MOE_API int moe_plan(moe_handle *h, int32_t T, const float *logits, const uint16_t *x,
-                     const moe_plan_buf *plan, void *ws, size_t ws_bytes, void *stream) {
-    NvtxRange nvtx_range("moe_plan");
+// moe_plan, or moe_plan_scored when `route` is set.
+static int plan_impl(moe_handle *h, int32_t T, const float *logits, const uint16_t *x,
+                     const moe_route_desc *route, const float *bias, const moe_plan_buf *plan,
+                     void *ws, size_t ws_bytes, void *stream) {
     if (!h || T < 0) return MOE_ERR_INVALID_ARG;
     if (T == 0) return MOE_OK;
     if (!plan_ok(plan)) return MOE_ERR_INVALID_ARG;
@@ -609,9 +591,36 @@ MOE_API int moe_plan(moe_handle *h, int32_t T, const float *logits, const uint16
         logits = lg;
     }
     void *pws = lg_bytes ? (void *)((unsigned char *)ws + lg_bytes) : ws;
-    cudaError_t err = moe_launch_plan(T, h->desc.n_experts, h->desc.top_k, logits, plan, pws,
-                                      h->status, st);
+    const int E = h->desc.n_experts, k = h->desc.top_k;
+    cudaError_t err =
+        route ? moe_launch_plan_scored(T, E, k, logits, *route, bias, plan, pws, h->status, st)
+              : moe_launch_plan(T, E, k, logits, plan, pws, h->status, st);
     return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+MOE_API int moe_plan(moe_handle *h, int32_t T, const float *logits, const uint16_t *x,
+                     const moe_plan_buf *plan, void *ws, size_t ws_bytes, void *stream) {
+    NvtxRange nvtx_range("moe_plan");
+    return plan_impl(h, T, logits, x, NULL, NULL, plan, ws, ws_bytes, stream);
+}
+
+static bool route_ok(const moe_route_desc *r, int E, int k) {
+    if (!r || (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID)) return false;
+    if (r->n_groups < 1 || r->n_groups > 32 || E % r->n_groups) return false;
+    if (r->topk_groups < 1 || r->topk_groups > r->n_groups) return false;
+    const int gs = E / r->n_groups;
+    if (r->group_top < 1 || r->group_top > 2 || r->group_top > gs) return false;
+    if (r->topk_groups * gs < k) return false;
+    return (r->renormalise == 0 || r->renormalise == 1) && finite_f32(r->scale);
+}
+
+MOE_API int moe_plan_scored(moe_handle *h, int32_t T, const float *logits, const uint16_t *x,
+                            const moe_route_desc *route, const float *bias,
+                            const moe_plan_buf *plan, void *ws, size_t ws_bytes, void *stream) {
+    NvtxRange nvtx_range("moe_plan_scored");
+    if (!h || !route_ok(route, h->desc.n_experts, h->desc.top_k)) return MOE_ERR_INVALID_ARG;
+    if ((uintptr_t)bias & 3u) return MOE_ERR_INVALID_ARG;
+    return plan_impl(h, T, logits, x, route, bias, plan, ws, ws_bytes, stream);
 }
 
 MOE_API int moe_router_logits(moe_handle *h, int32_t T, const uint16_t *x, float *logits,

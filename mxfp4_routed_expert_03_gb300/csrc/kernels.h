@@ -25,6 +25,14 @@ static inline bool moe_plan_is_small(int T) { return T <= 64; }
 size_t moe_plan_ws_bytes(int T, int E);
 cudaError_t moe_launch_plan(int T, int E, int k, const float *logits, const moe_plan_buf *p,
                             void *ws, int *status, cudaStream_t st);
+// The plan of a large batch (not moe_plan_is_small) whose topk_idx is there.
+cudaError_t moe_launch_plan_build(int T, int E, int k, const moe_plan_buf *p, void *ws, int *status,
+                                  cudaStream_t st);
+
+// route_scored.cu
+cudaError_t moe_launch_plan_scored(int T, int E, int k, const float *logits,
+                                   const moe_route_desc &r, const float *bias,
+                                   const moe_plan_buf *p, void *ws, int *status, cudaStream_t st);
 
 // decode.cu
 int moe_decode_per_lane(int K);
@@ -242,3 +250,50 @@ int moe_dense_tiles(int epi, int M, int N);
 cudaError_t moe_launch_dense(int epi, const CUtensorMap *a0, const CUtensorMap *a1,
                              const CUtensorMap *a2, const CUtensorMap *b,
                              const MoeDenseArgs *args, int grid, cudaStream_t st);
+
+// qk_rope.cu: norm and rotation of queries and keys (moe_qk_norm_rope)
+struct MoeRopeArgs {
+    int n_q, n_k;  // head rows of q and of k per token (0: that part is left out)
+    int rope_dim, interleaved, n_pos;
+    float eps;
+    const float *cos_sin;
+    const uint16_t *q_weight, *k_weight;
+    const int32_t *positions;
+    const uint16_t *q, *k;
+    uint16_t *q_out, *k_out;
+    int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+    int *status;
+};
+cudaError_t moe_launch_qk_norm_rope(int T, int head_dim, const MoeRopeArgs &a, int nsm,
+                                    cudaStream_t st);
+
+// kv_cache.cu: writing (k, v) and reading back (k_out, v_out) cache slots
+struct MoeKvArgs {
+    int n, n_kv, n_slots, page_shift;  // tokens, heads, n_pages << page_shift, log2(page_size)
+    const int32_t *slots;
+    const uint16_t *k, *v;
+    uint16_t *k_out, *v_out;
+    int64_t k_stride, v_stride;
+    moe_kv_cache c;
+    int *status;
+};
+cudaError_t moe_launch_kv_append(int head_dim, const MoeKvArgs &a, cudaStream_t st);
+cudaError_t moe_launch_kv_read(int head_dim, const MoeKvArgs &a, cudaStream_t st);
+
+// attn.cu: attention over the cache
+struct MoeAttnArgs {
+    int n_kv, group;           // key/value heads, query heads of each
+    int page_shift, n_pages;
+    moe_kv_cache c;
+    moe_attn_batch b;
+    const uint16_t *q;
+    int64_t q_stride;
+    uint16_t *out;
+    int64_t out_stride;
+    float *lse;                // or NULL
+    float *part;               // partial results (workspace)
+    int *status;
+    long long timeout_cycles;
+};
+size_t moe_attn_ws_bytes(int head_dim, int group, int max_q, int max_kv, int nsm);
+cudaError_t moe_launch_attn(int head_dim, const MoeAttnArgs &a, int nsm, cudaStream_t st);

@@ -1,0 +1,165 @@
+// The MXFP4 key/value cache: written token by token, read back.
+//
+// Per 32 elements: scale 2^e, e = floor(log2 max|x|) - 2 clamped to E8M0's
+// range, elements x / 2^e rounded to the nearest E2M1 value (ties to even,
+// clamped to 6): powers of two and one rounding, so codes are exact. Bound:
+// 2 bytes an element on one side, 17/32 on the other.
+//
+// Layout: the 16-byte blocks of 8 consecutive tokens lie together (128 bytes
+// per 8 tokens and 32 dimensions), which is the 8x8 tile of 16-bit units that
+// ldmatrix reads: attention gets a key fragment, or a transposed value
+// fragment, of packed codes with one conflict-free load.
+//
+// A warp takes 8 tokens of one head of K or V: 4 lanes per token, lane t of
+// them elements 8t .. 8t+7 of every block, so that each code store of a warp
+// covers whole 128-byte lines when the tokens' slots are consecutive.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "mx8.cuh"
+
+namespace {
+
+constexpr int kWarps = 4;
+
+// Slot of a token, split into page-head base and offset; false: skip it.
+__device__ __forceinline__ bool slot_ok(const MoeKvArgs &a, int slot) {
+    if (slot >= 0 && slot < a.n_slots) return true;
+    if (slot != -1) moe_flag(a.status, MOE_ERR_BAD_INDEX);
+    return false;
+}
+
+// Byte offset of block 0 of a token's codes (blocks 128 bytes apart).
+template <int NB>
+__device__ __forceinline__ int64_t code_offset(const MoeKvArgs &a, int slot, int head) {
+    const int page = slot >> a.page_shift, o = slot & ((1 << a.page_shift) - 1);
+    const int64_t ph = (int64_t)page * a.n_kv + head;
+    return ((ph << a.page_shift) * NB + (int64_t)(o >> 3) * 8 * NB + (o & 7)) * 16;
+}
+
+// Offset of the scale byte of block b: [token][block] for the keys,
+// [token pair][block][2] for the values.
+template <int NB>
+__device__ __forceinline__ int64_t scale_offset(const MoeKvArgs &a, int slot, int head, int b,
+                                                bool is_v) {
+    const int page = slot >> a.page_shift, o = slot & ((1 << a.page_shift) - 1);
+    const int64_t tok = (((int64_t)page * a.n_kv + head) << a.page_shift) + o;
+    return is_v ? ((tok >> 1) * NB + b) * 2 + (o & 1) : tok * NB + b;
+}
+
+template <int D>
+__global__ void __launch_bounds__(32 * kWarps) moe_kv_append_kernel(MoeKvArgs a) {
+    constexpr int NB = D / 32;
+    const int lane = threadIdx.x & 31;
+    const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int tok = (int)(unit / (2 * a.n_kv)) * 8 + (lane >> 2);
+    const int sub = (int)(unit % (2 * a.n_kv)), head = sub >> 1, q = lane & 3;
+    const bool is_v = sub & 1;
+    grid_dep_wait();
+    grid_dep_launch();
+    int slot = -1;
+    if (tok < a.n) slot = a.slots[tok];
+    const bool ok = slot_ok(a, slot);
+    const uint16_t *src = (is_v ? a.v + (int64_t)tok * a.v_stride : a.k + (int64_t)tok * a.k_stride) +
+                          head * D + 8 * q;
+    uint4 raw[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+        raw[b] = ok ? *(const uint4 *)(src + 32 * b) : make_uint4(0u, 0u, 0u, 0u);
+    uint32_t scale = 0u;  // lane q keeps block q's byte (NB <= 4)
+    uint32_t code[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const uint32_t w[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
+        // the largest magnitude as bf16 bits (ordered as integers, NaN highest)
+        uint32_t m = 0u;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m = __vmaxu2(m, w[j] & 0x7FFF7FFFu);
+        m = max(m & 0xFFFFu, m >> 16);
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        const int e = mx4::scale_exp(__uint_as_float(m << 16));
+        const float inv = mx8::exp2i(-e);
+        code[b] = 0u;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            code[b] |= mx4::to_e2m1x2(__uint_as_float(w[j] << 16) * inv,
+                                      __uint_as_float(w[j] & 0xFFFF0000u) * inv)
+                       << (8 * j);
+        const uint32_t byte = m >= 0x7F80u ? 255u : (uint32_t)(e + 127);
+        if (q == b) scale = byte;
+    }
+    if (!ok) return;
+    uint8_t *dq = (is_v ? a.c.v_q : a.c.k_q) + code_offset<NB>(a, slot, head) + 4 * q;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) *(uint32_t *)(dq + 128 * b) = code[b];
+    if (q < NB) (is_v ? a.c.v_s : a.c.k_s)[scale_offset<NB>(a, slot, head, q, is_v)] = (uint8_t)scale;
+}
+
+// Two E2M1 codes (a byte) to fp32.
+__device__ __forceinline__ float2 e2m1x2_to_f32(uint32_t byte) {
+    uint32_t h;
+    asm("{\n\t.reg .b8 b;\n\tcvt.u8.u32 b, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}"
+        : "=r"(h)
+        : "r"(byte));
+    return __half22float2(*reinterpret_cast<__half2 *>(&h));
+}
+
+template <int D>
+__global__ void __launch_bounds__(32 * kWarps) moe_kv_read_kernel(MoeKvArgs a) {
+    constexpr int NB = D / 32;
+    const int lane = threadIdx.x & 31;
+    const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int tok = (int)(unit / (2 * a.n_kv)) * 8 + (lane >> 2);
+    const int sub = (int)(unit % (2 * a.n_kv)), head = sub >> 1, q = lane & 3;
+    const bool is_v = sub & 1;
+    grid_dep_wait();
+    grid_dep_launch();
+    if (tok >= a.n) return;
+    const int slot = a.slots[tok];
+    if (!slot_ok(a, slot)) return;
+    uint16_t *out = is_v ? a.v_out : a.k_out;
+    if (!out) return;
+    out += (int64_t)tok * (is_v ? a.v_stride : a.k_stride) + head * D + 8 * q;
+    const uint8_t *sq = (is_v ? a.c.v_q : a.c.k_q) + code_offset<NB>(a, slot, head) + 4 * q;
+    const uint8_t *ss = is_v ? a.c.v_s : a.c.k_s;
+    uint32_t code[NB], byte[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        code[b] = *(const uint32_t *)(sq + 128 * b);
+        byte[b] = ss[scale_offset<NB>(a, slot, head, b, is_v)];
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const float s = e8m0_to_f32(byte[b]);  // value x 2^e is exact in bf16
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = e2m1x2_to_f32((code[b] >> (8 * j)) & 0xFFu);
+            const __nv_bfloat162 r = __floats2bfloat162_rn(f.x * s, f.y * s);
+            w[j] = *reinterpret_cast<const uint32_t *>(&r);
+        }
+        *(uint4 *)(out + 32 * b) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+int blocks(const MoeKvArgs &a) {
+    const int64_t units = (int64_t)((a.n + 7) / 8) * 2 * a.n_kv;
+    return (int)((units + kWarps - 1) / kWarps);
+}
+
+}  // namespace
+
+cudaError_t moe_launch_kv_append(int head_dim, const MoeKvArgs &a, cudaStream_t st) {
+    return head_dim == 64
+               ? launch_pdl(moe_kv_append_kernel<64>, dim3(blocks(a)), dim3(32 * kWarps), 0, st, a)
+               : launch_pdl(moe_kv_append_kernel<128>, dim3(blocks(a)), dim3(32 * kWarps), 0, st, a);
+}
+
+cudaError_t moe_launch_kv_read(int head_dim, const MoeKvArgs &a, cudaStream_t st) {
+    return head_dim == 64
+               ? launch_pdl(moe_kv_read_kernel<64>, dim3(blocks(a)), dim3(32 * kWarps), 0, st, a)
+               : launch_pdl(moe_kv_read_kernel<128>, dim3(blocks(a)), dim3(32 * kWarps), 0, st, a);
+}

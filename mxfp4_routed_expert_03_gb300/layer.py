@@ -9,8 +9,8 @@ import torch
 
 from . import (MOE_OP_DECODE, MOE_OP_FORWARD, MOE_OP_PLAN, MOE_ROUTER_XWR, check, moe_create,
                moe_create_streaming, moe_create_streaming_store, moe_decode, moe_desc,
-               moe_destroy, moe_forward, moe_plan, moe_plan_buf, moe_prepare, moe_prepared_bytes,
-               moe_router_logits, moe_status, moe_store, moe_store_blob_bound, moe_store_encode,
+               moe_destroy, moe_forward, moe_plan, moe_plan_buf, moe_plan_scored, moe_prepare,
+               moe_prepared_bytes, moe_route_desc, moe_router_logits, moe_status, moe_store, moe_store_blob_bound, moe_store_encode,
                moe_store_tiles_per_expert, moe_stream_state_bytes, moe_stream_stats, moe_weights,
                moe_workspace_bytes)
 
@@ -113,6 +113,14 @@ class Layer:
             self.prepare(stream)
         ws, n = self.workspace(T, MOE_OP_PLAN)
         return moe_plan(self.h, T, logits, x, plan.buf, ws, ws.numel(), stream)
+
+    def plan_scored(self, T, logits, x, plan: Plan, route: moe_route_desc, bias=None,
+                    stream=None) -> int:
+        """plan() with scored routing (softmax or sigmoid scores, a balance bias, groups)."""
+        if self.router_mode == MOE_ROUTER_XWR:
+            self.prepare(stream)
+        ws, n = self.workspace(T, MOE_OP_PLAN)
+        return moe_plan_scored(self.h, T, logits, x, route, bias, plan.buf, ws, ws.numel(), stream)
 
     def decode(self, T, x, plan: Plan, out, stream=None) -> int:
         ws, n = self.workspace(T, MOE_OP_DECODE)
