@@ -26,8 +26,9 @@
 //
 // Split. Tokens go in tiles of 32; all (sequence, column tile, head) items'
 // tiles form one line that is cut into equal pieces, one per CTA, so any mix
-// of lengths is balanced. A CTA's 4 warps take a piece's tiles in turn, each
-// with its own ring of bulk copies and its own m, l, o, and merge at the end;
+// of lengths is balanced. A CTA's fifth warp walks the piece ahead of the others and
+// fills a ring of stages with bulk copies, across item ends; four warps take a
+// tile of each stage, each with its own m, l, o, and merge at an item's end;
 // items cut between CTAs leave partial results that a second kernel joins in
 // a fixed order.
 #include <cuda_bf16.h>
@@ -42,10 +43,11 @@
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kTile = 32;      // tokens per tile
-constexpr int kStages = 3;     // tiles in flight per warp
-constexpr int kMinTiles = 4;   // per CTA: one for each warp
+constexpr int kWarps = 4;              // that compute, a tile each; one more fills the ring
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kTile = 32;              // tokens per tile
+constexpr int kStages = 3;
+constexpr int kMinTiles = kWarps;      // per CTA
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
 template <int D, int NT>
@@ -54,14 +56,14 @@ struct Cfg {
     static constexpr int NC = 8 * NT;             // columns of a tile
     static constexpr int kCode = kTile * D / 2;   // bytes of a tile's K (or V) codes
     static constexpr int kScale = kTile * NB;
-    static constexpr int kStage = 2 * (kCode + kScale);
+    static constexpr int kTileBytes = 2 * (kCode + kScale);
+    static constexpr int kStage = kWarps * kTileBytes;
     static constexpr int kOStride = D + 4;
-    static constexpr int kSmemO = kWarps * kStages * kStage;
-    static constexpr int kSmemMl = kSmemO + kWarps * NC * kOStride * 4;
-    static constexpr int kSmemBar = kSmemMl + 2 * kWarps * NC * 4;
-    static constexpr int kSmem = kSmemBar + kWarps * kStages * 8 + kWarps * kStages * 4 + 64;
+    static constexpr int kSmemO = kStages * kStage;
+    static constexpr int kSmem = kSmemO + kWarps * NC * kOStride * 4;
     static constexpr int kCtasPerSm = NT == 1 ? 3 : 2;
     static constexpr int kRec = NC * (D + 2);     // floats of a partial result: o, m, l
+    static constexpr int kHead = 8;               // words of a CTA's header: see Cut
 };
 
 // ------------------------------------------------------------------ PTX
@@ -89,6 +91,15 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same from a zero accumulator.
+__device__ __forceinline__ void mma_f16_0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 // The four bytes of w (two codes each, low nibble first) as four f16 pairs.
 __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&h)[4]) {
@@ -122,6 +133,9 @@ __device__ __forceinline__ void bulk_g2s(void *dst, const void *src, uint32_t by
 __device__ __forceinline__ float pow2(int e) {  // 2^e for e in [-127, 127]
     return __uint_as_float(e == -127 ? 0x00400000u : (uint32_t)(e + 127) << 23);
 }
+
+// R of a stored (15 - R) x 65537.
+__device__ __forceinline__ int max_exp(uint32_t r15) { return 15 - (int)r15 / 65537; }
 
 // ------------------------------------------------------------------ schedule
 // A sequence as scheduled: its rows, and its items (column tile x head) of
@@ -171,8 +185,8 @@ __device__ __forceinline__ long long seq_work(const MoeAttnArgs &a, int b, bool 
     return (long long)s.cts * a.n_kv * (whole ? 1 : s.tiles);
 }
 
-// Sum of v over the block's 4 warps (all threads get it) and each thread's
-// inclusive prefix; tot: 4 words of shared memory.
+// Sum of v over the block (all threads get it) and each thread's inclusive
+// prefix; tot: a word of shared memory per warp.
 __device__ __forceinline__ long long block_scan(long long v, long long *tot, long long &incl) {
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     incl = v;
@@ -186,7 +200,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long *tot, lon
     __syncthreads();
     long long sum = 0, before = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w <= kWarps; ++w) {
         if (w == wid) before = sum;
         sum += tot[w];
     }
@@ -194,14 +208,21 @@ __device__ __forceinline__ long long block_scan(long long v, long long *tot, lon
     return sum;
 }
 
-// Units of all sequences.
+// Units of all sequences. `mine` gets the calling thread's sequence of the
+// first round (the only one for up to kThreads sequences): its units and their
+// inclusive prefix.
+struct Prefix {
+    long long units, incl;
+};
 template <int NC>
-__device__ long long total_work(const MoeAttnArgs &a, bool whole, long long *tot) {
+__device__ long long total_work(const MoeAttnArgs &a, bool whole, long long *tot, Prefix &mine) {
     long long w = 0;
-    for (int base = 0; base < a.b.n_seqs; base += 32 * kWarps) {
+    for (int base = 0; base < a.b.n_seqs; base += kThreads) {
         const int b = base + threadIdx.x;
+        const long long v = b < a.b.n_seqs ? seq_work<NC>(a, b, whole) : 0;
         long long incl;
-        w += block_scan(b < a.b.n_seqs ? seq_work<NC>(a, b, whole) : 0, tot, incl);
+        w += block_scan(v, tot, incl);
+        if (base == 0) mine = {v, incl};
     }
     return w;
 }
@@ -209,29 +230,36 @@ __device__ long long total_work(const MoeAttnArgs &a, bool whole, long long *tot
 // The sequence that holds unit `pos` (0 <= pos < total) and the unit's offset
 // in it; res: 2 words of shared memory.
 template <int NC>
-__device__ void find_unit(const MoeAttnArgs &a, bool whole, long long pos, long long *tot,
-                          long long *res, int &seq, long long &off) {
+__device__ void find_unit(const MoeAttnArgs &a, bool whole, long long pos, const Prefix &mine,
+                          long long *tot, long long *res, int &seq, long long &off) {
     long long before = 0;
-    for (int base = 0; base < a.b.n_seqs; base += 32 * kWarps) {
+    for (int base = 0; base < a.b.n_seqs; base += kThreads) {
         const int b = base + threadIdx.x;
-        const long long v = b < a.b.n_seqs ? seq_work<NC>(a, b, whole) : 0;
-        long long incl;
-        const long long sum = block_scan(v, tot, incl);
-        if (pos < before + sum) {  // block-uniform
-            const long long first = before + incl - v;
-            if (pos >= first && pos < first + v) {
-                res[0] = b;
-                res[1] = pos - first;
-            }
-            break;
+        Prefix p = mine;
+        long long sum = -1;  // (not needed when the first round is the only one)
+        if (a.b.n_seqs > kThreads) {
+            p.units = b < a.b.n_seqs ? seq_work<NC>(a, b, whole) : 0;
+            sum = block_scan(p.units, tot, p.incl);
         }
+        const long long first = before + p.incl - p.units;
+        if (pos >= first && pos < first + p.units) {
+            res[0] = b;
+            res[1] = pos - first;
+        }
+        if (pos < before + sum) break;  // block-uniform
         before += sum;
     }
     __syncthreads();
     seq = (int)res[0];
     off = res[1];
-    __syncthreads();
 }
+
+// Written by every CTA of the split kernel: the item that it began and did not
+// finish (parts CTAs hold its pieces), parts = 0 if there is none.
+struct Cut {
+    int parts, q0, c0, ncol, head;
+    int pad[3];
+};
 
 // Units per CTA.
 __device__ __forceinline__ long long piece_of(long long total, int ctas, bool whole) {
@@ -239,75 +267,197 @@ __device__ __forceinline__ long long piece_of(long long total, int ctas, bool wh
     return whole ? (per > 0 ? per : 1) : (per > kMinTiles ? per : kMinTiles);
 }
 
-// Output of one column: o / l, or 0 where no key was seen.
-__device__ __forceinline__ void store_row(const MoeAttnArgs &a, int row, int d, float o0, float o1,
-                                          float l) {
+// Output of elements d, d + 1 of one row and head: o / l, or 0 where no key was seen.
+__device__ __forceinline__ void store_out(const MoeAttnArgs &a, int row, int head, int D, int d,
+                                          float o0, float o1, float m, float l) {
     const float r = l == 0.f ? 0.f : 1.f / l;
-    const __nv_bfloat162 v = __floats2bfloat162_rn(l == 0.f ? 0.f : o0 * r, l == 0.f ? 0.f : o1 * r);
-    *(__nv_bfloat162 *)(a.out + (int64_t)row * a.out_stride + d) = v;
+    *(__nv_bfloat162 *)(a.out + (int64_t)row * a.out_stride + head * D + d) =
+        __floats2bfloat162_rn(l == 0.f ? 0.f : o0 * r, l == 0.f ? 0.f : o1 * r);
+    if (d == 0 && a.lse)
+        a.lse[(int64_t)row * a.n_kv * a.group + head] =
+            l == 0.f ? -INFINITY : (m + log2f(l)) * CUDART_LN2_F;
+}
+
+__device__ __forceinline__ void consumers_sync() {
+    asm volatile("bar.sync 1, %0;" ::"r"(32 * kWarps) : "memory");
 }
 
 // ------------------------------------------------------------------ kernel
+// A CTA's piece of the line, item by item.
+struct Walk {
+    long long pos, end, off;  // units; off: of the next item's first unit in its sequence
+    int b;
+};
+
+// One item of a piece: a column tile and head of a sequence, token tiles
+// [x_lo, x_hi) of which hold keys that some column sees.
+struct Item {
+    Seq s;
+    int c0, h;
+    int p0;                              // position of query row 0
+    int hi_min, hi_max, lo_min, lo_max;  // key bounds over the columns
+    int x_lo, x_hi;
+    int rest;                            // units of the item beyond this piece
+    bool starts;                         // its first unit is in this piece
+    int b;
+};
+
+template <int NC>
+__device__ __forceinline__ bool next_item(const MoeAttnArgs &a, bool whole, Walk &w, Item &it) {
+    while (w.pos < w.end) {
+        it.s = seq_of<NC>(a, w.b);
+        const Seq &s = it.s;
+        const int units = whole ? 1 : s.tiles;
+        if (w.off >= (long long)s.cts * a.n_kv * units) {  // past the sequence's last item
+            ++w.b;
+            w.off = 0;
+            continue;
+        }
+        const int item = (int)(w.off / units), u0 = (int)(w.off % units);
+        const int take = (int)min((long long)(units - u0), w.end - w.pos);
+        const int tb = whole ? 0 : u0, te = whole ? s.tiles : u0 + take;
+        it.b = w.b;
+        it.starts = u0 == 0;
+        it.rest = units - u0 - take;
+        it.c0 = item / a.n_kv * NC;
+        it.h = item % a.n_kv;
+        const int i0 = it.c0 / a.group, i1 = (min(it.c0 + NC, s.ncol) - 1) / a.group;
+        it.p0 = s.kv - s.nq;
+        it.hi_max = it.p0 + i1 + 1;
+        it.hi_min = it.p0 + i0 + 1;
+        it.lo_min = a.b.window > 0 ? max(0, it.hi_min - a.b.window) : 0;
+        it.lo_max = a.b.window > 0 ? max(0, it.hi_max - a.b.window) : 0;
+        it.x_lo = max(tb, (it.lo_min - s.lo) / kTile);
+        it.x_hi = it.hi_max <= s.lo ? it.x_lo
+                                    : max(it.x_lo, min(te, (it.hi_max - s.lo + kTile - 1) / kTile));
+        w.pos += take;
+        w.off += take;
+        return true;
+    }
+    return false;
+}
+
+// The warp that fills the ring: for every item of the piece, stage by stage,
+// K codes, V codes, K scales and V scales of 4 tiles. Lane = tile * 8 + array
+// * 2 + page of the tile (two where pages hold 16 tokens).
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * kWarps, Cfg<D, NT>::kCtasPerSm)
+__device__ __forceinline__ void fill_ring(const MoeAttnArgs &a, bool whole, Walk walk, uint8_t *smem,
+                                          uint64_t *full, uint64_t *empty, uint32_t (*valid)[kWarps],
+                                          int *abort_flag) {
+    using C = Cfg<D, NT>;
+    const int lane = threadIdx.x & 31;
+    const int tile = lane >> 3, which = (lane >> 1) & 3, part = lane & 1;
+    const int parts = a.page_shift == 4 ? 2 : 1;
+    const int unit = which < 2 ? C::NB * 16 : C::NB;  // bytes of a token
+    const uint8_t *src0 = which == 0   ? a.c.k_q
+                          : which == 1 ? a.c.v_q
+                          : which == 2 ? a.c.k_s
+                                       : a.c.v_s;
+    uint8_t *const dst0 = smem + tile * C::kTileBytes +
+                          (which < 2 ? which * C::kCode : 2 * C::kCode + (which - 2) * C::kScale) +
+                          16 * part * unit;
+    const uint32_t bytes = (uint32_t)(unit * kTile) / parts;
+    int st = 0;
+    uint32_t par = 1;  // of the empty barriers: a fresh one counts as passed
+    int fills = 0;
+    Item it;
+    while (next_item<C::NC>(a, whole, walk, it)) {
+        const int32_t *pages = a.b.page_table + (int64_t)it.b * a.b.table_stride;
+        // the page of this lane's tile of the stage at tile x (-2: not needed)
+        auto page_at = [&](int x) {
+            const int tok = it.s.lo + kTile * (x + tile) + 16 * part;
+            if (part >= parts || x + tile >= it.x_hi || tok >= it.hi_max) return -2;
+            const int id = pages[tok >> a.page_shift];
+            return id >= 0 && id < a.n_pages ? id : -1;
+        };
+        int id = page_at(it.x_lo);
+        for (int x = it.x_lo; x < it.x_hi; x += kWarps) {
+            if (id == -1) moe_flag(a.status, MOE_ERR_BAD_INDEX);
+            const int next = page_at(x + kWarps);  // in flight over the wait
+            const bool ok = tc::mbar_wait_sleep(&empty[st], par, a.timeout_cycles, abort_flag);
+            if (!__all_sync(kFull, ok)) {
+                if (lane == 0) {
+                    moe_flag(a.status, MOE_ERR_DEVICE_TIMEOUT);
+                    *(volatile int *)abort_flag = 1;
+                }
+                goto wind_down;
+            }
+            const uint32_t have = __ballot_sync(kFull, which == 0 && id >= 0);
+            if ((lane & 7) == 0) {
+                const uint32_t two = have >> lane;  // bit 0: first page, bit 1: second
+                valid[st][tile] = parts == 2 ? (two & 1u ? 0xFFFFu : 0u) | (two & 2u ? 0xFFFF0000u : 0u)
+                                             : (two & 1u ? kFull : 0u);
+            }
+            __syncwarp();
+            if (lane == 0)
+                tc::mbar_arrive_expect_tx(&full[st], __popc(have) * (C::kTileBytes / parts));
+            __syncwarp();
+            if (id >= 0) {
+                const int in_page = (it.s.lo + kTile * (x + tile) + 16 * part) & ((1 << a.page_shift) - 1);
+                const int64_t row = (((int64_t)id * a.n_kv + it.h) << a.page_shift) + in_page;
+                bulk_g2s(dst0 + st * C::kStage, src0 + row * unit, bytes, &full[st]);
+            }
+            id = next;
+            ++fills;
+            if (++st == kStages) st = 0, par ^= 1u;
+        }
+    }
+    return;
+wind_down:  // copies still in flight land before the shared memory goes
+    int never = 0;
+    for (int i = 0; i < kStages; ++i) {
+        const int rounds = fills > i ? (fills - i + kStages - 1) / kStages : 0;
+        if (rounds > 0)
+            tc::mbar_wait(&full[i], (uint32_t)((rounds - 1) & 1), a.timeout_cycles / 100 + 100000, &never);
+    }
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
     moe_attn_split_kernel(MoeAttnArgs a, bool whole) {
     using C = Cfg<D, NT>;
     constexpr int NB = C::NB, NC = C::NC;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long s_tot[kWarps], s_res[2];
+    __shared__ long long s_tot[kWarps + 1], s_res[2];
+    __shared__ __align__(8) uint64_t full[kStages], empty[kStages];
+    __shared__ uint32_t valid[kStages][kWarps];
+    __shared__ float s_m[kWarps * NC], s_l[kWarps * NC];
     __shared__ int s_abort;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
-    uint8_t *ring = smem + wid * kStages * C::kStage;
     float *s_o = (float *)(smem + C::kSmemO);
-    float *s_m = (float *)(smem + C::kSmemMl), *s_l = s_m + kWarps * NC;
-    uint64_t *full = (uint64_t *)(smem + C::kSmemBar) + wid * kStages;
-    uint32_t *valid = (uint32_t *)(smem + C::kSmemBar + kWarps * kStages * 8) + wid * kStages;
-    if (lane == 0)
-        for (int i = 0; i < kStages; ++i) tc::mbar_init(&full[i], 1);
-    if (tid == 0) s_abort = 0;
-    tc::fence_mbar_init();
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            tc::mbar_init(&full[i], 1);
+            tc::mbar_init(&empty[i], kWarps);
+        }
+        s_abort = 0;
+        tc::fence_mbar_init();
+    }
     grid_dep_wait();
     grid_dep_launch();
-    __syncthreads();
-
-    const long long total = total_work<NC>(a, whole, s_tot);
+    Prefix mine = {0, 0};
+    const long long total = total_work<NC>(a, whole, s_tot, mine);
     const long long per = piece_of(total, gridDim.x, whole);
-    long long pos = blockIdx.x * per;
-    const long long end = min(total, pos + per);
-    if (pos >= end) return;
-    int b;
-    long long off;
-    find_unit<NC>(a, whole, pos, s_tot, s_res, b, off);
-
-    uint32_t fills = 0, uses = 0;  // of this warp's ring, over all items
-    bool dead = false;             // a wait ran out: no more copies or waits
-    const int parts = a.page_shift == 4 ? 2 : 1;  // pages of a tile
-    const int ids_cap = 32 / parts;               // tiles whose page ids a warp holds
-
-    while (pos < end) {
-        const Seq s = seq_of<NC>(a, b);
-        const int units = whole ? 1 : s.tiles;
-        const long long items = (long long)s.cts * a.n_kv;
-        if (items == 0 || off >= items * units) {  // no rows, or past the sequence's last item
-            ++b;
-            off = 0;
-            continue;
-        }
-        const int item = (int)(off / units), u0 = (int)(off % units);
-        const int take = (int)min((long long)(units - u0), end - pos);
-        const int tb = whole ? 0 : u0, te = whole ? s.tiles : u0 + take;
-        const bool starts = u0 == 0, ends = u0 + take == units;
-        const int ct = item / a.n_kv, h = item % a.n_kv;
-        const int c0 = ct * NC;
-        const int i0 = c0 / a.group, i1 = (min(c0 + NC, s.ncol) - 1) / a.group;
-        const int p0 = s.kv - s.nq;                 // position of query row 0
-        const int hi_max = p0 + i1 + 1, hi_min = p0 + i0 + 1;  // key bounds over the columns
-        const int lo_min = a.b.window > 0 ? max(0, hi_min - a.b.window) : 0;
-        const int lo_max = a.b.window > 0 ? max(0, hi_max - a.b.window) : 0;
-        const int x_lo = max(tb, (lo_min - s.lo) / kTile);
-        const int x_hi = hi_max <= s.lo ? 0 : min(te, (hi_max - s.lo + kTile - 1) / kTile);
-        const int n_my = x_hi - x_lo > wid ? (x_hi - x_lo - wid + kWarps - 1) / kWarps : 0;
+    Walk walk;
+    walk.pos = blockIdx.x * per;
+    walk.end = min(total, walk.pos + per);
+    Cut *cut = (Cut *)a.part + blockIdx.x;
+    float *const recs = a.part + (size_t)gridDim.x * C::kHead;
+    if (tid == 0 && !whole) cut->parts = 0;
+    if (walk.pos >= walk.end) return;
+    find_unit<NC>(a, whole, walk.pos, mine, s_tot, s_res, walk.b, walk.off);
+    if (wid == kWarps) {
+        fill_ring<D, NT>(a, whole, walk, smem, full, empty, valid, &s_abort);
+        return;
+    }
+    int use_st = 0;
+    uint32_t use_par = 0;
+    bool dead = false;  // a wait ran out
+    Item it;
+    while (next_item<NC>(a, whole, walk, it)) {
+        const Seq &s = it.s;
+        const int c0 = it.c0, h = it.h, p0 = it.p0;
 
         // --- queries: fp16 with one power of two per column, and key bounds
         uint32_t qf[NT][NB][4];
@@ -354,11 +504,12 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NT>::kCtasPerSm)
             }
         }
 
-        float o[NB][2][NT][4], m[NT][2], l[NT][2];
-        uint32_t R[NB];
+        // ms: the maximum that weights are taken against, 0 while there is none
+        float o[NB][2][NT][4], m[NT][2], ms[NT][2], l[NT][2];
+        uint32_t r15[NB];  // (15 - R) in both halves (as one product: no carry between them)
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
-            R[k] = 0u;
+            r15[k] = 15u * 65537u;
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
@@ -367,84 +518,40 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NT>::kCtasPerSm)
                     for (int c = 0; c < 4; ++c) o[k][hh][n][c] = 0.f;
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.f;
+        for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = -INFINITY, ms[n][0] = ms[n][1] = l[n][0] = l[n][1] = 0.f;
 
-        // --- ring: the warp's tile j covers tokens first + 32 * 4 * j ..
-        const int first = s.lo + kTile * (x_lo + wid);
-        int ids = -1;
-        auto issue = [&](int j) {
-            const int part = parts == 2 ? lane & 1 : 0;
-            if (j % ids_cap == 0) {  // page ids of the next tiles, a lane each
-                const int jj = j + (parts == 2 ? lane >> 1 : lane);
-                const int tok = first + kTile * kWarps * jj + 16 * part;
-                ids = -2;  // no token of that page is needed
-                if (jj < n_my && tok < hi_max) {
-                    ids = a.b.page_table[(int64_t)b * a.b.table_stride + (tok >> a.page_shift)];
-                    if (ids < 0 || ids >= a.n_pages) {
-                        moe_flag(a.status, MOE_ERR_BAD_INDEX);
-                        ids = -1;
-                    }
-                }
+        for (int x = it.x_lo; x < it.x_hi && !dead; x += kWarps) {
+            const int st = use_st;
+            const uint32_t par = use_par;
+            if (++use_st == kStages) use_st = 0, use_par ^= 1u;
+            if (x + wid >= it.x_hi) {  // no tile of this stage for this warp
+                if (lane == 0) tc::mbar_arrive(&empty[st]);
+                continue;
             }
-            const int at = (j % ids_cap) * parts;
-            const int id0 = __shfl_sync(kFull, ids, at);
-            const int id1 = parts == 2 ? __shfl_sync(kFull, ids, at + 1) : id0;
-            const int st = fills % kStages;
-            uint8_t *dst = ring + st * C::kStage;
-            const int ok0 = id0 >= 0, ok1 = parts == 2 && id1 >= 0;
-            const uint32_t half = C::kStage / parts;
-            if (lane == 0) {
-                valid[st] = parts == 2 ? (ok0 ? 0xFFFFu : 0u) | (ok1 ? 0xFFFF0000u : 0u)
-                                       : (ok0 ? kFull : 0u);
-                tc::mbar_arrive_expect_tx(&full[st], (ok0 + ok1) * half);
-            }
-            __syncwarp();
-            // lane 0..3 (and 4..7): K codes, V codes, K scales, V scales of a page
-            const int which = lane & 3, pt = lane >> 2;
-            const int id = pt ? id1 : id0;
-            if (lane < 4 * parts && id >= 0) {
-                const int tok = first + kTile * kWarps * j + 16 * pt;
-                const int64_t row = (((int64_t)id * a.n_kv + h) << a.page_shift) +
-                                    (tok & ((1 << a.page_shift) - 1));
-                const uint8_t *src = which == 0   ? a.c.k_q + row * (NB * 16)
-                                     : which == 1 ? a.c.v_q + row * (NB * 16)
-                                     : which == 2 ? a.c.k_s + row * NB
-                                                  : a.c.v_s + row * NB;
-                const int bytes = (which < 2 ? C::kCode : C::kScale) / parts;
-                uint8_t *to = dst + (which < 2 ? which * C::kCode
-                                               : 2 * C::kCode + (which - 2) * C::kScale) + pt * bytes;
-                bulk_g2s(to, src, bytes, &full[st]);
-            }
-            ++fills;
-        };
-        if (!dead)
-            for (int j = 0; j < kStages && j < n_my; ++j) issue(j);
-
-        for (int j = 0; j < n_my && !dead; ++j) {
-            const int st = uses % kStages;
-            const bool ok = tc::mbar_wait(&full[st], (uses / kStages) & 1, a.timeout_cycles, &s_abort);
+            const bool ok = tc::mbar_wait(&full[st], par, a.timeout_cycles, &s_abort);
             if (!__all_sync(kFull, ok)) {
                 if (lane == 0) {
                     moe_flag(a.status, MOE_ERR_DEVICE_TIMEOUT);
-                    s_abort = 1;
+                    *(volatile int *)&s_abort = 1;
                 }
                 dead = true;
                 break;
             }
-            const uint32_t base = tc::smem_u32(ring + st * C::kStage);
-            const uint8_t *ks = ring + st * C::kStage + 2 * C::kCode, *vs = ks + C::kScale;
-            const int tok0 = first + kTile * kWarps * j;
-            const uint32_t live = valid[st];
-            const bool edge = tok0 + kTile > hi_min || tok0 < lo_max || live != kFull;
+            const uint8_t *buf = smem + st * C::kStage + wid * C::kTileBytes;
+            const uint32_t base = tc::smem_u32(buf);
+            const uint8_t *ks = buf + 2 * C::kCode, *vs = ks + C::kScale;
+            const int tok0 = s.lo + kTile * (x + wid);
+            const uint32_t live = valid[st][wid];
+            const bool edge = tok0 + kTile > it.hi_min || tok0 < it.lo_max || live != kFull;
 
-            // --- S^T = K Q^T of 2 x 16 tokens
-            float sc[2][NT][4];
-#pragma unroll
+            // 16 tokens at a time, not unrolled: the body has to stay small for
+            // the instruction cache (12 to 16 warps run it out of step)
+#pragma unroll 1
             for (int u = 0; u < 2; ++u) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) sc[u][n][c] = 0.f;
+                const uint32_t at = base + 2 * u * (NB * 128) +
+                                    (lane & 8) * (NB * 16) + (lane >> 4) * 128 + (lane & 7) * 16;
+                // --- S^T = K Q^T
+                float sc[NT][4];
                 uint32_t w0, w1;  // scale bytes of tokens g and g + 8
                 if constexpr (NB == 4) {
                     w0 = *(const uint32_t *)(ks + (16 * u + g) * 4);
@@ -456,9 +563,7 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NT>::kCtasPerSm)
 #pragma unroll
                 for (int kk = 0; kk < NB / 2; ++kk) {
                     uint32_t r[4];  // (octet 0, 1) of block 2kk, then of block 2kk + 1
-                    const int mat = lane >> 3;
-                    ldsm4(r, base + ((2 * u + (mat & 1)) * NB + 2 * kk + (mat >> 1)) * 128 +
-                                 (lane & 7) * 16);
+                    ldsm4(r, at + 2 * kk * 128);
 #pragma unroll
                     for (int k2 = 0; k2 < 2; ++k2) {
                         const int k = 2 * kk + k2;
@@ -473,159 +578,172 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NT>::kCtasPerSm)
                         const float f1 = __uint_as_float((e1 & 0x7F800000u) | 1u);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            float c[4] = {0.f, 0.f, 0.f, 0.f};
-                            mma_f16(c, ha[0], hb[0], ha[1], hb[1], qf[n][k][0], qf[n][k][1]);
+                            float c[4];
+                            mma_f16_0(c, ha[0], hb[0], ha[1], hb[1], qf[n][k][0], qf[n][k][1]);
                             mma_f16(c, ha[2], hb[2], ha[3], hb[3], qf[n][k][2], qf[n][k][3]);
-                            sc[u][n][0] = fmaf(c[0], f0, sc[u][n][0]);
-                            sc[u][n][1] = fmaf(c[1], f0, sc[u][n][1]);
-                            sc[u][n][2] = fmaf(c[2], f1, sc[u][n][2]);
-                            sc[u][n][3] = fmaf(c[3], f1, sc[u][n][3]);
+                            sc[n][0] = k == 0 ? c[0] * f0 : fmaf(c[0], f0, sc[n][0]);
+                            sc[n][1] = k == 0 ? c[1] * f0 : fmaf(c[1], f0, sc[n][1]);
+                            sc[n][2] = k == 0 ? c[2] * f1 : fmaf(c[2], f1, sc[n][2]);
+                            sc[n][3] = k == 0 ? c[3] * f1 : fmaf(c[3], f1, sc[n][3]);
                         }
                     }
                 }
-            }
-            // --- running maximum
-            bool grew = false;
-            float mx[NT][2];
+                // --- exponents of the value scales, tokens 2t, 2t + 1 of each octet
+                uint32_t v2[2][NB];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+                for (int q = 0; q < 2; ++q)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float v = -INFINITY;
+                    for (int kk = 0; kk < NB / 2; ++kk) {
+                        const uint32_t w =
+                            *(const uint32_t *)(vs + (4 * (2 * u + q) + t) * (2 * NB) + 4 * kk);
+                        v2[q][2 * kk] = __byte_perm(w, 0u, 0x4140);
+                        v2[q][2 * kk + 1] = __byte_perm(w, 0u, 0x4342);
+                    }
+                // --- log2 domain, masks
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            float &x = sc[u][n][2 * r + c];
-                            x *= mul[n][c];
-                            if (edge) {
-                                const int i = 16 * u + 8 * r + g, tk = tok0 + i;
-                                if (tk >= hi[n][c] || tk < lo[n][c] || !((live >> i) & 1u))
-                                    x = -INFINITY;
-                            }
-                            v = fmaxf(v, x);
+                    for (int c = 0; c < 4; ++c) sc[n][c] *= mul[n][c & 1];
+                if (edge) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const int i = 16 * u + 8 * (c >> 1) + g, tk = tok0 + i;
+                            if (tk >= hi[n][c & 1] || tk < lo[n][c & 1] || !((live >> i) & 1u))
+                                sc[n][c] = -INFINITY;
                         }
-                    v = fmaxf(v, __shfl_xor_sync(kFull, v, 4));
-                    v = fmaxf(v, __shfl_xor_sync(kFull, v, 8));
-                    v = fmaxf(v, __shfl_xor_sync(kFull, v, 16));
-                    mx[n][c] = fmaxf(m[n][c], v);
-                    grew |= mx[n][c] > m[n][c];
+                    // tokens that no column sees must not move R (their weight is 0)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int i = 16 * u + 8 * q + 2 * t + e, tk = tok0 + i;
+                            if (tk >= it.hi_max || tk < it.lo_min || !((live >> i) & 1u)) {
+                                const uint32_t half = 0xFFFFu << (16 * e);
+#pragma unroll
+                                for (int k = 0; k < NB; ++k)
+                                    v2[q][k] = (v2[q][k] & ~half) | ((uint32_t)max_exp(r15[k]) << (16 * e));
+                            }
+                        }
                 }
-            if (__any_sync(kFull, grew)) {
+                // --- running maximum
+                bool grew = false;
+                float mx[NT][2];
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const float f = mx[n][c] == -INFINITY ? 1.f : ex2(m[n][c] - mx[n][c]);
-                        m[n][c] = mx[n][c];
-                        l[n][c] *= f;
-#pragma unroll
-                        for (int k = 0; k < NB; ++k)
-#pragma unroll
-                            for (int hh = 0; hh < 2; ++hh) {
-                                o[k][hh][n][c] *= f;
-                                o[k][hh][n][c + 2] *= f;
-                            }
+                        float v = fmaxf(sc[n][c], sc[n][c + 2]);
+                        v = fmaxf(v, __shfl_xor_sync(kFull, v, 4));
+                        v = fmaxf(v, __shfl_xor_sync(kFull, v, 8));
+                        v = fmaxf(v, __shfl_xor_sync(kFull, v, 16));
+                        mx[n][c] = fmaxf(m[n][c], v);
+                        grew |= mx[n][c] > m[n][c];
                     }
-            }
-            // --- O^T += V^T P^T, 16 tokens at a time
+                // --- weights' exponents: e - R + 15, in 0 .. 15 for all but rare tokens
+                uint32_t d2[2][NB], any = 0u;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                uint32_t pt[NT][2];  // weights of tokens (2t, 2t + 1) of octet 0, 1; column g
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int k = 0; k < NB; ++k) {
+                        d2[q][k] = v2[q][k] + r15[k];
+                        any |= d2[q][k];
+                    }
+                const bool odd = (any & 0xFFF0FFF0u) != 0u;
+                bool special = false;  // a value scale that is NaN
+                if (__any_sync(kFull, grew || odd)) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const float f = mx[n][c] == -INFINITY ? 1.f : ex2(m[n][c] - mx[n][c]);
+                            m[n][c] = mx[n][c];
+                            ms[n][c] = mx[n][c] == -INFINITY ? 0.f : mx[n][c];
+                            l[n][c] *= f;
+#pragma unroll
+                            for (int k = 0; k < NB; ++k)
+#pragma unroll
+                                for (int hh = 0; hh < 2; ++hh) {
+                                    o[k][hh][n][c] *= f;
+                                    o[k][hh][n][c + 2] *= f;
+                                }
+                        }
+                    if (__any_sync(kFull, odd)) {
+#pragma unroll
+                        for (int k = 0; k < NB; ++k) {
+                            uint32_t top = (uint32_t)max_exp(r15[k]);
+#pragma unroll
+                            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const uint32_t x = (v2[q][k] >> (16 * e)) & 0xFFFFu;
+                                    if (x == 255u) special = true;
+                                    else top = max(top, x);
+                                }
+                            top = max(top, __shfl_xor_sync(kFull, top, 1));
+                            top = max(top, __shfl_xor_sync(kFull, top, 2));
+                            const float f = exp2f((float)(max_exp(r15[k]) - (int)top));
+                            r15[k] = (15u - top) * 65537u;
+#pragma unroll
+                            for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                    for (int c = 0; c < 4; ++c) o[k][hh][n][c] *= f;
+                            // clamped at a zero factor (exponent field 0)
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                const int x0 = (int)(v2[q][k] & 0xFFFFu) - (int)top + 15;
+                                const int x1 = (int)(v2[q][k] >> 16) - (int)top + 15;
+                                d2[q][k] = (uint32_t)(min(max(x1, -15), 15) * 65536 + min(max(x0, -15), 15));
+                            }
+                        }
+                        special = __any_sync(kFull, special);
+                    }
+                }
+                // --- weights of tokens (2t, 2t + 1) of octets 0 and 1, column g
+                uint32_t pt[NT][2], pv[NT][2][NB];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float p[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        const float mm = m[n][c & 1];
-                        p[c] = ex2(sc[u][n][c] - (mm == -INFINITY ? 0.f : mm));
+                        p[c] = ex2(sc[n][c] - ms[n][c & 1]);
                         l[n][c & 1] += p[c];
                     }
                     pt[n][0] = transpose8(pack_f16(p[0], p[1]));
                     pt[n][1] = transpose8(pack_f16(p[2], p[3]));
                 }
-                uint32_t v2[2][NB], d2[2][NB], any = 0u;  // exponents of tokens 2t, 2t + 1
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const uint8_t *src = vs + (4 * (2 * u + q) + t) * (2 * NB);
-                    uint32_t keep = kFull;
-                    if (edge) {  // tokens that no column sees must not set R
-                        const int i = 16 * u + 8 * q + 2 * t, tk = tok0 + i;
-                        const bool s0 = tk < hi_max && tk >= lo_min && ((live >> i) & 1u);
-                        const bool s1 = tk + 1 < hi_max && tk + 1 >= lo_min && ((live >> (i + 1)) & 1u);
-                        keep = (s0 ? 0xFFFFu : 0u) | (s1 ? 0xFFFF0000u : 0u);
-                    }
-#pragma unroll
-                    for (int kk = 0; kk < NB / 2; ++kk) {
-                        const uint32_t w = *(const uint32_t *)(src + 4 * kk);
-                        v2[q][2 * kk] = __byte_perm(w, 0u, 0x4140) & keep;
-                        v2[q][2 * kk + 1] = __byte_perm(w, 0u, 0x4342) & keep;
-                    }
-#pragma unroll
-                    for (int k = 0; k < NB; ++k) {
-                        // e + 31 - R, at least 1; above 31 the running maximum is stale
-                        d2[q][k] = __viaddmax_s16x2(v2[q][k], ((31u - R[k]) & 0xFFFFu) * 0x00010001u, 0x00010001u);
-                        any |= d2[q][k];
-                    }
-                }
-                bool special = false;  // a value scale that is NaN
-                if (__any_sync(kFull, (any & 0x01E001E0u) != 0u)) {
-#pragma unroll
-                    for (int k = 0; k < NB; ++k) {
-                        uint32_t top = R[k];
-#pragma unroll
-                        for (int q = 0; q < 2; ++q)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const uint32_t x = (v2[q][k] >> (16 * e)) & 0xFFFFu;
-                                if (x == 255u) special = true;
-                                else top = max(top, x);
-                            }
-                        top = max(top, __shfl_xor_sync(kFull, top, 1));
-                        top = max(top, __shfl_xor_sync(kFull, top, 2));
-                        const float f = exp2f((float)((int)R[k] - (int)top));
-                        R[k] = top;
-#pragma unroll
-                        for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                for (int c = 0; c < 4; ++c) o[k][hh][n][c] *= f;
-#pragma unroll
-                        for (int q = 0; q < 2; ++q)
-                            d2[q][k] = __viaddmax_s16x2(v2[q][k], ((31u - R[k]) & 0xFFFFu) * 0x00010001u, 0x00010001u);
-                    }
-                    special = __any_sync(kFull, special);
-                }
-                uint32_t pv[NT][2][NB];  // weight x 2^(15 + e - R)
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
 #pragma unroll
                     for (int k = 0; k < NB; ++k) {
-                        const uint32_t f = d2[q][k] * 1024u - 0x04000400u;
+                        const uint32_t f = d2[q][k] * 1024u + 0x3C003C00u;  // 2^(e - R + 15)
 #pragma unroll
                         for (int n = 0; n < NT; ++n) pv[n][q][k] = mul_f16x2(pt[n][q], f);
-                        if (special) {
+                    }
+                if (special) {  // NaN for the columns that give the token any weight
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int k = 0; k < NB; ++k)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 const uint32_t half = 0xFFFFu << (16 * e);
                                 if (((v2[q][k] >> (16 * e)) & 0xFFFFu) == 255u) {
 #pragma unroll
-                                    for (int n = 0; n < NT; ++n) {
-                                        pv[n][q][k] &= ~half;
-                                        if (pt[n][q] & half) pv[n][q][k] |= 0x7E007E00u & half;
-                                    }
+                                    for (int n = 0; n < NT; ++n)
+                                        pv[n][q][k] = (pv[n][q][k] & ~half) |
+                                                      ((pt[n][q] & half) ? 0x7E007E00u & half : 0u);
                                 }
                             }
-                        }
-                    }
+                }
+                // --- O^T += V^T P^T
 #pragma unroll
                 for (int kk = 0; kk < NB / 2; ++kk) {
                     uint32_t r[4];  // (octet 0, 1) of block 2kk, then of block 2kk + 1
-                    const int mat = lane >> 3;
-                    ldsm4_t(r, base + C::kCode +
-                                   ((2 * u + (mat & 1)) * NB + 2 * kk + (mat >> 1)) * 128 +
-                                   (lane & 7) * 16);
+                    ldsm4_t(r, at + C::kCode + 2 * kk * 128);
 #pragma unroll
                     for (int k2 = 0; k2 < 2; ++k2) {
                         const int k = 2 * kk + k2;
@@ -645,9 +763,8 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NT>::kCtasPerSm)
                     }
                 }
             }
-            ++uses;
             __syncwarp();
-            if (j + kStages < n_my) issue(j + kStages);
+            if (lane == 0) tc::mbar_arrive(&empty[st]);
         }
 
         // --- the 4 warps' results: o, m, l of each column
@@ -667,15 +784,22 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NT>::kCtasPerSm)
                 float *dst = s_o + (wid * NC + col) * C::kOStride + 4 * g;
 #pragma unroll
                 for (int k = 0; k < NB; ++k) {
-                    const float f = exp2f((float)((int)R[k] - 142));  // 2^(R - 127) / 2^15
+                    const float f = exp2f((float)(max_exp(r15[k]) - 142));  // 2^(R - 127) / 2^15
                     *(float4 *)(dst + 32 * k) =
                         make_float4(o[k][0][n][c] * f, o[k][0][n][c + 2] * f, o[k][1][n][c] * f,
                                     o[k][1][n][c + 2] * f);
                 }
             }
-        __syncthreads();
-        const bool done = starts && ends;
-        float *rec = a.part + ((int64_t)blockIdx.x * 2 + (starts ? 1 : 0)) * C::kRec;
+        consumers_sync();
+        const bool done = it.starts && it.rest == 0;
+        float *rec = recs + ((int64_t)blockIdx.x * 2 + (it.starts ? 1 : 0)) * C::kRec;
+        if (tid == 0 && it.starts && it.rest > 0) {
+            cut->q0 = s.q0;
+            cut->c0 = c0;
+            cut->ncol = s.ncol;
+            cut->head = h;
+            cut->parts = 1 + (int)((it.rest + per - 1) / per);
+        }
         for (int i = tid; i < NC * (D / 2); i += 32 * kWarps) {
             const int col = i / (D / 2), d = i % (D / 2) * 2;
             float mt = -INFINITY;
@@ -699,68 +823,88 @@ __global__ void __launch_bounds__(32 * kWarps, Cfg<D, NT>::kCtasPerSm)
                     rec[NC * D + NC + col] = lt;
                 }
             } else if (c0 + col < s.ncol) {
-                const int row = s.q0 + (c0 + col) / a.group, head = h * a.group + (c0 + col) % a.group;
-                store_row(a, row, head * D + d, o0, o1, lt);
-                if (d == 0 && a.lse)
-                    a.lse[(int64_t)row * a.n_kv * a.group + head] =
-                        lt == 0.f ? -INFINITY : (mt + log2f(lt)) * CUDART_LN2_F;
+                store_out(a, s.q0 + (c0 + col) / a.group, h * a.group + (c0 + col) % a.group, D, d, o0, o1,
+                          mt, lt);
             }
         }
-        __syncthreads();
-        pos += take;
-        off += take;
-    }
-    if (dead) {  // copies still in flight land before the shared memory goes
-        int never = 0;
-        for (; uses < fills; ++uses)
-            tc::mbar_wait(&full[uses % kStages], (uses / kStages) & 1, a.timeout_cycles / 100 + 100000,
-                          &never);
+        consumers_sync();  // the merge buffer is read before the next item's results come
     }
 }
 
 // Joins the partial results of the item that CTA blockIdx.x of the split
-// kernel began and did not finish, in CTA order.
+// kernel began and did not finish, always in the same order: each of 8 warps
+// takes every eighth part, the loads of four in flight, and the warps' sums are joined in warp order.
+constexpr int kJoinWarps = 8, kJoinCols = 2;
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * kWarps) moe_attn_join_kernel(MoeAttnArgs a, int ctas) {
+__global__ void __launch_bounds__(32 * kJoinWarps) moe_attn_join_kernel(MoeAttnArgs a) {
     using C = Cfg<D, NT>;
-    constexpr int NC = C::NC;
-    __shared__ long long s_tot[kWarps], s_res[2];
+    constexpr int NC = kJoinCols, V = NC * D / 128;  // columns of a block; float4s of a lane
+    __shared__ float4 s_o[kJoinWarps][V][32];
+    __shared__ float s_m[kJoinWarps][NC], s_l[kJoinWarps][NC];
     grid_dep_wait();
     grid_dep_launch();
-    const long long total = total_work<NC>(a, false, s_tot);
-    const long long per = piece_of(total, ctas, false);
-    const long long cut = (blockIdx.x + 1) * per;  // where this CTA's piece ends
-    if (cut >= total) return;
-    int b;
-    long long off;
-    find_unit<NC>(a, false, cut - 1, s_tot, s_res, b, off);
-    const Seq s = seq_of<NC>(a, b);
-    const int item = (int)(off / s.tiles), u = (int)(off % s.tiles);
-    if (u + 1 == s.tiles || u + 1 > per) return;  // ends here, or began before this CTA
-    const int parts = 1 + (int)((s.tiles - (u + 1) + per - 1) / per);
-    const int c0 = item / a.n_kv * NC, h = item % a.n_kv;
-    const float *rec0 = a.part + ((int64_t)blockIdx.x * 2 + 1) * C::kRec;
-    for (int i = threadIdx.x; i < NC * (D / 2); i += 32 * kWarps) {
-        const int col = i / (D / 2), d = i % (D / 2) * 2;
-        if (c0 + col >= s.ncol) continue;
-        float mt = -INFINITY, lt = 0.f, o0 = 0.f, o1 = 0.f;
-        for (int p = 0; p < parts; ++p) {
-            const float *rec = p == 0 ? rec0 : a.part + ((int64_t)(blockIdx.x + p) * 2) * C::kRec;
-            const float mp = rec[NC * D + col], lp = rec[NC * D + NC + col];
-            const float2 v = *(const float2 *)(rec + col * D + d);
-            const float mn = fmaxf(mt, mp);
-            if (mp == -INFINITY) continue;  // no keys there
-            const float f = ex2(mt - mn), w = ex2(mp - mn);
-            lt = fmaf(lt, f, w * lp);
-            o0 = fmaf(o0, f, w * v.x);
-            o1 = fmaf(o1, f, w * v.y);
-            mt = mn;
+    const Cut cut = ((const Cut *)a.part)[blockIdx.x];
+    const int col0 = NC * blockIdx.y;
+    if (cut.parts == 0 || cut.c0 + col0 >= cut.ncol) return;
+    const float *recs = a.part + (size_t)gridDim.x * C::kHead;
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    auto rec = [&](int p) {
+        return recs + ((int64_t)(blockIdx.x + p) * 2 + (p == 0 ? 1 : 0)) * C::kRec;
+    };
+    // float4 i of a lane belongs to column (32 i + lane) / (D / 4)
+    float mt[V], lt[V];
+    float4 o[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) mt[i] = -INFINITY, lt[i] = 0.f, o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int p = wid; p < cut.parts; p += kJoinWarps) {
+        const float *r = rec(p);
+        float4 v[V];
+        float mp[V], lp[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int col = col0 + (32 * i + lane) / (D / 4);
+            v[i] = ((const float4 *)(r + col0 * D))[32 * i + lane];
+            mp[i] = r[C::NC * D + col];
+            lp[i] = r[C::NC * D + C::NC + col];
         }
-        const int row = s.q0 + (c0 + col) / a.group, head = h * a.group + (c0 + col) % a.group;
-        store_row(a, row, head * D + d, o0, o1, lt);
-        if (d == 0 && a.lse)
-            a.lse[(int64_t)row * a.n_kv * a.group + head] =
-                lt == 0.f ? -INFINITY : (mt + log2f(lt)) * CUDART_LN2_F;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float mn = fmaxf(mt[i], mp[i]), sf = mn == -INFINITY ? 0.f : mn;
+            const float f = ex2(mt[i] - sf), w = ex2(mp[i] - sf);
+            mt[i] = mn;
+            lt[i] = fmaf(lt[i], f, w * lp[i]);
+            o[i].x = fmaf(o[i].x, f, w * v[i].x);
+            o[i].y = fmaf(o[i].y, f, w * v[i].y);
+            o[i].z = fmaf(o[i].z, f, w * v[i].z);
+            o[i].w = fmaf(o[i].w, f, w * v[i].w);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        s_o[wid][i][lane] = o[i];
+        const int x = 32 * i + lane;
+        if (x % (D / 4) == 0) {
+            s_m[wid][x / (D / 4)] = mt[i];
+            s_l[wid][x / (D / 4)] = lt[i];
+        }
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < NC * D / 2; x += 32 * kJoinWarps) {
+        const int col = x / (D / 2), d = x % (D / 2) * 2, c = cut.c0 + col0 + col;
+        if (c >= cut.ncol) continue;
+        float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, s_m[w][col]);
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            const float f = s_m[w][col] == -INFINITY ? 0.f : ex2(s_m[w][col] - m);
+            const float2 v = ((const float2 *)&s_o[w][0][0])[x];
+            l = fmaf(f, s_l[w][col], l);
+            o0 = fmaf(f, v.x, o0);
+            o1 = fmaf(f, v.y, o1);
+        }
+        store_out(a, cut.q0 + c / a.group, cut.head * a.group + c % a.group, D, d, o0, o1, m, l);
     }
 }
 
@@ -781,9 +925,9 @@ cudaError_t launch(const MoeAttnArgs &a, int nsm, cudaStream_t st) {
     cudaError_t err = cudaFuncSetAttribute(moe_attn_split_kernel<D, NT>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (err != cudaSuccess) return err;
-    err = launch_pdl(moe_attn_split_kernel<D, NT>, dim3(ctas), dim3(32 * kWarps), C::kSmem, st, a, whole);
+    err = launch_pdl(moe_attn_split_kernel<D, NT>, dim3(ctas), dim3(kThreads), C::kSmem, st, a, whole);
     if (err != cudaSuccess || whole) return err;
-    return launch_pdl(moe_attn_join_kernel<D, NT>, dim3(ctas), dim3(32 * kWarps), 0, st, a, ctas);
+    return launch_pdl(moe_attn_join_kernel<D, NT>, dim3(ctas, C::NC / kJoinCols), dim3(32 * kJoinWarps), 0, st, a);
 }
 
 }  // namespace
@@ -791,7 +935,7 @@ cudaError_t launch(const MoeAttnArgs &a, int nsm, cudaStream_t st) {
 size_t moe_attn_ws_bytes(int head_dim, int group, int max_q, int max_kv, int nsm) {
     if (whole_items(max_kv)) return 0;
     const int nt = wide(group, max_q) ? 2 : 1, per_sm = nt == 2 ? 2 : 3;
-    return (size_t)nsm * per_sm * 2 * (8 * nt * (head_dim + 2)) * sizeof(float);
+    return (size_t)nsm * per_sm * (2 * (8 * nt * (head_dim + 2)) + 8) * sizeof(float);
 }
 
 cudaError_t moe_launch_attn(int head_dim, const MoeAttnArgs &a, int nsm, cudaStream_t st) {
