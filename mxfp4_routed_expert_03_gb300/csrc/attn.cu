@@ -31,24 +31,18 @@
 // tile of each stage, each with its own m, l, o, and merge at an item's end;
 // items cut between CTAs leave partial results that a second kernel joins in
 // a fixed order.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <math_constants.h>
-
 #include <algorithm>
 
-#include "common.cuh"
-#include "kernels.h"
-#include "tc_ptx.cuh"
+#include "attn.cuh"
+
+using namespace moe_attention;
 
 namespace {
 
 constexpr int kWarps = 4;              // that compute, a tile each; one more fills the ring
 constexpr int kThreads = 32 * (kWarps + 1);
-constexpr int kTile = 32;              // tokens per tile
 constexpr int kStages = 3;
 constexpr int kMinTiles = kWarps;      // per CTA
-constexpr uint32_t kFull = 0xFFFFFFFFu;
 
 template <int D, int NT>
 struct Cfg {
@@ -101,27 +95,6 @@ __device__ __forceinline__ void mma_f16_0(float (&c)[4], uint32_t a0, uint32_t a
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-// The four bytes of w (two codes each, low nibble first) as four f16 pairs.
-__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&h)[4]) {
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-        : "r"(w));
-}
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-    const __half2 r = __hmul2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
 __device__ __forceinline__ void bulk_g2s(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
     asm volatile(
         "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -130,54 +103,10 @@ __device__ __forceinline__ void bulk_g2s(void *dst, const void *src, uint32_t by
         : "memory");
 }
 
-__device__ __forceinline__ float pow2(int e) {  // 2^e for e in [-127, 127]
-    return __uint_as_float(e == -127 ? 0x00400000u : (uint32_t)(e + 127) << 23);
-}
-
 // R of a stored (15 - R) x 65537.
 __device__ __forceinline__ int max_exp(uint32_t r15) { return 15 - (int)r15 / 65537; }
 
 // ------------------------------------------------------------------ schedule
-// A sequence as scheduled: its rows, and its items (column tile x head) of
-// `tiles` token tiles each, the first at token lo (a multiple of the tile).
-struct Seq {
-    int q0, nq, kv, lo, tiles, ncol, cts;
-};
-
-template <int NC>
-__device__ __forceinline__ Seq seq_of(const MoeAttnArgs &a, int b) {
-    Seq s;
-    const moe_attn_batch &B = a.b;
-    int q1 = b + 1;
-    s.q0 = b;
-    if (B.cu_q) {
-        s.q0 = B.cu_q[b];
-        q1 = B.cu_q[b + 1];
-    }
-    s.nq = q1 - s.q0;
-    if (s.q0 < 0 || q1 < s.q0 || q1 > B.n_tokens) {
-        moe_flag(a.status, MOE_ERR_BAD_INDEX);
-        s.q0 = s.nq = 0;
-    }
-    if (s.nq > B.max_q) {
-        moe_flag(a.status, MOE_ERR_BAD_INDEX);
-        s.nq = B.max_q;
-    }
-    s.kv = B.kv_len[b];
-    if (s.kv < 0 || s.kv > B.max_kv) {
-        moe_flag(a.status, MOE_ERR_BAD_INDEX);
-        s.kv = s.kv < 0 ? 0 : B.max_kv;
-    }
-    s.ncol = s.nq * a.group;
-    s.cts = (s.ncol + NC - 1) / NC;
-    int lo = 0;
-    if (B.window > 0) lo = max(0, s.kv - s.nq + 1 - B.window);
-    s.lo = lo / kTile * kTile;
-    // at least one tile: rows that see nothing are written too
-    s.tiles = max(1, (s.kv - s.lo + kTile - 1) / kTile);
-    return s;
-}
-
 // Units of the line: token tiles, or whole items where max_kv is short.
 template <int NC>
 __device__ __forceinline__ long long seq_work(const MoeAttnArgs &a, int b, bool whole) {
@@ -265,17 +194,6 @@ struct Cut {
 __device__ __forceinline__ long long piece_of(long long total, int ctas, bool whole) {
     const long long per = (total + ctas - 1) / ctas;
     return whole ? (per > 0 ? per : 1) : (per > kMinTiles ? per : kMinTiles);
-}
-
-// Output of elements d, d + 1 of one row and head: o / l, or 0 where no key was seen.
-__device__ __forceinline__ void store_out(const MoeAttnArgs &a, int row, int head, int D, int d,
-                                          float o0, float o1, float m, float l) {
-    const float r = l == 0.f ? 0.f : 1.f / l;
-    *(__nv_bfloat162 *)(a.out + (int64_t)row * a.out_stride + head * D + d) =
-        __floats2bfloat162_rn(l == 0.f ? 0.f : o0 * r, l == 0.f ? 0.f : o1 * r);
-    if (d == 0 && a.lse)
-        a.lse[(int64_t)row * a.n_kv * a.group + head] =
-            l == 0.f ? -INFINITY : (m + log2f(l)) * CUDART_LN2_F;
 }
 
 __device__ __forceinline__ void consumers_sync() {
@@ -932,13 +850,18 @@ cudaError_t launch(const MoeAttnArgs &a, int nsm, cudaStream_t st) {
 
 }  // namespace
 
-size_t moe_attn_ws_bytes(int head_dim, int group, int max_q, int max_kv, int nsm) {
+size_t moe_attn_ws_bytes(int head_dim, int n_seqs, int n_kv, int group, int max_q, int max_kv,
+                         int nsm) {
+    if (moe_attn_prefill_fits(n_seqs, n_kv, group, max_q, max_kv, nsm))
+        return moe_attn_prefill_ws_bytes(head_dim, n_seqs, n_kv, group, max_q, max_kv, nsm);
     if (whole_items(max_kv)) return 0;
     const int nt = wide(group, max_q) ? 2 : 1, per_sm = nt == 2 ? 2 : 3;
     return (size_t)nsm * per_sm * (2 * (8 * nt * (head_dim + 2)) + 8) * sizeof(float);
 }
 
 cudaError_t moe_launch_attn(int head_dim, const MoeAttnArgs &a, int nsm, cudaStream_t st) {
+    if (moe_attn_prefill_fits(a.b.n_seqs, a.n_kv, a.group, a.b.max_q, a.b.max_kv, nsm))
+        return moe_launch_attn_prefill(head_dim, a, nsm, st);
     const bool w = wide(a.group, a.b.max_q);
     if (head_dim == 64) return w ? launch<64, 2>(a, nsm, st) : launch<64, 1>(a, nsm, st);
     return w ? launch<128, 2>(a, nsm, st) : launch<128, 1>(a, nsm, st);

@@ -1,0 +1,715 @@
+// Attention over the MXFP4 cache with many query rows per sequence: the same
+// mathematics as the split kernel, on tcgen05 tensor cores.
+//
+// A CTA owns 256 columns (query rows x heads of one key/value head) of one
+// sequence as two tiles A and B of 128, and runs over the keys 128 at a time:
+//   S_t = Q_t K^T        (128 x 128 x D, operands in shared memory, S in TMEM)
+//   P_t = 2^(S_t - m)    (a thread per row: TMEM -> registers -> TMEM, fp16)
+//   O_t += P_t V         (P from TMEM over S's columns, V from shared memory)
+// so the tensor cores work on one tile while the other's softmax runs: warps
+// 0-3 hold tile A's rows, 4-7 tile B's, 8-11 turn the cache's codes into
+// operands (each key and value once per CTA, i.e. once per 256 columns), 12
+// issues the MMAs. TMEM is full: S_A, S_B, O_A, O_B of 128 columns each.
+//
+// Operands are fp16: a code is exact, and its scale enters as 2^(e - R + 12)
+// with R the largest key exponent (or, per block of 32 dimensions, the largest
+// value exponent) that the CTA's rows can see, found in a pass over the scales
+// before the loop; what lies over 2^26 below the largest loses bits, over
+// 2^36 it vanishes. Queries as in the split kernel. The running maximum only
+// moves when it would rise by more than 2^8 (P stays far inside fp16's range),
+// so O is rescaled a few times per row and not once per tile.
+//
+// Bound: 4 D flops per column and key on the tensor cores; one exponential per
+// column and key (32 a cycle and SM) is next.
+#include <algorithm>
+
+#include "attn.cuh"
+
+using namespace moe_attention;
+
+namespace {
+
+constexpr int kM = 128;          // rows of a tile (columns of the item)
+constexpr int kCols = 2 * kM;    // columns of a CTA
+constexpr int kN = 128;          // keys per step
+constexpr int kWarpsP = 13;
+constexpr int kThreadsP = 32 * kWarpsP;
+constexpr int kInfo = 4;         // steps whose masks are kept
+constexpr int kHead = 12;        // operands carry 2^12
+constexpr float kLag = 8.f;      // log2 that a row's maximum may lie above the one in use
+
+template <int D>
+struct PCfg {
+    static constexpr int NB = D / 32;
+    static constexpr int kHalf = kM * 128;            // 128 rows of 64 elements
+    static constexpr int kOp = kM * D * 2;            // an operand tile
+    static constexpr int kSmemQ = 0, kSmemK = 2 * kOp, kSmemV = 4 * kOp;
+    // + alignment; a second CTA on the SM would only wait for tensor memory
+    static constexpr int kSmem = std::max(6 * kOp + 1024, 120 * 1024);
+    static constexpr int kRec = kCols * (D + 2);      // floats of a partial result
+};
+
+struct StepInfo {
+    uint32_t live[4];     // tokens whose page is in the cache
+    uint32_t nan[4][4];   // [block][word]: values that are NaN
+    uint32_t any_nan[4];  // by word
+};
+
+// 32 consecutive TMEM columns of each lane, complete on return.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+        "%30, %31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+          "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+        "%30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+        "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+        "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// D[tmem] (+)= A[tmem] x B[smem], fp16 operands, 16 K per instruction.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Descriptor of an MN-major operand, 128-byte swizzle: atoms of 64 elements
+// (128 bytes) along MN x 8 along K; `mn` bytes between atoms along MN, 1024
+// between atoms along K.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t mn) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(mn >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+// kind::f16, fp16 operands, fp32 accumulator; bt: B is MN-major.
+__device__ __forceinline__ uint32_t idesc_f16(int M, int N, bool bt) {
+    return (1u << 4) | ((bt ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Byte maximum of the bytes of v that are not 255.
+__device__ __forceinline__ uint32_t finite_bytes(uint32_t v) { return v & ~__vcmpeq4(v, 0xFFFFFFFFu); }
+
+// Factor pair 2^(e - R + 12) of a scale byte; 0 below fp16's normal range.
+__device__ __forceinline__ uint32_t factor_of(uint32_t e, int R) {
+    return (uint32_t)min(max((int)e - R + 15 + kHead, 0), 15 + kHead) * 0x04000400u;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreadsP, 1)
+    moe_attn_prefill_kernel(MoeAttnArgs a, int tiles_max, int splits) {
+    using C = PCfg<D>;
+    constexpr int NB = C::NB;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    __shared__ __align__(8) uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2],
+        o_full[2], drain;
+    __shared__ StepInfo info[kInfo];
+    __shared__ int s_rk, s_rv[NB], s_abort;
+    __shared__ uint32_t s_tmem;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+
+    grid_dep_wait();
+    grid_dep_launch();
+    // the last column tiles (the longest, under a causal mask) first
+    const int n_items = a.b.n_seqs * a.n_kv;
+    const int split = blockIdx.x % splits, blk = blockIdx.x / splits;
+    const int ct_rev = blk / n_items, b = blk % n_items / a.n_kv, h = blk % a.n_kv;
+    const Seq s = seq_of<kCols>(a, b);
+    const int ct = tiles_max - 1 - ct_rev, c0 = ct * kCols;
+    if (c0 >= s.ncol) return;
+    const int G = a.group, p0 = s.kv - s.nq;
+    const int i0 = c0 / G, i1 = (min(c0 + kCols, s.ncol) - 1) / G;
+    const bool two = c0 + kM < s.ncol;  // tile B has columns
+    const int hi_all = p0 + i1 + 1, W = a.b.window;
+    const int lo_all = W > 0 ? max(0, p0 + i0 + 1 - W) : 0;
+    const int begin = lo_all / 16 * 16;
+    const int steps = hi_all > begin ? (hi_all - begin + kN - 1) / kN : 0;
+    const int j0 = (int)((int64_t)steps * split / splits), j1 = (int)((int64_t)steps * (split + 1) / splits);
+    const int n = j1 - j0, first = begin + kN * j0;
+    const int32_t *pages = a.b.page_table + (int64_t)b * a.b.table_stride;
+    const int in_page_mask = (1 << a.page_shift) - 1;
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&k_full[i], 4);
+            tc::mbar_init(&k_empty[i], 1);
+            tc::mbar_init(&v_full[i], 4);
+            tc::mbar_init(&v_empty[i], 1);
+            tc::mbar_init(&s_full[i], 2);
+            tc::mbar_init(&p_full[i], 4);
+            tc::mbar_init(&o_full[i], 1);
+        }
+        tc::mbar_init(&drain, 1);
+        tc::fence_mbar_init();
+        s_abort = 0;
+        s_rk = 0;
+        for (int k = 0; k < NB; ++k) s_rv[k] = 0;
+    }
+    if (wid == kWarpsP - 1) {
+        tc::tmem_alloc(&s_tmem, 512);
+        tc::tmem_relinquish();
+    }
+    // --- queries: fp16 with one power of two per row
+    float mul = 0.f;  // of this thread's row: back from that power, |scale| log2(e)
+    if (wid < 8) {
+        const int c = c0 + tid, r = tid & (kM - 1);
+        uint4 raw[D / 8];
+        uint32_t top = 0u;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            raw[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (c < s.ncol)
+                raw[i] = *(const uint4 *)(a.q + (int64_t)(s.q0 + c / G) * a.q_stride +
+                                          (h * G + c % G) * D + 8 * i);
+            top = __vmaxu2(top, raw[i].x & 0x7FFF7FFFu);
+            top = __vmaxu2(top, raw[i].y & 0x7FFF7FFFu);
+            top = __vmaxu2(top, raw[i].z & 0x7FFF7FFFu);
+            top = __vmaxu2(top, raw[i].w & 0x7FFF7FFFu);
+        }
+        top = max(top & 0xFFFFu, top >> 16);
+        const bool bad = top >= 0x7F80u;  // the row is NaN: zero operand, NaN factor
+        const int sh = min(141 - (int)(top >> 7), 127);
+        // a negative scale's sign goes into the queries, so that the largest
+        // product is the largest logit
+        const float up = bad ? 0.f : copysignf(pow2(sh), a.b.scale);
+        mul = bad ? CUDART_NAN_F : pow2(-sh) * (fabsf(a.b.scale) * CUDART_L2E_F);
+        uint8_t *dst = smem + C::kSmemQ + (tid >> 7) * C::kOp + (r >> 3) * 1024 + (r & 7) * 128;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+            uint32_t f[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float x = bad ? 0.f : __uint_as_float(w[j] << 16) * up;
+                const float y = bad ? 0.f : __uint_as_float(w[j] & 0xFFFF0000u) * up;
+                f[j] = pack_f16(x, y);
+            }
+            *(uint4 *)(dst + (i >> 3) * C::kHalf + (((i & 7) ^ (r & 7)) << 4)) =
+                make_uint4(f[0], f[1], f[2], f[3]);
+        }
+        tc::fence_proxy_async_smem();
+    }
+    __syncthreads();
+    // --- the largest exponents that a row can see: 16 tokens (of one page) a thread
+    {
+        uint32_t mk = 0u, mv[NB];
+#pragma unroll
+        for (int k = 0; k < NB; ++k) mv[k] = 0u;
+        for (int tok = first + 16 * tid; tok < min(hi_all, first + kN * n); tok += 16 * kThreadsP) {
+            const int id = pages[tok >> a.page_shift];
+            if (id < 0 || id >= a.n_pages) {
+                moe_flag(a.status, MOE_ERR_BAD_INDEX);
+                continue;
+            }
+            const int64_t row = (((int64_t)id * a.n_kv + h) << a.page_shift) + (tok & in_page_mask);
+            const uint8_t *ks = a.c.k_s + row * NB, *vs = a.c.v_s + row * NB;
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                uint32_t k0, k1, v0, v1;  // K: tokens i, i + 1; V: blocks 0, 1 and 2, 3 of both
+                if constexpr (NB == 4) {
+                    const uint2 x = *(const uint2 *)(ks + 4 * i), y = *(const uint2 *)(vs + 4 * i);
+                    k0 = x.x, k1 = x.y, v0 = y.x, v1 = y.y;
+                } else {
+                    const uint32_t x = *(const uint32_t *)(ks + 2 * i);
+                    k0 = x & 0xFFFFu, k1 = x >> 16, v0 = *(const uint32_t *)(vs + 2 * i), v1 = 0u;
+                }
+                const bool see0 = tok + i >= lo_all && tok + i < hi_all;
+                const bool see1 = tok + i + 1 >= lo_all && tok + i + 1 < hi_all;
+                const uint32_t keep = (see0 ? 0x00FF00FFu : 0u) | (see1 ? 0xFF00FF00u : 0u);
+                mk = __vmaxu4(mk, __vmaxu4(see0 ? finite_bytes(k0) : 0u, see1 ? finite_bytes(k1) : 0u));
+                v0 = finite_bytes(v0) & keep;
+                v1 = finite_bytes(v1) & keep;
+                mv[0] = max(mv[0], max(v0 & 0xFFu, (v0 >> 8) & 0xFFu));
+                mv[1] = max(mv[1], max((v0 >> 16) & 0xFFu, v0 >> 24));
+                if constexpr (NB == 4) {
+                    mv[2] = max(mv[2], max(v1 & 0xFFu, (v1 >> 8) & 0xFFu));
+                    mv[3] = max(mv[3], max((v1 >> 16) & 0xFFu, v1 >> 24));
+                }
+            }
+        }
+        mk = max(max(mk & 0xFFu, (mk >> 8) & 0xFFu), max((mk >> 16) & 0xFFu, mk >> 24));
+        mk = __reduce_max_sync(kFull, mk);
+        if (lane == 0) atomicMax(&s_rk, (int)mk);
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+            const uint32_t v = __reduce_max_sync(kFull, mv[k]);
+            if (lane == 0) atomicMax(&s_rv[k], (int)v);
+        }
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const long long limit = a.timeout_cycles;
+    // a bounded wait of a whole warp; false: give up
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        const bool ok = tc::mbar_wait(bar, parity & 1u, limit, &s_abort);
+        if (__all_sync(kFull, ok)) return true;
+        if (lane == 0) {
+            moe_flag(a.status, MOE_ERR_DEVICE_TIMEOUT);
+            *(volatile int *)&s_abort = 1;
+        }
+        return false;
+    };
+
+    if (wid < 8) {
+        // ------------------------------------------------ softmax: a thread per row
+        const int t = wid >> 2;
+        const int c = c0 + tid;
+        if (t == 0 || two) {
+            const uint32_t lanes = (uint32_t)(32 * (wid & 3)) << 16;
+            const uint32_t sp = tmem + lanes + 128 * t, op = tmem + lanes + 256 + 128 * t;
+            const int it0 = (c0 + kM * t) / G, it1 = (min(c0 + kM * (t + 1), s.ncol) - 1) / G;
+            const int hi_min = p0 + it0 + 1, lo_max = W > 0 ? max(0, p0 + it1 + 1 - W) : 0;
+            const int hi = c < s.ncol ? p0 + c / G + 1 : 0x7FFFFFFF;
+            const int lo = c < s.ncol && W > 0 ? hi - W : 0;
+            // logits: S x mul x 2^(R - 127 - 12)
+            const float mr = mul * exp2f((float)(s_rk - 127 - kHead));
+            float m = -INFINITY, l = 0.f;  // m: the maximum in use
+            uint32_t nan_blocks = 0u;
+            bool ok = true;
+            for (int j = 0; j < n; ++j) {
+                if (!wait(&s_full[t], j)) {
+                    ok = false;
+                    break;
+                }
+                tc::tc_fence_after();
+                const StepInfo &f = info[j % kInfo];
+                const int tok0 = first + kN * j;
+                const bool edge = tok0 + kN > hi_min || tok0 < lo_max ||
+                                  (f.live[0] & f.live[1] & f.live[2] & f.live[3]) != kFull;
+                // tokens of 32-column chunk q that the row sees
+                auto seen = [&](int q) {
+                    const int above = min(max(hi - (tok0 + 32 * q), 0), 32);
+                    const int below = min(max(lo - (tok0 + 32 * q), 0), 32);
+                    const uint32_t up = above == 32 ? kFull : (1u << above) - 1u;
+                    const uint32_t dn = below == 32 ? kFull : (1u << below) - 1u;
+                    return up & ~dn & f.live[q];
+                };
+                float mx = -INFINITY;
+                uint32_t x[32];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    tmem_ld32(sp + 32 * q, x);
+                    if (edge) {
+                        const uint32_t see = seen(q);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            mx = fmaxf(mx, (see >> i) & 1u ? __uint_as_float(x[i]) : -INFINITY);
+                    } else {
+                        float m1 = -INFINITY;
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            mx = fmaxf(mx, __uint_as_float(x[i]));
+                            m1 = fmaxf(m1, __uint_as_float(x[i + 1]));
+                        }
+                        mx = fmaxf(mx, m1);
+                    }
+                }
+                if ((f.any_nan[0] | f.any_nan[1] | f.any_nan[2] | f.any_nan[3]) != 0u) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int k = 0; k < NB; ++k)
+                            if (seen(q) & f.nan[k][q]) nan_blocks |= 1u << k;
+                }
+                const float top = mx * mr;  // (-inf x 0 is NaN: no key seen)
+                const bool rise = mx > -INFINITY && top > m + (m == -INFINITY ? 0.f : kLag);
+                if (__any_sync(kFull, rise)) {
+                    const float mn = rise ? top : m;
+                    const float fac = m == -INFINITY ? 0.f : ex2(m - mn);
+                    if (j > 0) {  // O holds step j - 1
+                        if (!wait(&o_full[t], j - 1)) {
+                            ok = false;
+                            break;
+                        }
+                        tc::tc_fence_after();
+                        const float fo = rise ? fac : 1.f;
+#pragma unroll 1
+                        for (int q = 0; q < D / 32; ++q) {
+                            tmem_ld32(op + 32 * q, x);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * fo);
+                            tmem_st32(op + 32 * q, x);
+                        }
+                        tmem_st_wait();
+                    }
+                    if (rise) {
+                        l *= fac;
+                        m = mn;
+                    }
+                }
+                const float ms = m == -INFINITY ? 0.f : m;
+                float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    tmem_ld32(sp + 32 * q, x);
+                    uint32_t p[16];
+                    const uint32_t see = edge ? seen(q) : kFull;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float y0 = ex2(fmaf(__uint_as_float(x[2 * i]), mr, -ms));
+                        float y1 = ex2(fmaf(__uint_as_float(x[2 * i + 1]), mr, -ms));
+                        if (edge) {
+                            y0 = (see >> (2 * i)) & 1u ? y0 : 0.f;
+                            y1 = (see >> (2 * i + 1)) & 1u ? y1 : 0.f;
+                        }
+                        l0 += y0;
+                        l1 += y1;
+                        p[i] = pack_f16(y0, y1);
+                    }
+                    tmem_st16(sp + 16 * q, p);
+                }
+                l += l0 + l1;
+                tmem_st_wait();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&p_full[t]);
+            }
+            // ------------------------------------------------ output
+            if (ok && n > 0) ok = wait(&o_full[t], n - 1);
+            if (ok) {
+                tc::tc_fence_after();
+                const bool live_row = c < s.ncol;
+                const int row = s.q0 + c / G, head = h * G + c % G;
+                float *rec = a.part + (int64_t)blockIdx.x * C::kRec + (int64_t)tid * (D + 2);
+                const float r = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+                for (int q = 0; q < D / 32; ++q) {
+                    uint32_t x[32];
+                    if (n > 0) tmem_ld32(op + 32 * q, x);
+                    const float back = exp2f((float)(s_rv[q] - 127 - kHead));
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        float v = n > 0 ? __uint_as_float(x[i]) * back : 0.f;
+                        if ((nan_blocks >> q) & 1u) v = CUDART_NAN_F;
+                        x[i] = __float_as_uint(v);
+                    }
+                    if (!live_row) continue;
+                    if (splits > 1) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2)
+                            *(float2 *)(rec + 32 * q + i) =
+                                make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+                    } else {
+                        uint4 *dst = (uint4 *)(a.out + (int64_t)row * a.out_stride + head * D + 32 * q);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float y0 = __uint_as_float(x[8 * i + 2 * e]);
+                                const float y1 = __uint_as_float(x[8 * i + 2 * e + 1]);
+                                const __nv_bfloat162 v = __floats2bfloat162_rn(l == 0.f ? 0.f : y0 * r,
+                                                                               l == 0.f ? 0.f : y1 * r);
+                                w[e] = *reinterpret_cast<const uint32_t *>(&v);
+                            }
+                            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                }
+                if (live_row && splits > 1) {
+                    rec[D] = m;
+                    rec[D + 1] = l;
+                } else if (live_row && a.lse) {
+                    a.lse[(int64_t)row * a.n_kv * G + head] =
+                        l == 0.f ? -INFINITY : (m + log2f(l)) * CUDART_LN2_F;
+                }
+            }
+            tc::tc_fence_before();
+        }
+    } else if (wid < kWarpsP - 1) {
+        // ------------------------------------------------ codes to operands
+        const int dw = wid - 8;  // tokens 32 dw .. of a step
+        const int tl = lane & 7, k = (lane >> 3) % NB;
+        constexpr int OCT = 4 / NB;  // octets that a load of the warp covers
+        const int rk = s_rk, rv = s_rv[k];
+        uint4 kq[NB], vq[NB];
+        uint32_t kb[NB], vb[NB];  // scale bytes; bit 8: the page is there; bit 9: some row may see it
+        int id[NB], nid[NB];
+        auto token_of = [&](int j, int i) {  // of load i
+            return first + kN * j + 32 * dw + 8 * (i * OCT + (lane >> 3) / NB) + tl;
+        };
+        auto page_ids = [&](int j, int (&o)[NB]) {
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const int tok = token_of(j, i);
+                o[i] = j < n && tok < hi_all ? pages[tok >> a.page_shift] : -1;
+            }
+        };
+        auto load = [&](int j) {
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const int tok = token_of(j, i);
+                kq[i] = vq[i] = make_uint4(0u, 0u, 0u, 0u);
+                kb[i] = vb[i] = 0u;
+                if (j < n && tok < hi_all && id[i] >= 0 && id[i] < a.n_pages) {
+                    const int o = tok & in_page_mask;
+                    const int64_t row = (((int64_t)id[i] * a.n_kv + h) << a.page_shift) + (o & ~7);
+                    const int64_t code = row * (NB * 16) + k * 128 + tl * 16;
+                    kq[i] = *(const uint4 *)(a.c.k_q + code);
+                    vq[i] = *(const uint4 *)(a.c.v_q + code);
+                    kb[i] = a.c.k_s[(row + tl) * NB + k] | 0x100u | (tok >= lo_all ? 0x200u : 0u);
+                    vb[i] = a.c.v_s[((row + tl) >> 1) * (2 * NB) + 2 * k + (tl & 1)] | 0x100u;
+                }
+            }
+        };
+        page_ids(0, id);
+        load(0);
+        page_ids(1, nid);
+        for (int j = 0; j < n; ++j) {
+            const int st = j & 1;
+            const uint32_t free_par = ((j >> 1) & 1) ^ 1;  // a fresh barrier counts as passed
+            if (!wait(&k_empty[st], free_par)) break;
+            uint32_t live = 0u, nan = 0u;
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const uint32_t bit = 1u << (8 * (i * OCT + (lane >> 3) / NB) + tl);
+                if (kb[i] & 0x100u) live |= bit;
+                if ((vb[i] & 0xFFu) == 255u && (kb[i] & 0x200u)) nan |= bit;
+            }
+            live = __reduce_or_sync(kFull, live);
+            const bool any_nan = __any_sync(kFull, nan != 0u);
+            StepInfo &f = info[j % kInfo];
+            if (any_nan) {
+#pragma unroll
+                for (int b4 = 0; b4 < NB; ++b4) {
+                    const uint32_t w = __reduce_or_sync(kFull, k == b4 ? nan : 0u);
+                    if (lane == 0) f.nan[b4][dw] = w;
+                }
+            } else if (lane < NB) {
+                f.nan[lane][dw] = 0u;
+            }
+            if (lane == 0) {
+                f.live[dw] = live;
+                f.any_nan[dw] = any_nan ? 1u : 0u;
+            }
+            // K rows (tokens) of 64 elements, 128-byte swizzle
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const int r = 32 * dw + 8 * (i * OCT + (lane >> 3) / NB) + tl;
+                const uint32_t e = kb[i] & 0xFFu;
+                const uint32_t fac = e == 255u && (kb[i] & 0x200u) ? 0x7E007E00u : factor_of(e, rk);
+                uint8_t *dst = smem + C::kSmemK + st * C::kOp + (k >> 1) * C::kHalf + (r >> 3) * 1024 + (r & 7) * 128;
+                const uint32_t w[4] = {kq[i].x, kq[i].y, kq[i].z, kq[i].w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t x[4];
+                    codes_f16(w[q], x);
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) x[z] = mul_f16x2(x[z], fac);
+                    *(uint4 *)(dst + (((4 * (k & 1) + q) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+                }
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&k_full[st]);
+            if (!wait(&v_empty[st], free_par)) break;
+            // V the same way: rows are the contracted index there
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const int r = 32 * dw + 8 * (i * OCT + (lane >> 3) / NB) + tl;
+                const uint32_t e = vb[i] & 0xFFu;
+                const uint32_t fac = e == 255u ? 0u : factor_of(e, rv);
+                uint8_t *dst = smem + C::kSmemV + st * C::kOp + (k >> 1) * C::kHalf + (r >> 3) * 1024 + (r & 7) * 128;
+                const uint32_t w[4] = {vq[i].x, vq[i].y, vq[i].z, vq[i].w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t x[4];
+                    codes_f16(w[q], x);
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) x[z] = mul_f16x2(x[z], fac);
+                    *(uint4 *)(dst + (((4 * (k & 1) + q) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+                }
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&v_full[st]);
+#pragma unroll
+            for (int i = 0; i < NB; ++i) id[i] = nid[i];
+            load(j + 1);
+            page_ids(j + 2, nid);
+        }
+    } else {
+        // ------------------------------------------------ MMA issue (lane 0)
+        const uint32_t idesc_s = idesc_f16(kM, kN, false), idesc_o = idesc_f16(kM, D, true);
+        const uint32_t sb = tc::smem_u32(smem);
+        auto qk = [&](int t, int j) {
+            const uint64_t ad = tc::sdesc_sw128(sb + C::kSmemQ + t * C::kOp);
+            const uint64_t bd = tc::sdesc_sw128(sb + C::kSmemK + (j & 1) * C::kOp);
+            if (lane == 0) {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint64_t o = (uint64_t)(((i >> 2) * C::kHalf + (i & 3) * 32) >> 4);
+                    tc::mma_bf16(tmem + 128 * t, ad + o, bd + o, idesc_s, i > 0);
+                }
+                tc::mma_commit(&s_full[t]);
+                // (orders the step's masks, seen behind k_full, before the softmax)
+                tc::mbar_arrive(&s_full[t]);
+            }
+        };
+        auto pv = [&](int t, int j) {
+            const uint64_t bd = sdesc_mn(sb + C::kSmemV + (j & 1) * C::kOp, C::kHalf);
+            if (lane == 0) {
+#pragma unroll
+                for (int i = 0; i < kN / 16; ++i)
+                    mma_f16_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * i, bd + (uint64_t)(i * 2048 >> 4),
+                               idesc_o, (j > 0 || i > 0) ? 1u : 0u);
+                tc::mma_commit(&o_full[t]);
+            }
+        };
+        bool ok = true;
+        if (n > 0) {
+            ok = wait(&k_full[0], 0);
+            if (ok) {
+                qk(0, 0);
+                if (two) qk(1, 0);
+                if (lane == 0) tc::mma_commit(&k_empty[0]);
+            }
+        }
+        for (int j = 0; j < n && ok; ++j) {
+            const bool more = j + 1 < n;
+            ok = wait(&v_full[j & 1], j >> 1) && wait(&p_full[0], j);
+            if (!ok) break;
+            tc::tc_fence_after();
+            pv(0, j);
+            if (more) {
+                ok = wait(&k_full[(j + 1) & 1], (j + 1) >> 1);
+                if (!ok) break;
+                qk(0, j + 1);
+            }
+            if (two) {
+                ok = wait(&p_full[1], j);
+                if (!ok) break;
+                tc::tc_fence_after();
+                pv(1, j);
+            }
+            if (lane == 0) tc::mma_commit(&v_empty[j & 1]);
+            if (more) {
+                if (two) qk(1, j + 1);
+                if (lane == 0) tc::mma_commit(&k_empty[(j + 1) & 1]);
+            }
+        }
+        if (lane == 0 && !ok) tc::drain_mmas(&drain, limit);  // MMAs in flight end before TMEM goes
+        __syncwarp();
+    }
+    __syncthreads();
+    if (wid == kWarpsP - 1) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the splits of every column, in order: a warp per column.
+template <int D>
+__global__ void __launch_bounds__(256) moe_attn_prefill_join_kernel(MoeAttnArgs a, int tiles_max, int splits) {
+    using C = PCfg<D>;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int col = (blockIdx.x % (kCols / 8)) * 8 + (threadIdx.x >> 5), blk = blockIdx.x / (kCols / 8);
+    const int n_items = a.b.n_seqs * a.n_kv, lane = threadIdx.x & 31;
+    const int b = blk % n_items / a.n_kv, h = blk % a.n_kv;
+    const Seq s = seq_of<kCols>(a, b);
+    const int c = (tiles_max - 1 - blk / n_items) * kCols + col;
+    if (c >= s.ncol) return;
+    const float *rec = a.part + (int64_t)blk * splits * C::kRec + (int64_t)col * (D + 2);
+    float m = -INFINITY, l = 0.f, o[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
+    for (int p = 0; p < splits; ++p) m = fmaxf(m, rec[p * C::kRec + D]);
+#pragma unroll 4
+    for (int p = 0; p < splits; ++p) {
+        const float *r = rec + p * C::kRec;
+        const float f = r[D] == -INFINITY && r[D + 1] == 0.f ? 0.f : ex2(r[D] - m);
+        l = fmaf(f, r[D + 1], l);
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+            const float2 v = *(const float2 *)(r + 64 * i + 2 * lane);
+            // (a part without keys holds zeros)
+            o[2 * i] = fmaf(f, v.x, o[2 * i]);
+            o[2 * i + 1] = fmaf(f, v.y, o[2 * i + 1]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i)
+        store_out(a, s.q0 + c / a.group, h * a.group + c % a.group, D, 64 * i + 2 * lane, o[2 * i], o[2 * i + 1], m, l);
+}
+
+struct Shape {
+    int tiles_max, splits;
+    int64_t ctas;
+};
+
+Shape shape_of(int n_seqs, int n_kv, int group, int max_q, int max_kv, int nsm) {
+    Shape r;
+    r.tiles_max = (int)(((int64_t)max_q * group + kCols - 1) / kCols);
+    const int64_t items = (int64_t)r.tiles_max * n_seqs * n_kv;
+    // few items: split the keys so that the SMs are all used, in pieces of 4 steps at least
+    const int64_t most = std::max(1, max_kv / (4 * kN));
+    r.splits = (int)std::max<int64_t>(1, std::min<int64_t>(nsm / std::max<int64_t>(items, 1), most));
+    r.ctas = items * r.splits;
+    return r;
+}
+
+template <int D>
+cudaError_t launch(const MoeAttnArgs &a, int nsm, cudaStream_t st) {
+    using C = PCfg<D>;
+    const Shape g = shape_of(a.b.n_seqs, a.n_kv, a.group, a.b.max_q, a.b.max_kv, nsm);
+    cudaError_t err = cudaFuncSetAttribute(moe_attn_prefill_kernel<D>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (err != cudaSuccess) return err;
+    err = launch_pdl(moe_attn_prefill_kernel<D>, dim3((unsigned)g.ctas), dim3(kThreadsP), C::kSmem, st, a,
+                     g.tiles_max, g.splits);
+    if (err != cudaSuccess || g.splits == 1) return err;
+    return launch_pdl(moe_attn_prefill_join_kernel<D>, dim3((unsigned)(g.ctas / g.splits * (kCols / 8))),
+                      dim3(256), 0, st, a, g.tiles_max, g.splits);
+}
+
+}  // namespace
+
+bool moe_attn_prefill_fits(int n_seqs, int n_kv, int group, int max_q, int max_kv, int nsm) {
+    if ((int64_t)group * max_q < MOE_ATTN_PREFILL_COLS) return false;
+    return shape_of(n_seqs, n_kv, group, max_q, max_kv, nsm).ctas <= (1 << 24);
+}
+
+size_t moe_attn_prefill_ws_bytes(int head_dim, int n_seqs, int n_kv, int group, int max_q, int max_kv,
+                                 int nsm) {
+    const Shape g = shape_of(n_seqs, n_kv, group, max_q, max_kv, nsm);
+    return g.splits == 1 ? 0 : (size_t)g.ctas * kCols * (head_dim + 2) * sizeof(float);
+}
+
+cudaError_t moe_launch_attn_prefill(int head_dim, const MoeAttnArgs &a, int nsm, cudaStream_t st) {
+    return head_dim == 64 ? launch<64>(a, nsm, st) : launch<128>(a, nsm, st);
+}

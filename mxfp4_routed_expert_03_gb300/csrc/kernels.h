@@ -295,5 +295,14 @@ struct MoeAttnArgs {
     int *status;
     long long timeout_cycles;
 };
-size_t moe_attn_ws_bytes(int head_dim, int group, int max_q, int max_kv, int nsm);
+size_t moe_attn_ws_bytes(int head_dim, int n_seqs, int n_kv, int group, int max_q, int max_kv,
+                         int nsm);
 cudaError_t moe_launch_attn(int head_dim, const MoeAttnArgs &a, int nsm, cudaStream_t st);
+
+// attn_prefill.cu: the same with many query rows per sequence, from this many
+// columns (query rows x heads of a key/value head) of the longest sequence on
+#define MOE_ATTN_PREFILL_COLS 64
+bool moe_attn_prefill_fits(int n_seqs, int n_kv, int group, int max_q, int max_kv, int nsm);
+size_t moe_attn_prefill_ws_bytes(int head_dim, int n_seqs, int n_kv, int group, int max_q, int max_kv,
+                                 int nsm);
+cudaError_t moe_launch_attn_prefill(int head_dim, const MoeAttnArgs &a, int nsm, cudaStream_t st);

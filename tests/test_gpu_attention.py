@@ -453,3 +453,80 @@ def test_refusals():
     assert a.norm_rope(2, s.q, None, None, rope, s.q, None) == bad
     assert a.norm_rope(2, s.q, None, pos, rope, None, None) == bad
     assert a.status() == 0
+
+
+# ------------------------------------------------------------------ many query rows
+@pytest.mark.parametrize("H,KV,d,page", [(8, 1, 128, 16), (16, 2, 64, 64), (6, 2, 128, 128), (33, 1, 64, 32)])
+@pytest.mark.parametrize("window", [0, 1, 100, 200])
+def test_many_rows_per_sequence(H, KV, d, page, window):
+    """Column tiles of 128 and 256 begun, filled and passed; sequences without
+    keys, with fewer keys than rows, and with keys that split over the SMs."""
+    Setup(H, KV, d, page, [64, 3, 31, 40], [130, 700, 31, 0], seed=window + H, window=window).check()
+
+
+def test_many_rows_long_keys_split_over_the_gpu():
+    s = Setup(8, 1, 128, 32, [10, 9], [5000, 2600], seed=30)
+    s.check()
+    first = s.out.clone()
+    s.run()
+    assert torch.equal(first, s.out)
+
+
+def test_many_rows_large_logits_and_value_magnitudes():
+    Setup(8, 2, 128, 32, [40], [500], seed=31, q_scale=30.0).check()
+    Setup(8, 2, 64, 32, [40], [300], seed=32, v_scale=1e30).check()
+    Setup(8, 2, 128, 32, [40], [300], seed=33, v_scale=1e-30).check()
+    Setup(8, 2, 128, 32, [40], [300], seed=34, v_exp=5).check()
+    Setup(8, 2, 64, 32, [40], [200], seed=35, scale=-0.3).check()
+    Setup(8, 2, 64, 32, [40], [200], seed=36, scale=0.0).check()
+
+
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+@pytest.mark.parametrize("window", [0, 20])
+def test_many_rows_non_finite_keys_values_queries(bad, window):
+    from mxfp4_routed_expert_03_gb300 import check
+    s = Setup(8, 2, 64, 16, [40], [200], seed=37, window=window)
+    at = 170                               # seen by rows from 10 on (and, windowed, before 30)
+    slot = (s.table[0, at // 16] * 16 + at % 16).view(1).int()
+    k, v = _randn(1, 128, seed=97), _randn(1, 128, seed=96)
+    s.k[0][at], s.v[0][at] = ref.mxfp4(k).view(2, 64), ref.mxfp4(v).view(2, 64)
+    v[0, 64 + 40] = bad
+    check(s.attn.append(1, k, v, slot), "append")
+    last = 10 + window if window else 40
+    o, l_, mag, big = s.want()
+    hit = torch.zeros(40, 8, 64, dtype=torch.bool, device=DEV)
+    hit[10:last, 4:, 32:] = True
+    for step in range(3):
+        if step == 1:                      # a key of head 0: its rows
+            k[0, 3] = bad
+            check(s.attn.append(1, k, v, slot), "append")
+            hit[10:last, :4] = True
+        if step == 2:                      # a query row of one head
+            s.q[5, 6 * 64 + 1] = bad
+            hit[5, 6] = True
+        out, lse = s.run()
+        assert s.attn.status() == 0
+        out = out.double().view(40, 8, 64)
+        assert bool(torch.isnan(out[hit]).all())
+        ok = (out - o).abs() <= BF16_EPS * o.abs() + 2.0 ** -9 * mag
+        assert bool(ok[~hit].all())
+
+
+def test_many_rows_bad_pages_are_left_out():
+    from mxfp4_routed_expert_03_gb300 import MOE_ERR_BAD_INDEX
+    s = Setup(8, 2, 64, 16, [40], [200], seed=38)
+    s.check()
+    s.table[0, 2] = -1                     # tokens 32 .. 47
+    s.run()
+    assert s.attn.status() == MOE_ERR_BAD_INDEX
+    keep = [j for j in range(200) if not 32 <= j < 48]
+    s.k[0], s.v[0], s.kv = s.k[0][keep], s.v[0][keep], [184]
+    o, l_, mag, big = s.want()             # (every row sits behind token 47)
+    _close(s.out, s.lse, o.view(40, -1), l_, mag.view(40, -1), big)
+
+
+def test_both_kernels_agree_at_their_border():
+    """63 and 64 columns of the same sequence: the rows they share are the
+    same to the bounds of either kernel."""
+    for n in (63, 64):
+        Setup(1, 1, 128, 16, [n], [300], seed=39).check()
