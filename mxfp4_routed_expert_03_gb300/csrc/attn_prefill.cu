@@ -7,9 +7,10 @@
 //   P_t = 2^(S_t - m)    (a thread per row: TMEM -> registers -> TMEM, fp16)
 //   O_t += P_t V         (P from TMEM over S's columns, V from shared memory)
 // so the tensor cores work on one tile while the other's softmax runs: warps
-// 0-3 hold tile A's rows, 4-7 tile B's, 8-11 turn the cache's codes into
-// operands (each key and value once per CTA, i.e. once per 256 columns), 12
-// issues the MMAs. TMEM is full: S_A, S_B, O_A, O_B of 128 columns each.
+// 0-3 hold tile A's rows, 4-7 tile B's, 8-13 turn the cache's codes into
+// operands (each key and value once per CTA, i.e. once per 256 columns), 14
+// and 15 issue the tiles' MMAs. TMEM is full: S_A, S_B, O_A, O_B of 128
+// columns each.
 //
 // Operands are fp16: a code is exact, and its scale enters as 2^(e - R + 12)
 // with R the largest key exponent (or, per block of 32 dimensions, the largest
@@ -32,7 +33,14 @@ namespace {
 constexpr int kM = 128;          // rows of a tile (columns of the item)
 constexpr int kCols = 2 * kM;    // columns of a CTA
 constexpr int kN = 128;          // keys per step
-constexpr int kWarpsP = 13;
+// warps 0-7 rows, 8-10 keys, 11-13 values, 14 and 15 MMA issue of tile A and B
+// (one issuer's instructions take longer than the products: about 90 cycles
+// each, against 64)
+constexpr int kWarpsP = 16;
+constexpr int kWarpK = 8, kWarpV = 11, kWarpMma = 14, kConv = 3;
+// registers of a thread: 128 at launch, moved to the warps that hold rows (a
+// row's 128 logits stay in registers): 8 x 176 + 8 x 80 = 16 x 128
+constexpr int kRegsRows = 176, kRegsRest = 80;
 constexpr int kThreadsP = 32 * kWarpsP;
 constexpr int kInfo = 4;         // steps whose masks are kept
 constexpr int kHead = 12;        // operands carry 2^12
@@ -50,17 +58,18 @@ struct PCfg {
 };
 
 struct StepInfo {
-    uint32_t live[4];     // tokens whose page is in the cache
-    uint32_t nan[4][4];   // [block][word]: values that are NaN
-    uint32_t any_nan[4];  // by word
+    uint32_t any_gone[kConv], any_nan[kConv];  // by key or value warp
+    uint32_t gone[kConv][4];    // [warp][word]: tokens without a page in the cache
+    uint32_t nan[kConv][4][4];  // [warp][block][word]: values that are NaN
 };
 
-// 32 consecutive TMEM columns of each lane, complete on return.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+// 32 consecutive TMEM columns of each lane; the registers hold them after
+// tc::tmem_ld_wait().
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
         "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-        "%30, %31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+        "%30, %31}, [%32];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
           "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
           "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
@@ -69,7 +78,7 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         : "r"(taddr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
         "%12, %13, %14, %15, %16};" ::"r"(taddr),
@@ -77,7 +86,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
         "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
@@ -126,6 +135,149 @@ __device__ __forceinline__ uint32_t factor_of(uint32_t e, int R) {
     return (uint32_t)min(max((int)e - R + 15 + kHead, 0), 15 + kHead) * 0x04000400u;
 }
 
+// A warp's share of the codes of K or V (3 warps each, loads dealt in turn):
+// each step into the operand buffer of its stage, the next step's codes on
+// their way meanwhile. A lane takes one block of 32 dimensions of one token; 8
+// tokens a quarter warp, so that codes are read in whole lines and written
+// without bank conflicts. rmax: the exponent that the lane's block is taken
+// against. (One code for both, which the six warps share in the instruction
+// cache.)
+template <int D, typename Wait>
+__device__ __forceinline__ void convert(const MoeAttnArgs &a, bool v, int h, const int32_t *pages, int first,
+                                        int n, int lo_all, int hi_all, int w, int rmax, uint8_t *ops,
+                                        uint64_t *full, uint64_t *empty, StepInfo *info, const Wait &wait) {
+    using C = PCfg<D>;
+    constexpr int NB = C::NB, OCT = 4 / NB;  // octets of tokens that a load of the warp covers
+    constexpr int LOADS = (16 / OCT + kConv - 1) / kConv;
+    const int lane = threadIdx.x & 31, tl = lane & 7, k = (lane >> 3) % NB;
+    const int in_page_mask = (1 << a.page_shift) - 1;
+    const uint8_t *codes = v ? a.c.v_q : a.c.k_q, *scales = v ? a.c.v_s : a.c.k_s;
+    uint4 cq[LOADS];
+    uint32_t sb[LOADS], have = 0u;  // scale bytes; bit i: load i has its page
+    int id[LOADS];                  // pages of the next step's loads
+    auto row_of = [&](int i) {      // token of load i within a step (kN and more: none)
+        return 8 * ((w + kConv * i) * OCT + (lane >> 3) / NB) + tl;
+    };
+    auto page_id = [&](int j, int i) {
+        const int tok = first + kN * j + row_of(i);
+        return j < n && row_of(i) < kN && tok < hi_all ? pages[tok >> a.page_shift] : -1;
+    };
+    auto load = [&](int j, int i) {
+        cq[i] = make_uint4(0u, 0u, 0u, 0u);
+        sb[i] = 0u;
+        have &= ~(1u << i);
+        // (nothing here may look at a loaded value: it would wait for it)
+        if (id[i] >= 0 && id[i] < a.n_pages) {
+            have |= 1u << i;
+            const int o = (first + kN * j + row_of(i)) & in_page_mask;
+            const int64_t row = (((int64_t)id[i] * a.n_kv + h) << a.page_shift) + (o & ~7);
+            cq[i] = *(const uint4 *)(codes + row * (NB * 16) + k * 128 + tl * 16);
+            sb[i] = scales[(row + (v ? tl & 6 : tl)) * NB + (v ? 2 * k + (tl & 1) : k)];
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+        id[i] = page_id(0, i);
+        load(0, i);
+        id[i] = page_id(1, i);
+    }
+    for (int j = 0; j < n; ++j) {
+        const int st = j & 1;
+        if (!wait(&empty[st], ((j >> 1) & 1) ^ 1)) return;  // (a fresh barrier counts as passed)
+        uint32_t odd = 0u;  // loads with tokens that every row leaves out, or NaN values: rare
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int r = row_of(i);
+            if (r < kN) {
+                // a NaN key makes its token's logits NaN (rows that do not see it
+                // mask them); a NaN value counts as 0 here and reaches its rows at the end
+                const bool nan = sb[i] == 255u;
+                const uint32_t fac = nan ? (v ? 0u : 0x7E007E00u) : factor_of(sb[i], rmax);
+                if (v ? nan && first + kN * j + r >= lo_all : !((have >> i) & 1u)) odd |= 1u << i;
+                uint8_t *dst = ops + st * C::kOp + (k >> 1) * C::kHalf + (r >> 3) * 1024 + (r & 7) * 128;
+                const uint32_t wd[4] = {cq[i].x, cq[i].y, cq[i].z, cq[i].w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t x[4];
+                    codes_f16(wd[q], x);
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) x[z] = mul_f16x2(x[z], fac);
+                    *(uint4 *)(dst + (((4 * (k & 1) + q) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+                }
+            }
+            // the next step's, on its way over the other loads and the wait
+            load(j + 1, i);
+            id[i] = page_id(j + 2, i);
+        }
+        StepInfo &f = info[j % kInfo];
+        const bool any = __any_sync(kFull, odd != 0u);
+        if (any) {
+#pragma unroll 1
+            for (int q = 0; q < 4 * NB; ++q) {  // word q % 4 (of block q / 4)
+                uint32_t bits = 0u;
+#pragma unroll
+                for (int i = 0; i < LOADS; ++i)
+                    if (((odd >> i) & 1u) && row_of(i) >> 5 == q % 4 && (!v || k == q / 4))
+                        bits |= 1u << (row_of(i) & 31);
+                bits = __reduce_or_sync(kFull, bits);
+                if (lane == 0) {
+                    if (v) f.nan[w][q / 4][q % 4] = bits;
+                    else f.gone[w][q % 4] = bits;
+                }
+            }
+        }
+        if (lane == 0) (v ? f.any_nan : f.any_gone)[w] = any ? 1u : 0u;
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&full[st]);
+    }
+}
+
+// Column tiles of sequence b whose last column sees L keys or more (its last
+// ones), L >= 1.
+__device__ __forceinline__ int tiles_from(const Seq &s, int group, int L) {
+    const int64_t c = (int64_t)(L - 1 - (s.kv - s.nq)) * group;  // the first column that does
+    return c <= 0 ? s.cts : c >= s.ncol ? 0 : s.cts - (int)(c / kCols);
+}
+
+// The r-th (sequence, column tile): the longest first, so that the last CTAs to
+// start are short. The order is by the keys that a tile sees, found by
+// bisection; for many sequences (whose CTAs are many) by column tile alone.
+// False if there are fewer. Warp-collective.
+__device__ __forceinline__ bool item_of(const MoeAttnArgs &a, int tiles_max, int r, int &b, int &ct) {
+    const int lane = threadIdx.x & 31, B = a.b.n_seqs;
+    if (B > 32) {
+        b = r % B;
+        ct = tiles_max - 1 - r / B;
+        return ct >= 0 && ct * (int64_t)kCols < seq_of<kCols>(a, b).ncol;
+    }
+    Seq s = {};
+    if (lane < B) s = seq_of<kCols>(a, lane);
+    // the largest L with more than r tiles of L keys or more (0: any tile)
+    int L = 0;
+    for (int bit = 30; bit >= 0; --bit) {
+        const int t = L | (1 << bit);
+        if (t <= a.b.max_kv &&
+            (int)__reduce_add_sync(kFull, lane < B ? (unsigned)tiles_from(s, a.group, t) : 0u) > r)
+            L = t;
+    }
+    // those of exactly L keys, in order of sequence and tile, behind the longer ones
+    const int more = lane < B ? tiles_from(s, a.group, L + 1) : 0;
+    const int from = lane < B ? (L == 0 ? s.cts : tiles_from(s, a.group, L)) : 0;
+    int skip = r - (int)__reduce_add_sync(kFull, (unsigned)more), at = from - more;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(kFull, at, off);
+        if (lane >= off) at += o;
+    }
+    const uint32_t m = __ballot_sync(kFull, at > skip);
+    if (m == 0u) return false;
+    b = __ffs(m) - 1;
+    skip -= __shfl_sync(kFull, at - (from - more), b);
+    ct = __shfl_sync(kFull, s.cts - from, b) + skip;
+    return true;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreadsP, 1)
     moe_attn_prefill_kernel(MoeAttnArgs a, int tiles_max, int splits) {
@@ -134,7 +286,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     __shared__ __align__(8) uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2],
-        o_full[2], drain;
+        o_full[2], drain[2], b_start;
     __shared__ StepInfo info[kInfo];
     __shared__ int s_rk, s_rv[NB], s_abort;
     __shared__ uint32_t s_tmem;
@@ -142,13 +294,11 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 
     grid_dep_wait();
     grid_dep_launch();
-    // the last column tiles (the longest, under a causal mask) first
-    const int n_items = a.b.n_seqs * a.n_kv;
-    const int split = blockIdx.x % splits, blk = blockIdx.x / splits;
-    const int ct_rev = blk / n_items, b = blk % n_items / a.n_kv, h = blk % a.n_kv;
+    const int split = blockIdx.x % splits, blk = blockIdx.x / splits, h = blk % a.n_kv;
+    int b, ct;
+    if (!item_of(a, tiles_max, blk / a.n_kv, b, ct)) return;
     const Seq s = seq_of<kCols>(a, b);
-    const int ct = tiles_max - 1 - ct_rev, c0 = ct * kCols;
-    if (c0 >= s.ncol) return;
+    const int c0 = ct * kCols;
     const int G = a.group, p0 = s.kv - s.nq;
     const int i0 = c0 / G, i1 = (min(c0 + kCols, s.ncol) - 1) / G;
     const bool two = c0 + kM < s.ncol;  // tile B has columns
@@ -163,21 +313,22 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&k_full[i], 4);
-            tc::mbar_init(&k_empty[i], 1);
-            tc::mbar_init(&v_full[i], 4);
-            tc::mbar_init(&v_empty[i], 1);
+            tc::mbar_init(&k_full[i], kConv);
+            tc::mbar_init(&k_empty[i], two ? 2 : 1);
+            tc::mbar_init(&v_full[i], kConv);
+            tc::mbar_init(&v_empty[i], two ? 2 : 1);
+            tc::mbar_init(&drain[i], 1);
             tc::mbar_init(&s_full[i], 2);
             tc::mbar_init(&p_full[i], 4);
-            tc::mbar_init(&o_full[i], 1);
+            tc::mbar_init(&o_full[i], 2);
         }
-        tc::mbar_init(&drain, 1);
+        tc::mbar_init(&b_start, 4);
         tc::fence_mbar_init();
         s_abort = 0;
         s_rk = 0;
         for (int k = 0; k < NB; ++k) s_rv[k] = 0;
     }
-    if (wid == kWarpsP - 1) {
+    if (wid == kWarpMma) {
         tc::tmem_alloc(&s_tmem, 512);
         tc::tmem_relinquish();
     }
@@ -284,6 +435,10 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         return false;
     };
 
+    if (wid < 8)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRows));
+    else
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (wid < 8) {
         // ------------------------------------------------ softmax: a thread per row
         const int t = wid >> 2;
@@ -295,9 +450,31 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             const int hi_min = p0 + it0 + 1, lo_max = W > 0 ? max(0, p0 + it1 + 1 - W) : 0;
             const int hi = c < s.ncol ? p0 + c / G + 1 : 0x7FFFFFFF;
             const int lo = c < s.ncol && W > 0 ? hi - W : 0;
-            // logits: S x mul x 2^(R - 127 - 12)
-            const float mr = mul * exp2f((float)(s_rk - 127 - kHead));
+            // logits: S x mul x 2^(R - 127 - 12); not 0, for masked columns are -inf
+            float mr = mul * exp2f((float)(s_rk - 127 - kHead));
+            if (mr == 0.f) mr = 1.17549435e-38f;
             float m = -INFINITY, l = 0.f;  // m: the maximum in use
+            // tokens tok0 + 32 q .. + 31 that the row sees
+            auto seen = [&](int tok0, int q) {
+                const int above = min(max(hi - (tok0 + 32 * q), 0), 32);
+                const int below = min(max(lo - (tok0 + 32 * q), 0), 32);
+                const uint32_t up = above == 32 ? kFull : (1u << above) - 1u;
+                const uint32_t dn = below == 32 ? kFull : (1u << below) - 1u;
+                return up & ~dn;
+            };
+            // blocks in which the row sees a NaN value in step j (read once PV(j)
+            // was issued, so behind the value warps' masks)
+            auto nan_seen = [&](int j) {
+                const StepInfo &f = info[j % kInfo];
+                uint32_t r = 0u;
+                if ((f.any_nan[0] | f.any_nan[1] | f.any_nan[2]) != 0u)
+                    for (int w = 0; w < kConv; ++w)
+                        if (f.any_nan[w])
+                            for (int q = 0; q < 4; ++q)
+                                for (int k = 0; k < NB; ++k)
+                                    if (seen(first + kN * j, q) & f.nan[w][k][q]) r |= 1u << k;
+                return r;
+            };
             uint32_t nan_blocks = 0u;
             bool ok = true;
             for (int j = 0; j < n; ++j) {
@@ -308,43 +485,33 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 tc::tc_fence_after();
                 const StepInfo &f = info[j % kInfo];
                 const int tok0 = first + kN * j;
-                const bool edge = tok0 + kN > hi_min || tok0 < lo_max ||
-                                  (f.live[0] & f.live[1] & f.live[2] & f.live[3]) != kFull;
-                // tokens of 32-column chunk q that the row sees
-                auto seen = [&](int q) {
-                    const int above = min(max(hi - (tok0 + 32 * q), 0), 32);
-                    const int below = min(max(lo - (tok0 + 32 * q), 0), 32);
-                    const uint32_t up = above == 32 ? kFull : (1u << above) - 1u;
-                    const uint32_t dn = below == 32 ? kFull : (1u << below) - 1u;
-                    return up & ~dn & f.live[q];
+                const bool gone = (f.any_gone[0] | f.any_gone[1] | f.any_gone[2]) != 0u;
+                const bool edge = tok0 + kN > hi_min || tok0 < lo_max || gone;
+                // columns of chunk q that the row does not see become -inf
+                auto hide = [&](int q, uint32_t *y) {
+                    uint32_t see = seen(tok0, q);
+                    if (gone)
+                        for (int w = 0; w < kConv; ++w)
+                            if (f.any_gone[w]) see &= ~f.gone[w][q];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (!((see >> i) & 1u)) y[i] = 0xFF800000u;
                 };
-                float mx = -INFINITY;
-                uint32_t x[32];
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                if (j > 0) nan_blocks |= nan_seen(j - 1);
+                {
+                    uint32_t x[128];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    tmem_ld32(sp + 32 * q, x);
+                    for (int q = 0; q < 4; ++q) tmem_ld32(sp + 32 * q, x + 32 * q);
+                    tc::tmem_ld_wait();
                     if (edge) {
-                        const uint32_t see = seen(q);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            mx = fmaxf(mx, (see >> i) & 1u ? __uint_as_float(x[i]) : -INFINITY);
-                    } else {
-                        float m1 = -INFINITY;
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            mx = fmaxf(mx, __uint_as_float(x[i]));
-                            m1 = fmaxf(m1, __uint_as_float(x[i + 1]));
-                        }
-                        mx = fmaxf(mx, m1);
+                        for (int q = 0; q < 4; ++q) hide(q, x + 32 * q);
                     }
-                }
-                if ((f.any_nan[0] | f.any_nan[1] | f.any_nan[2] | f.any_nan[3]) != 0u) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-#pragma unroll
-                        for (int k = 0; k < NB; ++k)
-                            if (seen(q) & f.nan[k][q]) nan_blocks |= 1u << k;
+                    for (int i = 0; i < 128; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(x[i]));
                 }
+                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 const float top = mx * mr;  // (-inf x 0 is NaN: no key seen)
                 const bool rise = mx > -INFINITY && top > m + (m == -INFINITY ? 0.f : kLag);
                 if (__any_sync(kFull, rise)) {
@@ -359,10 +526,12 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                         const float fo = rise ? fac : 1.f;
 #pragma unroll 1
                         for (int q = 0; q < D / 32; ++q) {
-                            tmem_ld32(op + 32 * q, x);
+                            uint32_t y[32];
+                            tmem_ld32(op + 32 * q, y);
+                            tc::tmem_ld_wait();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * fo);
-                            tmem_st32(op + 32 * q, x);
+                            for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * fo);
+                            tmem_st32(op + 32 * q, y);
                         }
                         tmem_st_wait();
                     }
@@ -372,20 +541,19 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                     }
                 }
                 const float ms = m == -INFINITY ? 0.f : m;
+                // (a small loop body, read again from TMEM: unrolled over the step the
+                // code alone outran the instruction cache)
                 float l0 = 0.f, l1 = 0.f;
-#pragma unroll
+#pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
+                    uint32_t x[32], p[16];
                     tmem_ld32(sp + 32 * q, x);
-                    uint32_t p[16];
-                    const uint32_t see = edge ? seen(q) : kFull;
+                    tc::tmem_ld_wait();
+                    if (edge) hide(q, x);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        float y0 = ex2(fmaf(__uint_as_float(x[2 * i]), mr, -ms));
-                        float y1 = ex2(fmaf(__uint_as_float(x[2 * i + 1]), mr, -ms));
-                        if (edge) {
-                            y0 = (see >> (2 * i)) & 1u ? y0 : 0.f;
-                            y1 = (see >> (2 * i + 1)) & 1u ? y1 : 0.f;
-                        }
+                        const float y0 = ex2(fmaf(__uint_as_float(x[2 * i]), mr, -ms));
+                        const float y1 = ex2(fmaf(__uint_as_float(x[2 * i + 1]), mr, -ms));
                         l0 += y0;
                         l1 += y1;
                         p[i] = pack_f16(y0, y1);
@@ -396,12 +564,16 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 tmem_st_wait();
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&p_full[t]);
+                if (lane == 0) {
+                    tc::mbar_arrive(&p_full[t]);
+                    if (t == 0 && j == 0) tc::mbar_arrive(&b_start);
+                }
             }
             // ------------------------------------------------ output
             if (ok && n > 0) ok = wait(&o_full[t], n - 1);
             if (ok) {
                 tc::tc_fence_after();
+                if (n > 0) nan_blocks |= nan_seen(n - 1);
                 const bool live_row = c < s.ncol;
                 const int row = s.q0 + c / G, head = h * G + c % G;
                 float *rec = a.part + (int64_t)blockIdx.x * C::kRec + (int64_t)tid * (D + 2);
@@ -410,6 +582,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 for (int q = 0; q < D / 32; ++q) {
                     uint32_t x[32];
                     if (n > 0) tmem_ld32(op + 32 * q, x);
+                    tc::tmem_ld_wait();
                     const float back = exp2f((float)(s_rv[q] - 127 - kHead));
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
@@ -450,183 +623,66 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             }
             tc::tc_fence_before();
         }
-    } else if (wid < kWarpsP - 1) {
+    } else if (wid < kWarpMma) {
         // ------------------------------------------------ codes to operands
-        const int dw = wid - 8;  // tokens 32 dw .. of a step
-        const int tl = lane & 7, k = (lane >> 3) % NB;
-        constexpr int OCT = 4 / NB;  // octets that a load of the warp covers
-        const int rk = s_rk, rv = s_rv[k];
-        uint4 kq[NB], vq[NB];
-        uint32_t kb[NB], vb[NB];  // scale bytes; bit 8: the page is there; bit 9: some row may see it
-        int id[NB], nid[NB];
-        auto token_of = [&](int j, int i) {  // of load i
-            return first + kN * j + 32 * dw + 8 * (i * OCT + (lane >> 3) / NB) + tl;
-        };
-        auto page_ids = [&](int j, int (&o)[NB]) {
-#pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                const int tok = token_of(j, i);
-                o[i] = j < n && tok < hi_all ? pages[tok >> a.page_shift] : -1;
-            }
-        };
-        auto load = [&](int j) {
-#pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                const int tok = token_of(j, i);
-                kq[i] = vq[i] = make_uint4(0u, 0u, 0u, 0u);
-                kb[i] = vb[i] = 0u;
-                if (j < n && tok < hi_all && id[i] >= 0 && id[i] < a.n_pages) {
-                    const int o = tok & in_page_mask;
-                    const int64_t row = (((int64_t)id[i] * a.n_kv + h) << a.page_shift) + (o & ~7);
-                    const int64_t code = row * (NB * 16) + k * 128 + tl * 16;
-                    kq[i] = *(const uint4 *)(a.c.k_q + code);
-                    vq[i] = *(const uint4 *)(a.c.v_q + code);
-                    kb[i] = a.c.k_s[(row + tl) * NB + k] | 0x100u | (tok >= lo_all ? 0x200u : 0u);
-                    vb[i] = a.c.v_s[((row + tl) >> 1) * (2 * NB) + 2 * k + (tl & 1)] | 0x100u;
-                }
-            }
-        };
-        page_ids(0, id);
-        load(0);
-        page_ids(1, nid);
-        for (int j = 0; j < n; ++j) {
-            const int st = j & 1;
-            const uint32_t free_par = ((j >> 1) & 1) ^ 1;  // a fresh barrier counts as passed
-            if (!wait(&k_empty[st], free_par)) break;
-            uint32_t live = 0u, nan = 0u;
-#pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                const uint32_t bit = 1u << (8 * (i * OCT + (lane >> 3) / NB) + tl);
-                if (kb[i] & 0x100u) live |= bit;
-                if ((vb[i] & 0xFFu) == 255u && (kb[i] & 0x200u)) nan |= bit;
-            }
-            live = __reduce_or_sync(kFull, live);
-            const bool any_nan = __any_sync(kFull, nan != 0u);
-            StepInfo &f = info[j % kInfo];
-            if (any_nan) {
-#pragma unroll
-                for (int b4 = 0; b4 < NB; ++b4) {
-                    const uint32_t w = __reduce_or_sync(kFull, k == b4 ? nan : 0u);
-                    if (lane == 0) f.nan[b4][dw] = w;
-                }
-            } else if (lane < NB) {
-                f.nan[lane][dw] = 0u;
-            }
-            if (lane == 0) {
-                f.live[dw] = live;
-                f.any_nan[dw] = any_nan ? 1u : 0u;
-            }
-            // K rows (tokens) of 64 elements, 128-byte swizzle
-#pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                const int r = 32 * dw + 8 * (i * OCT + (lane >> 3) / NB) + tl;
-                const uint32_t e = kb[i] & 0xFFu;
-                const uint32_t fac = e == 255u && (kb[i] & 0x200u) ? 0x7E007E00u : factor_of(e, rk);
-                uint8_t *dst = smem + C::kSmemK + st * C::kOp + (k >> 1) * C::kHalf + (r >> 3) * 1024 + (r & 7) * 128;
-                const uint32_t w[4] = {kq[i].x, kq[i].y, kq[i].z, kq[i].w};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t x[4];
-                    codes_f16(w[q], x);
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) x[z] = mul_f16x2(x[z], fac);
-                    *(uint4 *)(dst + (((4 * (k & 1) + q) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
-                }
-            }
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&k_full[st]);
-            if (!wait(&v_empty[st], free_par)) break;
-            // V the same way: rows are the contracted index there
-#pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                const int r = 32 * dw + 8 * (i * OCT + (lane >> 3) / NB) + tl;
-                const uint32_t e = vb[i] & 0xFFu;
-                const uint32_t fac = e == 255u ? 0u : factor_of(e, rv);
-                uint8_t *dst = smem + C::kSmemV + st * C::kOp + (k >> 1) * C::kHalf + (r >> 3) * 1024 + (r & 7) * 128;
-                const uint32_t w[4] = {vq[i].x, vq[i].y, vq[i].z, vq[i].w};
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t x[4];
-                    codes_f16(w[q], x);
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) x[z] = mul_f16x2(x[z], fac);
-                    *(uint4 *)(dst + (((4 * (k & 1) + q) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
-                }
-            }
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&v_full[st]);
-#pragma unroll
-            for (int i = 0; i < NB; ++i) id[i] = nid[i];
-            load(j + 1);
-            page_ids(j + 2, nid);
-        }
+        const bool v = wid >= kWarpV;
+        convert<D>(a, v, h, pages, first, n, lo_all, hi_all, wid - (v ? kWarpV : kWarpK),
+                   v ? s_rv[(lane >> 3) % NB] : s_rk, smem + (v ? C::kSmemV : C::kSmemK), v ? v_full : k_full,
+                   v ? v_empty : k_empty, info, wait);
     } else {
-        // ------------------------------------------------ MMA issue (lane 0)
+        // ------------------------------------------------ MMA issue of a tile (lane 0)
+        const int t = wid - kWarpMma;
         const uint32_t idesc_s = idesc_f16(kM, kN, false), idesc_o = idesc_f16(kM, D, true);
-        const uint32_t sb = tc::smem_u32(smem);
-        auto qk = [&](int t, int j) {
-            const uint64_t ad = tc::sdesc_sw128(sb + C::kSmemQ + t * C::kOp);
-            const uint64_t bd = tc::sdesc_sw128(sb + C::kSmemK + (j & 1) * C::kOp);
-            if (lane == 0) {
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    const uint64_t o = (uint64_t)(((i >> 2) * C::kHalf + (i & 3) * 32) >> 4);
-                    tc::mma_bf16(tmem + 128 * t, ad + o, bd + o, idesc_s, i > 0);
-                }
-                tc::mma_commit(&s_full[t]);
-                // (orders the step's masks, seen behind k_full, before the softmax)
-                tc::mbar_arrive(&s_full[t]);
-            }
-        };
-        auto pv = [&](int t, int j) {
-            const uint64_t bd = sdesc_mn(sb + C::kSmemV + (j & 1) * C::kOp, C::kHalf);
-            if (lane == 0) {
-#pragma unroll
-                for (int i = 0; i < kN / 16; ++i)
-                    mma_f16_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * i, bd + (uint64_t)(i * 2048 >> 4),
-                               idesc_o, (j > 0 || i > 0) ? 1u : 0u);
-                tc::mma_commit(&o_full[t]);
-            }
-        };
+        const uint32_t sb = tc::smem_u32(smem), ts = tmem + 128 * t, to = tmem + 256 + 128 * t;
+        const uint64_t qd = tc::sdesc_sw128(sb + C::kSmemQ + t * C::kOp);
         bool ok = true;
-        if (n > 0) {
-            ok = wait(&k_full[0], 0);
-            if (ok) {
-                qk(0, 0);
-                if (two) qk(1, 0);
-                if (lane == 0) tc::mma_commit(&k_empty[0]);
+        if (t == 0 || two) {
+            // tile B starts behind A's first softmax: in step, both tiles would
+            // wait for the tensor cores and then for the exponentials together
+            if (t == 1 && n > 0) ok = wait(&b_start, 0);
+            for (int j = 0; j <= n && n > 0 && ok; ++j) {
+                if (j > 0) {  // O += P V of step j - 1
+                    const int st = (j - 1) & 1;
+                    ok = wait(&v_full[st], (j - 1) >> 1) && wait(&p_full[t], j - 1);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    const uint64_t bd = sdesc_mn(sb + C::kSmemV + st * C::kOp, C::kHalf);
+                    if (lane == 0) {
+#pragma unroll
+                        for (int i = 0; i < kN / 16; ++i)
+                            mma_f16_ts(to, ts + 8 * i, bd + (uint64_t)(i * 2048 >> 4), idesc_o,
+                                       (j > 1 || i > 0) ? 1u : 0u);
+                        tc::mma_commit(&o_full[t]);
+                        tc::mma_commit(&v_empty[st]);
+                        // orders the step's masks, seen behind v_full, before the rows' reads
+                        tc::mbar_arrive(&o_full[t]);
+                    }
+                }
+                if (j < n) {  // S = Q K^T of step j (after PV, which reads P over S)
+                    const int st = j & 1;
+                    ok = wait(&k_full[st], j >> 1);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    const uint64_t bd = tc::sdesc_sw128(sb + C::kSmemK + st * C::kOp);
+                    if (lane == 0) {
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            const uint64_t o = (uint64_t)(((i >> 2) * C::kHalf + (i & 3) * 32) >> 4);
+                            tc::mma_bf16(ts, qd + o, bd + o, idesc_s, i > 0);
+                        }
+                        tc::mma_commit(&s_full[t]);
+                        tc::mma_commit(&k_empty[st]);
+                        tc::mbar_arrive(&s_full[t]);  // (as above, behind k_full)
+                    }
+                }
+                __syncwarp();
             }
+            if (lane == 0 && !ok) tc::drain_mmas(&drain[t], limit);  // MMAs in flight end before TMEM goes
         }
-        for (int j = 0; j < n && ok; ++j) {
-            const bool more = j + 1 < n;
-            ok = wait(&v_full[j & 1], j >> 1) && wait(&p_full[0], j);
-            if (!ok) break;
-            tc::tc_fence_after();
-            pv(0, j);
-            if (more) {
-                ok = wait(&k_full[(j + 1) & 1], (j + 1) >> 1);
-                if (!ok) break;
-                qk(0, j + 1);
-            }
-            if (two) {
-                ok = wait(&p_full[1], j);
-                if (!ok) break;
-                tc::tc_fence_after();
-                pv(1, j);
-            }
-            if (lane == 0) tc::mma_commit(&v_empty[j & 1]);
-            if (more) {
-                if (two) qk(1, j + 1);
-                if (lane == 0) tc::mma_commit(&k_empty[(j + 1) & 1]);
-            }
-        }
-        if (lane == 0 && !ok) tc::drain_mmas(&drain, limit);  // MMAs in flight end before TMEM goes
         __syncwarp();
     }
     __syncthreads();
-    if (wid == kWarpsP - 1) {
+    if (wid == kWarpMma) {
         tc::tc_fence_after();
         tc::tmem_dealloc(tmem, 512);
     }
@@ -639,10 +695,11 @@ __global__ void __launch_bounds__(256) moe_attn_prefill_join_kernel(MoeAttnArgs 
     grid_dep_wait();
     grid_dep_launch();
     const int col = (blockIdx.x % (kCols / 8)) * 8 + (threadIdx.x >> 5), blk = blockIdx.x / (kCols / 8);
-    const int n_items = a.b.n_seqs * a.n_kv, lane = threadIdx.x & 31;
-    const int b = blk % n_items / a.n_kv, h = blk % a.n_kv;
+    const int lane = threadIdx.x & 31, h = blk % a.n_kv;
+    int b, ct;
+    if (!item_of(a, tiles_max, blk / a.n_kv, b, ct)) return;
     const Seq s = seq_of<kCols>(a, b);
-    const int c = (tiles_max - 1 - blk / n_items) * kCols + col;
+    const int c = ct * kCols + col;
     if (c >= s.ncol) return;
     const float *rec = a.part + (int64_t)blk * splits * C::kRec + (int64_t)col * (D + 2);
     float m = -INFINITY, l = 0.f, o[D / 32];
