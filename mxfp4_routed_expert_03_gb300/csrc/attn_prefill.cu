@@ -58,7 +58,12 @@ struct PCfg {
 };
 
 struct StepInfo {
-    uint32_t any_gone[kConv], any_nan[kConv];  // by key or value warp
+    union {
+        struct {
+            uint8_t any_gone[8], any_nan[8];  // by key or value warp
+        };
+        uint64_t any[2];  // the same, all at once
+    };
     uint32_t gone[kConv][4];    // [warp][word]: tokens without a page in the cache
     uint32_t nan[kConv][4][4];  // [warp][block][word]: values that are NaN
 };
@@ -155,32 +160,38 @@ __device__ __forceinline__ void convert(const MoeAttnArgs &a, bool v, int h, con
     uint4 cq[LOADS];
     uint32_t sb[LOADS], have = 0u;  // scale bytes; bit i: load i has its page
     int id[LOADS];                  // pages of the next step's loads
-    auto row_of = [&](int i) {      // token of load i within a step (kN and more: none)
-        return 8 * ((w + kConv * i) * OCT + (lane >> 3) / NB) + tl;
-    };
-    auto page_id = [&](int j, int i) {
-        const int tok = first + kN * j + row_of(i);
-        return j < n && row_of(i) < kN && tok < hi_all ? pages[tok >> a.page_shift] : -1;
-    };
-    auto load = [&](int j, int i) {
-        cq[i] = make_uint4(0u, 0u, 0u, 0u);
-        sb[i] = 0u;
-        have &= ~(1u << i);
-        // (nothing here may look at a loaded value: it would wait for it)
-        if (id[i] >= 0 && id[i] < a.n_pages) {
-            have |= 1u << i;
-            const int o = (first + kN * j + row_of(i)) & in_page_mask;
-            const int64_t row = (((int64_t)id[i] * a.n_kv + h) << a.page_shift) + (o & ~7);
-            cq[i] = *(const uint4 *)(codes + row * (NB * 16) + k * 128 + tl * 16);
-            sb[i] = scales[(row + (v ? tl & 6 : tl)) * NB + (v ? 2 * k + (tl & 1) : k)];
+    const int row0 = 8 * (w * OCT + (lane >> 3) / NB) + tl;
+    auto row_of = [&](int i) { return row0 + 8 * kConv * OCT * i; };  // token of load i within a step
+    auto page_ids = [&](int j) {  // (-1: none; a step has kN tokens)
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int tok = first + kN * j + row_of(i);
+            id[i] = -1;
+            if (j < n && row_of(i) < kN && tok < hi_all) id[i] = pages[tok >> a.page_shift];
         }
     };
+    // this lane's block in the first octet of a page, and its scale
+    codes += k * 128 + tl * 16;
+    scales += v ? (tl & 6) * NB + 2 * k + (tl & 1) : tl * NB + k;
+    auto load = [&](int j) {
+        have = 0u;
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-        id[i] = page_id(0, i);
-        load(0, i);
-        id[i] = page_id(1, i);
-    }
+        for (int i = 0; i < LOADS; ++i) {
+            cq[i] = make_uint4(0u, 0u, 0u, 0u);
+            sb[i] = 0u;
+            // (nothing here may look at a loaded value: it would wait for it)
+            if ((uint32_t)id[i] < (uint32_t)a.n_pages) {
+                have |= 1u << i;
+                const uint64_t row = (((uint64_t)(uint32_t)id[i] * (uint32_t)a.n_kv + (uint32_t)h) << a.page_shift) +
+                                     (uint32_t)((first + kN * j + row_of(i)) & in_page_mask & ~7);
+                cq[i] = *(const uint4 *)(codes + row * (NB * 16));
+                sb[i] = scales[row * NB];
+            }
+        }
+    };
+    page_ids(0);
+    load(0);
+    page_ids(1);
     for (int j = 0; j < n; ++j) {
         const int st = j & 1;
         if (!wait(&empty[st], ((j >> 1) & 1) ^ 1)) return;  // (a fresh barrier counts as passed)
@@ -205,9 +216,6 @@ __device__ __forceinline__ void convert(const MoeAttnArgs &a, bool v, int h, con
                     *(uint4 *)(dst + (((4 * (k & 1) + q) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
                 }
             }
-            // the next step's, on its way over the other loads and the wait
-            load(j + 1, i);
-            id[i] = page_id(j + 2, i);
         }
         StepInfo &f = info[j % kInfo];
         const bool any = __any_sync(kFull, odd != 0u);
@@ -226,10 +234,12 @@ __device__ __forceinline__ void convert(const MoeAttnArgs &a, bool v, int h, con
                 }
             }
         }
-        if (lane == 0) (v ? f.any_nan : f.any_gone)[w] = any ? 1u : 0u;
+        if (lane == 0) (v ? f.any_nan : f.any_gone)[w] = any ? 1 : 0;
         tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&full[st]);
+        load(j + 1);  // on its way over the wait
+        page_ids(j + 2);
     }
 }
 
@@ -322,6 +332,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             tc::mbar_init(&p_full[i], 4);
             tc::mbar_init(&o_full[i], 2);
         }
+        for (int i = 0; i < kInfo; ++i) info[i].any[0] = info[i].any[1] = 0u;
         tc::mbar_init(&b_start, 4);
         tc::fence_mbar_init();
         s_abort = 0;
@@ -467,7 +478,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             auto nan_seen = [&](int j) {
                 const StepInfo &f = info[j % kInfo];
                 uint32_t r = 0u;
-                if ((f.any_nan[0] | f.any_nan[1] | f.any_nan[2]) != 0u)
+                if (f.any[1] != 0u)
                     for (int w = 0; w < kConv; ++w)
                         if (f.any_nan[w])
                             for (int q = 0; q < 4; ++q)
@@ -485,18 +496,24 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 tc::tc_fence_after();
                 const StepInfo &f = info[j % kInfo];
                 const int tok0 = first + kN * j;
-                const bool gone = (f.any_gone[0] | f.any_gone[1] | f.any_gone[2]) != 0u;
-                const bool edge = tok0 + kN > hi_min || tok0 < lo_max || gone;
-                // columns of chunk q that the row does not see become -inf
-                auto hide = [&](int q, uint32_t *y) {
-                    uint32_t see = seen(tok0, q);
-                    if (gone)
-                        for (int w = 0; w < kConv; ++w)
-                            if (f.any_gone[w]) see &= ~f.gone[w][q];
+                const bool gone = f.any[0] != 0u;
+                // few steps: columns that the row does not see become -inf in TMEM
+                if (tok0 + kN > hi_min || tok0 < lo_max || gone) {
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t x[32], see = seen(tok0, q);
+                        tmem_ld32(sp + 32 * q, x);
+                        if (gone)
+                            for (int w = 0; w < kConv; ++w)
+                                if (f.any_gone[w]) see &= ~f.gone[w][q];
+                        tc::tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (!((see >> i) & 1u)) y[i] = 0xFF800000u;
-                };
+                        for (int i = 0; i < 32; ++i)
+                            if (!((see >> i) & 1u)) x[i] = 0xFF800000u;
+                        tmem_st32(sp + 32 * q, x);
+                    }
+                    tmem_st_wait();
+                }
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                 if (j > 0) nan_blocks |= nan_seen(j - 1);
                 {
@@ -504,10 +521,6 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) tmem_ld32(sp + 32 * q, x + 32 * q);
                     tc::tmem_ld_wait();
-                    if (edge) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) hide(q, x + 32 * q);
-                    }
 #pragma unroll
                     for (int i = 0; i < 128; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(x[i]));
                 }
@@ -549,7 +562,6 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                     uint32_t x[32], p[16];
                     tmem_ld32(sp + 32 * q, x);
                     tc::tmem_ld_wait();
-                    if (edge) hide(q, x);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const float y0 = ex2(fmaf(__uint_as_float(x[2 * i]), mr, -ms));
