@@ -6,7 +6,7 @@
 
 #include "../../include/moe.h"
 
-#define MOE_PLAN_CHUNK 64
+#define MOE_PLAN_CHUNK 32  // tokens
 
 // Optional events bracketing one kernel (see moe_profile_kernel).
 struct MoeProf {
@@ -25,9 +25,10 @@ static inline bool moe_plan_is_small(int T) { return T <= 64; }
 size_t moe_plan_ws_bytes(int T, int E);
 cudaError_t moe_launch_plan(int T, int E, int k, const float *logits, const moe_plan_buf *p,
                             void *ws, int *status, cudaStream_t st);
-// The plan of a large batch (not moe_plan_is_small) whose topk_idx is there.
-cudaError_t moe_launch_plan_build(int T, int E, int k, const moe_plan_buf *p, void *ws, int *status,
-                                  cudaStream_t st);
+// The plan of a large batch (not moe_plan_is_small) whose topk_idx is there;
+// counted: the chunks' counts are in ws too.
+cudaError_t moe_launch_plan_build(int T, int E, int k, bool counted, const moe_plan_buf *p, void *ws,
+                                  int *status, cudaStream_t st);
 
 // route_scored.cu
 cudaError_t moe_launch_plan_scored(int T, int E, int k, const float *logits,

@@ -59,76 +59,103 @@ __global__ void __launch_bounds__(256) moe_topk_kernel(int T, int E, int k,
     if (__any_sync(FULL_MASK, nan_seen) && lane == 0) moe_flag(status, MOE_ERR_NAN_LOGIT);
 }
 
-// chunk_counts[c][e]: rows of expert e among tokens [c*CH, (c+1)*CH).
-__global__ void __launch_bounds__(256) moe_plan_count_kernel(int T, int E, int k, int CH,
+// chunk_counts[c][e]: rows of expert e among the 32 tokens of chunk c; a block
+// per chunk (see plan_chunk_mask).
+__global__ void __launch_bounds__(256) moe_plan_count_kernel(int T, int E, int k,
                                                              const int32_t *__restrict__ idx,
                                                              int32_t *chunk_counts, int *status) {
-    extern __shared__ int s_hist[];  // 8 warps x E
-    int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    int c = blockIdx.x * 8 + wid;
-    int nchunks = (T + CH - 1) / CH;
-    int *h = s_hist + wid * E;
-    for (int e = lane; e < E; e += 32) h[e] = 0;
-    __syncwarp();
-    if (c < nchunks) {
-        int64_t f0 = (int64_t)c * CH * k;
-        int64_t f1 = min((int64_t)(c + 1) * CH, (int64_t)T) * k;
-        for (int64_t f = f0 + lane; f < f1; f += 32) {
-            int e = idx[f];
-            if (e >= 0 && e < E) atomicAdd(&h[e], 1);
-            else moe_flag(status, MOE_ERR_BAD_INDEX);
-        }
-        __syncwarp();
-        for (int e = lane; e < E; e += 32) chunk_counts[(int64_t)c * E + e] = h[e];
-    }
+    __shared__ uint32_t s_mask[MOE_MAX_EXPERTS];
+    plan_chunk_mask(s_mask, T, E, k, blockIdx.x, idx, status);
+    for (int e = threadIdx.x; e < E; e += blockDim.x)
+        chunk_counts[(int64_t)blockIdx.x * E + e] = __popc(s_mask[e]);
 }
 
-// Column scan of chunk_counts (in place -> chunk bases), counts, offsets, active.
-__global__ void __launch_bounds__(1024) moe_plan_scan_kernel(int T, int E, int k, int nchunks,
-                                                             int32_t *chunk_counts,
-                                                             int32_t *counts, int32_t *offsets,
-                                                             int32_t *active) {
-    __shared__ int s_tot[33];
-    int e = threadIdx.x;
-    int run = 0;
+// Per expert, chunk_counts to exclusive prefixes over the chunks (in place) and
+// their total to counts. A block takes 32 experts (a 128-byte line per chunk),
+// each warp a range of chunks: its sum, the ranges' prefixes, then the chunks'.
+__global__ void __launch_bounds__(1024) moe_plan_scan_kernel(int E, int nchunks, int32_t *chunk_counts,
+                                                             int32_t *counts) {
+    __shared__ int s_sum[32][33];
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int per = (nchunks + 31) / 32, c0 = wid * per, c1 = min(c0 + per, nchunks);
+    int sum = 0;
     if (e < E) {
-        for (int c = 0; c < nchunks; ++c) {
-            int v = chunk_counts[(int64_t)c * E + e];
-            chunk_counts[(int64_t)c * E + e] = run;
-            run += v;
+#pragma unroll 8
+        for (int c = c0; c < c1; ++c) sum += chunk_counts[(int64_t)c * E + e];
+    }
+    s_sum[wid][lane] = sum;
+    __syncthreads();
+    int run = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < 32; ++w) {
+        if (w == wid) run = total;
+        total += s_sum[w][lane];
+    }
+    if (e >= E) return;
+    for (int c = c0; c < c1; c += 8) {
+        int v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c + i < c1 ? chunk_counts[(int64_t)(c + i) * E + e] : 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (c + i < c1) chunk_counts[(int64_t)(c + i) * E + e] = run;
+            run += v[i];
         }
     }
-    int total;
-    int off = block_exclusive_scan<32>(run, s_tot, total);
-    int a = block_exclusive_scan<32>(run > 0 ? 1 : 0, s_tot, total);
-    if (e < E) {
-        counts[e] = run;
-        offsets[e] = off;
-        if (run > 0) active[1 + a] = e;
-    }
-    if (e == 0) {
-        offsets[E] = T * k;
-        active[0] = total;
-    }
+    if (wid == 0) counts[e] = total;
 }
 
-__global__ void __launch_bounds__(256) moe_plan_scatter_kernel(int T, int E, int k, int CH,
+// A block per chunk: position of every entry = offsets[e] (scanned from counts
+// by each block) + rows of e in earlier chunks + tokens of the chunk before it
+// that chose e. Block 0 writes offsets and active.
+__global__ void __launch_bounds__(256) moe_plan_scatter_kernel(int T, int E, int k,
                                                                const int32_t *__restrict__ idx,
-                                                               const int32_t *chunk_base,
-                                                               const int32_t *offsets,
-                                                               int32_t *perm, int32_t *inv,
-                                                               int *status) {
-    extern __shared__ int s_next[];  // 8 warps x E
-    int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    int c = blockIdx.x * 8 + wid;
-    int nchunks = (T + CH - 1) / CH;
-    if (c >= nchunks) return;
-    int *nx = s_next + wid * E;
-    for (int e = lane; e < E; e += 32) nx[e] = offsets[e] + chunk_base[(int64_t)c * E + e];
-    __syncwarp();
-    int64_t f0 = (int64_t)c * CH * k;
-    int64_t f1 = min((int64_t)(c + 1) * CH, (int64_t)T) * k;
-    warp_stable_scatter(idx, f0, f1, E, nx, perm, inv, status);
+                                                               const int32_t *__restrict__ chunk_base,
+                                                               moe_plan_buf p, int *status) {
+    __shared__ uint32_t s_mask[MOE_MAX_EXPERTS];
+    __shared__ int s_off[MOE_MAX_EXPERTS], s_tot[33];
+    static_assert(MOE_MAX_EXPERTS == 4 * 256, "four experts per thread in the scans");
+    grid_dep_wait();
+    grid_dep_launch();
+    const int e0 = 4 * threadIdx.x, c = blockIdx.x;
+    int n[4], sum = 0, used = 0, total;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        n[i] = e0 + i < E ? p.counts[e0 + i] : 0;
+        sum += n[i];
+        used += n[i] > 0 ? 1 : 0;
+    }
+    plan_chunk_mask(s_mask, T, E, k, c, idx, status);
+    int off = block_exclusive_scan<8>(sum, s_tot, total);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        s_off[e0 + i] = off;
+        if (c == 0 && e0 + i < E) p.offsets[e0 + i] = off;
+        off += n[i];
+    }
+    if (c == 0) {
+        int at = block_exclusive_scan<8>(used, s_tot, total);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n[i] > 0) p.active[1 + at++] = e0 + i;
+        if (threadIdx.x == 0) {
+            p.offsets[E] = T * k;
+            p.active[0] = total;
+        }
+    }
+    __syncthreads();
+    const int64_t f0 = (int64_t)c * MOE_PLAN_CHUNK * k;
+    const int nf = (int)(min((int64_t)(c + 1) * MOE_PLAN_CHUNK, (int64_t)T) * k - f0);
+    for (int i = threadIdx.x; i < nf; i += 256) {
+        const int e = idx[f0 + i];
+        if (e < 0 || e >= E) continue;  // (flagged above)
+        const int pos = s_off[e] + chunk_base[(int64_t)c * E + e] +
+                        __popc(s_mask[e] & ((1u << (i / k)) - 1u));
+        p.perm[pos] = (int32_t)(f0 + i);
+        p.inv[f0 + i] = pos;
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -147,21 +174,21 @@ cudaError_t moe_launch_plan(int T, int E, int k, const float *logits, const moe_
                           T, E, k, logits, *p, status);
     }
     moe_topk_kernel<<<(T + 7) / 8, 256, 0, st>>>(T, E, k, logits, p->topk_idx, p->topk_w, status);
-    return moe_launch_plan_build(T, E, k, p, ws, status, st);
+    return moe_launch_plan_build(T, E, k, false, p, ws, status, st);
 }
 
-cudaError_t moe_launch_plan_build(int T, int E, int k, const moe_plan_buf *p, void *ws, int *status,
-                                  cudaStream_t st) {
-    int CH = MOE_PLAN_CHUNK;
-    int nchunks = (T + CH - 1) / CH;
+cudaError_t moe_launch_plan_build(int T, int E, int k, bool counted, const moe_plan_buf *p, void *ws,
+                                  int *status, cudaStream_t st) {
+    const int nchunks = (T + MOE_PLAN_CHUNK - 1) / MOE_PLAN_CHUNK;
     int32_t *chunk = (int32_t *)ws;
-    size_t sm = (size_t)8 * E * sizeof(int);
-    moe_plan_count_kernel<<<(nchunks + 7) / 8, 256, sm, st>>>(T, E, k, CH, p->topk_idx, chunk,
-                                                              status);
-    moe_plan_scan_kernel<<<1, 1024, 0, st>>>(T, E, k, nchunks, chunk, p->counts, p->offsets,
-                                             p->active);
-    moe_plan_scatter_kernel<<<(nchunks + 7) / 8, 256, sm, st>>>(T, E, k, CH, p->topk_idx, chunk,
-                                                                p->offsets, p->perm, p->inv,
-                                                                status);
-    return cudaGetLastError();
+    if (!counted)
+        moe_plan_count_kernel<<<nchunks, 256, 0, st>>>(T, E, k, p->topk_idx, chunk, status);
+    cudaError_t err = cudaGetLastError();
+    if (err == cudaSuccess)
+        err = launch_pdl(moe_plan_scan_kernel, dim3((E + 31) / 32), dim3(1024), 0, st, E, nchunks, chunk,
+                         p->counts);
+    if (err == cudaSuccess)
+        err = launch_pdl(moe_plan_scatter_kernel, dim3(nchunks), dim3(256), 0, st, T, E, k,
+                         (const int32_t *)p->topk_idx, (const int32_t *)chunk, *p, status);
+    return err;
 }

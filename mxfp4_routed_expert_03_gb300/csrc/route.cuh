@@ -302,28 +302,22 @@ __device__ __forceinline__ int block_exclusive_scan(int v, int *warp_tot, int &t
     return r;
 }
 
-// Stable scatter of the flat entries [f0, f1) in flat order by one warp.
-// cnt[e] holds the next free position of expert e and is advanced.
-__device__ __forceinline__ void warp_stable_scatter(const int32_t *idx, int64_t f0, int64_t f1,
-                                                    int E, int *cnt, int32_t *perm, int32_t *inv,
-                                                    int *status) {
-    int lane = threadIdx.x & 31;
-    for (int64_t base = f0; base < f1; base += 32) {
-        int64_t f = base + lane;
-        bool valid = f < f1;
-        int e = valid ? idx[f] : -1;
-        if (valid && (e < 0 || e >= E)) { moe_flag(status, MOE_ERR_BAD_INDEX); e = -1; }
-        uint32_t m = __match_any_sync(FULL_MASK, e);
-        if (e >= 0) {
-            int rank = __popc(m & lanemask_lt());
-            int pos = cnt[e] + rank;
-            perm[pos] = (int32_t)f;
-            inv[f] = pos;
-        }
-        __syncwarp();
-        if (e >= 0 && lane == 31 - __clz(m)) cnt[e] += __popc(m);
-        __syncwarp();
+// mask[e]: the tokens of chunk c (of MOE_PLAN_CHUNK) that chose expert e, a bit
+// each; a token chooses an expert at most once, so a mask holds both the
+// expert's rows in the chunk and the order among them. Block-wide.
+__device__ __forceinline__ void plan_chunk_mask(uint32_t *mask, int T, int E, int k, int c,
+                                                const int32_t *__restrict__ idx, int *status) {
+    static_assert(MOE_PLAN_CHUNK == 32, "a bit per token");
+    for (int e = threadIdx.x; e < E; e += blockDim.x) mask[e] = 0u;
+    __syncthreads();
+    const int64_t f0 = (int64_t)c * MOE_PLAN_CHUNK * k;
+    const int nf = (int)(min((int64_t)(c + 1) * MOE_PLAN_CHUNK, (int64_t)T) * k - f0);
+    for (int i = threadIdx.x; i < nf; i += blockDim.x) {
+        const int e = idx[f0 + i];
+        if (e >= 0 && e < E) atomicOr(&mask[e], 1u << (i / k));
+        else moe_flag(status, MOE_ERR_BAD_INDEX);
     }
+    __syncthreads();
 }
 
 constexpr int kPlanSmallThreads = 512;

@@ -11,8 +11,14 @@
 // of the exponentials rounded once: a warp adds them as unevaluated pairs of
 // floats (Knuth's two-sum), whose total is exact to about 2^-45, in any order.
 //
-// Bound: 4 E bytes per token from HBM; one warp per token keeps the E <= 1024
-// sort keys in registers (32 per lane).
+// Bound: 4 E bytes per token from HBM; the instructions of the selection come
+// close to it. Without groups every score is first taken approximately (two
+// MUFU operations instead of expf and a divide); the k-th largest of the 32
+// lanes' maxima is a lower bound of the k-th score, what lies above it (less
+// the approximation's error, twice) is a candidate, and only the candidates,
+// about one per lane, get their exact score and are ranked. More than 64
+// candidates (many equal scores, k near 32) and groups take exact scores of
+// all experts.
 #include "route.cuh"
 
 using namespace moe_route;
@@ -60,26 +66,37 @@ __device__ __forceinline__ float load_logit(const float *row, int e, bool &nan_s
 template <int NK>
 __device__ __forceinline__ void keep_groups(uint32_t (&key)[NK], const ScoreArgs &a, int lane) {
     const int gs = a.E / a.r.n_groups;
-    uint32_t mine = 0u;  // lane g: group g's score as a key
-    for (int g = 0; g < a.r.n_groups; ++g) {
-        uint32_t m1 = 0u, m2 = 0u;
+    uint32_t b1 = 0u, b2 = 0u;  // lane g: group g's two largest keys
+    if (gs % 32 == 0) {         // row i (experts 32 i ..) lies in one group
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
-            const int e = lane + 32 * i;
-            const uint32_t v = (e >= g * gs && e < (g + 1) * gs) ? key[i] : 0u;
-            m2 = max(m2, min(m1, v));
-            m1 = max(m1, v);
+            const uint32_t t1 = __reduce_max_sync(FULL_MASK, key[i]);
+            const int first = __ffs(__ballot_sync(FULL_MASK, key[i] == t1)) - 1;
+            const uint32_t t2 = __reduce_max_sync(FULL_MASK, lane == first ? 0u : key[i]);
+            if (lane == 32 * i / gs) {
+                b2 = max(max(b2, min(b1, t1)), t2);
+                b1 = max(b1, t1);
+            }
         }
-        const uint32_t t1 = __reduce_max_sync(FULL_MASK, m1);
-        uint32_t sk = t1;
-        if (a.r.group_top == 2) {
+    } else {
+        for (int g = 0; g < a.r.n_groups; ++g) {
+            uint32_t m1 = 0u, m2 = 0u;
+#pragma unroll
+            for (int i = 0; i < NK; ++i) {
+                const int e = lane + 32 * i;
+                const uint32_t v = (e >= g * gs && e < (g + 1) * gs) ? key[i] : 0u;
+                m2 = max(m2, min(m1, v));
+                m1 = max(m1, v);
+            }
+            const uint32_t t1 = __reduce_max_sync(FULL_MASK, m1);
             const int first = __ffs(__ballot_sync(FULL_MASK, m1 == t1)) - 1;
             const uint32_t t2 = __reduce_max_sync(FULL_MASK, lane == first ? m2 : m1);
-            const float v = __fadd_rn(key_logit(t1), key_logit(t2));
-            sk = logit_key(v);
+            if (lane == g) b1 = t1, b2 = t2;
         }
-        if (lane == g) mine = sk;
     }
+    const uint32_t mine = lane >= a.r.n_groups ? 0u
+                          : a.r.group_top == 1 ? b1
+                                               : logit_key(__fadd_rn(key_logit(b1), key_logit(b2)));
     int better = 0;
     for (int g = 0; g < a.r.n_groups; ++g) {
         const uint32_t o = __shfl_sync(FULL_MASK, mine, g);
@@ -94,31 +111,93 @@ __device__ __forceinline__ void keep_groups(uint32_t (&key)[NK], const ScoreArgs
     }
 }
 
-// One warp's token: lane j < k gets the j-th selected expert and its weight.
-// scratch as for warp_topk.
-template <int NK, bool SIGMOID, bool THR>
-__device__ __forceinline__ void warp_scored_topk(const float *row, const ScoreArgs &a, int lane,
-                                                 int &my_e, float &my_w, bool &nan_seen,
-                                                 uint2 *scratch) {
-    uint32_t key[NK];
-    float mx = -INFINITY, sum = 1.f;
-    float v[NK];
+// The sort key of an exact score.
+__device__ __forceinline__ uint32_t select_key(float p, float bias, bool &nan_seen) {
+    p = __fadd_rn(p, bias);
+    if (!(p < INFINITY)) {  // NaN, or an infinite bias
+        nan_seen = true;
+        p = -INFINITY;
+    }
+    return logit_key(p);
+}
+
+// Values of lanes in descending order over the lanes (bitonic).
+__device__ __forceinline__ uint32_t warp_sort32(uint32_t m, int lane) {
+#pragma unroll
+    for (int K = 2; K <= 32; K <<= 1) {
+#pragma unroll
+        for (int J = K >> 1; J > 0; J >>= 1) {
+            const uint32_t o = __shfl_xor_sync(FULL_MASK, m, J);
+            const bool take_max = ((lane & K) == 0) == ((lane & J) == 0);
+            m = take_max ? (m > o ? m : o) : (m > o ? o : m);
+        }
+    }
+    return m;
+}
+
+// The k first of n <= 64 candidates (key, expert) that lie in scratch in
+// ascending order of experts: lane j < k gets the j-th.
+__device__ __forceinline__ void rank_candidates(uint2 *scratch, int n, int k, int lane, int &e_out) {
+    const uint2 c0 = lane < n ? scratch[lane] : make_uint2(0u, 0u);
+    const uint2 c1 = lane + 32 < n ? scratch[lane + 32] : make_uint2(0u, 0u);
+    int r0 = 0, r1 = 0;
+    // before a candidate come larger keys, and equal ones further up
+#pragma unroll 4
+    for (int q = 0; q < n; ++q) {
+        const uint32_t o = scratch[q].x;
+        r0 += o + (q < lane ? 1u : 0u) > c0.x ? 1 : 0;
+        if (n > 32) r1 += o + (q < lane + 32 ? 1u : 0u) > c1.x ? 1 : 0;
+    }
+    __syncwarp();
+    if (lane < n && r0 < k) scratch[r0] = c0;
+    if (lane + 32 < n && r1 < k) scratch[r1] = c1;
+    __syncwarp();
+    e_out = lane < k ? (int)scratch[lane].y : -1;
+    __syncwarp();
+}
+
+// Row positions of a lane: expert lane + 32 i in slot i.
+template <int NK>
+__device__ __forceinline__ void load_bias(const ScoreArgs &a, int lane, float (&bias)[NK]) {
 #pragma unroll
     for (int i = 0; i < NK; ++i) {
         const int e = lane + 32 * i;
-        v[i] = e < a.E ? load_logit(row, e, nan_seen) : -INFINITY;
+        bias[i] = a.bias && e < a.E ? a.bias[e] : 0.f;
     }
-    if constexpr (!SIGMOID) {
+}
+
+// One warp's token: lane j < k gets the j-th selected expert and its weight.
+// v: the token's logits (-inf past E). scratch: 64 entries of warp-private
+// shared memory.
+template <int NK, bool SIGMOID>
+__device__ __forceinline__ void warp_scored_topk(const float *row, float (&v)[NK], const float (&bias)[NK],
+                                                 const ScoreArgs &a, int lane, int &my_e, float &my_w,
+                                                 bool &nan_seen, uint2 *scratch) {
+    const float L2E = 1.44269504088896341f;
+    bool odd = false;  // a NaN logit
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+        if (v[i] != v[i]) {
+            odd = true;
+            v[i] = -INFINITY;
+        }
+    }
+    nan_seen |= odd;
+    float mx = -INFINITY, sum = 1.f;
+    if constexpr (!SIGMOID) {  // v becomes the exponentials
 #pragma unroll
         for (int i = 0; i < NK; ++i) mx = fmaxf(mx, v[i]);
 #pragma unroll
         for (int off = 16; off; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, off));
-        float s = 0.f, c = 0.f;
+        // each lane sums from 1, which no exponential exceeds: the rounding
+        // error of a sum is then three operations; the 32 ones go at the end
+        float s = 1.f, c = 0.f;
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
-            const int e = lane + 32 * i;
-            v[i] = e < a.E ? soft_exp(v[i], mx) : 0.f;
-            two_add(s, c, v[i]);
+            v[i] = lane + 32 * i < a.E ? soft_exp(v[i], mx) : 0.f;
+            const float t = __fadd_rn(s, v[i]);
+            c = __fadd_rn(c, __fsub_rn(v[i], __fsub_rn(t, s)));
+            s = t;
         }
 #pragma unroll
         for (int off = 16; off; off >>= 1) {
@@ -126,28 +205,73 @@ __device__ __forceinline__ void warp_scored_topk(const float *row, const ScoreAr
             c = __fadd_rn(c, __shfl_xor_sync(FULL_MASK, c, off));
             two_add(s, c, so);
         }
-        sum = __fadd_rn(s, c);
+        sum = __fadd_rn(__fsub_rn(s, 32.f), c);  // (the difference is exact)
     }
+    bool done = false;
+    if (a.r.n_groups == 1 && a.k <= 16) {
+        // approximate scores; error below 2^-21 (sigmoid) or 2^-22 of the
+        // largest score (softmax), and an addition's rounding
+        const float inv = SIGMOID ? 1.f : __frcp_rn(sum);
+        float s[NK], best = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < NK; ++i) {
-        const int e = lane + 32 * i;
-        key[i] = 0u;
-        if (e < a.E) {
-            float p = SIGMOID ? score_of<true>(v[i], 0.f, 1.f) : __fdiv_rn(v[i], sum);
-            if (a.bias) p = __fadd_rn(p, a.bias[e]);
-            if (!(p < INFINITY)) {  // NaN, or an infinite bias
-                nan_seen = true;
-                p = -INFINITY;
+        for (int i = 0; i < NK; ++i) {
+            float p;
+            if constexpr (SIGMOID) {
+                float x;
+                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(v[i] * -L2E));
+                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(1.f + x));
+            } else {
+                p = v[i] * inv;
             }
-            key[i] = logit_key(p);
+            s[i] = lane + 32 * i < a.E ? p + bias[i] : -INFINITY;
+            best = fmaxf(best, s[i]);  // (NaN is left out; +inf ends below)
+        }
+        const float t = key_logit(__shfl_sync(FULL_MASK, warp_sort32(logit_key(best), lane), a.k - 1));
+        const float bound = t - 2.f * (SIGMOID ? 0x1p-19f : 0x1p-20f) * ((SIGMOID ? 1.f : inv) + fabsf(t));
+        bool bad = false;
+        int n = 0;
+        if (t > -INFINITY && t < INFINITY) {
+#pragma unroll
+            for (int i = 0; i < NK; ++i) {
+                // NaN counts as a candidate here, so that it is seen
+                const bool c = !(s[i] < bound);
+                const uint32_t m = __ballot_sync(FULL_MASK, c);
+                const int at = n + __popc(m & lanemask_lt());
+                if (c && at < 64) scratch[at].y = (uint32_t)(lane + 32 * i);
+                n += __popc(m);
+            }
+            __syncwarp();
+            if (n <= 64) {  // exact keys
+#pragma unroll
+                for (int j = lane; j < 64; j += 32)
+                    if (j < n) {
+                        const int e = (int)scratch[j].y;
+                        bool ignored = false;
+                        const float p = score_of<SIGMOID>(load_logit(row, e, ignored), mx, sum);
+                        scratch[j].x = select_key(p, a.bias ? a.bias[e] : 0.f, bad);
+                    }
+                __syncwarp();
+                // (an expert that counts as -inf is no candidate: the other way)
+                if (!__any_sync(FULL_MASK, bad)) {
+                    rank_candidates(scratch, n, a.k, lane, my_e);
+                    done = true;
+                }
+            }
         }
     }
-    if (a.r.n_groups > 1) keep_groups<NK>(key, a, lane);
-    uint32_t kv;
-    if constexpr (THR)
+    if (!done) {
+        uint32_t key[NK];
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+            key[i] = 0u;
+            if (lane + 32 * i < a.E)
+                key[i] = select_key(SIGMOID ? score_of<true>(v[i], 0.f, 1.f) : __fdiv_rn(v[i], sum), bias[i],
+                                    nan_seen);
+        }
+        if (a.r.n_groups > 1) keep_groups<NK>(key, a, lane);
+        uint32_t kv;
         warp_select_thr<NK>(key, a.k, lane, scratch, my_e, kv);
-    else
-        warp_select<NK>(key, a.k, lane, scratch, my_e, kv);
+    }
     float w = 0.f;
     if (lane < a.k) {
         bool ignored = false;
@@ -162,6 +286,12 @@ __device__ __forceinline__ void warp_scored_topk(const float *row, const ScoreAr
     my_w = w * a.r.scale;
 }
 
+template <int NK>
+__device__ __forceinline__ void load_row(const float *row, int E, int lane, float (&v)[NK]) {
+#pragma unroll
+    for (int i = 0; i < NK; ++i) v[i] = lane + 32 * i < E ? row[lane + 32 * i] : -INFINITY;
+}
+
 // Small batches: as moe_plan_small_kernel, one CTA, a warp per token.
 template <int NK, bool SIGMOID>
 __global__ void __launch_bounds__(kPlanSmallThreads) moe_plan_scored_small_kernel(
@@ -172,35 +302,54 @@ __global__ void __launch_bounds__(kPlanSmallThreads) moe_plan_scored_small_kerne
     grid_dep_launch();
     plan_small_init(s);
     bool nan_seen = false;
+    float bias[NK], v[NK];
+    load_bias(a, lane, bias);
     for (int t = wid; t < T; t += kPlanSmallWarps) {
         int my_e;
         float my_w;
-        warp_scored_topk<NK, SIGMOID, true>(logits + (int64_t)t * a.E, a, lane, my_e, my_w,
-                                            nan_seen, s.scr[wid]);
+        load_row(logits + (int64_t)t * a.E, a.E, lane, v);
+        warp_scored_topk<NK, SIGMOID>(logits + (int64_t)t * a.E, v, bias, a, lane, my_e, my_w, nan_seen,
+                                      s.scr[wid]);
         plan_small_put(s, t, a.k, lane, my_e, my_w, p.topk_idx, p.topk_w);
     }
     plan_small_finish(s, T, a.E, a.k, nan_seen, p, status);
 }
 
+// Large batches: a block per chunk of 32 tokens, four tokens a warp, and the
+// chunk's rows per expert.
 template <int NK, bool SIGMOID>
-__global__ void __launch_bounds__(256) moe_topk_scored_kernel(int T, ScoreArgs a,
+__global__ void __launch_bounds__(256, 2) moe_topk_scored_kernel(int T, ScoreArgs a,
                                                               const float *__restrict__ logits,
                                                               int32_t *topk_idx, float *topk_w,
-                                                              int *status) {
+                                                              int32_t *chunk_counts, int *status) {
     __shared__ uint2 s_scratch[8][64];
+    __shared__ uint32_t s_mask[MOE_MAX_EXPERTS];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    const int t = blockIdx.x * 8 + wid;
-    if (t >= T) return;
-    int my_e;
-    float my_w;
+    grid_dep_wait();
+    grid_dep_launch();
+    for (int e = threadIdx.x; e < a.E; e += 256) s_mask[e] = 0u;
+    __syncthreads();
     bool nan_seen = false;
-    warp_scored_topk<NK, SIGMOID, false>(logits + (int64_t)t * a.E, a, lane, my_e, my_w, nan_seen,
-                                         s_scratch[wid]);
-    if (lane < a.k) {
-        topk_idx[(int64_t)t * a.k + lane] = my_e;
-        topk_w[(int64_t)t * a.k + lane] = my_w;
+    float bias[NK], v[NK];
+    load_bias(a, lane, bias);
+    for (int i = wid; i < MOE_PLAN_CHUNK; i += 8) {
+        const int t = blockIdx.x * MOE_PLAN_CHUNK + i;
+        if (t >= T) break;
+        int my_e;
+        float my_w;
+        load_row(logits + (int64_t)t * a.E, a.E, lane, v);
+        warp_scored_topk<NK, SIGMOID>(logits + (int64_t)t * a.E, v, bias, a, lane, my_e, my_w, nan_seen,
+                                      s_scratch[wid]);
+        if (lane < a.k) {
+            topk_idx[(int64_t)t * a.k + lane] = my_e;
+            topk_w[(int64_t)t * a.k + lane] = my_w;
+            atomicOr(&s_mask[my_e], 1u << i);
+        }
     }
     if (__any_sync(FULL_MASK, nan_seen) && lane == 0) moe_flag(status, MOE_ERR_NAN_LOGIT);
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += 256)
+        chunk_counts[(int64_t)blockIdx.x * a.E + e] = __popc(s_mask[e]);
 }
 
 template <int NK, bool SIGMOID>
@@ -209,9 +358,10 @@ cudaError_t launch(int T, const ScoreArgs &a, const float *logits, const moe_pla
     if (moe_plan_is_small(T))
         return launch_pdl(moe_plan_scored_small_kernel<NK, SIGMOID>, dim3(1),
                           dim3(kPlanSmallThreads), 0, st, T, a, logits, *p, status);
-    moe_topk_scored_kernel<NK, SIGMOID><<<(T + 7) / 8, 256, 0, st>>>(T, a, logits, p->topk_idx,
-                                                                    p->topk_w, status);
-    return moe_launch_plan_build(T, a.E, a.k, p, ws, status, st);
+    const int nchunks = (T + MOE_PLAN_CHUNK - 1) / MOE_PLAN_CHUNK;
+    const cudaError_t err = launch_pdl(moe_topk_scored_kernel<NK, SIGMOID>, dim3(nchunks), dim3(256), 0, st, T,
+                                       a, logits, p->topk_idx, p->topk_w, (int32_t *)ws, status);
+    return err != cudaSuccess ? err : moe_launch_plan_build(T, a.E, a.k, true, p, ws, status, st);
 }
 
 }  // namespace
@@ -224,6 +374,9 @@ cudaError_t moe_launch_plan_scored(int T, int E, int k, const float *logits,
     if (E <= 256)
         return sig ? launch<8, true>(T, a, logits, p, ws, status, st)
                    : launch<8, false>(T, a, logits, p, ws, status, st);
+    if (E <= 896)
+        return sig ? launch<28, true>(T, a, logits, p, ws, status, st)
+                   : launch<28, false>(T, a, logits, p, ws, status, st);
     return sig ? launch<32, true>(T, a, logits, p, ws, status, st)
                : launch<32, false>(T, a, logits, p, ws, status, st);
 }
