@@ -60,6 +60,14 @@ __device__ __forceinline__ float load_logit(const float *row, int e, bool &nan_s
     return l;
 }
 
+// The two largest keys of the lanes with `in` set.
+__device__ __forceinline__ void warp_top2(uint32_t key, bool in, int lane, uint32_t &t1, uint32_t &t2) {
+    const uint32_t v = in ? key : 0u;
+    t1 = __reduce_max_sync(FULL_MASK, v);
+    const int first = __ffs(__ballot_sync(FULL_MASK, v == t1)) - 1;
+    t2 = __reduce_max_sync(FULL_MASK, lane == first ? 0u : v);
+}
+
 // Keeps in key[] only the experts of the best groups (the others become 0,
 // below every real key). A group's score comes from its largest keys, found
 // with warp-wide maxima; lane g then ranks group g.
@@ -67,20 +75,33 @@ template <int NK>
 __device__ __forceinline__ void keep_groups(uint32_t (&key)[NK], const ScoreArgs &a, int lane) {
     const int gs = a.E / a.r.n_groups;
     uint32_t b1 = 0u, b2 = 0u;  // lane g: group g's two largest keys
-    if (gs % 32 == 0) {         // row i (experts 32 i ..) lies in one group
+    auto add = [&](int g, uint32_t t1, uint32_t t2) {
+        if (lane == g) {
+            b2 = max(max(b2, min(b1, t1)), t2);
+            b1 = max(b1, t1);
+        }
+    };
+    if (gs >= 32) {  // a row (experts 32 i ..) lies in one group or two
+        int g = 0, end = gs;
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
-            const uint32_t t1 = __reduce_max_sync(FULL_MASK, key[i]);
-            const int first = __ffs(__ballot_sync(FULL_MASK, key[i] == t1)) - 1;
-            const uint32_t t2 = __reduce_max_sync(FULL_MASK, lane == first ? 0u : key[i]);
-            if (lane == 32 * i / gs) {
-                b2 = max(max(b2, min(b1, t1)), t2);
-                b1 = max(b1, t1);
+            if (32 * i < a.E) {
+                uint32_t t1, t2;
+                if (end >= 32 * i + 32) {
+                    warp_top2(key[i], true, lane, t1, t2);
+                    add(g, t1, t2);
+                } else {
+                    warp_top2(key[i], 32 * i + lane < end, lane, t1, t2);
+                    add(g, t1, t2);
+                    warp_top2(key[i], 32 * i + lane >= end, lane, t1, t2);
+                    add(g + 1, t1, t2);
+                }
+                if (end <= 32 * i + 32) ++g, end += gs;
             }
         }
     } else {
         for (int g = 0; g < a.r.n_groups; ++g) {
-            uint32_t m1 = 0u, m2 = 0u;
+            uint32_t m1 = 0u, m2 = 0u, t2;
 #pragma unroll
             for (int i = 0; i < NK; ++i) {
                 const int e = lane + 32 * i;
@@ -90,8 +111,8 @@ __device__ __forceinline__ void keep_groups(uint32_t (&key)[NK], const ScoreArgs
             }
             const uint32_t t1 = __reduce_max_sync(FULL_MASK, m1);
             const int first = __ffs(__ballot_sync(FULL_MASK, m1 == t1)) - 1;
-            const uint32_t t2 = __reduce_max_sync(FULL_MASK, lane == first ? m2 : m1);
-            if (lane == g) b1 = t1, b2 = t2;
+            t2 = __reduce_max_sync(FULL_MASK, lane == first ? m2 : m1);
+            add(g, t1, t2);
         }
     }
     const uint32_t mine = lane >= a.r.n_groups ? 0u
@@ -104,10 +125,16 @@ __device__ __forceinline__ void keep_groups(uint32_t (&key)[NK], const ScoreArgs
     }
     const uint32_t kept =
         __ballot_sync(FULL_MASK, lane < a.r.n_groups && better < a.r.topk_groups);
+    // group of expert lane + 32 i, without a division per slot
+    int g = lane / gs, rem = lane % gs;
+    const int dg = 32 / gs, dr = 32 % gs;
 #pragma unroll
     for (int i = 0; i < NK; ++i) {
-        const int e = lane + 32 * i;
-        if (e < a.E && !((kept >> (e / gs)) & 1u)) key[i] = 0u;
+        if (!((kept >> g) & 1u)) key[i] = 0u;  // (past E the key is 0 already)
+        g += dg;
+        rem += dr;
+        if (rem >= gs) rem -= gs, ++g;
+        g = min(g, 31);
     }
 }
 
@@ -135,142 +162,203 @@ __device__ __forceinline__ uint32_t warp_sort32(uint32_t m, int lane) {
     return m;
 }
 
-// The k first of n <= 64 candidates (key, expert) that lie in scratch in
-// ascending order of experts: lane j < k gets the j-th.
-__device__ __forceinline__ void rank_candidates(uint2 *scratch, int n, int k, int lane, int &e_out) {
+// Positions of a warp's candidates: bit i of `mine` is expert lane + 32 i. Writes
+// the experts of up to 64 to scratch[].y and returns how many there are.
+__device__ __forceinline__ int gather_candidates(uint32_t mine, int lane, uint2 *scratch) {
+    const int c = __popc(mine);
+    int at = c;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(FULL_MASK, at, d);
+        if (lane >= d) at += o;
+    }
+    const int n = __shfl_sync(FULL_MASK, at, 31);
+    at -= c;
+    if (n <= 64)
+        for (; mine; mine &= mine - 1u) scratch[at++].y = (uint32_t)(lane + 32 * (__ffs(mine) - 1));
+    __syncwarp();
+    return n;
+}
+
+// The k first of n <= 64 candidates (key, expert) in scratch: lane j < k gets
+// the j-th expert.
+__device__ __forceinline__ int rank_candidates(uint2 *scratch, int n, int k, int lane) {
     const uint2 c0 = lane < n ? scratch[lane] : make_uint2(0u, 0u);
-    const uint2 c1 = lane + 32 < n ? scratch[lane + 32] : make_uint2(0u, 0u);
-    int r0 = 0, r1 = 0;
-    // before a candidate come larger keys, and equal ones further up
+    int r0 = 0;
 #pragma unroll 4
     for (int q = 0; q < n; ++q) {
-        const uint32_t o = scratch[q].x;
-        r0 += o + (q < lane ? 1u : 0u) > c0.x ? 1 : 0;
-        if (n > 32) r1 += o + (q < lane + 32 ? 1u : 0u) > c1.x ? 1 : 0;
+        const uint2 o = scratch[q];
+        r0 += o.x > c0.x || (o.x == c0.x && o.y < c0.y) ? 1 : 0;
+    }
+    uint2 c1 = make_uint2(0u, 0u);
+    int r1 = k;
+    if (n > 32) {
+        if (lane + 32 < n) c1 = scratch[lane + 32], r1 = 0;
+        for (int q = 0; q < n; ++q) {
+            const uint2 o = scratch[q];
+            r1 += o.x > c1.x || (o.x == c1.x && o.y < c1.y) ? 1 : 0;
+        }
     }
     __syncwarp();
     if (lane < n && r0 < k) scratch[r0] = c0;
-    if (lane + 32 < n && r1 < k) scratch[r1] = c1;
+    if (r1 < k) scratch[r1] = c1;
     __syncwarp();
-    e_out = lane < k ? (int)scratch[lane].y : -1;
+    const int e = lane < k ? (int)scratch[lane].y : -1;
     __syncwarp();
+    return e;
 }
 
-// Row positions of a lane: expert lane + 32 i in slot i.
 template <int NK>
-__device__ __forceinline__ void load_bias(const ScoreArgs &a, int lane, float (&bias)[NK]) {
+__device__ __forceinline__ void load_row(const float *row, int E, int lane, float (&v)[NK]) {
+#pragma unroll
+    for (int i = 0; i < NK; ++i) v[i] = lane + 32 * i < E ? row[lane + 32 * i] : -INFINITY;
+}
+
+// The biases, 0 without, -inf past E, up to 32 NK. Block-wide, not synchronised.
+template <int NK>
+__device__ __forceinline__ void load_bias(const ScoreArgs &a, float *bias) {
+    for (int e = threadIdx.x; e < 32 * NK; e += blockDim.x)
+        bias[e] = e >= a.E ? -INFINITY : a.bias ? a.bias[e] : 0.f;
+}
+
+// Softmax of the lane's logits in place: v becomes the exponentials. Returns
+// their sum, rounded once; mx: the largest logit. Each lane sums from 1, which
+// no exponential exceeds: the rounding error of a sum is then three operations;
+// the 32 ones go at the end.
+template <int NK>
+__device__ __forceinline__ float warp_exps(float (&v)[NK], float &mx) {
+    mx = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NK; ++i) mx = fmaxf(mx, v[i]);
+#pragma unroll
+    for (int off = 16; off; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, off));
+    float s = 1.f, c = 0.f;
 #pragma unroll
     for (int i = 0; i < NK; ++i) {
-        const int e = lane + 32 * i;
-        bias[i] = a.bias && e < a.E ? a.bias[e] : 0.f;
+        v[i] = soft_exp(v[i], mx);
+        const float t = __fadd_rn(s, v[i]);
+        c = __fadd_rn(c, __fsub_rn(v[i], __fsub_rn(t, s)));
+        s = t;
     }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) {
+        const float so = __shfl_xor_sync(FULL_MASK, s, off);
+        c = __fadd_rn(c, __shfl_xor_sync(FULL_MASK, c, off));
+        two_add(s, c, so);
+    }
+    return __fadd_rn(__fsub_rn(s, 32.f), c);  // (the difference is exact)
+}
+
+// Selection from approximate scores, -1 in all lanes where it does not apply.
+// v: the logits, or for the softmax the exponentials; overwritten. The approximation's
+// error is below 2^-21 (sigmoid) or 2^-22 of the largest score (softmax), and
+// an addition's rounding; the bound takes off four times that, twice.
+template <int NK, bool SIGMOID>
+__device__ __forceinline__ int warp_select_approx(const float *row, float (&v)[NK], const float *bias,
+                                                  const ScoreArgs &a, float mx, float sum, int lane,
+                                                  uint2 *scratch) {
+    const float L2E = 1.44269504088896341f;
+    const float inv = SIGMOID ? 1.f : __frcp_rn(sum);
+    float best = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+        float p;
+        if constexpr (SIGMOID) {
+            float x;
+            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(v[i] * -L2E));
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(1.f + x));
+        } else {
+            p = v[i] * inv;
+        }
+        v[i] = p + bias[lane + 32 * i];
+        best = fmaxf(best, v[i]);  // (leaves NaN out)
+    }
+    const float t = key_logit(__shfl_sync(FULL_MASK, warp_sort32(logit_key(best), lane), a.k - 1));
+    if (!(fabsf(t) < INFINITY)) return -1;  // warp-uniform
+    const float bound = t - (SIGMOID ? 0x1p-18f : 0x1p-19f) * (inv + fabsf(t));
+    uint32_t mine = 0u;
+#pragma unroll
+    for (int i = 0; i < NK; ++i)
+        if (!(v[i] < bound)) mine |= 1u << i;  // (NaN too, so that it is seen below)
+    const int n = gather_candidates(mine, lane, scratch);
+    if (n > 64) return -1;
+    bool bad = false;  // an expert that counts as -inf is no candidate
+    for (int j = lane; j < n; j += 32) {
+        const int e = (int)scratch[j].y;
+        const float p = score_of<SIGMOID>(load_logit(row, e, bad), mx, sum);
+        scratch[j].x = select_key(p, bias[e], bad);
+    }
+    __syncwarp();
+    if (__any_sync(FULL_MASK, bad)) return -1;
+    return rank_candidates(scratch, n, a.k, lane);
 }
 
 // One warp's token: lane j < k gets the j-th selected expert and its weight.
-// v: the token's logits (-inf past E). scratch: 64 entries of warp-private
-// shared memory.
+// v: the token's logits (-inf past E), overwritten. scratch: 64 entries of
+// warp-private shared memory.
 template <int NK, bool SIGMOID>
-__device__ __forceinline__ void warp_scored_topk(const float *row, float (&v)[NK], const float (&bias)[NK],
+__device__ __forceinline__ void warp_scored_topk(const float *row, float (&v)[NK], const float *bias,
                                                  const ScoreArgs &a, int lane, int &my_e, float &my_w,
                                                  bool &nan_seen, uint2 *scratch) {
-    const float L2E = 1.44269504088896341f;
-    bool odd = false;  // a NaN logit
+    float mx = 0.f, sum = 1.f;
+    if constexpr (!SIGMOID) sum = warp_exps<NK>(v, mx);
+    my_e = -1;
+    // (a row without a finite logit or with a NaN takes the other way)
+    const bool plain = a.r.n_groups == 1 && a.k <= 16 &&
+                       (SIGMOID || (fabsf(mx) < INFINITY && sum > 0.f));
+    if (plain) my_e = warp_select_approx<NK, SIGMOID>(row, v, bias, a, mx, sum, lane, scratch);
+    if (!plain || !__any_sync(FULL_MASK, my_e >= 0)) {
+        load_row(row, a.E, lane, v);
 #pragma unroll
-    for (int i = 0; i < NK; ++i) {
-        if (v[i] != v[i]) {
-            odd = true;
-            v[i] = -INFINITY;
-        }
-    }
-    nan_seen |= odd;
-    float mx = -INFINITY, sum = 1.f;
-    if constexpr (!SIGMOID) {  // v becomes the exponentials
-#pragma unroll
-        for (int i = 0; i < NK; ++i) mx = fmaxf(mx, v[i]);
-#pragma unroll
-        for (int off = 16; off; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL_MASK, mx, off));
-        // each lane sums from 1, which no exponential exceeds: the rounding
-        // error of a sum is then three operations; the 32 ones go at the end
-        float s = 1.f, c = 0.f;
-#pragma unroll
-        for (int i = 0; i < NK; ++i) {
-            v[i] = lane + 32 * i < a.E ? soft_exp(v[i], mx) : 0.f;
-            const float t = __fadd_rn(s, v[i]);
-            c = __fadd_rn(c, __fsub_rn(v[i], __fsub_rn(t, s)));
-            s = t;
-        }
-#pragma unroll
-        for (int off = 16; off; off >>= 1) {
-            const float so = __shfl_xor_sync(FULL_MASK, s, off);
-            c = __fadd_rn(c, __shfl_xor_sync(FULL_MASK, c, off));
-            two_add(s, c, so);
-        }
-        sum = __fadd_rn(__fsub_rn(s, 32.f), c);  // (the difference is exact)
-    }
-    bool done = false;
-    if (a.r.n_groups == 1 && a.k <= 16) {
-        // approximate scores; error below 2^-21 (sigmoid) or 2^-22 of the
-        // largest score (softmax), and an addition's rounding
-        const float inv = SIGMOID ? 1.f : __frcp_rn(sum);
-        float s[NK], best = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < NK; ++i) {
-            float p;
-            if constexpr (SIGMOID) {
-                float x;
-                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(v[i] * -L2E));
-                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(1.f + x));
-            } else {
-                p = v[i] * inv;
+        for (int i = 0; i < NK; ++i)
+            if (v[i] != v[i]) {
+                nan_seen = true;
+                v[i] = -INFINITY;
             }
-            s[i] = lane + 32 * i < a.E ? p + bias[i] : -INFINITY;
-            best = fmaxf(best, s[i]);  // (NaN is left out; +inf ends below)
+        if constexpr (!SIGMOID) {
+            sum = warp_exps<NK>(v, mx);
+            if (mx == -INFINITY) sum = (float)a.E;  // (slots past E count 1 too, then)
         }
-        const float t = key_logit(__shfl_sync(FULL_MASK, warp_sort32(logit_key(best), lane), a.k - 1));
-        const float bound = t - 2.f * (SIGMOID ? 0x1p-19f : 0x1p-20f) * ((SIGMOID ? 1.f : inv) + fabsf(t));
-        bool bad = false;
-        int n = 0;
-        if (t > -INFINITY && t < INFINITY) {
-#pragma unroll
-            for (int i = 0; i < NK; ++i) {
-                // NaN counts as a candidate here, so that it is seen
-                const bool c = !(s[i] < bound);
-                const uint32_t m = __ballot_sync(FULL_MASK, c);
-                const int at = n + __popc(m & lanemask_lt());
-                if (c && at < 64) scratch[at].y = (uint32_t)(lane + 32 * i);
-                n += __popc(m);
-            }
-            __syncwarp();
-            if (n <= 64) {  // exact keys
-#pragma unroll
-                for (int j = lane; j < 64; j += 32)
-                    if (j < n) {
-                        const int e = (int)scratch[j].y;
-                        bool ignored = false;
-                        const float p = score_of<SIGMOID>(load_logit(row, e, ignored), mx, sum);
-                        scratch[j].x = select_key(p, a.bias ? a.bias[e] : 0.f, bad);
-                    }
-                __syncwarp();
-                // (an expert that counts as -inf is no candidate: the other way)
-                if (!__any_sync(FULL_MASK, bad)) {
-                    rank_candidates(scratch, n, a.k, lane, my_e);
-                    done = true;
-                }
-            }
-        }
-    }
-    if (!done) {
-        uint32_t key[NK];
+        uint32_t key[NK], best = 0u;
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
             key[i] = 0u;
             if (lane + 32 * i < a.E)
-                key[i] = select_key(SIGMOID ? score_of<true>(v[i], 0.f, 1.f) : __fdiv_rn(v[i], sum), bias[i],
+                key[i] = select_key(SIGMOID ? score_of<true>(v[i], 0.f, 1.f) : __fdiv_rn(v[i], sum),
+                                    bias[lane + 32 * i],
                                     nan_seen);
         }
         if (a.r.n_groups > 1) keep_groups<NK>(key, a, lane);
-        uint32_t kv;
-        warp_select_thr<NK>(key, a.k, lane, scratch, my_e, kv);
+        int n = 65;
+        if (a.k <= 16) {  // as above, with exact keys
+#pragma unroll
+            for (int i = 0; i < NK; ++i) best = max(best, key[i]);
+            const uint32_t t = __shfl_sync(FULL_MASK, warp_sort32(best, lane), a.k - 1);
+            uint32_t mine = 0u;
+#pragma unroll
+            for (int i = 0; i < NK; ++i)
+                if (key[i] >= t && key[i] > 0u) mine |= 1u << i;
+            n = gather_candidates(mine, lane, scratch);
+            if (n <= 64) {
+                const int c = __popc(mine);
+                int at = c;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int o = __shfl_up_sync(FULL_MASK, at, d);
+                    if (lane >= d) at += o;
+                }
+                at -= c;
+#pragma unroll
+                for (int i = 0; i < NK; ++i)
+                    if ((mine >> i) & 1u) scratch[at++].x = key[i];
+                __syncwarp();
+                my_e = rank_candidates(scratch, n, a.k, lane);
+            }
+        }
+        if (n > 64) {
+            uint32_t kv;
+            warp_select<NK>(key, a.k, lane, scratch, my_e, kv);
+        }
     }
     float w = 0.f;
     if (lane < a.k) {
@@ -286,59 +374,60 @@ __device__ __forceinline__ void warp_scored_topk(const float *row, float (&v)[NK
     my_w = w * a.r.scale;
 }
 
-template <int NK>
-__device__ __forceinline__ void load_row(const float *row, int E, int lane, float (&v)[NK]) {
-#pragma unroll
-    for (int i = 0; i < NK; ++i) v[i] = lane + 32 * i < E ? row[lane + 32 * i] : -INFINITY;
-}
-
 // Small batches: as moe_plan_small_kernel, one CTA, a warp per token.
 template <int NK, bool SIGMOID>
 __global__ void __launch_bounds__(kPlanSmallThreads) moe_plan_scored_small_kernel(
     int T, ScoreArgs a, const float *__restrict__ logits, moe_plan_buf p, int *status) {
     __shared__ PlanSmall s;
+    __shared__ float s_bias[32 * NK];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     grid_dep_wait();
     grid_dep_launch();
+    load_bias<NK>(a, s_bias);
     plan_small_init(s);
     bool nan_seen = false;
-    float bias[NK], v[NK];
-    load_bias(a, lane, bias);
+    float v[NK];
     for (int t = wid; t < T; t += kPlanSmallWarps) {
         int my_e;
         float my_w;
         load_row(logits + (int64_t)t * a.E, a.E, lane, v);
-        warp_scored_topk<NK, SIGMOID>(logits + (int64_t)t * a.E, v, bias, a, lane, my_e, my_w, nan_seen,
+        warp_scored_topk<NK, SIGMOID>(logits + (int64_t)t * a.E, v, s_bias, a, lane, my_e, my_w, nan_seen,
                                       s.scr[wid]);
         plan_small_put(s, t, a.k, lane, my_e, my_w, p.topk_idx, p.topk_w);
     }
     plan_small_finish(s, T, a.E, a.k, nan_seen, p, status);
 }
 
-// Large batches: a block per chunk of 32 tokens, four tokens a warp, and the
-// chunk's rows per expert.
+// Large batches: a block per chunk of 32 tokens, and the chunk's rows per expert.
+// Threads of a block: with few keys a warp per token; else two blocks an SM at
+// 64 registers.
+template <int NK>
+constexpr int kChunkThreads = NK <= 8 ? 32 * MOE_PLAN_CHUNK : 512;
+
 template <int NK, bool SIGMOID>
-__global__ void __launch_bounds__(256, 2) moe_topk_scored_kernel(int T, ScoreArgs a,
+__global__ void __launch_bounds__(kChunkThreads<NK>, 1024 / kChunkThreads<NK>) moe_topk_scored_kernel(int T, ScoreArgs a,
                                                               const float *__restrict__ logits,
                                                               int32_t *topk_idx, float *topk_w,
                                                               int32_t *chunk_counts, int *status) {
-    __shared__ uint2 s_scratch[8][64];
+    constexpr int kThreads = kChunkThreads<NK>, kWarps = kThreads / 32;
+    __shared__ uint2 s_scratch[kWarps][64];
     __shared__ uint32_t s_mask[MOE_MAX_EXPERTS];
+    __shared__ float s_bias[32 * NK];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     grid_dep_wait();
     grid_dep_launch();
-    for (int e = threadIdx.x; e < a.E; e += 256) s_mask[e] = 0u;
+    for (int e = threadIdx.x; e < a.E; e += kThreads) s_mask[e] = 0u;
+    load_bias<NK>(a, s_bias);
     __syncthreads();
     bool nan_seen = false;
-    float bias[NK], v[NK];
-    load_bias(a, lane, bias);
-    for (int i = wid; i < MOE_PLAN_CHUNK; i += 8) {
+    float v[NK];
+    for (int i = wid; i < MOE_PLAN_CHUNK; i += kWarps) {
         const int t = blockIdx.x * MOE_PLAN_CHUNK + i;
         if (t >= T) break;
         int my_e;
         float my_w;
         load_row(logits + (int64_t)t * a.E, a.E, lane, v);
-        warp_scored_topk<NK, SIGMOID>(logits + (int64_t)t * a.E, v, bias, a, lane, my_e, my_w, nan_seen,
+        warp_scored_topk<NK, SIGMOID>(logits + (int64_t)t * a.E, v, s_bias, a, lane, my_e, my_w, nan_seen,
                                       s_scratch[wid]);
         if (lane < a.k) {
             topk_idx[(int64_t)t * a.k + lane] = my_e;
@@ -348,7 +437,7 @@ __global__ void __launch_bounds__(256, 2) moe_topk_scored_kernel(int T, ScoreArg
     }
     if (__any_sync(FULL_MASK, nan_seen) && lane == 0) moe_flag(status, MOE_ERR_NAN_LOGIT);
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += 256)
+    for (int e = threadIdx.x; e < a.E; e += kThreads)
         chunk_counts[(int64_t)blockIdx.x * a.E + e] = __popc(s_mask[e]);
 }
 
@@ -359,7 +448,7 @@ cudaError_t launch(int T, const ScoreArgs &a, const float *logits, const moe_pla
         return launch_pdl(moe_plan_scored_small_kernel<NK, SIGMOID>, dim3(1),
                           dim3(kPlanSmallThreads), 0, st, T, a, logits, *p, status);
     const int nchunks = (T + MOE_PLAN_CHUNK - 1) / MOE_PLAN_CHUNK;
-    const cudaError_t err = launch_pdl(moe_topk_scored_kernel<NK, SIGMOID>, dim3(nchunks), dim3(256), 0, st, T,
+    const cudaError_t err = launch_pdl(moe_topk_scored_kernel<NK, SIGMOID>, dim3(nchunks), dim3(kChunkThreads<NK>), 0, st, T,
                                        a, logits, p->topk_idx, p->topk_w, (int32_t *)ws, status);
     return err != cudaSuccess ? err : moe_launch_plan_build(T, a.E, a.k, true, p, ws, status, st);
 }
