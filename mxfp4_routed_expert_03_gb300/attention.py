@@ -30,13 +30,14 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _row(t):
-    """Row stride of a token-row tensor (0 for None), whose rows must be contiguous."""
+def _rows(t):
+    """Pointer and row stride of a tensor of token rows ((None, 0) for None)."""
     if t is None:
-        return 0
-    if t.dim() != 2 or t.stride(1) != 1:
+        return None, 0
+    s = t.stride()
+    if len(s) != 2 or s[1] != 1:
         raise ValueError("token rows: a 2D tensor with contiguous rows")
-    return t.stride(0)
+    return t.data_ptr(), s[0]
 
 
 class Rope:
@@ -93,14 +94,14 @@ class Attention:
             pass
 
     def norm_rope(self, T, q, k, positions, rope: Rope, q_out, k_out, stream=None) -> int:
-        return moe_qk_norm_rope(self.h, T, rope.desc, positions, q, _row(q), k, _row(k), q_out,
-                                _row(q_out), k_out, _row(k_out), stream)
+        return moe_qk_norm_rope(self.h, T, rope.desc, positions, *_rows(q), *_rows(k), *_rows(q_out),
+                                *_rows(k_out), stream)
 
     def append(self, T, k, v, slots, stream=None) -> int:
-        return moe_kv_append(self.h, T, k, _row(k), v, _row(v), slots, stream)
+        return moe_kv_append(self.h, T, *_rows(k), *_rows(v), slots, stream)
 
     def read(self, n, slots, k, v, stream=None) -> int:
-        return moe_kv_read(self.h, n, slots, k, _row(k), v, _row(v), stream)
+        return moe_kv_read(self.h, n, slots, *_rows(k), *_rows(v), stream)
 
     def workspace(self, batch: Batch) -> tuple:
         if self._need[0] != batch.key:
@@ -112,8 +113,7 @@ class Attention:
 
     def forward(self, batch: Batch, q, out, lse=None, stream=None) -> int:
         ws, n = self.workspace(batch)
-        return moe_attn_forward(self.h, batch.desc, q, _row(q), out, _row(out), lse, ws, ws.numel(),
-                                stream)
+        return moe_attn_forward(self.h, batch.desc, *_rows(q), *_rows(out), lse, ws, n, stream)
 
     def status(self, stream=None) -> int:
         return moe_attn_status(self.h, stream)

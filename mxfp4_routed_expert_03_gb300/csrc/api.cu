@@ -221,6 +221,7 @@ static int create_impl(const moe_desc *d, const moe_weights *w, int wE, moe_hand
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
         return MOE_ERR_CUDA;
     if (major != 10 || minor != 3) return MOE_ERR_UNSUPPORTED;
+    if (moe_plan_setup() != cudaSuccess) return MOE_ERR_CUDA;
 
     moe_handle *h = (moe_handle *)calloc(1, sizeof(moe_handle));
     if (!h) return MOE_ERR_INVALID_ARG;

@@ -840,15 +840,26 @@ cudaError_t launch(const MoeAttnArgs &a, int nsm, cudaStream_t st) {
     const int64_t items = (int64_t)a.n_kv * ((int64_t)a.b.n_tokens * a.group / C::NC + a.b.n_seqs);
     const int64_t units = whole ? items : items * ((a.b.max_kv + kTile - 1) / kTile + 1) / kMinTiles + 1;
     const int ctas = (int)std::min<int64_t>(units, (int64_t)nsm * C::kCtasPerSm);
-    cudaError_t err = cudaFuncSetAttribute(moe_attn_split_kernel<D, NT>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (err != cudaSuccess) return err;
-    err = launch_pdl(moe_attn_split_kernel<D, NT>, dim3(ctas), dim3(kThreads), C::kSmem, st, a, whole);
+    const cudaError_t err = launch_pdl_ready(moe_attn_split_kernel<D, NT>, dim3(ctas), dim3(kThreads), C::kSmem, st, a, whole);
     if (err != cudaSuccess || whole) return err;
-    return launch_pdl(moe_attn_join_kernel<D, NT>, dim3(ctas, C::NC / kJoinCols), dim3(32 * kJoinWarps), 0, st, a);
+    return launch_pdl_ready(moe_attn_join_kernel<D, NT>, dim3(ctas, C::NC / kJoinCols), dim3(32 * kJoinWarps), 0, st, a);
+}
+
+template <int D, int NT>
+cudaError_t setup() {
+    const cudaError_t err = set_kernel((const void *)moe_attn_split_kernel<D, NT>, Cfg<D, NT>::kSmem);
+    return err != cudaSuccess ? err : set_kernel((const void *)moe_attn_join_kernel<D, NT>);
 }
 
 }  // namespace
+
+cudaError_t moe_attn_setup() {
+    cudaError_t err = setup<64, 1>();
+    if (err == cudaSuccess) err = setup<64, 2>();
+    if (err == cudaSuccess) err = setup<128, 1>();
+    if (err == cudaSuccess) err = setup<128, 2>();
+    return err != cudaSuccess ? err : moe_attn_prefill_setup();
+}
 
 size_t moe_attn_ws_bytes(int head_dim, int n_seqs, int n_kv, int group, int max_q, int max_kv,
                          int nsm) {

@@ -58,6 +58,9 @@ MOE_API int moe_attn_create(const moe_attn_desc *d, const moe_kv_cache *c, moe_a
         cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return MOE_ERR_CUDA;
     if (major != 10 || minor != 3) return MOE_ERR_UNSUPPORTED;
+    if (moe_qk_norm_rope_setup() != cudaSuccess || moe_kv_setup() != cudaSuccess ||
+        moe_attn_setup() != cudaSuccess)
+        return MOE_ERR_CUDA;
     moe_attn *a = (moe_attn *)calloc(1, sizeof(moe_attn));
     if (!a) return MOE_ERR_INVALID_ARG;
     a->desc = *d;

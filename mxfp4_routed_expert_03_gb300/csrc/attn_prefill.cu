@@ -756,17 +756,25 @@ template <int D>
 cudaError_t launch(const MoeAttnArgs &a, int nsm, cudaStream_t st) {
     using C = PCfg<D>;
     const Shape g = shape_of(a.b.n_seqs, a.n_kv, a.group, a.b.max_q, a.b.max_kv, nsm);
-    cudaError_t err = cudaFuncSetAttribute(moe_attn_prefill_kernel<D>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (err != cudaSuccess) return err;
-    err = launch_pdl(moe_attn_prefill_kernel<D>, dim3((unsigned)g.ctas), dim3(kThreadsP), C::kSmem, st, a,
+    const cudaError_t err = launch_pdl_ready(moe_attn_prefill_kernel<D>, dim3((unsigned)g.ctas), dim3(kThreadsP), C::kSmem, st, a,
                      g.tiles_max, g.splits);
     if (err != cudaSuccess || g.splits == 1) return err;
-    return launch_pdl(moe_attn_prefill_join_kernel<D>, dim3((unsigned)(g.ctas / g.splits * (kCols / 8))),
+    return launch_pdl_ready(moe_attn_prefill_join_kernel<D>, dim3((unsigned)(g.ctas / g.splits * (kCols / 8))),
                       dim3(256), 0, st, a, g.tiles_max, g.splits);
 }
 
+template <int D>
+cudaError_t setup() {
+    const cudaError_t err = set_kernel((const void *)moe_attn_prefill_kernel<D>, PCfg<D>::kSmem);
+    return err != cudaSuccess ? err : set_kernel((const void *)moe_attn_prefill_join_kernel<D>);
+}
+
 }  // namespace
+
+cudaError_t moe_attn_prefill_setup() {
+    const cudaError_t err = setup<64>();
+    return err != cudaSuccess ? err : setup<128>();
+}
 
 bool moe_attn_prefill_fits(int n_seqs, int n_kv, int group, int max_q, int max_kv, int nsm) {
     if ((int64_t)group * max_q < MOE_ATTN_PREFILL_COLS) return false;

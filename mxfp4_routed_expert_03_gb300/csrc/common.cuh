@@ -58,18 +58,10 @@ __device__ __forceinline__ uint32_t lanemask_lt() {
 }
 
 // Host: launch `kern` with programmatic dependent launch allowed (see
-// grid_dep_wait). Every kernel of a chain asks for the largest shared-memory
-// carve-out: an SM's L1 / shared split changes only when the SM is idle, so
-// a small kernel's CTA left on an SM in the default split keeps the next
-// kernel's large-shared-memory CTA (the grouped GEMMs) off that SM until it
-// exits, even where both fit.
+// grid_dep_wait); its attributes are as set_kernel left them.
 template <typename... KArgs, typename... Args>
-inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                              cudaStream_t st, Args... args) {
-    cudaError_t err = cudaFuncSetAttribute((const void *)kern,
-                                           cudaFuncAttributePreferredSharedMemoryCarveout,
-                                           (int)cudaSharedmemCarveoutMaxShared);
-    if (err != cudaSuccess) return err;
+inline cudaError_t launch_pdl_ready(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                                    cudaStream_t st, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
@@ -81,4 +73,30 @@ inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, siz
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// Host: the attributes of a kernel for the current device, set once (when a
+// handle is created) rather than at every launch: the largest shared-memory
+// carve-out (see launch_pdl) and `smem` bytes of dynamic shared memory.
+inline cudaError_t set_kernel(const void *kern, size_t smem = 0) {
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                           (int)cudaSharedmemCarveoutMaxShared);
+    if (err == cudaSuccess && smem > 0)
+        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    return err;
+}
+
+// Host: launch `kern` with programmatic dependent launch allowed (see
+// grid_dep_wait). Every kernel of a chain asks for the largest shared-memory
+// carve-out: an SM's L1 / shared split changes only when the SM is idle, so
+// a small kernel's CTA left on an SM in the default split keeps the next
+// kernel's large-shared-memory CTA (the grouped GEMMs) off that SM until it
+// exits, even where both fit.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                              cudaStream_t st, Args... args) {
+    cudaError_t err = cudaFuncSetAttribute((const void *)kern,
+                                           cudaFuncAttributePreferredSharedMemoryCarveout,
+                                           (int)cudaSharedmemCarveoutMaxShared);
+    return err != cudaSuccess ? err : launch_pdl_ready(kern, grid, block, smem, st, args...);
 }

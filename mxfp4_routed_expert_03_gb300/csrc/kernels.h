@@ -25,6 +25,10 @@ static inline bool moe_plan_is_small(int T) { return T <= 64; }
 size_t moe_plan_ws_bytes(int T, int E);
 cudaError_t moe_launch_plan(int T, int E, int k, const float *logits, const moe_plan_buf *p,
                             void *ws, int *status, cudaStream_t st);
+// Kernel attributes for the current device (moe_create): this file's and
+// route_scored.cu's.
+cudaError_t moe_plan_setup();
+cudaError_t moe_plan_scored_setup();
 // The plan of a large batch (not moe_plan_is_small) whose topk_idx is there;
 // counted: the chunks' counts are in ws too.
 cudaError_t moe_launch_plan_build(int T, int E, int k, bool counted, const moe_plan_buf *p, void *ws,
@@ -265,6 +269,7 @@ struct MoeRopeArgs {
     int64_t q_stride, k_stride, q_out_stride, k_out_stride;
     int *status;
 };
+cudaError_t moe_qk_norm_rope_setup();  // kernel attributes (moe_attn_create), as below
 cudaError_t moe_launch_qk_norm_rope(int T, int head_dim, const MoeRopeArgs &a, int nsm,
                                     cudaStream_t st);
 
@@ -278,6 +283,7 @@ struct MoeKvArgs {
     moe_kv_cache c;
     int *status;
 };
+cudaError_t moe_kv_setup();
 cudaError_t moe_launch_kv_append(int head_dim, const MoeKvArgs &a, cudaStream_t st);
 cudaError_t moe_launch_kv_read(int head_dim, const MoeKvArgs &a, cudaStream_t st);
 
@@ -296,6 +302,7 @@ struct MoeAttnArgs {
     int *status;
     long long timeout_cycles;
 };
+cudaError_t moe_attn_setup();  // attn_prefill.cu's too
 size_t moe_attn_ws_bytes(int head_dim, int n_seqs, int n_kv, int group, int max_q, int max_kv,
                          int nsm);
 cudaError_t moe_launch_attn(int head_dim, const MoeAttnArgs &a, int nsm, cudaStream_t st);
@@ -303,6 +310,7 @@ cudaError_t moe_launch_attn(int head_dim, const MoeAttnArgs &a, int nsm, cudaStr
 // attn_prefill.cu: the same with many query rows per sequence, from this many
 // columns (query rows x heads of a key/value head) of the longest sequence on
 #define MOE_ATTN_PREFILL_COLS 64
+cudaError_t moe_attn_prefill_setup();
 bool moe_attn_prefill_fits(int n_seqs, int n_kv, int group, int max_q, int max_kv, int nsm);
 size_t moe_attn_prefill_ws_bytes(int head_dim, int n_seqs, int n_kv, int group, int max_q, int max_kv,
                                  int nsm);

@@ -152,14 +152,24 @@ int blocks(const MoeKvArgs &a) {
 
 }  // namespace
 
+cudaError_t moe_kv_setup() {
+    const void *kernels[] = {(const void *)moe_kv_append_kernel<64>, (const void *)moe_kv_append_kernel<128>,
+                             (const void *)moe_kv_read_kernel<64>, (const void *)moe_kv_read_kernel<128>};
+    for (const void *k : kernels) {
+        const cudaError_t err = set_kernel(k);
+        if (err != cudaSuccess) return err;
+    }
+    return cudaSuccess;
+}
+
 cudaError_t moe_launch_kv_append(int head_dim, const MoeKvArgs &a, cudaStream_t st) {
     return head_dim == 64
-               ? launch_pdl(moe_kv_append_kernel<64>, dim3(blocks(a)), dim3(32 * kWarps), 0, st, a)
-               : launch_pdl(moe_kv_append_kernel<128>, dim3(blocks(a)), dim3(32 * kWarps), 0, st, a);
+               ? launch_pdl_ready(moe_kv_append_kernel<64>, dim3(blocks(a)), dim3(32 * kWarps), 0, st, a)
+               : launch_pdl_ready(moe_kv_append_kernel<128>, dim3(blocks(a)), dim3(32 * kWarps), 0, st, a);
 }
 
 cudaError_t moe_launch_kv_read(int head_dim, const MoeKvArgs &a, cudaStream_t st) {
     return head_dim == 64
-               ? launch_pdl(moe_kv_read_kernel<64>, dim3(blocks(a)), dim3(32 * kWarps), 0, st, a)
-               : launch_pdl(moe_kv_read_kernel<128>, dim3(blocks(a)), dim3(32 * kWarps), 0, st, a);
+               ? launch_pdl_ready(moe_kv_read_kernel<64>, dim3(blocks(a)), dim3(32 * kWarps), 0, st, a)
+               : launch_pdl_ready(moe_kv_read_kernel<128>, dim3(blocks(a)), dim3(32 * kWarps), 0, st, a);
 }

@@ -140,10 +140,21 @@ template <int D, int P>
 cudaError_t launch(int T, const MoeRopeArgs &a, cudaStream_t st) {
     const int per_block = kWarps * P * (32 / (D / 16));
     const dim3 grid(T, (a.n_q + a.n_k + per_block - 1) / per_block);
-    return launch_pdl(moe_qk_norm_rope_kernel<D, P>, grid, dim3(32 * kWarps), 0, st, a);
+    return launch_pdl_ready(moe_qk_norm_rope_kernel<D, P>, grid, dim3(32 * kWarps), 0, st, a);
 }
 
 }  // namespace
+
+cudaError_t moe_qk_norm_rope_setup() {
+    const void *kernels[] = {
+        (const void *)moe_qk_norm_rope_kernel<64, 1>, (const void *)moe_qk_norm_rope_kernel<64, 4>,
+        (const void *)moe_qk_norm_rope_kernel<128, 1>, (const void *)moe_qk_norm_rope_kernel<128, 4>};
+    for (const void *k : kernels) {
+        const cudaError_t err = set_kernel(k);
+        if (err != cudaSuccess) return err;
+    }
+    return cudaSuccess;
+}
 
 cudaError_t moe_launch_qk_norm_rope(int T, int head_dim, const MoeRopeArgs &a, int nsm,
                                     cudaStream_t st) {

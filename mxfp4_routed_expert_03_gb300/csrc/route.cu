@@ -177,6 +177,12 @@ cudaError_t moe_launch_plan(int T, int E, int k, const float *logits, const moe_
     return moe_launch_plan_build(T, E, k, false, p, ws, status, st);
 }
 
+cudaError_t moe_plan_setup() {
+    cudaError_t err = set_kernel((const void *)moe_plan_scan_kernel);
+    if (err == cudaSuccess) err = set_kernel((const void *)moe_plan_scatter_kernel);
+    return err != cudaSuccess ? err : moe_plan_scored_setup();
+}
+
 cudaError_t moe_launch_plan_build(int T, int E, int k, bool counted, const moe_plan_buf *p, void *ws,
                                   int *status, cudaStream_t st) {
     const int nchunks = (T + MOE_PLAN_CHUNK - 1) / MOE_PLAN_CHUNK;
@@ -185,10 +191,10 @@ cudaError_t moe_launch_plan_build(int T, int E, int k, bool counted, const moe_p
         moe_plan_count_kernel<<<nchunks, 256, 0, st>>>(T, E, k, p->topk_idx, chunk, status);
     cudaError_t err = cudaGetLastError();
     if (err == cudaSuccess)
-        err = launch_pdl(moe_plan_scan_kernel, dim3((E + 31) / 32), dim3(1024), 0, st, E, nchunks, chunk,
+        err = launch_pdl_ready(moe_plan_scan_kernel, dim3((E + 31) / 32), dim3(1024), 0, st, E, nchunks, chunk,
                          p->counts);
     if (err == cudaSuccess)
-        err = launch_pdl(moe_plan_scatter_kernel, dim3(nchunks), dim3(256), 0, st, T, E, k,
+        err = launch_pdl_ready(moe_plan_scatter_kernel, dim3(nchunks), dim3(256), 0, st, T, E, k,
                          (const int32_t *)p->topk_idx, (const int32_t *)chunk, *p, status);
     return err;
 }

@@ -445,15 +445,34 @@ template <int NK, bool SIGMOID>
 cudaError_t launch(int T, const ScoreArgs &a, const float *logits, const moe_plan_buf *p, void *ws,
                    int *status, cudaStream_t st) {
     if (moe_plan_is_small(T))
-        return launch_pdl(moe_plan_scored_small_kernel<NK, SIGMOID>, dim3(1),
+        return launch_pdl_ready(moe_plan_scored_small_kernel<NK, SIGMOID>, dim3(1),
                           dim3(kPlanSmallThreads), 0, st, T, a, logits, *p, status);
     const int nchunks = (T + MOE_PLAN_CHUNK - 1) / MOE_PLAN_CHUNK;
-    const cudaError_t err = launch_pdl(moe_topk_scored_kernel<NK, SIGMOID>, dim3(nchunks), dim3(kChunkThreads<NK>), 0, st, T,
+    const cudaError_t err = launch_pdl_ready(moe_topk_scored_kernel<NK, SIGMOID>, dim3(nchunks), dim3(kChunkThreads<NK>), 0, st, T,
                                        a, logits, p->topk_idx, p->topk_w, (int32_t *)ws, status);
     return err != cudaSuccess ? err : moe_launch_plan_build(T, a.E, a.k, true, p, ws, status, st);
 }
 
+template <int NK>
+cudaError_t setup() {
+    const void *kernels[] = {(const void *)moe_plan_scored_small_kernel<NK, true>,
+                             (const void *)moe_plan_scored_small_kernel<NK, false>,
+                             (const void *)moe_topk_scored_kernel<NK, true>,
+                             (const void *)moe_topk_scored_kernel<NK, false>};
+    for (const void *k : kernels) {
+        const cudaError_t err = set_kernel(k);
+        if (err != cudaSuccess) return err;
+    }
+    return cudaSuccess;
+}
+
 }  // namespace
+
+cudaError_t moe_plan_scored_setup() {
+    cudaError_t err = setup<8>();
+    if (err == cudaSuccess) err = setup<28>();
+    return err != cudaSuccess ? err : setup<32>();
+}
 
 cudaError_t moe_launch_plan_scored(int T, int E, int k, const float *logits,
                                    const moe_route_desc &r, const float *bias,
