@@ -24,9 +24,10 @@
 // Queries are put into fp16 with one power of two per row, exact for elements
 // within 2^-29 of the row's largest.
 //
-// Split. Tokens go in tiles of 32; all (sequence, column tile, head) items'
-// tiles form one line that is cut into equal pieces, one per CTA, so any mix
-// of lengths is balanced. A CTA's fifth warp walks the piece ahead of the others and
+// Split. Tokens go in tiles of 32. The tiles of all (sequence, column tile,
+// head) items form one line, with a fixed cost before each item's, that is cut
+// into equal pieces, one per CTA, so any mix of lengths is balanced; few items
+// are cut into equal parts instead, so that no CTA meets two of them. A CTA's fifth warp walks the piece ahead of the others and
 // fills a ring of stages with bulk copies, across item ends; four warps take a
 // tile of each stage, each with its own m, l, o, and merge at an item's end;
 // items cut between CTAs leave partial results that a second kernel joins in
@@ -42,7 +43,8 @@ namespace {
 constexpr int kWarps = 4;              // that compute, a tile each; one more fills the ring
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kStages = 3;
-constexpr int kMinTiles = kWarps;      // per CTA
+constexpr int kMinTiles = kWarps;      // of a piece
+constexpr int kItemCost = 8;           // an item's start and end (3 us) in tiles
 
 template <int D, int NT>
 struct Cfg {
@@ -107,80 +109,108 @@ __device__ __forceinline__ void bulk_g2s(void *dst, const void *src, uint32_t by
 __device__ __forceinline__ int max_exp(uint32_t r15) { return 15 - (int)r15 / 65537; }
 
 // ------------------------------------------------------------------ schedule
-// Units of the line: token tiles, or whole items where max_kv is short.
+// How the items are dealt to the CTAs.
+enum Deal {
+    DEAL_WHOLE,  // whole items, a contiguous run of them each (short sequences)
+    DEAL_PARTS,  // few items: each cut into the same number of parts, a CTA per part
+    DEAL_LINE    // all items' tiles, and kItemCost units before each item's, on one
+                 // line that is cut into equal pieces
+};
+
+// A sequence's share: items and units of the line.
+struct Share {
+    long long items, units;
+};
 template <int NC>
-__device__ __forceinline__ long long seq_work(const MoeAttnArgs &a, int b, bool whole) {
+__device__ __forceinline__ Share share_of(const MoeAttnArgs &a, int b, int &tiles) {
     const Seq s = seq_of<NC>(a, b);
-    return (long long)s.cts * a.n_kv * (whole ? 1 : s.tiles);
+    Share r;
+    r.items = (long long)s.cts * a.n_kv;
+    r.units = r.items * (kItemCost + s.tiles);
+    tiles = r.items > 0 ? s.tiles : 0;
+    return r;
 }
 
-// Sum of v over the block (all threads get it) and each thread's inclusive
-// prefix; tot: a word of shared memory per warp.
-__device__ __forceinline__ long long block_scan(long long v, long long *tot, long long &incl) {
+struct ScanSpace {
+    Share tot[kWarps + 1];
+    int tiles[kWarps + 1];
+    long long res[2];
+};
+
+// Inclusive prefix over the block's threads, their sum, and the largest `tiles`.
+__device__ __forceinline__ Share block_scan(Share v, int &tiles, ScanSpace &sp, Share &incl) {
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     incl = v;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const long long o = __shfl_up_sync(kFull, incl, off);
-        if (lane >= off) incl += o;
+        const long long i = __shfl_up_sync(kFull, incl.items, off), u = __shfl_up_sync(kFull, incl.units, off);
+        if (lane >= off) incl.items += i, incl.units += u;
     }
+    tiles = __reduce_max_sync(kFull, tiles);
     __syncthreads();
-    if (lane == 31) tot[wid] = incl;
+    if (lane == 31) sp.tot[wid] = incl, sp.tiles[wid] = tiles;
     __syncthreads();
-    long long sum = 0, before = 0;
+    Share sum = {0, 0}, before = {0, 0};
 #pragma unroll
     for (int w = 0; w <= kWarps; ++w) {
         if (w == wid) before = sum;
-        sum += tot[w];
+        sum.items += sp.tot[w].items;
+        sum.units += sp.tot[w].units;
+        tiles = max(tiles, sp.tiles[w]);
     }
-    incl += before;
+    incl.items += before.items;
+    incl.units += before.units;
     return sum;
 }
 
-// Units of all sequences. `mine` gets the calling thread's sequence of the
-// first round (the only one for up to kThreads sequences): its units and their
-// inclusive prefix.
-struct Prefix {
-    long long units, incl;
-};
+// The whole batch's share and its longest item. `mine` and `incl` get the
+// calling thread's sequence of the first round (the only one for up to kThreads
+// sequences) and its inclusive prefix.
 template <int NC>
-__device__ long long total_work(const MoeAttnArgs &a, bool whole, long long *tot, Prefix &mine) {
-    long long w = 0;
+__device__ Share total_share(const MoeAttnArgs &a, ScanSpace &sp, int &tiles, Share &mine, Share &incl) {
+    Share sum = {0, 0};
+    tiles = 0;
     for (int base = 0; base < a.b.n_seqs; base += kThreads) {
         const int b = base + threadIdx.x;
-        const long long v = b < a.b.n_seqs ? seq_work<NC>(a, b, whole) : 0;
-        long long incl;
-        w += block_scan(v, tot, incl);
-        if (base == 0) mine = {v, incl};
+        Share v = {0, 0}, in;
+        int t = 0;
+        if (b < a.b.n_seqs) v = share_of<NC>(a, b, t);
+        const Share r = block_scan(v, t, sp, in);
+        sum.items += r.items;
+        sum.units += r.units;
+        tiles = max(tiles, t);
+        if (base == 0) mine = v, incl = in;
     }
-    return w;
+    return sum;
 }
 
-// The sequence that holds unit `pos` (0 <= pos < total) and the unit's offset
-// in it; res: 2 words of shared memory.
+// The sequence that holds position `pos` (0 <= pos < total) of the items (or,
+// `line`, of the units), and the position's offset in it.
 template <int NC>
-__device__ void find_unit(const MoeAttnArgs &a, bool whole, long long pos, const Prefix &mine,
-                          long long *tot, long long *res, int &seq, long long &off) {
+__device__ void find_seq(const MoeAttnArgs &a, bool line, long long pos, Share mine, Share incl, ScanSpace &sp,
+                         int &seq, long long &off) {
     long long before = 0;
     for (int base = 0; base < a.b.n_seqs; base += kThreads) {
         const int b = base + threadIdx.x;
-        Prefix p = mine;
         long long sum = -1;  // (not needed when the first round is the only one)
         if (a.b.n_seqs > kThreads) {
-            p.units = b < a.b.n_seqs ? seq_work<NC>(a, b, whole) : 0;
-            sum = block_scan(p.units, tot, p.incl);
+            int t = 0;
+            mine = {0, 0};
+            if (b < a.b.n_seqs) mine = share_of<NC>(a, b, t);
+            const Share r = block_scan(mine, t, sp, incl);
+            sum = line ? r.units : r.items;
         }
-        const long long first = before + p.incl - p.units;
-        if (pos >= first && pos < first + p.units) {
-            res[0] = b;
-            res[1] = pos - first;
+        const long long n = line ? mine.units : mine.items, first = before + (line ? incl.units : incl.items) - n;
+        if (pos >= first && pos < first + n) {
+            sp.res[0] = b;
+            sp.res[1] = pos - first;
         }
         if (pos < before + sum) break;  // block-uniform
         before += sum;
     }
     __syncthreads();
-    seq = (int)res[0];
-    off = res[1];
+    seq = (int)sp.res[0];
+    off = sp.res[1];
 }
 
 // Written by every CTA of the split kernel: the item that it began and did not
@@ -190,53 +220,72 @@ struct Cut {
     int pad[3];
 };
 
-// Units per CTA.
-__device__ __forceinline__ long long piece_of(long long total, int ctas, bool whole) {
-    const long long per = (total + ctas - 1) / ctas;
-    return whole ? (per > 0 ? per : 1) : (per > kMinTiles ? per : kMinTiles);
-}
-
 __device__ __forceinline__ void consumers_sync() {
     asm volatile("bar.sync 1, %0;" ::"r"(32 * kWarps) : "memory");
 }
 
 // ------------------------------------------------------------------ kernel
-// A CTA's piece of the line, item by item.
+// A CTA's work, item by item.
 struct Walk {
-    long long pos, end, off;  // units; off: of the next item's first unit in its sequence
+    int deal;
+    long long pos, end;  // items or units still to take
+    long long off;       // of the next one in its sequence
     int b;
+    int part, parts;     // DEAL_PARTS: the CTA's part of its item
+    long long per;       // DEAL_LINE: units of a piece
 };
 
-// One item of a piece: a column tile and head of a sequence, token tiles
-// [x_lo, x_hi) of which hold keys that some column sees.
+// One item (or part) of a CTA: a column tile and head of a sequence, token
+// tiles [x_lo, x_hi) of which hold keys that some column sees.
 struct Item {
     Seq s;
     int c0, h;
     int p0;                              // position of query row 0
     int hi_min, hi_max, lo_min, lo_max;  // key bounds over the columns
     int x_lo, x_hi;
-    int rest;                            // units of the item beyond this piece
-    bool starts;                         // its first unit is in this piece
+    int parts;                           // CTAs that hold a part of the item, from the first on
+    bool starts;                         // this is the first
     int b;
 };
 
 template <int NC>
-__device__ __forceinline__ bool next_item(const MoeAttnArgs &a, bool whole, Walk &w, Item &it) {
+__device__ __forceinline__ bool next_item(const MoeAttnArgs &a, Walk &w, Item &it) {
     while (w.pos < w.end) {
         it.s = seq_of<NC>(a, w.b);
         const Seq &s = it.s;
-        const int units = whole ? 1 : s.tiles;
+        const int units = w.deal == DEAL_LINE ? kItemCost + s.tiles : 1;
         if (w.off >= (long long)s.cts * a.n_kv * units) {  // past the sequence's last item
             ++w.b;
             w.off = 0;
             continue;
         }
-        const int item = (int)(w.off / units), u0 = (int)(w.off % units);
-        const int take = (int)min((long long)(units - u0), w.end - w.pos);
-        const int tb = whole ? 0 : u0, te = whole ? s.tiles : u0 + take;
+        int item, tb = 0, te = s.tiles;
+        it.starts = true;
+        it.parts = 1;
+        if (w.deal == DEAL_LINE) {
+            item = (int)(w.off / units);
+            const int u0 = (int)(w.off - (long long)item * units);
+            const int take = (int)min((long long)(units - u0), w.end - w.pos);
+            w.pos += take;
+            w.off += take;
+            tb = max(0, u0 - kItemCost);
+            te = u0 + take - kItemCost;
+            if (te <= tb) continue;  // the piece ends before the item's first tile
+            it.starts = tb == 0;
+            it.parts = 1 + (int)((units - u0 - take + w.per - 1) / w.per) + (it.starts ? 0 : 1);
+        } else {
+            item = (int)w.off;
+            ++w.pos;
+            ++w.off;
+            if (w.deal == DEAL_PARTS) {
+                it.parts = min(w.parts, s.tiles);
+                if (w.part >= it.parts) continue;
+                tb = (int)((long long)s.tiles * w.part / it.parts);
+                te = (int)((long long)s.tiles * (w.part + 1) / it.parts);
+                it.starts = w.part == 0;
+            }
+        }
         it.b = w.b;
-        it.starts = u0 == 0;
-        it.rest = units - u0 - take;
         it.c0 = item / a.n_kv * NC;
         it.h = item % a.n_kv;
         const int i0 = it.c0 / a.group, i1 = (min(it.c0 + NC, s.ncol) - 1) / a.group;
@@ -248,8 +297,6 @@ __device__ __forceinline__ bool next_item(const MoeAttnArgs &a, bool whole, Walk
         it.x_lo = max(tb, (it.lo_min - s.lo) / kTile);
         it.x_hi = it.hi_max <= s.lo ? it.x_lo
                                     : max(it.x_lo, min(te, (it.hi_max - s.lo + kTile - 1) / kTile));
-        w.pos += take;
-        w.off += take;
         return true;
     }
     return false;
@@ -259,7 +306,7 @@ __device__ __forceinline__ bool next_item(const MoeAttnArgs &a, bool whole, Walk
 // K codes, V codes, K scales and V scales of 4 tiles. Lane = tile * 8 + array
 // * 2 + page of the tile (two where pages hold 16 tokens).
 template <int D, int NT>
-__device__ __forceinline__ void fill_ring(const MoeAttnArgs &a, bool whole, Walk walk, uint8_t *smem,
+__device__ __forceinline__ void fill_ring(const MoeAttnArgs &a, Walk walk, uint8_t *smem,
                                           uint64_t *full, uint64_t *empty, uint32_t (*valid)[kWarps],
                                           int *abort_flag) {
     using C = Cfg<D, NT>;
@@ -279,7 +326,7 @@ __device__ __forceinline__ void fill_ring(const MoeAttnArgs &a, bool whole, Walk
     uint32_t par = 1;  // of the empty barriers: a fresh one counts as passed
     int fills = 0;
     Item it;
-    while (next_item<C::NC>(a, whole, walk, it)) {
+    while (next_item<C::NC>(a, walk, it)) {
         const int32_t *pages = a.b.page_table + (int64_t)it.b * a.b.table_stride;
         // the page of this lane's tile of the stage at tile x (-2: not needed)
         auto page_at = [&](int x) {
@@ -336,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
     using C = Cfg<D, NT>;
     constexpr int NB = C::NB, NC = C::NC;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long s_tot[kWarps + 1], s_res[2];
+    __shared__ ScanSpace s_scan;
     __shared__ __align__(8) uint64_t full[kStages], empty[kStages];
     __shared__ uint32_t valid[kStages][kWarps];
     __shared__ float s_m[kWarps * NC], s_l[kWarps * NC];
@@ -354,26 +401,45 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
     }
     grid_dep_wait();
     grid_dep_launch();
-    Prefix mine = {0, 0};
-    const long long total = total_work<NC>(a, whole, s_tot, mine);
-    const long long per = piece_of(total, gridDim.x, whole);
-    Walk walk;
-    walk.pos = blockIdx.x * per;
-    walk.end = min(total, walk.pos + per);
+    Share mine = {0, 0}, incl = {0, 0};
+    int longest;
+    const Share all = total_share<NC>(a, s_scan, longest, mine, incl);
     Cut *cut = (Cut *)a.part + blockIdx.x;
     float *const recs = a.part + (size_t)gridDim.x * C::kHead;
     if (tid == 0 && !whole) cut->parts = 0;
+    if (all.items == 0) return;
+    Walk walk;
+    walk.part = 0;
+    walk.parts = 1;
+    walk.per = 1;
+    // parts of an item, if every CTA took one; at the finest
+    const int cap = (int)((long long)gridDim.x / all.items), fine = (longest + kMinTiles - 1) / kMinTiles;
+    walk.deal = whole ? DEAL_WHOLE : cap >= min(fine, 4) ? DEAL_PARTS : DEAL_LINE;
+    if (walk.deal == DEAL_WHOLE) {
+        const long long per = (all.items + gridDim.x - 1) / gridDim.x;
+        walk.pos = blockIdx.x * per;
+        walk.end = min(all.items, walk.pos + per);
+    } else if (walk.deal == DEAL_PARTS) {
+        walk.parts = min(cap, fine);
+        walk.pos = blockIdx.x / walk.parts;
+        walk.part = blockIdx.x % walk.parts;
+        walk.end = min(all.items, walk.pos + 1);
+    } else {
+        walk.per = max((all.units + gridDim.x - 1) / gridDim.x, (long long)(kItemCost + kMinTiles));
+        walk.pos = blockIdx.x * walk.per;
+        walk.end = min(all.units, walk.pos + walk.per);
+    }
     if (walk.pos >= walk.end) return;
-    find_unit<NC>(a, whole, walk.pos, mine, s_tot, s_res, walk.b, walk.off);
+    find_seq<NC>(a, walk.deal == DEAL_LINE, walk.pos, mine, incl, s_scan, walk.b, walk.off);
     if (wid == kWarps) {
-        fill_ring<D, NT>(a, whole, walk, smem, full, empty, valid, &s_abort);
+        fill_ring<D, NT>(a, walk, smem, full, empty, valid, &s_abort);
         return;
     }
     int use_st = 0;
     uint32_t use_par = 0;
     bool dead = false;  // a wait ran out
     Item it;
-    while (next_item<NC>(a, whole, walk, it)) {
+    while (next_item<NC>(a, walk, it)) {
         const Seq &s = it.s;
         const int c0 = it.c0, h = it.h, p0 = it.p0;
 
@@ -709,14 +775,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
                 }
             }
         consumers_sync();
-        const bool done = it.starts && it.rest == 0;
+        const bool done = it.parts == 1;
         float *rec = recs + ((int64_t)blockIdx.x * 2 + (it.starts ? 1 : 0)) * C::kRec;
-        if (tid == 0 && it.starts && it.rest > 0) {
+        if (tid == 0 && it.starts && it.parts > 1) {
             cut->q0 = s.q0;
             cut->c0 = c0;
             cut->ncol = s.ncol;
             cut->head = h;
-            cut->parts = 1 + (int)((it.rest + per - 1) / per);
+            cut->parts = it.parts;
         }
         for (int i = tid; i < NC * (D / 2); i += 32 * kWarps) {
             const int col = i / (D / 2), d = i % (D / 2) * 2;
@@ -836,10 +902,10 @@ template <int D, int NT>
 cudaError_t launch(const MoeAttnArgs &a, int nsm, cudaStream_t st) {
     using C = Cfg<D, NT>;
     const bool whole = whole_items(a.b.max_kv);
-    // no more CTAs than the bounds allow units
+    // no more CTAs than the bounds allow items, or parts of the least size
     const int64_t items = (int64_t)a.n_kv * ((int64_t)a.b.n_tokens * a.group / C::NC + a.b.n_seqs);
-    const int64_t units = whole ? items : items * ((a.b.max_kv + kTile - 1) / kTile + 1) / kMinTiles + 1;
-    const int ctas = (int)std::min<int64_t>(units, (int64_t)nsm * C::kCtasPerSm);
+    const int64_t parts = whole ? 1 : (a.b.max_kv / kTile + 2 + kMinTiles - 1) / kMinTiles;
+    const int ctas = (int)std::min<int64_t>(items * parts, (int64_t)nsm * C::kCtasPerSm);
     const cudaError_t err = launch_pdl_ready(moe_attn_split_kernel<D, NT>, dim3(ctas), dim3(kThreads), C::kSmem, st, a, whole);
     if (err != cudaSuccess || whole) return err;
     return launch_pdl_ready(moe_attn_join_kernel<D, NT>, dim3(ctas, C::NC / kJoinCols), dim3(32 * kJoinWarps), 0, st, a);
