@@ -384,6 +384,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
     constexpr int NB = C::NB, NC = C::NC;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ ScanSpace s_scan;
+    __shared__ __align__(16) uint32_t s_scale[kWarps][kTile * NB + kTile / 2 * NB];
     __shared__ __align__(8) uint64_t full[kStages], empty[kStages];
     __shared__ uint32_t valid[kStages][kWarps];
     __shared__ float s_m[kWarps * NC], s_l[kWarps * NC];
@@ -435,6 +436,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
         fill_ring<D, NT>(a, walk, smem, full, empty, valid, &s_abort);
         return;
     }
+    uint32_t *const kf = s_scale[wid], *const vf = kf + kTile * NB;  // scales of the warp's tile
+    const int vpair = NB == 4 ? lane >> 1 : lane & 15, vhalf = NB == 4 ? lane & 1 : 0;
+    const uint32_t lane_off = (lane & 8) * (NB * 16) + (lane >> 4) * 128 + (lane & 7) * 16;
     int use_st = 0;
     uint32_t use_par = 0;
     bool dead = false;  // a wait ran out
@@ -490,10 +494,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
 
         // ms: the maximum that weights are taken against, 0 while there is none
         float o[NB][2][NT][4], m[NT][2], ms[NT][2], l[NT][2];
-        uint32_t r15[NB];  // (15 - R) in both halves (as one product: no carry between them)
+        // (15 - R) in both halves, as one product so that nothing carries between
+        // them, of this lane's two blocks (see the scales below)
+        uint32_t r15[2] = {15u * 65537u, 15u * 65537u};
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
-            r15[k] = 15u * 65537u;
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
@@ -523,26 +528,103 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
             }
             const uint8_t *buf = smem + st * C::kStage + wid * C::kTileBytes;
             const uint32_t base = tc::smem_u32(buf);
-            const uint8_t *ks = buf + 2 * C::kCode, *vs = ks + C::kScale;
             const int tok0 = s.lo + kTile * (x + wid);
             const uint32_t live = valid[st][wid];
             const bool edge = tok0 + kTile > it.hi_min || tok0 < it.lo_max || live != kFull;
 
+            // --- scales, once for the warp. Keys: lane = token, 2^(byte - 127) of its
+            // blocks in fp32; the lowest bit set makes 255 a NaN (and is a 2^-23
+            // error otherwise).
+            {
+                const uint8_t *ks = buf + 2 * C::kCode + lane * NB;
+                const uint32_t w = NB == 4 ? *(const uint32_t *)ks : *(const uint16_t *)ks;
+                uint32_t f[NB];
+#pragma unroll
+                for (int k = 0; k < NB; ++k)
+                    f[k] = ((k == 0 ? w << 23 : k == 1 ? w << 15 : k == 2 ? w << 7 : w >> 1) & 0x7F800000u) | 1u;
+                if constexpr (NB == 4) *(uint4 *)(kf + 4 * lane) = make_uint4(f[0], f[1], f[2], f[3]);
+                else *(uint2 *)(kf + 2 * lane) = make_uint2(f[0], f[1]);
+            }
+            // Values: lane = token pair and pair of blocks, 2^(15 + e - R) of both
+            // tokens as an fp16 pair. e - R + 15 is in 0 .. 15 for all but few tiles.
+            bool special = false;  // a scale that is NaN
+            {
+                const uint32_t w = *(const uint32_t *)(buf + 2 * C::kCode + C::kScale + vpair * (2 * NB) + 4 * vhalf);
+                uint32_t e2[2] = {__byte_perm(w, 0u, 0x4140), __byte_perm(w, 0u, 0x4342)};
+                if (edge) {  // tokens that no column sees must not move R (their weight is 0)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int i = 2 * vpair + e, tk = tok0 + i;
+                        if (tk >= it.hi_max || tk < it.lo_min || !((live >> i) & 1u)) {
+                            const uint32_t half = 0xFFFFu << (16 * e);
+                            e2[0] = (e2[0] & ~half) | ((uint32_t)max_exp(r15[0]) << (16 * e));
+                            e2[1] = (e2[1] & ~half) | ((uint32_t)max_exp(r15[1]) << (16 * e));
+                        }
+                    }
+                }
+                uint32_t d0 = e2[0] + r15[0], d1 = e2[1] + r15[1];
+                if (__any_sync(kFull, ((d0 | d1) & 0xFFF0FFF0u) != 0u)) {
+                    float back[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t old = (uint32_t)max_exp(r15[j]);
+                        uint32_t top = old;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t y = (e2[j] >> (16 * e)) & 0xFFFFu;
+                            if (y == 255u) special = true;
+                            else top = max(top, y);
+                        }
+#pragma unroll
+                        for (int off = NB / 2; off < 32; off <<= 1) top = max(top, __shfl_xor_sync(kFull, top, off));
+                        back[j] = exp2f((float)((int)old - (int)top));
+                        r15[j] = (15u - top) * 65537u;
+                        // clamped at a zero factor (exponent field 0)
+                        const int y0 = (int)(e2[j] & 0xFFFFu) - (int)top, y1 = (int)(e2[j] >> 16) - (int)top;
+                        const uint32_t d = (uint32_t)((max(min(y1, 0), -30) + 15) * 65536 + max(min(y0, 0), -30) + 15);
+                        if (j == 0) d0 = d;
+                        else d1 = d;
+                    }
+                    special = __any_sync(kFull, special);
+#pragma unroll
+                    for (int k = 0; k < NB; ++k) {
+                        const float f = __shfl_sync(kFull, back[k & 1], k >> 1);
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) o[k][hh][n][c] *= f;
+                    }
+                }
+                d0 = d0 * 1024u + 0x3C003C00u;
+                d1 = d1 * 1024u + 0x3C003C00u;
+                if (special) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t half = 0xFFFFu << (16 * e);
+                        if (((e2[0] >> (16 * e)) & 0xFFFFu) == 255u) d0 = (d0 & ~half) | (0x7E007E00u & half);
+                        if (((e2[1] >> (16 * e)) & 0xFFFFu) == 255u) d1 = (d1 & ~half) | (0x7E007E00u & half);
+                    }
+                }
+                *(uint2 *)(vf + vpair * NB + 2 * vhalf) = make_uint2(d0, d1);
+            }
+            __syncwarp();
+
             // 16 tokens at a time, not unrolled: the body has to stay small for
-            // the instruction cache (12 to 16 warps run it out of step)
+            // the instruction cache (12 warps run it out of step)
 #pragma unroll 1
             for (int u = 0; u < 2; ++u) {
-                const uint32_t at = base + 2 * u * (NB * 128) +
-                                    (lane & 8) * (NB * 16) + (lane >> 4) * 128 + (lane & 7) * 16;
+                const uint32_t at = base + lane_off + 2 * u * (NB * 128);
                 // --- S^T = K Q^T
                 float sc[NT][4];
-                uint32_t w0, w1;  // scale bytes of tokens g and g + 8
+                float f0[NB], f1[NB];  // scales of tokens g and g + 8
                 if constexpr (NB == 4) {
-                    w0 = *(const uint32_t *)(ks + (16 * u + g) * 4);
-                    w1 = *(const uint32_t *)(ks + (16 * u + g + 8) * 4);
+                    *(float4 *)f0 = *(const float4 *)(kf + 4 * (16 * u + g));
+                    *(float4 *)f1 = *(const float4 *)(kf + 4 * (16 * u + g + 8));
                 } else {
-                    w0 = *(const uint16_t *)(ks + (16 * u + g) * 2);
-                    w1 = *(const uint16_t *)(ks + (16 * u + g + 8) * 2);
+                    *(float2 *)f0 = *(const float2 *)(kf + 2 * (16 * u + g));
+                    *(float2 *)f1 = *(const float2 *)(kf + 2 * (16 * u + g + 8));
                 }
 #pragma unroll
                 for (int kk = 0; kk < NB / 2; ++kk) {
@@ -554,35 +636,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
                         uint32_t ha[4], hb[4];
                         codes_f16(r[2 * k2], ha);
                         codes_f16(r[2 * k2 + 1], hb);
-                        // 2^(byte - 127); the lowest bit set makes 255 a NaN
-                        // (and is a 2^-23 error otherwise)
-                        const uint32_t e0 = k == 0 ? w0 << 23 : k == 1 ? w0 << 15 : k == 2 ? w0 << 7 : w0 >> 1;
-                        const uint32_t e1 = k == 0 ? w1 << 23 : k == 1 ? w1 << 15 : k == 2 ? w1 << 7 : w1 >> 1;
-                        const float f0 = __uint_as_float((e0 & 0x7F800000u) | 1u);
-                        const float f1 = __uint_as_float((e1 & 0x7F800000u) | 1u);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             float c[4];
                             mma_f16_0(c, ha[0], hb[0], ha[1], hb[1], qf[n][k][0], qf[n][k][1]);
                             mma_f16(c, ha[2], hb[2], ha[3], hb[3], qf[n][k][2], qf[n][k][3]);
-                            sc[n][0] = k == 0 ? c[0] * f0 : fmaf(c[0], f0, sc[n][0]);
-                            sc[n][1] = k == 0 ? c[1] * f0 : fmaf(c[1], f0, sc[n][1]);
-                            sc[n][2] = k == 0 ? c[2] * f1 : fmaf(c[2], f1, sc[n][2]);
-                            sc[n][3] = k == 0 ? c[3] * f1 : fmaf(c[3], f1, sc[n][3]);
+                            sc[n][0] = k == 0 ? c[0] * f0[k] : fmaf(c[0], f0[k], sc[n][0]);
+                            sc[n][1] = k == 0 ? c[1] * f0[k] : fmaf(c[1], f0[k], sc[n][1]);
+                            sc[n][2] = k == 0 ? c[2] * f1[k] : fmaf(c[2], f1[k], sc[n][2]);
+                            sc[n][3] = k == 0 ? c[3] * f1[k] : fmaf(c[3], f1[k], sc[n][3]);
                         }
                     }
                 }
-                // --- exponents of the value scales, tokens 2t, 2t + 1 of each octet
-                uint32_t v2[2][NB];
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-#pragma unroll
-                    for (int kk = 0; kk < NB / 2; ++kk) {
-                        const uint32_t w =
-                            *(const uint32_t *)(vs + (4 * (2 * u + q) + t) * (2 * NB) + 4 * kk);
-                        v2[q][2 * kk] = __byte_perm(w, 0u, 0x4140);
-                        v2[q][2 * kk + 1] = __byte_perm(w, 0u, 0x4342);
-                    }
                 // --- log2 domain, masks
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -596,19 +661,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
                             const int i = 16 * u + 8 * (c >> 1) + g, tk = tok0 + i;
                             if (tk >= hi[n][c & 1] || tk < lo[n][c & 1] || !((live >> i) & 1u))
                                 sc[n][c] = -INFINITY;
-                        }
-                    // tokens that no column sees must not move R (their weight is 0)
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int i = 16 * u + 8 * q + 2 * t + e, tk = tok0 + i;
-                            if (tk >= it.hi_max || tk < it.lo_min || !((live >> i) & 1u)) {
-                                const uint32_t half = 0xFFFFu << (16 * e);
-#pragma unroll
-                                for (int k = 0; k < NB; ++k)
-                                    v2[q][k] = (v2[q][k] & ~half) | ((uint32_t)max_exp(r15[k]) << (16 * e));
-                            }
                         }
                 }
                 // --- running maximum
@@ -625,18 +677,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
                         mx[n][c] = fmaxf(m[n][c], v);
                         grew |= mx[n][c] > m[n][c];
                     }
-                // --- weights' exponents: e - R + 15, in 0 .. 15 for all but rare tokens
-                uint32_t d2[2][NB], any = 0u;
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-#pragma unroll
-                    for (int k = 0; k < NB; ++k) {
-                        d2[q][k] = v2[q][k] + r15[k];
-                        any |= d2[q][k];
-                    }
-                const bool odd = (any & 0xFFF0FFF0u) != 0u;
-                bool special = false;  // a value scale that is NaN
-                if (__any_sync(kFull, grew || odd)) {
+                if (__any_sync(kFull, grew)) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -653,38 +694,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
                                     o[k][hh][n][c + 2] *= f;
                                 }
                         }
-                    if (__any_sync(kFull, odd)) {
-#pragma unroll
-                        for (int k = 0; k < NB; ++k) {
-                            uint32_t top = (uint32_t)max_exp(r15[k]);
-#pragma unroll
-                            for (int q = 0; q < 2; ++q)
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    const uint32_t x = (v2[q][k] >> (16 * e)) & 0xFFFFu;
-                                    if (x == 255u) special = true;
-                                    else top = max(top, x);
-                                }
-                            top = max(top, __shfl_xor_sync(kFull, top, 1));
-                            top = max(top, __shfl_xor_sync(kFull, top, 2));
-                            const float f = exp2f((float)(max_exp(r15[k]) - (int)top));
-                            r15[k] = (15u - top) * 65537u;
-#pragma unroll
-                            for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-                                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                    for (int c = 0; c < 4; ++c) o[k][hh][n][c] *= f;
-                            // clamped at a zero factor (exponent field 0)
-#pragma unroll
-                            for (int q = 0; q < 2; ++q) {
-                                const int x0 = (int)(v2[q][k] & 0xFFFFu) - (int)top + 15;
-                                const int x1 = (int)(v2[q][k] >> 16) - (int)top + 15;
-                                d2[q][k] = (uint32_t)(min(max(x1, -15), 15) * 65536 + min(max(x0, -15), 15));
-                            }
-                        }
-                        special = __any_sync(kFull, special);
-                    }
                 }
                 // --- weights of tokens (2t, 2t + 1) of octets 0 and 1, column g
                 uint32_t pt[NT][2], pv[NT][2][NB];
@@ -700,28 +709,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
                     pt[n][1] = transpose8(pack_f16(p[2], p[3]));
                 }
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t f[NB];  // factors of the same tokens
+                    const uint32_t *src = vf + (8 * u + 4 * q + t) * NB;
+                    if constexpr (NB == 4) *(uint4 *)f = *(const uint4 *)src;
+                    else *(uint2 *)f = *(const uint2 *)src;
 #pragma unroll
-                    for (int k = 0; k < NB; ++k) {
-                        const uint32_t f = d2[q][k] * 1024u + 0x3C003C00u;  // 2^(e - R + 15)
+                    for (int k = 0; k < NB; ++k)
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) pv[n][q][k] = mul_f16x2(pt[n][q], f);
-                    }
-                if (special) {  // NaN for the columns that give the token any weight
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-#pragma unroll
-                        for (int k = 0; k < NB; ++k)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const uint32_t half = 0xFFFFu << (16 * e);
-                                if (((v2[q][k] >> (16 * e)) & 0xFFFFu) == 255u) {
-#pragma unroll
-                                    for (int n = 0; n < NT; ++n)
-                                        pv[n][q][k] = (pv[n][q][k] & ~half) |
-                                                      ((pt[n][q] & half) ? 0x7E007E00u & half : 0u);
-                                }
+                        for (int n = 0; n < NT; ++n) {
+                            pv[n][q][k] = mul_f16x2(pt[n][q], f[k]);
+                            if (special) {  // a NaN value is none for the columns that give it no weight
+                                if ((pt[n][q] & 0xFFFFu) == 0u) pv[n][q][k] &= 0xFFFF0000u;
+                                if ((pt[n][q] >> 16) == 0u) pv[n][q][k] &= 0x0000FFFFu;
                             }
+                        }
                 }
                 // --- O^T += V^T P^T
 #pragma unroll
@@ -752,6 +754,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
         }
 
         // --- the 4 warps' results: o, m, l of each column
+        float back[NB];  // 2^(R - 127) / 2^15
+#pragma unroll
+        for (int k = 0; k < NB; ++k)
+            back[k] = exp2f((float)(max_exp(__shfl_sync(kFull, r15[k & 1], k >> 1)) - 142));
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -768,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
                 float *dst = s_o + (wid * NC + col) * C::kOStride + 4 * g;
 #pragma unroll
                 for (int k = 0; k < NB; ++k) {
-                    const float f = exp2f((float)(max_exp(r15[k]) - 142));  // 2^(R - 127) / 2^15
+                    const float f = back[k];  // 2^(R - 127) / 2^15
                     *(float4 *)(dst + 32 * k) =
                         make_float4(o[k][0][n][c] * f, o[k][0][n][c + 2] * f, o[k][1][n][c] * f,
                                     o[k][1][n][c + 2] * f);
