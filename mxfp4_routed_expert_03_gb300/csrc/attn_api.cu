@@ -113,6 +113,7 @@ MOE_API int moe_qk_norm_rope(moe_attn *a, int32_t T, const moe_rope_desc *r,
         return MOE_ERR_INVALID_ARG;
     if (k && (!rows_ok(k, k_stride, kw) || !rows_ok(k_out, k_out_stride, kw)))
         return MOE_ERR_INVALID_ARG;
+    if ((int64_t)T * (d.n_heads + d.n_kv_heads) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
     MoeRopeArgs g = {};
     g.n_q = q ? d.n_heads : 0;
     g.n_k = k ? d.n_kv_heads : 0;

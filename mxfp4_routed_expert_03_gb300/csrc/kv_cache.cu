@@ -18,11 +18,23 @@
 
 #include "common.cuh"
 #include "kernels.h"
-#include "mx8.cuh"
 
 namespace {
 
 constexpr int kWarps = 4;
+
+// Eight fp32 values to E2M1 codes, the first in the lowest nibble (round to
+// nearest even, saturating).
+__device__ __forceinline__ uint32_t to_e2m1x8(const float (&v)[8]) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
 
 // Slot of a token, split into page-head base and offset; false: skip it.
 __device__ __forceinline__ bool slot_ok(const MoeKvArgs &a, int slot) {
@@ -53,23 +65,25 @@ template <int D>
 __global__ void __launch_bounds__(32 * kWarps) moe_kv_append_kernel(MoeKvArgs a) {
     constexpr int NB = D / 32;
     const int lane = threadIdx.x & 31;
-    const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int tok = (int)(unit / (2 * a.n_kv)) * 8 + (lane >> 2);
-    const int sub = (int)(unit % (2 * a.n_kv)), head = sub >> 1, q = lane & 3;
+    const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5), group = unit / (2u * a.n_kv);
+    const int tok = (int)group * 8 + (lane >> 2);
+    const int sub = (int)(unit - group * (2u * a.n_kv)), head = sub >> 1, q = lane & 3;
     const bool is_v = sub & 1;
     grid_dep_wait();
     grid_dep_launch();
     int slot = -1;
     if (tok < a.n) slot = a.slots[tok];
-    const bool ok = slot_ok(a, slot);
     const uint16_t *src = (is_v ? a.v + (int64_t)tok * a.v_stride : a.k + (int64_t)tok * a.k_stride) +
                           head * D + 8 * q;
     uint4 raw[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
-        raw[b] = ok ? *(const uint4 *)(src + 32 * b) : make_uint4(0u, 0u, 0u, 0u);
+        raw[b] = tok < a.n ? *(const uint4 *)(src + 32 * b) : make_uint4(0u, 0u, 0u, 0u);
+    const bool ok = slot_ok(a, slot);  // (behind the loads, which do not wait for it)
     uint32_t scale = 0u;  // lane q keeps block q's byte (NB <= 4)
     uint32_t code[NB];
+    // The scale byte of a block whose largest magnitude has the bf16 bits m:
+    // exponent field - 2, at least 0 (2^-127); its inverse is 2^(127 - byte).
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         const uint32_t w[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
@@ -80,16 +94,16 @@ __global__ void __launch_bounds__(32 * kWarps) moe_kv_append_kernel(MoeKvArgs a)
         m = max(m & 0xFFFFu, m >> 16);
         m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
         m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-        const int e = mx4::scale_exp(__uint_as_float(m << 16));
-        const float inv = mx8::exp2i(-e);
-        code[b] = 0u;
+        const uint32_t byte = (uint32_t)max((int)(m >> 7) - 2, 0);
+        const float inv = __uint_as_float((254u - byte) << 23);
+        float v[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            code[b] |= mx4::to_e2m1x2(__uint_as_float(w[j] << 16) * inv,
-                                      __uint_as_float(w[j] & 0xFFFF0000u) * inv)
-                       << (8 * j);
-        const uint32_t byte = m >= 0x7F80u ? 255u : (uint32_t)(e + 127);
-        if (q == b) scale = byte;
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = __uint_as_float(w[j] << 16) * inv;
+            v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u) * inv;
+        }
+        code[b] = to_e2m1x8(v);
+        if (q == b) scale = m >= 0x7F80u ? 255u : byte;
     }
     if (!ok) return;
     uint8_t *dq = (is_v ? a.c.v_q : a.c.k_q) + code_offset<NB>(a, slot, head) + 4 * q;
@@ -111,9 +125,9 @@ template <int D>
 __global__ void __launch_bounds__(32 * kWarps) moe_kv_read_kernel(MoeKvArgs a) {
     constexpr int NB = D / 32;
     const int lane = threadIdx.x & 31;
-    const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int tok = (int)(unit / (2 * a.n_kv)) * 8 + (lane >> 2);
-    const int sub = (int)(unit % (2 * a.n_kv)), head = sub >> 1, q = lane & 3;
+    const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5), group = unit / (2u * a.n_kv);
+    const int tok = (int)group * 8 + (lane >> 2);
+    const int sub = (int)(unit - group * (2u * a.n_kv)), head = sub >> 1, q = lane & 3;
     const bool is_v = sub & 1;
     grid_dep_wait();
     grid_dep_launch();

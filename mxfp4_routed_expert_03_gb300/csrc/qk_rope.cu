@@ -38,29 +38,24 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// P passes of 32 / (D / 16) head rows per warp; rows [0, n_q) are the
-// queries', the next n_k the keys'.
+// A warp takes P passes of 32 / (D / 16) head rows of one token; rows [0, n_q)
+// are the queries', the next n_k the keys'. `groups` warps share a token.
 template <int D, int P>
-__global__ void __launch_bounds__(32 * kWarps) moe_qk_norm_rope_kernel(MoeRopeArgs a) {
+__global__ void __launch_bounds__(32 * kWarps) moe_qk_norm_rope_kernel(MoeRopeArgs a, int T, int groups) {
     constexpr int TPH = D / 16;   // threads per head row
     constexpr int HP = 32 / TPH;  // head rows per warp and pass
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    const int64_t t = blockIdx.x;
+    const uint32_t task = blockIdx.x * kWarps + wid, token = task / groups, group = task - token * groups;
+    if (token >= (uint32_t)T) return;
+    const int64_t t = token;
     const int i = lane % TPH, rows = a.n_q + a.n_k;
-    const int row0 = (blockIdx.y * kWarps + wid) * P * HP + lane / TPH;
+    const int row0 = group * P * HP + lane / TPH;
     grid_dep_wait();
     grid_dep_launch();
     const int np = a.rope_dim / 16;
     const bool turn = i < np;
     const int c0 = turn ? i : 2 * np + 2 * (i - np), c1 = turn ? i + np : c0 + 1;
-    int pos = 0;
-    if (np > 0) {
-        pos = a.positions[t];
-        if (pos < 0 || pos >= a.n_pos) {
-            if (threadIdx.x == 0 && blockIdx.y == 0) moe_flag(a.status, MOE_ERR_BAD_INDEX);
-            return;
-        }
-    }
+    const int pos = np > 0 ? a.positions[t] : 0;  // (in flight beside the rows)
     uint4 raw[P][2];
 #pragma unroll
     for (int p = 0; p < P; ++p) {
@@ -71,6 +66,12 @@ __global__ void __launch_bounds__(32 * kWarps) moe_qk_norm_rope_kernel(MoeRopeAr
                                             : a.k + t * a.k_stride + (int64_t)(r - a.n_q) * D;
             raw[p][0] = *(const uint4 *)(src + 8 * c0);
             raw[p][1] = *(const uint4 *)(src + 8 * c1);
+        }
+    }
+    if (np > 0) {
+        if (pos < 0 || pos >= a.n_pos) {
+            if (lane == 0 && group == 0) moe_flag(a.status, MOE_ERR_BAD_INDEX);
+            return;
         }
     }
     // halves: cs[j] / sn[j] belong to pair j of the thread (element j of both
@@ -138,17 +139,36 @@ __global__ void __launch_bounds__(32 * kWarps) moe_qk_norm_rope_kernel(MoeRopeAr
 
 template <int D, int P>
 cudaError_t launch(int T, const MoeRopeArgs &a, cudaStream_t st) {
-    const int per_block = kWarps * P * (32 / (D / 16));
-    const dim3 grid(T, (a.n_q + a.n_k + per_block - 1) / per_block);
-    return launch_pdl_ready(moe_qk_norm_rope_kernel<D, P>, grid, dim3(32 * kWarps), 0, st, a);
+    const int per_warp = P * (32 / (D / 16)), groups = (a.n_q + a.n_k + per_warp - 1) / per_warp;
+    const int64_t tasks = (int64_t)T * groups;
+    return launch_pdl_ready(moe_qk_norm_rope_kernel<D, P>, dim3((unsigned)((tasks + kWarps - 1) / kWarps)),
+                            dim3(32 * kWarps), 0, st, a, T, groups);
+}
+
+template <int D>
+cudaError_t launch(int T, const MoeRopeArgs &a, int nsm, cudaStream_t st) {
+    const int passes = (a.n_q + a.n_k + 32 / (D / 16) - 1) / (32 / (D / 16));
+    // few tokens: one pass per warp, so that the rows spread over the SMs; else
+    // the largest of 4, 3 and 2 that wastes the fewest passes (more loads in
+    // flight: 8191 tokens of 72 heads 73 us with 4 passes a warp of which a
+    // quarter were empty, 56 us with 3)
+    if ((int64_t)T * (a.n_q + a.n_k) < (int64_t)nsm * 64) return launch<D, 1>(T, a, st);
+    int best = 4, waste = (passes + 3) / 4 * 4 - passes;
+    for (int p = 3; p >= 2; --p) {
+        const int w = (passes + p - 1) / p * p - passes;
+        if (w < waste) best = p, waste = w;
+    }
+    return best == 4 ? launch<D, 4>(T, a, st) : best == 3 ? launch<D, 3>(T, a, st) : launch<D, 2>(T, a, st);
 }
 
 }  // namespace
 
 cudaError_t moe_qk_norm_rope_setup() {
     const void *kernels[] = {
-        (const void *)moe_qk_norm_rope_kernel<64, 1>, (const void *)moe_qk_norm_rope_kernel<64, 4>,
-        (const void *)moe_qk_norm_rope_kernel<128, 1>, (const void *)moe_qk_norm_rope_kernel<128, 4>};
+        (const void *)moe_qk_norm_rope_kernel<64, 1>,  (const void *)moe_qk_norm_rope_kernel<64, 2>,
+        (const void *)moe_qk_norm_rope_kernel<64, 3>,  (const void *)moe_qk_norm_rope_kernel<64, 4>,
+        (const void *)moe_qk_norm_rope_kernel<128, 1>, (const void *)moe_qk_norm_rope_kernel<128, 2>,
+        (const void *)moe_qk_norm_rope_kernel<128, 3>, (const void *)moe_qk_norm_rope_kernel<128, 4>};
     for (const void *k : kernels) {
         const cudaError_t err = set_kernel(k);
         if (err != cudaSuccess) return err;
@@ -158,8 +178,5 @@ cudaError_t moe_qk_norm_rope_setup() {
 
 cudaError_t moe_launch_qk_norm_rope(int T, int head_dim, const MoeRopeArgs &a, int nsm,
                                     cudaStream_t st) {
-    // few tokens: one pass per warp, so that the rows spread over the SMs
-    const bool few = (int64_t)T * (a.n_q + a.n_k) < (int64_t)nsm * 64;
-    if (head_dim == 64) return few ? launch<64, 1>(T, a, st) : launch<64, 4>(T, a, st);
-    return few ? launch<128, 1>(T, a, st) : launch<128, 4>(T, a, st);
+    return head_dim == 64 ? launch<64>(T, a, nsm, st) : launch<128>(T, a, nsm, st);
 }
