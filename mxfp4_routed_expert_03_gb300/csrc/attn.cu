@@ -44,7 +44,7 @@ constexpr int kWarps = 4;              // that compute, a tile each; one more fi
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kStages = 3;
 constexpr int kMinTiles = kWarps;      // of a piece
-constexpr int kItemCost = 8;           // an item's start and end (3 us) in tiles
+constexpr int kItemCost = 12;          // an item's start and end in tiles (50 us for 64 ragged sequences, 53 with 8)
 
 template <int D, int NT>
 struct Cfg {
@@ -328,6 +328,14 @@ __device__ __forceinline__ void fill_ring(const MoeAttnArgs &a, Walk walk, uint8
     Item it;
     while (next_item<C::NC>(a, walk, it)) {
         const int32_t *pages = a.b.page_table + (int64_t)it.b * a.b.table_stride;
+        // the item's queries, which the other warps load when they get there
+        for (int i = lane; i < C::NC * (D / 64); i += 32) {
+            const int c = it.c0 + i / (D / 64);
+            if (c < it.s.ncol)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                    a.q + (int64_t)(it.s.q0 + c / a.group) * a.q_stride + (it.h * a.group + c % a.group) * D +
+                    i % (D / 64) * 64));
+        }
         // the page of this lane's tile of the stage at tile x (-2: not needed)
         auto page_at = [&](int x) {
             const int tok = it.s.lo + kTile * (x + tile) + 16 * part;

@@ -46,12 +46,12 @@ __global__ void __launch_bounds__(32 * kWarps) moe_qk_norm_rope_kernel(MoeRopeAr
     constexpr int HP = 32 / TPH;  // head rows per warp and pass
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const uint32_t task = blockIdx.x * kWarps + wid, token = task / groups, group = task - token * groups;
-    if (token >= (uint32_t)T) return;
     const int64_t t = token;
     const int i = lane % TPH, rows = a.n_q + a.n_k;
     const int row0 = group * P * HP + lane / TPH;
     grid_dep_wait();
     grid_dep_launch();
+    if (token >= (uint32_t)T) return;
     const int np = a.rope_dim / 16;
     const bool turn = i < np;
     const int c0 = turn ? i : 2 * np + 2 * (i - np), c1 = turn ? i + np : c0 + 1;
