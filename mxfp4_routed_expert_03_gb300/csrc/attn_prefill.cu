@@ -2,23 +2,26 @@
 // mathematics as the split kernel, on tcgen05 tensor cores.
 //
 // A CTA owns 256 columns (query rows x heads of one key/value head) of one
-// sequence as two tiles A and B of 128, and runs over the keys 128 at a time:
-//   S_t = Q_t K^T        (128 x 128 x D, operands in shared memory, S in TMEM)
+// sequence as two tiles A and B of 128, and runs over the keys in steps of 128,
+// a step as two units of 64:
+//   S_t = Q_t K^T        (128 x 64 x D, operands in shared memory, S in TMEM)
 //   P_t = 2^(S_t - m)    (a thread per row: TMEM -> registers -> TMEM, fp16)
 //   O_t += P_t V         (P from TMEM over S's columns, V from shared memory)
-// so the tensor cores work on one tile while the other's softmax runs: warps
-// 0-3 hold tile A's rows, 4-7 tile B's, 8-13 turn the cache's codes into
-// operands (each key and value once per CTA, i.e. once per 256 columns), 14
-// and 15 issue the tiles' MMAs. TMEM is full: S_A, S_B, O_A, O_B of 128
-// columns each.
+// Each tile has two S buffers: the products of the next unit run while the rows
+// work on this one (one buffer of 128 keys instead, a step's products waiting
+// for its softmax and the other way round: 361 us against 341 for 3 prompts of
+// 2000 rows, 32 heads and up to 8000 keys). Warps 0-3 hold tile A's rows, 4-7
+// tile B's, 8-13 turn the cache's codes into operands (each key and value once
+// per CTA, i.e. once per 256 columns), 14 and 15 issue the tiles' MMAs. TMEM is
+// full: S_A, S_B (two units each), O_A, O_B of 128 columns each.
 //
 // Operands are fp16: a code is exact, and its scale enters as 2^(e - R + 12)
 // with R the largest key exponent (or, per block of 32 dimensions, the largest
 // value exponent) that the CTA's rows can see, found in a pass over the scales
-// before the loop; what lies over 2^26 below the largest loses bits, over
-// 2^36 it vanishes. Queries as in the split kernel. The running maximum only
+// before the loop; a block whose scale lies over 2^26 below the largest counts
+// as 0. Queries as in the split kernel. The running maximum only
 // moves when it would rise by more than 2^8 (P stays far inside fp16's range),
-// so O is rescaled a few times per row and not once per tile.
+// so O is rescaled a few times per row and not once per unit.
 //
 // Bound: 4 D flops per column and key on the tensor cores; one exponential per
 // column and key (32 a cycle and SM) is next.
@@ -33,14 +36,12 @@ namespace {
 constexpr int kM = 128;          // rows of a tile (columns of the item)
 constexpr int kCols = 2 * kM;    // columns of a CTA
 constexpr int kN = 128;          // keys per step
+constexpr int kU = kN / 2;       // keys per unit: of one S, one P
 // warps 0-7 rows, 8-10 keys, 11-13 values, 14 and 15 MMA issue of tile A and B
 // (one issuer's instructions take longer than the products: about 90 cycles
 // each, against 64)
 constexpr int kWarpsP = 16;
 constexpr int kWarpK = 8, kWarpV = 11, kWarpMma = 14, kConv = 3;
-// registers of a thread: 128 at launch, moved to the warps that hold rows (a
-// row's 128 logits stay in registers): 8 x 176 + 8 x 80 = 16 x 128
-constexpr int kRegsRows = 176, kRegsRest = 80;
 constexpr int kThreadsP = 32 * kWarpsP;
 constexpr int kInfo = 4;         // steps whose masks are kept
 constexpr int kHead = 12;        // operands carry 2^12
@@ -83,14 +84,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
         : "r"(taddr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-        "%12, %13, %14, %15, %16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
@@ -105,6 +98,36 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
 }
 __device__ __forceinline__ void tmem_st_wait() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() {  // of the thread's own copies
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+// Two fp32 operations an instruction.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &x, float &y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 // D[tmem] (+)= A[tmem] x B[smem], fp16 operands, 16 K per instruction.
 __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
@@ -265,7 +288,7 @@ __device__ __forceinline__ bool item_of(const MoeAttnArgs &a, int tiles_max, int
     if (lane < B) s = seq_of<kCols>(a, lane);
     // the largest L with more than r tiles of L keys or more (0: any tile)
     int L = 0;
-    for (int bit = 30; bit >= 0; --bit) {
+    for (int bit = 31 - __clz(max(a.b.max_kv, 1)); bit >= 0; --bit) {
         const int t = L | (1 << bit);
         if (t <= a.b.max_kv &&
             (int)__reduce_add_sync(kFull, lane < B ? (unsigned)tiles_from(s, a.group, t) : 0u) > r)
@@ -295,11 +318,12 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     constexpr int NB = C::NB;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    __shared__ __align__(8) uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2],
-        o_full[2], drain[2], b_start;
+    __shared__ __align__(8) uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2][2],
+        p_full[2][2], o_full[2][2], drain[2], b_start;
     __shared__ StepInfo info[kInfo];
     __shared__ int s_rk, s_rv[NB], s_abort;
     __shared__ uint32_t s_tmem;
+    __shared__ float s_mul[kCols];
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
 
     grid_dep_wait();
@@ -328,9 +352,11 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             tc::mbar_init(&v_full[i], kConv);
             tc::mbar_init(&v_empty[i], two ? 2 : 1);
             tc::mbar_init(&drain[i], 1);
-            tc::mbar_init(&s_full[i], 2);
-            tc::mbar_init(&p_full[i], 4);
-            tc::mbar_init(&o_full[i], 2);
+            for (int k = 0; k < 2; ++k) {
+                tc::mbar_init(&s_full[i][k], 2);
+                tc::mbar_init(&p_full[i][k], 4);
+                tc::mbar_init(&o_full[i][k], 2);
+            }
         }
         for (int i = 0; i < kInfo; ++i) info[i].any[0] = info[i].any[1] = 0u;
         tc::mbar_init(&b_start, 4);
@@ -343,52 +369,24 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         tc::tmem_alloc(&s_tmem, 512);
         tc::tmem_relinquish();
     }
-    // --- queries: fp16 with one power of two per row
-    float mul = 0.f;  // of this thread's row: back from that power, |scale| log2(e)
-    if (wid < 8) {
-        const int c = c0 + tid, r = tid & (kM - 1);
-        uint4 raw[D / 8];
-        uint32_t top = 0u;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-            raw[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (c < s.ncol)
-                raw[i] = *(const uint4 *)(a.q + (int64_t)(s.q0 + c / G) * a.q_stride +
-                                          (h * G + c % G) * D + 8 * i);
-            top = __vmaxu2(top, raw[i].x & 0x7FFF7FFFu);
-            top = __vmaxu2(top, raw[i].y & 0x7FFF7FFFu);
-            top = __vmaxu2(top, raw[i].z & 0x7FFF7FFFu);
-            top = __vmaxu2(top, raw[i].w & 0x7FFF7FFFu);
-        }
-        top = max(top & 0xFFFFu, top >> 16);
-        const bool bad = top >= 0x7F80u;  // the row is NaN: zero operand, NaN factor
-        const int sh = min(141 - (int)(top >> 7), 127);
-        // a negative scale's sign goes into the queries, so that the largest
-        // product is the largest logit
-        const float up = bad ? 0.f : copysignf(pow2(sh), a.b.scale);
-        mul = bad ? CUDART_NAN_F : pow2(-sh) * (fabsf(a.b.scale) * CUDART_L2E_F);
-        uint8_t *dst = smem + C::kSmemQ + (tid >> 7) * C::kOp + (r >> 3) * 1024 + (r & 7) * 128;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-            uint32_t f[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float x = bad ? 0.f : __uint_as_float(w[j] << 16) * up;
-                const float y = bad ? 0.f : __uint_as_float(w[j] & 0xFFFF0000u) * up;
-                f[j] = pack_f16(x, y);
-            }
-            *(uint4 *)(dst + (i >> 3) * C::kHalf + (((i & 7) ^ (r & 7)) << 4)) =
-                make_uint4(f[0], f[1], f[2], f[3]);
-        }
-        tc::fence_proxy_async_smem();
+    // --- queries: a row's chunks of 8 elements side by side in a warp, into the
+    // operand's place while the scales are read
+    constexpr int LPR = D / 8, ROWS = 32 / LPR;
+    const int chunk = lane % LPR;
+    auto q_at = [&](int r) {
+        return smem + C::kSmemQ + (r >> 7) * C::kOp + ((r & (kM - 1)) >> 3) * 1024 + (r & 7) * 128 +
+               (chunk >> 3) * C::kHalf + (((chunk & 7) ^ (r & 7)) << 4);
+    };
+#pragma unroll 1
+    for (int r = wid * ROWS + lane / LPR; r < kCols; r += ROWS * kWarpsP) {
+        const int c = min(c0 + r, s.ncol - 1);  // (columns past the last are not used)
+        cp_async16(q_at(r), a.q + (int64_t)(s.q0 + c / G) * a.q_stride + (h * G + c % G) * D + 8 * chunk);
     }
     __syncthreads();
     // --- the largest exponents that a row can see: 16 tokens (of one page) a thread
     {
-        uint32_t mk = 0u, mv[NB];
-#pragma unroll
-        for (int k = 0; k < NB; ++k) mv[k] = 0u;
+        constexpr int WORDS = 4 * NB;  // of 16 tokens
+        uint32_t mk = 0u, mv[2] = {0u, 0u};  // V: byte 2 k + (token & 1) of block k (of 0, 1 and 2, 3)
         for (int tok = first + 16 * tid; tok < min(hi_all, first + kN * n); tok += 16 * kThreadsP) {
             const int id = pages[tok >> a.page_shift];
             if (id < 0 || id >= a.n_pages) {
@@ -396,40 +394,66 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 continue;
             }
             const int64_t row = (((int64_t)id * a.n_kv + h) << a.page_shift) + (tok & in_page_mask);
-            const uint8_t *ks = a.c.k_s + row * NB, *vs = a.c.v_s + row * NB;
+            uint32_t ks[WORDS], vs[WORDS];
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-                uint32_t k0, k1, v0, v1;  // K: tokens i, i + 1; V: blocks 0, 1 and 2, 3 of both
+            for (int i = 0; i < WORDS; i += 4) {
+                *(uint4 *)(ks + i) = *(const uint4 *)(a.c.k_s + row * NB + 4 * i);
+                *(uint4 *)(vs + i) = *(const uint4 *)(a.c.v_s + row * NB + 4 * i);
+            }
+            auto see = [&](int i) { return tok + i >= lo_all && tok + i < hi_all; };
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) {
+                uint32_t kk, kv;  // bytes of tokens that are seen
                 if constexpr (NB == 4) {
-                    const uint2 x = *(const uint2 *)(ks + 4 * i), y = *(const uint2 *)(vs + 4 * i);
-                    k0 = x.x, k1 = x.y, v0 = y.x, v1 = y.y;
+                    kk = see(i) ? kFull : 0u;
+                    kv = (see(i & ~1) ? 0x00FF00FFu : 0u) | (see(i | 1) ? 0xFF00FF00u : 0u);
                 } else {
-                    const uint32_t x = *(const uint32_t *)(ks + 2 * i);
-                    k0 = x & 0xFFFFu, k1 = x >> 16, v0 = *(const uint32_t *)(vs + 2 * i), v1 = 0u;
+                    kk = (see(2 * i) ? 0xFFFFu : 0u) | (see(2 * i + 1) ? 0xFFFF0000u : 0u);
+                    kv = (see(2 * i) ? 0x00FF00FFu : 0u) | (see(2 * i + 1) ? 0xFF00FF00u : 0u);
                 }
-                const bool see0 = tok + i >= lo_all && tok + i < hi_all;
-                const bool see1 = tok + i + 1 >= lo_all && tok + i + 1 < hi_all;
-                const uint32_t keep = (see0 ? 0x00FF00FFu : 0u) | (see1 ? 0xFF00FF00u : 0u);
-                mk = __vmaxu4(mk, __vmaxu4(see0 ? finite_bytes(k0) : 0u, see1 ? finite_bytes(k1) : 0u));
-                v0 = finite_bytes(v0) & keep;
-                v1 = finite_bytes(v1) & keep;
-                mv[0] = max(mv[0], max(v0 & 0xFFu, (v0 >> 8) & 0xFFu));
-                mv[1] = max(mv[1], max((v0 >> 16) & 0xFFu, v0 >> 24));
-                if constexpr (NB == 4) {
-                    mv[2] = max(mv[2], max(v1 & 0xFFu, (v1 >> 8) & 0xFFu));
-                    mv[3] = max(mv[3], max((v1 >> 16) & 0xFFu, v1 >> 24));
-                }
+                mk = __vmaxu4(mk, finite_bytes(ks[i]) & kk);
+                uint32_t &m = mv[NB == 4 ? i & 1 : 0];
+                m = __vmaxu4(m, finite_bytes(vs[i]) & kv);
             }
         }
-        mk = max(max(mk & 0xFFu, (mk >> 8) & 0xFFu), max((mk >> 16) & 0xFFu, mk >> 24));
-        mk = __reduce_max_sync(kFull, mk);
+        mk = __vmaxu4(mk, mk >> 16);
+        mk = __reduce_max_sync(kFull, max(mk & 0xFFu, (mk >> 8) & 0xFFu));
         if (lane == 0) atomicMax(&s_rk, (int)mk);
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
-            const uint32_t v = __reduce_max_sync(kFull, mv[k]);
+            const uint32_t m = mv[k >> 1] >> (16 * (k & 1));
+            const uint32_t v = __reduce_max_sync(kFull, max(m & 0xFFu, (m >> 8) & 0xFFu));
             if (lane == 0) atomicMax(&s_rv[k], (int)v);
         }
     }
+    // --- queries: fp16 with one power of two per row
+    cp_async_wait();
+#pragma unroll 1
+    for (int r = wid * ROWS + lane / LPR; r < kCols; r += ROWS * kWarpsP) {
+        const uint4 raw = *(const uint4 *)q_at(r);
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+        uint32_t top = 0u, f[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = __vmaxu2(top, w[j] & 0x7FFF7FFFu);
+#pragma unroll
+        for (int o = LPR / 2; o; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(kFull, top, o));
+        top = max(top & 0xFFFFu, top >> 16);
+        const bool bad = top >= 0x7F80u;  // the row is NaN: zero operand, NaN factor
+        const int sh = min(141 - (int)(top >> 7), 127);
+        // a negative scale's sign goes into the queries, so that the largest
+        // product is the largest logit
+        const float up = bad ? 0.f : copysignf(pow2(sh), a.b.scale);
+        // back from that power, |scale| log2(e)
+        if (chunk == 0) s_mul[r] = bad ? CUDART_NAN_F : pow2(-sh) * (fabsf(a.b.scale) * CUDART_L2E_F);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float x = bad ? 0.f : __uint_as_float(w[j] << 16) * up;
+            const float y = bad ? 0.f : __uint_as_float(w[j] & 0xFFFF0000u) * up;
+            f[j] = pack_f16(x, y);
+        }
+        *(uint4 *)q_at(r) = make_uint4(f[0], f[1], f[2], f[3]);
+    }
+    tc::fence_proxy_async_smem();
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
@@ -437,7 +461,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     const long long limit = a.timeout_cycles;
     // a bounded wait of a whole warp; false: give up
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        const bool ok = tc::mbar_wait(bar, parity & 1u, limit, &s_abort);
+        const bool ok = tc::mbar_wait_sleep(bar, parity & 1u, limit, &s_abort);
         if (__all_sync(kFull, ok)) return true;
         if (lane == 0) {
             moe_flag(a.status, MOE_ERR_DEVICE_TIMEOUT);
@@ -446,10 +470,6 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         return false;
     };
 
-    if (wid < 8)
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRows));
-    else
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (wid < 8) {
         // ------------------------------------------------ softmax: a thread per row
         const int t = wid >> 2;
@@ -462,7 +482,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             const int hi = c < s.ncol ? p0 + c / G + 1 : 0x7FFFFFFF;
             const int lo = c < s.ncol && W > 0 ? hi - W : 0;
             // logits: S x mul x 2^(R - 127 - 12); not 0, for masked columns are -inf
-            float mr = mul * exp2f((float)(s_rk - 127 - kHead));
+            float mr = s_mul[tid] * exp2f((float)(s_rk - 127 - kHead));
             if (mr == 0.f) mr = 1.17549435e-38f;
             float m = -INFINITY, l = 0.f;  // m: the maximum in use
             // tokens tok0 + 32 q .. + 31 that the row sees
@@ -488,50 +508,46 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             };
             uint32_t nan_blocks = 0u;
             bool ok = true;
-            for (int j = 0; j < n; ++j) {
-                if (!wait(&s_full[t], j)) {
+            for (int u = 0; u < 2 * n; ++u) {
+                const int j = u >> 1, side = u & 1;
+                // (unit u - 2 is long done; waited for so that no phase is skipped)
+                if ((u > 1 && !wait(&o_full[t][side], j - 1)) || !wait(&s_full[t][side], j)) {
                     ok = false;
                     break;
                 }
                 tc::tc_fence_after();
                 const StepInfo &f = info[j % kInfo];
-                const int tok0 = first + kN * j;
+                const int tok0 = first + kU * u;
+                uint32_t x[kU];
+#pragma unroll
+                for (int q = 0; q < kU / 32; ++q) tmem_ld32(sp + kU * side + 32 * q, x + 32 * q);
+                if (side == 0 && j > 0) nan_blocks |= nan_seen(j - 1);
                 const bool gone = f.any[0] != 0u;
-                // few steps: columns that the row does not see become -inf in TMEM
-                if (tok0 + kN > hi_min || tok0 < lo_max || gone) {
-#pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t x[32], see = seen(tok0, q);
-                        tmem_ld32(sp + 32 * q, x);
+                tc::tmem_ld_wait();
+                if (tok0 + kU > hi_min || tok0 < lo_max || gone) {  // few units
+#pragma unroll
+                    for (int q = 0; q < kU / 32; ++q) {
+                        uint32_t see = seen(tok0, q);
                         if (gone)
                             for (int w = 0; w < kConv; ++w)
-                                if (f.any_gone[w]) see &= ~f.gone[w][q];
-                        tc::tmem_ld_wait();
+                                if (f.any_gone[w]) see &= ~f.gone[w][kU / 32 * side + q];
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (!((see >> i) & 1u)) x[i] = 0xFF800000u;
-                        tmem_st32(sp + 32 * q, x);
+                            if (!((see >> i) & 1u)) x[32 * q + i] = 0xFF800000u;
                     }
-                    tmem_st_wait();
                 }
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                if (j > 0) nan_blocks |= nan_seen(j - 1);
-                {
-                    uint32_t x[128];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_ld32(sp + 32 * q, x + 32 * q);
-                    tc::tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 128; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(x[i]));
-                }
-                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                for (int i = 0; i < kU; i += 2)
+                    m4[i / 2 & 3] = max3(m4[i / 2 & 3], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+                const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
                 const float top = mx * mr;  // (-inf x 0 is NaN: no key seen)
                 const bool rise = mx > -INFINITY && top > m + (m == -INFINITY ? 0.f : kLag);
                 if (__any_sync(kFull, rise)) {
                     const float mn = rise ? top : m;
                     const float fac = m == -INFINITY ? 0.f : ex2(m - mn);
-                    if (j > 0) {  // O holds step j - 1
-                        if (!wait(&o_full[t], j - 1)) {
+                    if (u > 0) {  // O holds the units before
+                        if (!wait(&o_full[t][side ^ 1], (u - 1) >> 1)) {
                             ok = false;
                             break;
                         }
@@ -554,35 +570,31 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                     }
                 }
                 const float ms = m == -INFINITY ? 0.f : m;
-                // (a small loop body, read again from TMEM: unrolled over the step the
-                // code alone outran the instruction cache)
-                float l0 = 0.f, l1 = 0.f;
-#pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t x[32], p[16];
-                    tmem_ld32(sp + 32 * q, x);
-                    tc::tmem_ld_wait();
+                const uint64_t mr2 = pair(mr, mr), ms2 = pair(-ms, -ms);
+                uint64_t l2 = 0u;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float y0 = ex2(fmaf(__uint_as_float(x[2 * i]), mr, -ms));
-                        const float y1 = ex2(fmaf(__uint_as_float(x[2 * i + 1]), mr, -ms));
-                        l0 += y0;
-                        l1 += y1;
-                        p[i] = pack_f16(y0, y1);
-                    }
-                    tmem_st16(sp + 16 * q, p);
+                for (int i = 0; i < kU / 2; ++i) {
+                    float y0, y1;
+                    unpair(fma2(pair(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), mr2, ms2), y0, y1);
+                    y0 = ex2(y0);
+                    y1 = ex2(y1);
+                    l2 = add2(l2, pair(y0, y1));
+                    x[i] = pack_f16(y0, y1);
                 }
+                float l0, l1;
+                unpair(l2, l0, l1);
+                tmem_st32(sp + kU * side, x);
                 l += l0 + l1;
                 tmem_st_wait();
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    tc::mbar_arrive(&p_full[t]);
-                    if (t == 0 && j == 0) tc::mbar_arrive(&b_start);
+                    tc::mbar_arrive(&p_full[t][side]);
+                    if (t == 0 && u == 0) tc::mbar_arrive(&b_start);
                 }
             }
             // ------------------------------------------------ output
-            if (ok && n > 0) ok = wait(&o_full[t], n - 1);
+            if (ok && n > 0) ok = wait(&o_full[t][0], n - 1) && wait(&o_full[t][1], n - 1);
             if (ok) {
                 tc::tc_fence_after();
                 if (n > 0) nan_blocks |= nan_seen(n - 1);
@@ -590,6 +602,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 const int row = s.q0 + c / G, head = h * G + c % G;
                 float *rec = a.part + (int64_t)blockIdx.x * C::kRec + (int64_t)tid * (D + 2);
                 const float r = l == 0.f ? 0.f : 1.f / l;
+                // rows of the output meet in the tile's queries, which no product reads
+                // any more, so that they leave in whole lines
+                uint8_t *const own = smem + C::kSmemQ + wid * (32 * 2 * D);
 #pragma unroll 1
                 for (int q = 0; q < D / 32; ++q) {
                     uint32_t x[32];
@@ -602,14 +617,13 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                         if ((nan_blocks >> q) & 1u) v = CUDART_NAN_F;
                         x[i] = __float_as_uint(v);
                     }
-                    if (!live_row) continue;
                     if (splits > 1) {
+                        if (!live_row) continue;
 #pragma unroll
                         for (int i = 0; i < 32; i += 2)
                             *(float2 *)(rec + 32 * q + i) =
                                 make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
                     } else {
-                        uint4 *dst = (uint4 *)(a.out + (int64_t)row * a.out_stride + head * D + 32 * q);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             uint32_t w[4];
@@ -621,8 +635,20 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                                                                                l == 0.f ? 0.f : y1 * r);
                                 w[e] = *reinterpret_cast<const uint32_t *>(&v);
                             }
-                            dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                            *(uint4 *)(own + lane * (2 * D) + (((4 * q + i) ^ (lane & 7)) << 4)) =
+                                make_uint4(w[0], w[1], w[2], w[3]);
                         }
+                    }
+                }
+                if (splits == 1) {
+                    __syncwarp();
+#pragma unroll 4
+                    for (int i = 0; i < 32; i += ROWS) {
+                        const int rr = i + lane / LPR, cc = c0 + (tid & ~31) + rr;
+                        if (cc < s.ncol)
+                            *(uint4 *)(a.out + (int64_t)(s.q0 + cc / G) * a.out_stride + (h * G + cc % G) * D +
+                                       8 * chunk) =
+                                *(const uint4 *)(own + rr * (2 * D) + ((chunk ^ (rr & 7)) << 4));
                     }
                 }
                 if (live_row && splits > 1) {
@@ -644,7 +670,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     } else {
         // ------------------------------------------------ MMA issue of a tile (lane 0)
         const int t = wid - kWarpMma;
-        const uint32_t idesc_s = idesc_f16(kM, kN, false), idesc_o = idesc_f16(kM, D, true);
+        const uint32_t idesc_s = idesc_f16(kM, kU, false), idesc_o = idesc_f16(kM, D, true);
         const uint32_t sb = tc::smem_u32(smem), ts = tmem + 128 * t, to = tmem + 256 + 128 * t;
         const uint64_t qd = tc::sdesc_sw128(sb + C::kSmemQ + t * C::kOp);
         bool ok = true;
@@ -652,42 +678,45 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             // tile B starts behind A's first softmax: in step, both tiles would
             // wait for the tensor cores and then for the exponentials together
             if (t == 1 && n > 0) ok = wait(&b_start, 0);
-            for (int j = 0; j <= n && n > 0 && ok; ++j) {
-                if (j > 0) {  // O += P V of step j - 1
-                    const int st = (j - 1) & 1;
-                    ok = wait(&v_full[st], (j - 1) >> 1) && wait(&p_full[t], j - 1);
-                    if (!ok) break;
-                    tc::tc_fence_after();
-                    const uint64_t bd = sdesc_mn(sb + C::kSmemV + st * C::kOp, C::kHalf);
-                    if (lane == 0) {
+            // S of unit u = Q K^T
+            auto issue_s = [&](int u) {
+                const int j = u >> 1, st = j & 1, side = u & 1;
+                if (side == 0 && !wait(&k_full[st], j >> 1)) return false;
+                tc::tc_fence_after();
+                const uint64_t bd = tc::sdesc_sw128(sb + C::kSmemK + st * C::kOp + side * (kU * 128));
+                if (lane == 0) {
 #pragma unroll
-                        for (int i = 0; i < kN / 16; ++i)
-                            mma_f16_ts(to, ts + 8 * i, bd + (uint64_t)(i * 2048 >> 4), idesc_o,
-                                       (j > 1 || i > 0) ? 1u : 0u);
-                        tc::mma_commit(&o_full[t]);
-                        tc::mma_commit(&v_empty[st]);
-                        // orders the step's masks, seen behind v_full, before the rows' reads
-                        tc::mbar_arrive(&o_full[t]);
+                    for (int i = 0; i < D / 16; ++i) {
+                        const uint64_t o = (uint64_t)(((i >> 2) * C::kHalf + (i & 3) * 32) >> 4);
+                        tc::mma_bf16(ts + kU * side, qd + o, bd + o, idesc_s, i > 0);
                     }
-                }
-                if (j < n) {  // S = Q K^T of step j (after PV, which reads P over S)
-                    const int st = j & 1;
-                    ok = wait(&k_full[st], j >> 1);
-                    if (!ok) break;
-                    tc::tc_fence_after();
-                    const uint64_t bd = tc::sdesc_sw128(sb + C::kSmemK + st * C::kOp);
-                    if (lane == 0) {
-#pragma unroll
-                        for (int i = 0; i < D / 16; ++i) {
-                            const uint64_t o = (uint64_t)(((i >> 2) * C::kHalf + (i & 3) * 32) >> 4);
-                            tc::mma_bf16(ts, qd + o, bd + o, idesc_s, i > 0);
-                        }
-                        tc::mma_commit(&s_full[t]);
-                        tc::mma_commit(&k_empty[st]);
-                        tc::mbar_arrive(&s_full[t]);  // (as above, behind k_full)
-                    }
+                    tc::mma_commit(&s_full[t][side]);
+                    if (side == 1) tc::mma_commit(&k_empty[st]);
+                    // orders the step's masks, seen behind k_full, before the rows' reads
+                    tc::mbar_arrive(&s_full[t][side]);
                 }
                 __syncwarp();
+                return true;
+            };
+            for (int u = 0; u < min(2, 2 * n) && ok; ++u) ok = issue_s(u);
+            for (int u = 0; u < 2 * n && ok; ++u) {  // O += P V of unit u, then S of unit u + 2 over its P
+                const int j = u >> 1, st = j & 1, side = u & 1;
+                if (side == 0) ok = wait(&v_full[st], j >> 1);
+                ok = ok && wait(&p_full[t][side], j);
+                if (!ok) break;
+                tc::tc_fence_after();
+                const uint64_t bd = sdesc_mn(sb + C::kSmemV + st * C::kOp, C::kHalf);
+                if (lane == 0) {
+#pragma unroll
+                    for (int i = 0; i < kU / 16; ++i)
+                        mma_f16_ts(to, ts + kU * side + 8 * i, bd + (uint64_t)((kU / 16 * side + i) * 2048 >> 4),
+                                   idesc_o, (u > 0 || i > 0) ? 1u : 0u);
+                    tc::mma_commit(&o_full[t][side]);
+                    if (side == 1) tc::mma_commit(&v_empty[st]);
+                    tc::mbar_arrive(&o_full[t][side]);  // (as above, behind v_full)
+                }
+                __syncwarp();
+                if (u + 2 < 2 * n) ok = issue_s(u + 2);
             }
             if (lane == 0 && !ok) tc::drain_mmas(&drain[t], limit);  // MMAs in flight end before TMEM goes
         }
