@@ -155,9 +155,6 @@ __device__ __forceinline__ uint32_t idesc_f16(int M, int N, bool bt) {
     return (1u << 4) | ((bt ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// Byte maximum of the bytes of v that are not 255.
-__device__ __forceinline__ uint32_t finite_bytes(uint32_t v) { return v & ~__vcmpeq4(v, 0xFFFFFFFFu); }
-
 // Factor pair 2^(e - R + 12) of a scale byte; 0 below fp16's normal range.
 __device__ __forceinline__ uint32_t factor_of(uint32_t e, int R) {
     return (uint32_t)min(max((int)e - R + 15 + kHead, 0), 15 + kHead) * 0x04000400u;
@@ -266,17 +263,28 @@ __device__ __forceinline__ void convert(const MoeAttnArgs &a, bool v, int h, con
     }
 }
 
-// Column tiles of sequence b whose last column sees L keys or more (its last
-// ones), L >= 1.
-__device__ __forceinline__ int tiles_from(const Seq &s, int group, int L) {
-    const int64_t c = (int64_t)(L - 1 - (s.kv - s.nq)) * group;  // the first column that does
-    return c <= 0 ? s.cts : c >= s.ncol ? 0 : s.cts - (int)(c / kCols);
+// Column tiles of a sequence (p0 keys before its first row) whose last column
+// sees L keys or more (its last ones), L >= 1.
+__device__ __forceinline__ int tiles_from(int p0, int ncol, int cts, int group, int L) {
+    const int64_t c = (int64_t)(L - 1 - p0) * group;  // the first column that does
+    return c <= 0 ? cts : c >= ncol ? 0 : cts - (int)c / kCols;
 }
 
+// A column's query row and head within the group, without a division per step.
+struct Column {
+    int row, head;
+    __device__ Column(int c, int group) : row(c / group), head(c - c / group * group) {}
+    __device__ void next(int by, int group) {  // (the divisions leave the loop)
+        row += by / group;
+        head += by % group;
+        if (head >= group) head -= group, ++row;
+    }
+};
+
 // The r-th (sequence, column tile): the longest first, so that the last CTAs to
-// start are short. The order is by the keys that a tile sees, found by
-// bisection; for many sequences (whose CTAs are many) by column tile alone.
-// False if there are fewer. Warp-collective.
+// start are short. The order is by the keys that a tile sees, found by a search
+// (32 numbers of keys at a time, a lane each); for many sequences (whose CTAs
+// are many) by column tile alone. False if there are fewer. Warp-collective.
 __device__ __forceinline__ bool item_of(const MoeAttnArgs &a, int tiles_max, int r, int &b, int &ct) {
     const int lane = threadIdx.x & 31, B = a.b.n_seqs;
     if (B > 32) {
@@ -286,17 +294,23 @@ __device__ __forceinline__ bool item_of(const MoeAttnArgs &a, int tiles_max, int
     }
     Seq s = {};
     if (lane < B) s = seq_of<kCols>(a, lane);
+    const int p0 = s.kv - s.nq;
     // the largest L with more than r tiles of L keys or more (0: any tile)
-    int L = 0;
-    for (int bit = 31 - __clz(max(a.b.max_kv, 1)); bit >= 0; --bit) {
-        const int t = L | (1 << bit);
-        if (t <= a.b.max_kv &&
-            (int)__reduce_add_sync(kFull, lane < B ? (unsigned)tiles_from(s, a.group, t) : 0u) > r)
-            L = t;
+    int L = 0, end = a.b.max_kv + 1;
+    while (end - L > 1) {
+        const int step = (end - L + 31) / 32;
+        const int t = (int)min((int64_t)L + (int64_t)(lane + 1) * step, (int64_t)end);
+        int count = 0;
+#pragma unroll 4
+        for (int i = 0; i < B; ++i)
+            count += tiles_from(__shfl_sync(kFull, p0, i), __shfl_sync(kFull, s.ncol, i),
+                                __shfl_sync(kFull, s.cts, i), a.group, t);
+        L += step * __popc(__ballot_sync(kFull, t < end && count > r));
+        end = min(end, L + step);
     }
     // those of exactly L keys, in order of sequence and tile, behind the longer ones
-    const int more = lane < B ? tiles_from(s, a.group, L + 1) : 0;
-    const int from = lane < B ? (L == 0 ? s.cts : tiles_from(s, a.group, L)) : 0;
+    const int more = lane < B ? tiles_from(p0, s.ncol, s.cts, a.group, L + 1) : 0;
+    const int from = lane < B ? (L == 0 ? s.cts : tiles_from(p0, s.ncol, s.cts, a.group, L)) : 0;
     int skip = r - (int)__reduce_add_sync(kFull, (unsigned)more), at = from - more;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -345,7 +359,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     const int32_t *pages = a.b.page_table + (int64_t)b * a.b.table_stride;
     const int in_page_mask = (1 << a.page_shift) - 1;
 
-    if (tid == 0) {
+    if (tid == 32 * kWarpK) {  // (a warp without queries to fetch first)
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&k_full[i], kConv);
             tc::mbar_init(&k_empty[i], two ? 2 : 1);
@@ -377,16 +391,21 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         return smem + C::kSmemQ + (r >> 7) * C::kOp + ((r & (kM - 1)) >> 3) * 1024 + (r & 7) * 128 +
                (chunk >> 3) * C::kHalf + (((chunk & 7) ^ (r & 7)) << 4);
     };
-#pragma unroll 1
-    for (int r = wid * ROWS + lane / LPR; r < kCols; r += ROWS * kWarpsP) {
-        const int c = min(c0 + r, s.ncol - 1);  // (columns past the last are not used)
-        cp_async16(q_at(r), a.q + (int64_t)(s.q0 + c / G) * a.q_stride + (h * G + c % G) * D + 8 * chunk);
+    Column col(c0 + wid * ROWS + lane / LPR, G);
+#pragma unroll 4
+    for (int r = wid * ROWS + lane / LPR; r < kCols; r += ROWS * kWarpsP, col.next(ROWS * kWarpsP, G)) {
+        if (c0 + r < s.ncol)
+            cp_async16(q_at(r), a.q + (int64_t)(s.q0 + col.row) * a.q_stride + (h * G + col.head) * D + 8 * chunk);
+        else
+            *(uint4 *)q_at(r) = make_uint4(0u, 0u, 0u, 0u);
     }
     __syncthreads();
     // --- the largest exponents that a row can see: 16 tokens (of one page) a thread
     {
         constexpr int WORDS = 4 * NB;  // of 16 tokens
-        uint32_t mk = 0u, mv[2] = {0u, 0u};  // V: byte 2 k + (token & 1) of block k (of 0, 1 and 2, 3)
+        // maxima of e + 1 (0: NaN, or not seen) in 16 bits; V: [0] of the even
+        // tokens (blocks 0, 1 and 2, 3), [1] of the odd ones
+        uint32_t mk = 0u, mv[2][2] = {};
         for (int tok = first + 16 * tid; tok < min(hi_all, first + kN * n); tok += 16 * kThreadsP) {
             const int id = pages[tok >> a.page_shift];
             if (id < 0 || id >= a.n_pages) {
@@ -400,35 +419,36 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 *(uint4 *)(ks + i) = *(const uint4 *)(a.c.k_s + row * NB + 4 * i);
                 *(uint4 *)(vs + i) = *(const uint4 *)(a.c.v_s + row * NB + 4 * i);
             }
-            auto see = [&](int i) { return tok + i >= lo_all && tok + i < hi_all; };
+            // bit i: token i is seen
+            const int above = min(hi_all - tok, 16), below = max(lo_all - tok, 0);
+            const uint32_t see = below >= 16 ? 0u : ((1u << above) - 1u) & ~((1u << below) - 1u);
+            auto next16 = [](uint32_t w) { return (w & 0x00FF00FFu) + 0x00010001u & 0x00FF00FFu; };
 #pragma unroll
             for (int i = 0; i < WORDS; ++i) {
-                uint32_t kk, kv;  // bytes of tokens that are seen
-                if constexpr (NB == 4) {
-                    kk = see(i) ? kFull : 0u;
-                    kv = (see(i & ~1) ? 0x00FF00FFu : 0u) | (see(i | 1) ? 0xFF00FF00u : 0u);
-                } else {
-                    kk = (see(2 * i) ? 0xFFFFu : 0u) | (see(2 * i + 1) ? 0xFFFF0000u : 0u);
-                    kv = (see(2 * i) ? 0x00FF00FFu : 0u) | (see(2 * i + 1) ? 0xFF00FF00u : 0u);
-                }
-                mk = __vmaxu4(mk, finite_bytes(ks[i]) & kk);
-                uint32_t &m = mv[NB == 4 ? i & 1 : 0];
-                m = __vmaxu4(m, finite_bytes(vs[i]) & kv);
+                const int t0 = NB == 4 ? i & ~1 : 2 * i;  // the word's tokens: K t0 (and, NB 2, t0 + 1)
+                const uint32_t s0 = (see >> t0) & 1u ? kFull : 0u, s1 = (see >> (t0 + 1)) & 1u ? kFull : 0u;
+                const uint32_t k0 = next16(ks[i]), k1 = next16(ks[i] >> 8);
+                if constexpr (NB == 4)
+                    mk = __vmaxu2(mk, __vmaxu2(k0, k1) & (i & 1 ? s1 : s0));
+                else
+                    mk = __vmaxu2(mk, __vmaxu2(k0, k1) & ((s0 & 0xFFFFu) | (s1 & 0xFFFF0000u)));
+                uint32_t(&m)[2] = mv[NB == 4 ? i & 1 : 0];
+                m[0] = __vmaxu2(m[0], next16(vs[i]) & s0);
+                m[1] = __vmaxu2(m[1], next16(vs[i] >> 8) & s1);
             }
         }
-        mk = __vmaxu4(mk, mk >> 16);
-        mk = __reduce_max_sync(kFull, max(mk & 0xFFu, (mk >> 8) & 0xFFu));
-        if (lane == 0) atomicMax(&s_rk, (int)mk);
+        mk = __reduce_max_sync(kFull, max(mk & 0xFFFFu, mk >> 16));
+        if (lane == 0 && mk > 0u) atomicMax(&s_rk, (int)mk - 1);
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
-            const uint32_t m = mv[k >> 1] >> (16 * (k & 1));
-            const uint32_t v = __reduce_max_sync(kFull, max(m & 0xFFu, (m >> 8) & 0xFFu));
-            if (lane == 0) atomicMax(&s_rv[k], (int)v);
+            const uint32_t m = __vmaxu2(mv[k >> 1][0], mv[k >> 1][1]);
+            const uint32_t v = __reduce_max_sync(kFull, k & 1 ? m >> 16 : m & 0xFFFFu);
+            if (lane == 0 && v > 0u) atomicMax(&s_rv[k], (int)v - 1);
         }
     }
     // --- queries: fp16 with one power of two per row
     cp_async_wait();
-#pragma unroll 1
+#pragma unroll 4
     for (int r = wid * ROWS + lane / LPR; r < kCols; r += ROWS * kWarpsP) {
         const uint4 raw = *(const uint4 *)q_at(r);
         const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -601,7 +621,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 const bool live_row = c < s.ncol;
                 const int row = s.q0 + c / G, head = h * G + c % G;
                 float *rec = a.part + (int64_t)blockIdx.x * C::kRec + (int64_t)tid * (D + 2);
-                const float r = l == 0.f ? 0.f : 1.f / l;
+                const float r = l == 0.f ? 0.f : 1.f / l;  // (a row without keys: O is 0 too)
                 // rows of the output meet in the tile's queries, which no product reads
                 // any more, so that they leave in whole lines
                 uint8_t *const own = smem + C::kSmemQ + wid * (32 * 2 * D);
@@ -612,10 +632,10 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                     tc::tmem_ld_wait();
                     const float back = exp2f((float)(s_rv[q] - 127 - kHead));
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        float v = n > 0 ? __uint_as_float(x[i]) * back : 0.f;
-                        if ((nan_blocks >> q) & 1u) v = CUDART_NAN_F;
-                        x[i] = __float_as_uint(v);
+                    for (int i = 0; i < 32; ++i) x[i] = n > 0 ? __float_as_uint(__uint_as_float(x[i]) * back) : 0u;
+                    if ((nan_blocks >> q) & 1u) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = 0x7FFFFFFFu;
                     }
                     if (splits > 1) {
                         if (!live_row) continue;
@@ -631,8 +651,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                             for (int e = 0; e < 4; ++e) {
                                 const float y0 = __uint_as_float(x[8 * i + 2 * e]);
                                 const float y1 = __uint_as_float(x[8 * i + 2 * e + 1]);
-                                const __nv_bfloat162 v = __floats2bfloat162_rn(l == 0.f ? 0.f : y0 * r,
-                                                                               l == 0.f ? 0.f : y1 * r);
+                                const __nv_bfloat162 v = __floats2bfloat162_rn(y0 * r, y1 * r);
                                 w[e] = *reinterpret_cast<const uint32_t *>(&v);
                             }
                             *(uint4 *)(own + lane * (2 * D) + (((4 * q + i) ^ (lane & 7)) << 4)) =
@@ -642,14 +661,13 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 }
                 if (splits == 1) {
                     __syncwarp();
-#pragma unroll 4
-                    for (int i = 0; i < 32; i += ROWS) {
-                        const int rr = i + lane / LPR, cc = c0 + (tid & ~31) + rr;
-                        if (cc < s.ncol)
-                            *(uint4 *)(a.out + (int64_t)(s.q0 + cc / G) * a.out_stride + (h * G + cc % G) * D +
+                    Column at(c0 + (tid & ~31) + lane / LPR, G);
+#pragma unroll 8
+                    for (int i = lane / LPR; i < 32; i += ROWS, at.next(ROWS, G))
+                        if (c0 + (tid & ~31) + i < s.ncol)
+                            *(uint4 *)(a.out + (int64_t)(s.q0 + at.row) * a.out_stride + (h * G + at.head) * D +
                                        8 * chunk) =
-                                *(const uint4 *)(own + rr * (2 * D) + ((chunk ^ (rr & 7)) << 4));
-                    }
+                                *(const uint4 *)(own + i * (2 * D) + ((chunk ^ (i & 7)) << 4));
                 }
                 if (live_row && splits > 1) {
                     rec[D] = m;
