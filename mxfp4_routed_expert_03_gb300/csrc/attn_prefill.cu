@@ -129,6 +129,14 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
+// One lane of the warp, the same one every time; the compiler then knows that the
+// branch has one thread and keeps an MMA's operands in uniform registers (297 us
+// for the prompts below with lane 0 instead, 290 with this).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0u;
+}
 // D[tmem] (+)= A[tmem] x B[smem], fp16 operands, 16 K per instruction.
 __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                            uint32_t accumulate) {
@@ -265,8 +273,8 @@ __device__ __forceinline__ void convert(const MoeAttnArgs &a, bool v, int h, con
 
 // Column tiles of a sequence (p0 keys before its first row) whose last column
 // sees L keys or more (its last ones), L >= 1.
-__device__ __forceinline__ int tiles_from(int p0, int ncol, int cts, int group, int L) {
-    const int64_t c = (int64_t)(L - 1 - p0) * group;  // the first column that does
+__device__ __forceinline__ int tiles_from(int p0, int ncol, int cts, int group, int64_t L) {
+    const int64_t c = (L - 1 - p0) * group;  // the first column that does
     return c <= 0 ? cts : c >= ncol ? 0 : cts - (int)c / kCols;
 }
 
@@ -282,8 +290,8 @@ struct Column {
 };
 
 // The r-th (sequence, column tile): the longest first, so that the last CTAs to
-// start are short. The order is by the keys that a tile sees, found by a search
-// (32 numbers of keys at a time, a lane each); for many sequences (whose CTAs
+// start are short. The order is by the whole steps of keys that a tile sees,
+// found by a search (32 lengths at a time, a lane each); for many sequences (whose CTAs
 // are many) by column tile alone. False if there are fewer. Warp-collective.
 __device__ __forceinline__ bool item_of(const MoeAttnArgs &a, int tiles_max, int r, int &b, int &ct) {
     const int lane = threadIdx.x & 31, B = a.b.n_seqs;
@@ -295,22 +303,22 @@ __device__ __forceinline__ bool item_of(const MoeAttnArgs &a, int tiles_max, int
     Seq s = {};
     if (lane < B) s = seq_of<kCols>(a, lane);
     const int p0 = s.kv - s.nq;
-    // the largest L with more than r tiles of L keys or more (0: any tile)
-    int L = 0, end = a.b.max_kv + 1;
+    // the largest L with more than r tiles of L steps or more (0: any tile)
+    int L = 0, end = a.b.max_kv / kN + 1;
     while (end - L > 1) {
         const int step = (end - L + 31) / 32;
-        const int t = (int)min((int64_t)L + (int64_t)(lane + 1) * step, (int64_t)end);
+        const int t = min(L + (lane + 1) * step, end);
         int count = 0;
 #pragma unroll 4
         for (int i = 0; i < B; ++i)
             count += tiles_from(__shfl_sync(kFull, p0, i), __shfl_sync(kFull, s.ncol, i),
-                                __shfl_sync(kFull, s.cts, i), a.group, t);
+                                __shfl_sync(kFull, s.cts, i), a.group, (int64_t)kN * t);
         L += step * __popc(__ballot_sync(kFull, t < end && count > r));
         end = min(end, L + step);
     }
-    // those of exactly L keys, in order of sequence and tile, behind the longer ones
-    const int more = lane < B ? tiles_from(p0, s.ncol, s.cts, a.group, L + 1) : 0;
-    const int from = lane < B ? (L == 0 ? s.cts : tiles_from(p0, s.ncol, s.cts, a.group, L)) : 0;
+    // those of L steps, in order of sequence and tile, behind the longer ones
+    const int more = lane < B ? tiles_from(p0, s.ncol, s.cts, a.group, (int64_t)kN * (L + 1)) : 0;
+    const int from = lane < B ? (L == 0 ? s.cts : tiles_from(p0, s.ncol, s.cts, a.group, (int64_t)kN * L)) : 0;
     int skip = r - (int)__reduce_add_sync(kFull, (unsigned)more), at = from - more;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -333,7 +341,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     __shared__ __align__(8) uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2][2],
-        p_full[2][2], o_full[2][2], drain[2], b_start;
+        p_full[2][2], o_part[2], o_full[2], drain[2], b_start;
     __shared__ StepInfo info[kInfo];
     __shared__ int s_rk, s_rv[NB], s_abort;
     __shared__ uint32_t s_tmem;
@@ -354,7 +362,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     const int lo_all = W > 0 ? max(0, p0 + i0 + 1 - W) : 0;
     const int begin = lo_all / 16 * 16;
     const int steps = hi_all > begin ? (hi_all - begin + kN - 1) / kN : 0;
-    const int j0 = (int)((int64_t)steps * split / splits), j1 = (int)((int64_t)steps * (split + 1) / splits);
+    // (under 2^24 steps; splits that are at most the SMs)
+    const int j0 = (int)((uint32_t)steps * split / splits), j1 = (int)((uint32_t)steps * (split + 1) / splits);
     const int n = j1 - j0, first = begin + kN * j0;
     const int32_t *pages = a.b.page_table + (int64_t)b * a.b.table_stride;
     const int in_page_mask = (1 << a.page_shift) - 1;
@@ -366,11 +375,11 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             tc::mbar_init(&v_full[i], kConv);
             tc::mbar_init(&v_empty[i], two ? 2 : 1);
             tc::mbar_init(&drain[i], 1);
-            for (int k = 0; k < 2; ++k) {
-                tc::mbar_init(&s_full[i][k], 2);
-                tc::mbar_init(&p_full[i][k], 4);
-                tc::mbar_init(&o_full[i][k], 2);
-            }
+            tc::mbar_init(&s_full[i][0], 2);
+            tc::mbar_init(&s_full[i][1], 1);
+            tc::mbar_init(&o_part[i], 1);
+            tc::mbar_init(&o_full[i], 2);
+            for (int k = 0; k < 2; ++k) tc::mbar_init(&p_full[i][k], 4);
         }
         for (int i = 0; i < kInfo; ++i) info[i].any[0] = info[i].any[1] = 0u;
         tc::mbar_init(&b_start, 4);
@@ -530,8 +539,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             bool ok = true;
             for (int u = 0; u < 2 * n; ++u) {
                 const int j = u >> 1, side = u & 1;
-                // (unit u - 2 is long done; waited for so that no phase is skipped)
-                if ((u > 1 && !wait(&o_full[t][side], j - 1)) || !wait(&s_full[t][side], j)) {
+                if (!wait(&s_full[t][side], j)) {
                     ok = false;
                     break;
                 }
@@ -566,8 +574,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 if (__any_sync(kFull, rise)) {
                     const float mn = rise ? top : m;
                     const float fac = m == -INFINITY ? 0.f : ex2(m - mn);
-                    if (u > 0) {  // O holds the units before
-                        if (!wait(&o_full[t][side ^ 1], (u - 1) >> 1)) {
+                    if (u > 0) {  // O holds the units before, once S of unit u + 1, issued behind them, is there
+                        if (!(u + 1 < 2 * n ? wait(&s_full[t][side ^ 1], (u + 1) >> 1) : wait(&o_part[t], 0))) {
                             ok = false;
                             break;
                         }
@@ -614,7 +622,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 }
             }
             // ------------------------------------------------ output
-            if (ok && n > 0) ok = wait(&o_full[t][0], n - 1) && wait(&o_full[t][1], n - 1);
+            if (ok && n > 0) ok = wait(&o_full[t], 0);
             if (ok) {
                 tc::tc_fence_after();
                 if (n > 0) nan_blocks |= nan_seen(n - 1);
@@ -686,10 +694,10 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                    v ? s_rv[(lane >> 3) % NB] : s_rk, smem + (v ? C::kSmemV : C::kSmemK), v ? v_full : k_full,
                    v ? v_empty : k_empty, info, wait);
     } else {
-        // ------------------------------------------------ MMA issue of a tile (lane 0)
-        const int t = wid - kWarpMma;
+        // ------------------------------------------------ MMA issue of a tile (one lane)
+        const int t = __shfl_sync(kFull, wid, 0) - kWarpMma;  // (uniform, to the compiler too)
         const uint32_t idesc_s = idesc_f16(kM, kU, false), idesc_o = idesc_f16(kM, D, true);
-        const uint32_t sb = tc::smem_u32(smem), ts = tmem + 128 * t, to = tmem + 256 + 128 * t;
+        const uint32_t sb = tc::smem_u32(smem), tm = __shfl_sync(kFull, tmem, 0), ts = tm + 128 * t, to = tm + 256 + 128 * t;
         const uint64_t qd = tc::sdesc_sw128(sb + C::kSmemQ + t * C::kOp);
         bool ok = true;
         if (t == 0 || two) {
@@ -702,7 +710,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 if (side == 0 && !wait(&k_full[st], j >> 1)) return false;
                 tc::tc_fence_after();
                 const uint64_t bd = tc::sdesc_sw128(sb + C::kSmemK + st * C::kOp + side * (kU * 128));
-                if (lane == 0) {
+                if (elect_one()) {
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {
                         const uint64_t o = (uint64_t)(((i >> 2) * C::kHalf + (i & 3) * 32) >> 4);
@@ -710,8 +718,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                     }
                     tc::mma_commit(&s_full[t][side]);
                     if (side == 1) tc::mma_commit(&k_empty[st]);
-                    // orders the step's masks, seen behind k_full, before the rows' reads
-                    tc::mbar_arrive(&s_full[t][side]);
+                    // orders the masks that were seen behind k_full (of this step) and v_full
+                    // (of the one before) before the rows' reads
+                    if (side == 0) tc::mbar_arrive(&s_full[t][0]);
                 }
                 __syncwarp();
                 return true;
@@ -724,19 +733,22 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 if (!ok) break;
                 tc::tc_fence_after();
                 const uint64_t bd = sdesc_mn(sb + C::kSmemV + st * C::kOp, C::kHalf);
-                if (lane == 0) {
+                if (elect_one()) {
 #pragma unroll
                     for (int i = 0; i < kU / 16; ++i)
                         mma_f16_ts(to, ts + kU * side + 8 * i, bd + (uint64_t)((kU / 16 * side + i) * 2048 >> 4),
                                    idesc_o, (u > 0 || i > 0) ? 1u : 0u);
-                    tc::mma_commit(&o_full[t][side]);
                     if (side == 1) tc::mma_commit(&v_empty[st]);
-                    tc::mbar_arrive(&o_full[t][side]);  // (as above, behind v_full)
+                    if (u == 2 * n - 2) tc::mma_commit(&o_part[t]);
+                    if (u == 2 * n - 1) {
+                        tc::mma_commit(&o_full[t]);
+                        tc::mbar_arrive(&o_full[t]);  // (as above)
+                    }
                 }
                 __syncwarp();
                 if (u + 2 < 2 * n) ok = issue_s(u + 2);
             }
-            if (lane == 0 && !ok) tc::drain_mmas(&drain[t], limit);  // MMAs in flight end before TMEM goes
+            if (!ok && elect_one()) tc::drain_mmas(&drain[t], limit);  // MMAs in flight end before TMEM goes
         }
         __syncwarp();
     }
