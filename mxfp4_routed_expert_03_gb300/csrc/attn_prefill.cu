@@ -19,13 +19,16 @@
 // with R the largest key exponent (or, per block of 32 dimensions, the largest
 // value exponent) that the CTA's rows can see, found in a pass over the scales
 // before the loop; a block whose scale lies over 2^26 below the largest counts
-// as 0. Queries as in the split kernel. The running maximum only
-// moves when it would rise by more than 2^8 (P stays far inside fp16's range),
-// so O is rescaled a few times per row and not once per unit.
+// as 0. Queries as in the split kernel. The maximum in use moves only when a
+// unit's weights add up to more than 2^10 with it (they stay far inside fp16's
+// range), so a unit is read once and no maximum of it is taken but for those
+// few, which also rescale O (267 us for the same prompts with a maximum first,
+// 254 without).
 //
 // Bound: 4 D flops per column and key on the tensor cores; one exponential per
 // column and key (32 a cycle and SM) is next.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn.cuh"
 
@@ -45,7 +48,7 @@ constexpr int kWarpK = 8, kWarpV = 11, kWarpMma = 14, kConv = 3;
 constexpr int kThreadsP = 32 * kWarpsP;
 constexpr int kInfo = 4;         // steps whose masks are kept
 constexpr int kHead = 12;        // operands carry 2^12
-constexpr float kLag = 8.f;      // log2 that a row's maximum may lie above the one in use
+constexpr float kLag = 1024.f;   // what a unit's weights may add up to (64 at most of the row's maximum)
 
 template <int D>
 struct PCfg {
@@ -82,6 +85,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
           "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
           "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
@@ -550,69 +561,89 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 #pragma unroll
                 for (int q = 0; q < kU / 32; ++q) tmem_ld32(sp + kU * side + 32 * q, x + 32 * q);
                 if (side == 0 && j > 0) nan_blocks |= nan_seen(j - 1);
-                const bool gone = f.any[0] != 0u;
-                tc::tmem_ld_wait();
-                if (tok0 + kU > hi_min || tok0 < lo_max || gone) {  // few units
+                const bool gone = f.any[0] != 0u, some = tok0 + kU > hi_min || tok0 < lo_max || gone;
+                // columns 32 q .. that the row does not see to -inf (few units have any)
+                auto mask = [&](int q, uint32_t *y) {
+                    uint32_t see = seen(tok0, q);
+                    if (gone)
+                        for (int w = 0; w < kConv; ++w)
+                            if (f.any_gone[w]) see &= ~f.gone[w][kU / 32 * side + q];
 #pragma unroll
-                    for (int q = 0; q < kU / 32; ++q) {
-                        uint32_t see = seen(tok0, q);
-                        if (gone)
-                            for (int w = 0; w < kConv; ++w)
-                                if (f.any_gone[w]) see &= ~f.gone[w][kU / 32 * side + q];
+                    for (int i = 0; i < 32; ++i)
+                        if (!((see >> i) & 1u)) y[i] = 0xFF800000u;
+                };
+                // weights of `count` logits, in place in half as many registers; their sum
+                auto weights = [&](uint32_t *y, float ms, auto count) {
+                    const uint64_t mr2 = pair(mr, mr), ms2 = pair(-ms, -ms);
+                    uint64_t l2 = 0u;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (!((see >> i) & 1u)) x[32 * q + i] = 0xFF800000u;
+                    for (int i = 0; i < decltype(count)::value / 2; ++i) {
+                        float y0, y1;
+                        unpair(fma2(pair(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), mr2, ms2), y0, y1);
+                        y0 = ex2(y0);
+                        y1 = ex2(y1);
+                        l2 = add2(l2, pair(y0, y1));
+                        y[i] = pack_f16(y0, y1);
                     }
-                }
-                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    float l0, l1;
+                    unpair(l2, l0, l1);
+                    return l0 + l1;
+                };
+                tc::tmem_ld_wait();
+                if (some)
 #pragma unroll
-                for (int i = 0; i < kU; i += 2)
-                    m4[i / 2 & 3] = max3(m4[i / 2 & 3], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-                const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
-                const float top = mx * mr;  // (-inf x 0 is NaN: no key seen)
-                const bool rise = mx > -INFINITY && top > m + (m == -INFINITY ? 0.f : kLag);
-                if (__any_sync(kFull, rise)) {
-                    const float mn = rise ? top : m;
-                    const float fac = m == -INFINITY ? 0.f : ex2(m - mn);
+                    for (int q = 0; q < kU / 32; ++q) mask(q, x + 32 * q);
+                float sum = weights(x, m == -INFINITY ? 0.f : m, std::integral_constant<int, kU>());
+                if (!__any_sync(kFull, m == -INFINITY || !(sum <= kLag))) {
+                    tmem_st32(sp + kU * side, x);
+                } else {
+                    // a row without a maximum yet, or one whose weights add up to too much:
+                    // the unit goes again, with the rows' largest logits as the maximum
+                    float mx = -INFINITY;
+#pragma unroll 1
+                    for (int q = 0; q < kU / 32; ++q) {
+                        uint32_t y[32];
+                        tmem_ld32(sp + kU * side + 32 * q, y);
+                        tc::tmem_ld_wait();
+                        if (some) mask(q, y);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) mx = max3(mx, __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
+                    }
+                    const float top = mx * mr;  // (-inf x 0 is NaN: no key seen)
+                    const bool rise = mx > -INFINITY && top > m;
+                    const float fac = rise && m > -INFINITY ? ex2(m - top) : 1.f;
                     if (u > 0) {  // O holds the units before, once S of unit u + 1, issued behind them, is there
                         if (!(u + 1 < 2 * n ? wait(&s_full[t][side ^ 1], (u + 1) >> 1) : wait(&o_part[t], 0))) {
                             ok = false;
                             break;
                         }
                         tc::tc_fence_after();
-                        const float fo = rise ? fac : 1.f;
 #pragma unroll 1
                         for (int q = 0; q < D / 32; ++q) {
                             uint32_t y[32];
                             tmem_ld32(op + 32 * q, y);
                             tc::tmem_ld_wait();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * fo);
+                            for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * fac);
                             tmem_st32(op + 32 * q, y);
                         }
-                        tmem_st_wait();
                     }
                     if (rise) {
                         l *= fac;
-                        m = mn;
+                        m = top;
+                    }
+                    sum = 0.f;
+#pragma unroll 1
+                    for (int q = 0; q < kU / 32; ++q) {
+                        uint32_t y[32];
+                        tmem_ld32(sp + kU * side + 32 * q, y);
+                        tc::tmem_ld_wait();
+                        if (some) mask(q, y);
+                        sum += weights(y, m == -INFINITY ? 0.f : m, std::integral_constant<int, 32>());
+                        tmem_st16(sp + kU * side + 16 * q, y);
                     }
                 }
-                const float ms = m == -INFINITY ? 0.f : m;
-                const uint64_t mr2 = pair(mr, mr), ms2 = pair(-ms, -ms);
-                uint64_t l2 = 0u;
-#pragma unroll
-                for (int i = 0; i < kU / 2; ++i) {
-                    float y0, y1;
-                    unpair(fma2(pair(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), mr2, ms2), y0, y1);
-                    y0 = ex2(y0);
-                    y1 = ex2(y1);
-                    l2 = add2(l2, pair(y0, y1));
-                    x[i] = pack_f16(y0, y1);
-                }
-                float l0, l1;
-                unpair(l2, l0, l1);
-                tmem_st32(sp + kU * side, x);
-                l += l0 + l1;
+                l += sum;
                 tmem_st_wait();
                 tc::tc_fence_before();
                 __syncwarp();
