@@ -289,14 +289,22 @@ __device__ __forceinline__ int tiles_from(int p0, int ncol, int cts, int group, 
     return c <= 0 ? cts : c >= ncol ? 0 : cts - (int)c / kCols;
 }
 
-// A column's query row and head within the group, without a division per step.
+// Offset of a column's head row in the queries or the output, without a division
+// per step of `by` columns.
 struct Column {
-    int row, head;
-    __device__ Column(int c, int group) : row(c / group), head(c - c / group * group) {}
-    __device__ void next(int by, int group) {  // (the divisions leave the loop)
-        row += by / group;
-        head += by % group;
-        if (head >= group) head -= group, ++row;
+    int64_t at, step, wrap;
+    int head, group, rem;
+    __device__ Column(int c, int by, int group_, int64_t stride, int width) : group(group_) {
+        head = c % group;
+        rem = by % group;
+        at = c / group * stride + head * width;
+        step = by / group * stride + rem * width;
+        wrap = stride - group * width;
+    }
+    __device__ void next() {
+        at += step;
+        head += rem;
+        if (head >= group) head -= group, at += wrap;
     }
 };
 
@@ -352,11 +360,10 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     __shared__ __align__(8) uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2][2],
-        p_full[2][2], o_part[2], o_full[2], drain[2], b_start;
+        p_full[2][2], o_part[2], o_full[2], q_full[2], drain[2], b_start;
     __shared__ StepInfo info[kInfo];
     __shared__ int s_rk, s_rv[NB], s_abort;
     __shared__ uint32_t s_tmem;
-    __shared__ float s_mul[kCols];
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
 
     grid_dep_wait();
@@ -388,6 +395,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             tc::mbar_init(&drain[i], 1);
             tc::mbar_init(&s_full[i][0], 2);
             tc::mbar_init(&s_full[i][1], 1);
+            tc::mbar_init(&q_full[i], 4);
             tc::mbar_init(&o_part[i], 1);
             tc::mbar_init(&o_full[i], 2);
             for (int k = 0; k < 2; ++k) tc::mbar_init(&p_full[i][k], 4);
@@ -403,21 +411,27 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         tc::tmem_alloc(&s_tmem, 512);
         tc::tmem_relinquish();
     }
-    // --- queries: a row's chunks of 8 elements side by side in a warp, into the
-    // operand's place while the scales are read
-    constexpr int LPR = D / 8, ROWS = 32 / LPR;
+    // --- queries: each row warp's 32 rows in whole lines into the operand's place,
+    // while the scales are read
+    constexpr int LPR = D / 8, ROWS = 32 / LPR;  // lanes of a row of 16-byte chunks, rows of a warp's pass
     const int chunk = lane % LPR;
-    auto q_at = [&](int r) {
+    auto q_at = [&](int r, int ch) {
         return smem + C::kSmemQ + (r >> 7) * C::kOp + ((r & (kM - 1)) >> 3) * 1024 + (r & 7) * 128 +
-               (chunk >> 3) * C::kHalf + (((chunk & 7) ^ (r & 7)) << 4);
+               (ch >> 3) * C::kHalf + (((ch & 7) ^ (r & 7)) << 4);
     };
-    Column col(c0 + wid * ROWS + lane / LPR, G);
+    const int scale_end = min(hi_all, first + kN * n);
+    const int scale_page = first + 16 * tid < scale_end ? pages[(first + 16 * tid) >> a.page_shift] : -1;
+    if (wid < 8) {
+        const int r0 = tid & ~31;
+        Column col(c0 + r0 + lane / LPR, ROWS, G, a.q_stride, D);
+        const uint16_t *src = a.q + s.q0 * a.q_stride + h * G * D + 8 * chunk;
 #pragma unroll 4
-    for (int r = wid * ROWS + lane / LPR; r < kCols; r += ROWS * kWarpsP, col.next(ROWS * kWarpsP, G)) {
-        if (c0 + r < s.ncol)
-            cp_async16(q_at(r), a.q + (int64_t)(s.q0 + col.row) * a.q_stride + (h * G + col.head) * D + 8 * chunk);
-        else
-            *(uint4 *)q_at(r) = make_uint4(0u, 0u, 0u, 0u);
+        for (int r = r0 + lane / LPR; r < r0 + 32; r += ROWS, col.next()) {
+            if (c0 + r < s.ncol)
+                cp_async16(q_at(r, chunk), src + col.at);
+            else
+                *(uint4 *)q_at(r, chunk) = make_uint4(0u, 0u, 0u, 0u);
+        }
     }
     __syncthreads();
     // --- the largest exponents that a row can see: 16 tokens (of one page) a thread
@@ -426,8 +440,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         // maxima of e + 1 (0: NaN, or not seen) in 16 bits; V: [0] of the even
         // tokens (blocks 0, 1 and 2, 3), [1] of the odd ones
         uint32_t mk = 0u, mv[2][2] = {};
-        for (int tok = first + 16 * tid; tok < min(hi_all, first + kN * n); tok += 16 * kThreadsP) {
-            const int id = pages[tok >> a.page_shift];
+        int id = scale_page;
+        for (int tok = first + 16 * tid; tok < scale_end; tok += 16 * kThreadsP) {
+            if (tok >= first + 16 * kThreadsP) id = pages[tok >> a.page_shift];
             if (id < 0 || id >= a.n_pages) {
                 moe_flag(a.status, MOE_ERR_BAD_INDEX);
                 continue;
@@ -466,34 +481,6 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             if (lane == 0 && v > 0u) atomicMax(&s_rv[k], (int)v - 1);
         }
     }
-    // --- queries: fp16 with one power of two per row
-    cp_async_wait();
-#pragma unroll 4
-    for (int r = wid * ROWS + lane / LPR; r < kCols; r += ROWS * kWarpsP) {
-        const uint4 raw = *(const uint4 *)q_at(r);
-        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-        uint32_t top = 0u, f[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) top = __vmaxu2(top, w[j] & 0x7FFF7FFFu);
-#pragma unroll
-        for (int o = LPR / 2; o; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(kFull, top, o));
-        top = max(top & 0xFFFFu, top >> 16);
-        const bool bad = top >= 0x7F80u;  // the row is NaN: zero operand, NaN factor
-        const int sh = min(141 - (int)(top >> 7), 127);
-        // a negative scale's sign goes into the queries, so that the largest
-        // product is the largest logit
-        const float up = bad ? 0.f : copysignf(pow2(sh), a.b.scale);
-        // back from that power, |scale| log2(e)
-        if (chunk == 0) s_mul[r] = bad ? CUDART_NAN_F : pow2(-sh) * (fabsf(a.b.scale) * CUDART_L2E_F);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float x = bad ? 0.f : __uint_as_float(w[j] << 16) * up;
-            const float y = bad ? 0.f : __uint_as_float(w[j] & 0xFFFF0000u) * up;
-            f[j] = pack_f16(x, y);
-        }
-        *(uint4 *)q_at(r) = make_uint4(f[0], f[1], f[2], f[3]);
-    }
-    tc::fence_proxy_async_smem();
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
@@ -515,6 +502,38 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         const int t = wid >> 2;
         const int c = c0 + tid;
         if (t == 0 || two) {
+            // --- queries: fp16 with one power of two per row
+            cp_async_wait();
+            __syncwarp();
+            uint32_t big = 0u;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const uint4 w = *(const uint4 *)q_at(tid, i);
+                big = __vmaxu2(big, __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                                             __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
+            }
+            big = max(big & 0xFFFFu, big >> 16);
+            const bool bad = big >= 0x7F80u;  // the row is NaN: zero operand, NaN factor
+            const int sh = min(141 - (int)(big >> 7), 127);
+            // a negative scale's sign goes into the queries, so that the largest
+            // product is the largest logit
+            const float up = copysignf(pow2(sh), a.b.scale);
+            // back from that power, |scale| log2(e)
+            const float mul = bad ? CUDART_NAN_F : pow2(-sh) * (fabsf(a.b.scale) * CUDART_L2E_F);
+            const uint32_t keep = bad ? 0u : kFull;
+#pragma unroll 4
+            for (int i = 0; i < D / 8; ++i) {
+                uint4 *const at = (uint4 *)q_at(tid, i);
+                uint32_t w[4] = {at->x, at->y, at->z, at->w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    w[k] = pack_f16(__uint_as_float((w[k] & keep) << 16) * up,
+                                    __uint_as_float(w[k] & keep & 0xFFFF0000u) * up);
+                *at = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&q_full[t]);
             const uint32_t lanes = (uint32_t)(32 * (wid & 3)) << 16;
             const uint32_t sp = tmem + lanes + 128 * t, op = tmem + lanes + 256 + 128 * t;
             const int it0 = (c0 + kM * t) / G, it1 = (min(c0 + kM * (t + 1), s.ncol) - 1) / G;
@@ -522,7 +541,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             const int hi = c < s.ncol ? p0 + c / G + 1 : 0x7FFFFFFF;
             const int lo = c < s.ncol && W > 0 ? hi - W : 0;
             // logits: S x mul x 2^(R - 127 - 12); not 0, for masked columns are -inf
-            float mr = s_mul[tid] * exp2f((float)(s_rk - 127 - kHead));
+            float mr = mul * exp2f((float)(s_rk - 127 - kHead));
             if (mr == 0.f) mr = 1.17549435e-38f;
             float m = -INFINITY, l = 0.f;  // m: the maximum in use
             // tokens tok0 + 32 q .. + 31 that the row sees
@@ -668,8 +687,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 for (int q = 0; q < D / 32; ++q) {
                     uint32_t x[32];
                     if (n > 0) tmem_ld32(op + 32 * q, x);
-                    tc::tmem_ld_wait();
                     const float back = exp2f((float)(s_rv[q] - 127 - kHead));
+                    tc::tmem_ld_wait();
 #pragma unroll
                     for (int i = 0; i < 32; ++i) x[i] = n > 0 ? __float_as_uint(__uint_as_float(x[i]) * back) : 0u;
                     if ((nan_blocks >> q) & 1u) {
@@ -700,13 +719,13 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 }
                 if (splits == 1) {
                     __syncwarp();
-                    Column at(c0 + (tid & ~31) + lane / LPR, G);
+                    const int w0 = c0 + (tid & ~31);  // the warp's first column
+                    Column col(w0 + lane / LPR, ROWS, G, a.out_stride, D);
+                    uint16_t *dst = a.out + s.q0 * a.out_stride + h * G * D + 8 * chunk;
 #pragma unroll 8
-                    for (int i = lane / LPR; i < 32; i += ROWS, at.next(ROWS, G))
-                        if (c0 + (tid & ~31) + i < s.ncol)
-                            *(uint4 *)(a.out + (int64_t)(s.q0 + at.row) * a.out_stride + (h * G + at.head) * D +
-                                       8 * chunk) =
-                                *(const uint4 *)(own + i * (2 * D) + ((chunk ^ (i & 7)) << 4));
+                    for (int i = lane / LPR; i < 32; i += ROWS, col.next())
+                        if (w0 + i < s.ncol)
+                            *(uint4 *)(dst + col.at) = *(const uint4 *)(own + i * (2 * D) + ((chunk ^ (i & 7)) << 4));
                 }
                 if (live_row && splits > 1) {
                     rec[D] = m;
@@ -734,7 +753,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         if (t == 0 || two) {
             // tile B starts behind A's first softmax: in step, both tiles would
             // wait for the tensor cores and then for the exponentials together
-            if (t == 1 && n > 0) ok = wait(&b_start, 0);
+            ok = wait(&q_full[t], 0);
+            if (t == 1 && n > 0 && ok) ok = wait(&b_start, 0);
             // S of unit u = Q K^T
             auto issue_s = [&](int u) {
                 const int j = u >> 1, st = j & 1, side = u & 1;
