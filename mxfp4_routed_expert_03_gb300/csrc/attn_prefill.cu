@@ -28,7 +28,6 @@
 // Bound: 4 D flops per column and key on the tensor cores; one exponential per
 // column and key (32 a cycle and SM) is next.
 #include <algorithm>
-#include <type_traits>
 
 #include "attn.cuh"
 
@@ -360,7 +359,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     __shared__ __align__(8) uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2][2],
-        p_full[2][2], o_part[2], o_full[2], q_full[2], drain[2], b_start;
+        p_full[2][2], o_part[2], o_full[2], q_full[2], drain[2];
     __shared__ StepInfo info[kInfo];
     __shared__ int s_rk, s_rv[NB], s_abort;
     __shared__ uint32_t s_tmem;
@@ -401,7 +400,6 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             for (int k = 0; k < 2; ++k) tc::mbar_init(&p_full[i][k], 4);
         }
         for (int i = 0; i < kInfo; ++i) info[i].any[0] = info[i].any[1] = 0u;
-        tc::mbar_init(&b_start, 4);
         tc::fence_mbar_init();
         s_abort = 0;
         s_rk = 0;
@@ -567,18 +565,25 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             };
             uint32_t nan_blocks = 0u;
             bool ok = true;
+            uint32_t x[kU];
+            bool there = false;  // the first half of the unit's logits is in x
             for (int u = 0; u < 2 * n; ++u) {
                 const int j = u >> 1, side = u & 1;
-                if (!wait(&s_full[t][side], j)) {
-                    ok = false;
-                    break;
+                if (!there) {
+                    if (!wait(&s_full[t][side], j)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::tc_fence_after();
+                    tmem_ld32(sp + kU * side, x);
+                    tmem_ld32(sp + kU * side + 32, x + 32);
+                    tc::tmem_ld_wait();  // (in the block of the loads: nothing may touch their registers before)
+                } else {
+                    tmem_ld32(sp + kU * side + 32, x + 32);
+                    tc::tmem_ld_wait();
                 }
-                tc::tc_fence_after();
                 const StepInfo &f = info[j % kInfo];
                 const int tok0 = first + kU * u;
-                uint32_t x[kU];
-#pragma unroll
-                for (int q = 0; q < kU / 32; ++q) tmem_ld32(sp + kU * side + 32 * q, x + 32 * q);
                 if (side == 0 && j > 0) nan_blocks |= nan_seen(j - 1);
                 const bool gone = f.any[0] != 0u, some = tok0 + kU > hi_min || tok0 < lo_max || gone;
                 // columns 32 q .. that the row does not see to -inf (few units have any)
@@ -591,30 +596,31 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                     for (int i = 0; i < 32; ++i)
                         if (!((see >> i) & 1u)) y[i] = 0xFF800000u;
                 };
-                // weights of `count` logits, in place in half as many registers; their sum
-                auto weights = [&](uint32_t *y, float ms, auto count) {
+                // weights of 32 logits into half as many registers; their sum
+                auto weights = [&](const uint32_t *y, float ms, uint32_t *p) {
                     const uint64_t mr2 = pair(mr, mr), ms2 = pair(-ms, -ms);
                     uint64_t l2 = 0u;
 #pragma unroll
-                    for (int i = 0; i < decltype(count)::value / 2; ++i) {
+                    for (int i = 15; i >= 0; --i) {
                         float y0, y1;
                         unpair(fma2(pair(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), mr2, ms2), y0, y1);
                         y0 = ex2(y0);
                         y1 = ex2(y1);
                         l2 = add2(l2, pair(y0, y1));
-                        y[i] = pack_f16(y0, y1);
+                        p[i] = pack_f16(y0, y1);
                     }
                     float l0, l1;
                     unpair(l2, l0, l1);
                     return l0 + l1;
                 };
-                tc::tmem_ld_wait();
                 if (some)
 #pragma unroll
                     for (int q = 0; q < kU / 32; ++q) mask(q, x + 32 * q);
-                float sum = weights(x, m == -INFINITY ? 0.f : m, std::integral_constant<int, kU>());
+                const float ms = m == -INFINITY ? 0.f : m;
+                uint32_t p[32];
+                float sum = weights(x + 32, ms, p + 16) + weights(x, ms, p);
                 if (!__any_sync(kFull, m == -INFINITY || !(sum <= kLag))) {
-                    tmem_st32(sp + kU * side, x);
+                    tmem_st32(sp + kU * side, p);
                 } else {
                     // a row without a maximum yet, or one whose weights add up to too much:
                     // the unit goes again, with the rows' largest logits as the maximum
@@ -658,17 +664,27 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                         tmem_ld32(sp + kU * side + 32 * q, y);
                         tc::tmem_ld_wait();
                         if (some) mask(q, y);
-                        sum += weights(y, m == -INFINITY ? 0.f : m, std::integral_constant<int, 32>());
-                        tmem_st16(sp + kU * side + 16 * q, y);
+                        sum += weights(y, m == -INFINITY ? 0.f : m, p);
+                        tmem_st16(sp + kU * side + 16 * q, p);
                     }
                 }
                 l += sum;
-                tmem_st_wait();
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    tc::mbar_arrive(&p_full[t][side]);
-                    if (t == 0 && u == 0) tc::mbar_arrive(&b_start);
+                // half of the next unit's logits, if there, over the wait for the weights' store
+                there = u + 1 < 2 * n &&
+                        __all_sync(kFull, tc::mbar_try_wait(&s_full[t][side ^ 1], ((u + 1) >> 1) & 1));
+                auto give = [&] {
+                    tmem_st_wait();
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&p_full[t][side]);
+                };
+                if (there) {
+                    tc::tc_fence_after();
+                    tmem_ld32(sp + kU * (side ^ 1), x);
+                    give();
+                    tc::tmem_ld_wait();
+                } else {
+                    give();
                 }
             }
             // ------------------------------------------------ output
@@ -686,9 +702,11 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 #pragma unroll 1
                 for (int q = 0; q < D / 32; ++q) {
                     uint32_t x[32];
-                    if (n > 0) tmem_ld32(op + 32 * q, x);
                     const float back = exp2f((float)(s_rv[q] - 127 - kHead));
-                    tc::tmem_ld_wait();
+                    if (n > 0) {
+                        tmem_ld32(op + 32 * q, x);
+                        tc::tmem_ld_wait();
+                    }
 #pragma unroll
                     for (int i = 0; i < 32; ++i) x[i] = n > 0 ? __float_as_uint(__uint_as_float(x[i]) * back) : 0u;
                     if ((nan_blocks >> q) & 1u) {
@@ -751,35 +769,36 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         const uint64_t qd = tc::sdesc_sw128(sb + C::kSmemQ + t * C::kOp);
         bool ok = true;
         if (t == 0 || two) {
-            // tile B starts behind A's first softmax: in step, both tiles would
-            // wait for the tensor cores and then for the exponentials together
             ok = wait(&q_full[t], 0);
-            if (t == 1 && n > 0 && ok) ok = wait(&b_start, 0);
-            // S of unit u = Q K^T
+            // S of unit u = Q K^T (by one lane)
             auto issue_s = [&](int u) {
                 const int j = u >> 1, st = j & 1, side = u & 1;
-                if (side == 0 && !wait(&k_full[st], j >> 1)) return false;
-                tc::tc_fence_after();
                 const uint64_t bd = tc::sdesc_sw128(sb + C::kSmemK + st * C::kOp + side * (kU * 128));
-                if (elect_one()) {
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        const uint64_t o = (uint64_t)(((i >> 2) * C::kHalf + (i & 3) * 32) >> 4);
-                        tc::mma_bf16(ts + kU * side, qd + o, bd + o, idesc_s, i > 0);
-                    }
-                    tc::mma_commit(&s_full[t][side]);
-                    if (side == 1) tc::mma_commit(&k_empty[st]);
-                    // orders the masks that were seen behind k_full (of this step) and v_full
-                    // (of the one before) before the rows' reads
-                    if (side == 0) tc::mbar_arrive(&s_full[t][0]);
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint64_t o = (uint64_t)(((i >> 2) * C::kHalf + (i & 3) * 32) >> 4);
+                    tc::mma_bf16(ts + kU * side, qd + o, bd + o, idesc_s, i > 0);
+                }
+                tc::mma_commit(&s_full[t][side]);
+                if (side == 1) tc::mma_commit(&k_empty[st]);
+                // orders the masks that were seen behind k_full (of this step) and v_full
+                // (of the one before) before the rows' reads
+                if (side == 0) tc::mbar_arrive(&s_full[t][0]);
+            };
+            if (n > 0 && ok) ok = wait(&k_full[0], 0);
+            if (n > 0 && ok) {
+                tc::tc_fence_after();
+                if (elect_one()) {
+                    issue_s(0);
+                    issue_s(1);
                 }
                 __syncwarp();
-                return true;
-            };
-            for (int u = 0; u < min(2, 2 * n) && ok; ++u) ok = issue_s(u);
+            }
             for (int u = 0; u < 2 * n && ok; ++u) {  // O += P V of unit u, then S of unit u + 2 over its P
                 const int j = u >> 1, st = j & 1, side = u & 1;
-                if (side == 0) ok = wait(&v_full[st], j >> 1);
+                const bool more = j + 1 < n;
+                // (the weights last: what they wait for is then issued without a pause)
+                if (side == 0) ok = wait(&v_full[st], j >> 1) && (!more || wait(&k_full[st ^ 1], (j + 1) >> 1));
                 ok = ok && wait(&p_full[t][side], j);
                 if (!ok) break;
                 tc::tc_fence_after();
@@ -795,9 +814,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                         tc::mma_commit(&o_full[t]);
                         tc::mbar_arrive(&o_full[t]);  // (as above)
                     }
+                    if (more) issue_s(u + 2);
                 }
                 __syncwarp();
-                if (u + 2 < 2 * n) ok = issue_s(u + 2);
             }
             if (!ok && elect_one()) tc::drain_mmas(&drain[t], limit);  // MMAs in flight end before TMEM goes
         }
