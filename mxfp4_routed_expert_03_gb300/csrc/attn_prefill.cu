@@ -906,7 +906,16 @@ cudaError_t moe_attn_prefill_setup() {
 }
 
 bool moe_attn_prefill_fits(int n_seqs, int n_kv, int group, int max_q, int max_kv, int nsm) {
-    if ((int64_t)group * max_q < MOE_ATTN_PREFILL_COLS) return false;
+    // The split kernel reads the cache once for every 16 columns, this one once for
+    // 256, but its CTAs take a while to start. 16 sequences of 4000 keys, 8
+    // key/value heads: 49 us there and 65 here with 16 columns, 81 and 66 with 24,
+    // 151 and 67 with 64; one such sequence: 18 and 25 with 32 columns, 22 and 27
+    // with 64, 31 and 29 with 128.
+    const int64_t cols = (int64_t)group * max_q;
+    if (cols <= 16) return false;
+    if (cols < MOE_ATTN_PREFILL_COLS &&
+        (double)cols * n_seqs * n_kv * max_kv < MOE_ATTN_PREFILL_LOGITS)
+        return false;
     return shape_of(n_seqs, n_kv, group, max_q, max_kv, nsm).ctas <= (1 << 24);
 }
 

@@ -307,9 +307,11 @@ size_t moe_attn_ws_bytes(int head_dim, int n_seqs, int n_kv, int group, int max_
                          int nsm);
 cudaError_t moe_launch_attn(int head_dim, const MoeAttnArgs &a, int nsm, cudaStream_t st);
 
-// attn_prefill.cu: the same with many query rows per sequence, from this many
-// columns (query rows x heads of a key/value head) of the longest sequence on
+// attn_prefill.cu: the same with many query rows per sequence: from so many
+// columns (query rows x heads of a key/value head) of the longest sequence on,
+// or from 17 with at least so many logits in the batch
 #define MOE_ATTN_PREFILL_COLS 64
+#define MOE_ATTN_PREFILL_LOGITS 4e6
 cudaError_t moe_attn_prefill_setup();
 bool moe_attn_prefill_fits(int n_seqs, int n_kv, int group, int max_q, int max_kv, int nsm);
 size_t moe_attn_prefill_ws_bytes(int head_dim, int n_seqs, int n_kv, int group, int max_q, int max_kv,

@@ -1,0 +1,62 @@
+"""Attention of many query rows at the sizes where its kernel changes: columns
+between the two kernels' ranges, lengths around a unit (64 keys) and a step
+(128 keys), and maxima that rise at chosen keys. References and tolerances are
+test_gpu_attention's."""
+import pytest
+import torch
+
+import attn_ref as ref
+from test_gpu_attention import DEV, Setup, _randn
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("H,KV,d,nq", [(48, 2, 128, 1), (32, 2, 128, 1), (20, 2, 64, 2), (34, 2, 128, 1),
+                                       (9, 1, 64, 7)])
+@pytest.mark.parametrize("window", [0, 300])
+def test_few_columns_in_a_large_batch(H, KV, d, nq, window):
+    """16 to 63 columns, with fewer and with more than 4e6 logits."""
+    kv = [3000, 1, 2999, 64, 0, 777] * 5
+    Setup(H, KV, d, 64, [nq] * len(kv), [max(n, nq) if n else 0 for n in kv], seed=H + d, window=window).check()
+
+
+@pytest.mark.parametrize("kv", [1, 2, 63, 64, 65, 127, 128, 129, 191, 192, 193, 255, 256, 257, 640])
+@pytest.mark.parametrize("d,page", [(128, 16), (64, 128)])
+def test_lengths_around_a_unit_of_keys(kv, d, page):
+    s = Setup(16, 1, d, page, [min(kv, 20), 9], [kv, kv + 9], seed=kv + d)
+    s.check()
+    first = s.out.clone()
+    s.run()
+    assert torch.equal(first, s.out)
+
+
+def _refill(s, b, k):
+    """Sequence b's keys again, as k (its values stay)."""
+    from mxfp4_routed_expert_03_gb300 import check
+    n = s.kv[b]
+    j = torch.arange(n, device=DEV)
+    slots = (s.table[b, j // s.page].long() * s.page + j % s.page).int()
+    v = torch.empty(n, s.KV * s.d, dtype=torch.bfloat16, device=DEV)
+    old = torch.empty_like(v)
+    check(s.attn.read(n, slots, old, v), "read")
+    check(s.attn.append(n, k, v, slots), "append")
+    s.k[b] = ref.mxfp4(k).view(n, s.KV, s.d)
+
+
+@pytest.mark.parametrize("window", [0, 90])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("at", ["rising", "falling", 63, 64, 130, 299])
+def test_maximum_that_moves(at, d, window):
+    """Keys that grow along the sequence, shrink along it, or stand out at one
+    token, in a unit's last and first place and in the last unit."""
+    s = Setup(8, 1, d, 32, [40], [300], seed=50, window=window)
+    k = _randn(300, d, seed=51)
+    if at == "rising":
+        f = torch.linspace(0.01, 12, 300)
+    elif at == "falling":
+        f = torch.linspace(12, 0.01, 300)
+    else:
+        f = torch.full((300,), 0.1)
+        f[at] = 20.0
+    _refill(s, 0, (k.float() * f.to(DEV)[:, None]).bfloat16())
+    s.check()
