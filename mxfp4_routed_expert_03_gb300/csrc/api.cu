@@ -594,7 +594,7 @@ static int plan_impl(moe_handle *h, int32_t T, const float *logits, const uint16
     void *pws = lg_bytes ? (void *)((unsigned char *)ws + lg_bytes) : ws;
     const int E = h->desc.n_experts, k = h->desc.top_k;
     cudaError_t err =
-        route ? moe_launch_plan_scored(T, E, k, logits, *route, bias, plan, pws, h->status, st)
+        route ? moe_launch_plan_scored(T, E, k, logits, *route, bias, plan, pws, h->status, h->num_sms, st)
               : moe_launch_plan(T, E, k, logits, plan, pws, h->status, st);
     return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

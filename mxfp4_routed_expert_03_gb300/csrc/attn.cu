@@ -421,7 +421,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
     walk.part = 0;
     walk.parts = 1;
     walk.per = 1;
-    // parts of an item, if every CTA took one; at the finest
+    // Parts of an item, if every CTA took one; at the finest. Equal parts where there
+    // are four of an item or all it can have: one sequence of 777 keys 9.4 us (on the
+    // line, where a CTA meets two items, 13.4), four of 5000 15.0 (15.7), two of
+    // 100000 67.5 (65.7).
     const int cap = (int)((long long)gridDim.x / all.items), fine = (longest + kMinTiles - 1) / kMinTiles;
     walk.deal = whole ? DEAL_WHOLE : cap >= min(fine, 4) ? DEAL_PARTS : DEAL_LINE;
     if (walk.deal == DEAL_WHOLE) {
@@ -909,7 +912,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) moe_attn_join_kernel(MoeAttnA
 // Two column tiles of 8 where a sequence may have more than 8 columns.
 bool wide(int group, int max_q) { return (int64_t)group * max_q > 8; }
 
-// A CTA takes whole items where each has at most a tile per warp.
+// A CTA takes whole items where each has at most a tile per warp, and nothing is
+// left to join: 48 sequences of 128 keys 9.2 us, on the line 11.4.
 bool whole_items(int max_kv) { return max_kv <= kWarps * kTile; }
 
 template <int D, int NT>

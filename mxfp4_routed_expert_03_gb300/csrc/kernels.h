@@ -37,7 +37,7 @@ cudaError_t moe_launch_plan_build(int T, int E, int k, bool counted, const moe_p
 // route_scored.cu
 cudaError_t moe_launch_plan_scored(int T, int E, int k, const float *logits,
                                    const moe_route_desc &r, const float *bias,
-                                   const moe_plan_buf *p, void *ws, int *status, cudaStream_t st);
+                                   const moe_plan_buf *p, void *ws, int *status, int nsm, cudaStream_t st);
 
 // decode.cu
 int moe_decode_per_lane(int K);

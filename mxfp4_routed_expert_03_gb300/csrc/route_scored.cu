@@ -16,14 +16,20 @@
 // MUFU operations instead of expf and a divide); the k-th largest of the 32
 // lanes' maxima is a lower bound of the k-th score, what lies above it (less
 // the approximation's error, twice) is a candidate, and only the candidates,
-// about one per lane, get their exact score and are ranked. More than 64
-// candidates (many equal scores, k near 32) and groups take exact scores of
+// about one per lane, get their exact score and are ranked (16384 tokens of 896
+// experts: 38 us, 56 with exact scores throughout; softmax 45 and 76). More than
+// 64 candidates (many equal scores, k near 32) and groups take exact scores of
 // all experts.
 #include "route.cuh"
 
 using namespace moe_route;
 
 namespace {
+
+// The largest k that is selected among candidates: 16384 tokens of 896 experts
+// take 44 us so with k = 20 and 58 with 24 (93 and 94 with a search over the bits
+// of all keys), but 108 (96) with 32, where few rows have at most 64 candidates.
+constexpr int kMaxCandidateK = 24;
 
 struct ScoreArgs {
     int E, k;
@@ -304,7 +310,7 @@ __device__ __forceinline__ void warp_scored_topk(const float *row, float (&v)[NK
     if constexpr (!SIGMOID) sum = warp_exps<NK>(v, mx);
     my_e = -1;
     // (a row without a finite logit or with a NaN takes the other way)
-    const bool plain = a.r.n_groups == 1 && a.k <= 16 &&
+    const bool plain = a.r.n_groups == 1 && a.k <= kMaxCandidateK &&
                        (SIGMOID || (fabsf(mx) < INFINITY && sum > 0.f));
     if (plain) my_e = warp_select_approx<NK, SIGMOID>(row, v, bias, a, mx, sum, lane, scratch);
     if (!plain || !__any_sync(FULL_MASK, my_e >= 0)) {
@@ -330,7 +336,7 @@ __device__ __forceinline__ void warp_scored_topk(const float *row, float (&v)[NK
         }
         if (a.r.n_groups > 1) keep_groups<NK>(key, a, lane);
         int n = 65;
-        if (a.k <= 16) {  // as above, with exact keys
+        if (a.k <= kMaxCandidateK) {  // as above, with exact keys
 #pragma unroll
             for (int i = 0; i < NK; ++i) best = max(best, key[i]);
             const uint32_t t = __shfl_sync(FULL_MASK, warp_sort32(best, lane), a.k - 1);
@@ -399,24 +405,25 @@ __global__ void __launch_bounds__(kPlanSmallThreads) moe_plan_scored_small_kerne
 }
 
 // Large batches: a block per chunk of 32 tokens, and the chunk's rows per expert.
-// Threads of a block: with few keys a warp per token; else two blocks an SM at
-// 64 registers.
-template <int NK>
-constexpr int kChunkThreads = NK <= 8 ? 32 * MOE_PLAN_CHUNK : 512;
+// Threads of a block: a warp per token while every SM has one block at most,
+// else half as many, two blocks an SM, so that one's start and end overlap the
+// other's work (us with 1024 and with 512 threads: 4099 tokens of 256 experts 15
+// and 18, 4096 of 1000 16 and 21; 16384 of 256 25 and 23, 16384 of 896 41 and 38).
+constexpr int kManyThreads = 32 * MOE_PLAN_CHUNK, kFewThreads = kManyThreads / 2;
 
-template <int NK, bool SIGMOID>
-__global__ void __launch_bounds__(kChunkThreads<NK>, 1024 / kChunkThreads<NK>) moe_topk_scored_kernel(int T, ScoreArgs a,
+template <int NK, bool SIGMOID, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) moe_topk_scored_kernel(int T, ScoreArgs a,
                                                               const float *__restrict__ logits,
                                                               int32_t *topk_idx, float *topk_w,
                                                               int32_t *chunk_counts, int *status) {
-    constexpr int kThreads = kChunkThreads<NK>, kWarps = kThreads / 32;
+    constexpr int kWarps = THREADS / 32;
     __shared__ uint2 s_scratch[kWarps][64];
     __shared__ uint32_t s_mask[MOE_MAX_EXPERTS];
     __shared__ float s_bias[32 * NK];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     grid_dep_wait();
     grid_dep_launch();
-    for (int e = threadIdx.x; e < a.E; e += kThreads) s_mask[e] = 0u;
+    for (int e = threadIdx.x; e < a.E; e += THREADS) s_mask[e] = 0u;
     load_bias<NK>(a, s_bias);
     __syncthreads();
     bool nan_seen = false;
@@ -437,19 +444,23 @@ __global__ void __launch_bounds__(kChunkThreads<NK>, 1024 / kChunkThreads<NK>) m
     }
     if (__any_sync(FULL_MASK, nan_seen) && lane == 0) moe_flag(status, MOE_ERR_NAN_LOGIT);
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += kThreads)
+    for (int e = threadIdx.x; e < a.E; e += THREADS)
         chunk_counts[(int64_t)blockIdx.x * a.E + e] = __popc(s_mask[e]);
 }
 
 template <int NK, bool SIGMOID>
 cudaError_t launch(int T, const ScoreArgs &a, const float *logits, const moe_plan_buf *p, void *ws,
-                   int *status, cudaStream_t st) {
+                   int *status, int nsm, cudaStream_t st) {
     if (moe_plan_is_small(T))
         return launch_pdl_ready(moe_plan_scored_small_kernel<NK, SIGMOID>, dim3(1),
                           dim3(kPlanSmallThreads), 0, st, T, a, logits, *p, status);
     const int nchunks = (T + MOE_PLAN_CHUNK - 1) / MOE_PLAN_CHUNK;
-    const cudaError_t err = launch_pdl_ready(moe_topk_scored_kernel<NK, SIGMOID>, dim3(nchunks), dim3(kChunkThreads<NK>), 0, st, T,
-                                       a, logits, p->topk_idx, p->topk_w, (int32_t *)ws, status);
+    const cudaError_t err =
+        nchunks <= nsm
+            ? launch_pdl_ready(moe_topk_scored_kernel<NK, SIGMOID, kManyThreads>, dim3(nchunks), dim3(kManyThreads), 0,
+                               st, T, a, logits, p->topk_idx, p->topk_w, (int32_t *)ws, status)
+            : launch_pdl_ready(moe_topk_scored_kernel<NK, SIGMOID, kFewThreads>, dim3(nchunks), dim3(kFewThreads), 0,
+                               st, T, a, logits, p->topk_idx, p->topk_w, (int32_t *)ws, status);
     return err != cudaSuccess ? err : moe_launch_plan_build(T, a.E, a.k, true, p, ws, status, st);
 }
 
@@ -457,8 +468,10 @@ template <int NK>
 cudaError_t setup() {
     const void *kernels[] = {(const void *)moe_plan_scored_small_kernel<NK, true>,
                              (const void *)moe_plan_scored_small_kernel<NK, false>,
-                             (const void *)moe_topk_scored_kernel<NK, true>,
-                             (const void *)moe_topk_scored_kernel<NK, false>};
+                             (const void *)moe_topk_scored_kernel<NK, true, kManyThreads>,
+                             (const void *)moe_topk_scored_kernel<NK, false, kManyThreads>,
+                             (const void *)moe_topk_scored_kernel<NK, true, kFewThreads>,
+                             (const void *)moe_topk_scored_kernel<NK, false, kFewThreads>};
     for (const void *k : kernels) {
         const cudaError_t err = set_kernel(k);
         if (err != cudaSuccess) return err;
@@ -476,15 +489,15 @@ cudaError_t moe_plan_scored_setup() {
 
 cudaError_t moe_launch_plan_scored(int T, int E, int k, const float *logits,
                                    const moe_route_desc &r, const float *bias,
-                                   const moe_plan_buf *p, void *ws, int *status, cudaStream_t st) {
+                                   const moe_plan_buf *p, void *ws, int *status, int nsm, cudaStream_t st) {
     const ScoreArgs a = {E, k, r, bias};
     const bool sig = r.score == MOE_SCORE_SIGMOID;
     if (E <= 256)
-        return sig ? launch<8, true>(T, a, logits, p, ws, status, st)
-                   : launch<8, false>(T, a, logits, p, ws, status, st);
+        return sig ? launch<8, true>(T, a, logits, p, ws, status, nsm, st)
+                   : launch<8, false>(T, a, logits, p, ws, status, nsm, st);
     if (E <= 896)
-        return sig ? launch<28, true>(T, a, logits, p, ws, status, st)
-                   : launch<28, false>(T, a, logits, p, ws, status, st);
-    return sig ? launch<32, true>(T, a, logits, p, ws, status, st)
-               : launch<32, false>(T, a, logits, p, ws, status, st);
+        return sig ? launch<28, true>(T, a, logits, p, ws, status, nsm, st)
+                   : launch<28, false>(T, a, logits, p, ws, status, nsm, st);
+    return sig ? launch<32, true>(T, a, logits, p, ws, status, nsm, st)
+               : launch<32, false>(T, a, logits, p, ws, status, nsm, st);
 }
