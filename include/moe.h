@@ -590,9 +590,11 @@ size_t moe_attn_workspace_bytes(const moe_attn *a, int32_t n_seqs, int32_t n_tok
 
 /* Attention of a batch over the cache: out = softmax(scale q . k) v in bf16
  * and, when lse is not NULL, lse fp32 [n_tokens][n_heads] = log(sum(exp(scale
- * q . k))). The products of the codes are exact; sums and the softmax are fp32, the
- * weights of v are rounded to fp16 or bf16. Within one sequence, head and block of 32 dimensions,
- * values whose scale is over 2^29 below the largest count as zero. An infinity or NaN in a query, a key or a
+ * q . k))). The products of the codes are exact; sums and the softmax are fp32,
+ * the weights of v are rounded to fp16. Scales over 2^26 below the largest that
+ * some row of the sequence sees may count as zero: a value's against the same
+ * block of 32 dimensions, a key's against all of the head (such keys add less
+ * than 2^-26 of the largest key's part to a logit). An infinity or NaN in a query, a key or a
  * value reaches the rows that see it and no others. Lengths outside the
  * bounds, cu_q that does not ascend from 0 to at most n_tokens and pages outside the
  * cache are reported as MOE_ERR_BAD_INDEX; lengths are clamped and tokens of
