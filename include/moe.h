@@ -584,7 +584,7 @@ typedef struct moe_attn_batch {
     const int32_t *page_table;  /* [n_seqs][table_stride] */
 } moe_attn_batch;
 
-/* Host. Scratch bytes of moe_attn_forward for a batch within these bounds. */
+/* Host. Scratch bytes of moe_attn_forward for any batch within these bounds. */
 size_t moe_attn_workspace_bytes(const moe_attn *a, int32_t n_seqs, int32_t n_tokens, int32_t max_q,
                                 int32_t max_kv);
 

@@ -945,13 +945,14 @@ cudaError_t moe_attn_setup() {
     return err != cudaSuccess ? err : moe_attn_prefill_setup();
 }
 
-size_t moe_attn_ws_bytes(int head_dim, int n_seqs, int n_kv, int group, int max_q, int max_kv,
-                         int nsm) {
-    if (moe_attn_prefill_fits(n_seqs, n_kv, group, max_q, max_kv, nsm))
-        return moe_attn_prefill_ws_bytes(head_dim, n_seqs, n_kv, group, max_q, max_kv, nsm);
-    if (whole_items(max_kv)) return 0;
-    const int nt = wide(group, max_q) ? 2 : 1, per_sm = nt == 2 ? 2 : 3;
-    return (size_t)nsm * per_sm * (2 * (8 * nt * (head_dim + 2)) + 8) * sizeof(float);
+size_t moe_attn_ws_bytes(int head_dim, int group, int max_q, int max_kv, int nsm) {
+    auto split = [&](int nt, int per_sm) {
+        return (size_t)nsm * per_sm * (2 * (8 * nt * (head_dim + 2)) + 8) * sizeof(float);
+    };
+    // (never less for larger bounds: a batch within them may go either way)
+    const size_t one = whole_items(max_kv) ? 0 : split(1, 3);
+    const size_t two = whole_items(max_kv) || !wide(group, max_q) ? 0 : split(2, 2);
+    return std::max({one, two, moe_attn_prefill_ws_bytes(head_dim, group, max_q, max_kv, nsm)});
 }
 
 cudaError_t moe_launch_attn(int head_dim, const MoeAttnArgs &a, int nsm, cudaStream_t st) {

@@ -197,9 +197,8 @@ static bool bounds_ok(int n_seqs, int n_tokens, int max_q, int max_kv) {
 MOE_API size_t moe_attn_workspace_bytes(const moe_attn *a, int32_t n_seqs, int32_t n_tokens,
                                         int32_t max_q, int32_t max_kv) {
     if (!a || !bounds_ok(n_seqs, n_tokens, max_q, max_kv) || n_seqs == 0 || n_tokens == 0) return 0;
-    return align_up(moe_attn_ws_bytes(a->desc.head_dim, n_seqs, a->desc.n_kv_heads,
-                                      a->desc.n_heads / a->desc.n_kv_heads, max_q, max_kv,
-                                      a->num_sms),
+    return align_up(moe_attn_ws_bytes(a->desc.head_dim, a->desc.n_heads / a->desc.n_kv_heads, max_q,
+                                      max_kv, a->num_sms),
                     256);
 }
 

@@ -868,6 +868,9 @@ __global__ void __launch_bounds__(256) moe_attn_prefill_join_kernel(MoeAttnArgs 
         store_out(a, s.q0 + c / a.group, h * a.group + c % a.group, D, 64 * i + 2 * lane, o[2 * i], o[2 * i + 1], m, l);
 }
 
+constexpr int kSplitKeys = 4 * kN;   // keys of a split at least
+constexpr int kOneReadCols = 16;     // columns for which the split kernel reads the cache once
+
 struct Shape {
     int tiles_max, splits;
     int64_t ctas;
@@ -877,8 +880,8 @@ Shape shape_of(int n_seqs, int n_kv, int group, int max_q, int max_kv, int nsm) 
     Shape r;
     r.tiles_max = (int)(((int64_t)max_q * group + kCols - 1) / kCols);
     const int64_t items = (int64_t)r.tiles_max * n_seqs * n_kv;
-    // few items: split the keys so that the SMs are all used, in pieces of 4 steps at least
-    const int64_t most = std::max(1, max_kv / (4 * kN));
+    // few items: split the keys so that the SMs are all used
+    const int64_t most = std::max(1, max_kv / kSplitKeys);
     r.splits = (int)std::max<int64_t>(1, std::min<int64_t>(nsm / std::max<int64_t>(items, 1), most));
     r.ctas = items * r.splits;
     return r;
@@ -915,17 +918,17 @@ bool moe_attn_prefill_fits(int n_seqs, int n_kv, int group, int max_q, int max_k
     // 151 and 67 with 64; one such sequence: 18 and 25 with 32 columns, 22 and 27
     // with 64, 31 and 29 with 128.
     const int64_t cols = (int64_t)group * max_q;
-    if (cols <= 16) return false;
+    if (cols <= kOneReadCols) return false;
     if (cols < MOE_ATTN_PREFILL_COLS &&
         (double)cols * n_seqs * n_kv * max_kv < MOE_ATTN_PREFILL_LOGITS)
         return false;
     return shape_of(n_seqs, n_kv, group, max_q, max_kv, nsm).ctas <= (1 << 24);
 }
 
-size_t moe_attn_prefill_ws_bytes(int head_dim, int n_seqs, int n_kv, int group, int max_q, int max_kv,
-                                 int nsm) {
-    const Shape g = shape_of(n_seqs, n_kv, group, max_q, max_kv, nsm);
-    return g.splits == 1 ? 0 : (size_t)g.ctas * kCols * (head_dim + 2) * sizeof(float);
+size_t moe_attn_prefill_ws_bytes(int head_dim, int group, int max_q, int max_kv, int nsm) {
+    // a partial result per CTA where the keys are split: then there are nsm CTAs at most
+    if ((int64_t)group * max_q <= kOneReadCols || max_kv < 2 * kSplitKeys) return 0;
+    return (size_t)nsm * kCols * (head_dim + 2) * sizeof(float);
 }
 
 cudaError_t moe_launch_attn_prefill(int head_dim, const MoeAttnArgs &a, int nsm, cudaStream_t st) {

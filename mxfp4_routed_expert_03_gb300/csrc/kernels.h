@@ -303,8 +303,7 @@ struct MoeAttnArgs {
     long long timeout_cycles;
 };
 cudaError_t moe_attn_setup();  // attn_prefill.cu's too
-size_t moe_attn_ws_bytes(int head_dim, int n_seqs, int n_kv, int group, int max_q, int max_kv,
-                         int nsm);
+size_t moe_attn_ws_bytes(int head_dim, int group, int max_q, int max_kv, int nsm);
 cudaError_t moe_launch_attn(int head_dim, const MoeAttnArgs &a, int nsm, cudaStream_t st);
 
 // attn_prefill.cu: the same with many query rows per sequence: from so many
@@ -314,6 +313,5 @@ cudaError_t moe_launch_attn(int head_dim, const MoeAttnArgs &a, int nsm, cudaStr
 #define MOE_ATTN_PREFILL_LOGITS 4e6
 cudaError_t moe_attn_prefill_setup();
 bool moe_attn_prefill_fits(int n_seqs, int n_kv, int group, int max_q, int max_kv, int nsm);
-size_t moe_attn_prefill_ws_bytes(int head_dim, int n_seqs, int n_kv, int group, int max_q, int max_kv,
-                                 int nsm);
+size_t moe_attn_prefill_ws_bytes(int head_dim, int group, int max_q, int max_kv, int nsm);
 cudaError_t moe_launch_attn_prefill(int head_dim, const MoeAttnArgs &a, int nsm, cudaStream_t st);

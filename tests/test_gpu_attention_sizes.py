@@ -60,3 +60,18 @@ def test_maximum_that_moves(at, d, window):
         f[at] = 20.0
     _refill(s, 0, (k.float() * f.to(DEV)[:, None]).bfloat16())
     s.check()
+
+
+def test_workspace_of_the_bounds_serves_every_batch_within_them():
+    from mxfp4_routed_expert_03_gb300 import moe_attn_workspace_bytes as need
+    s = Setup(8, 1, 128, 64, [2], [4000], seed=60)
+    sizes = [(n, n * q, q, kv) for n in (1, 16, 300) for q in (1, 2, 3, 8, 200) for kv in (100, 1000, 4000, 100000)]
+    for small in sizes:
+        for large in sizes:
+            if all(a <= b for a, b in zip(small, large)):
+                assert need(s.attn.h, *small) <= need(s.attn.h, *large)
+    # 2 rows a sequence with the workspace of bounds that the other kernel serves
+    s.attn._ws = torch.empty(need(s.attn.h, 300, 900, 3, 4000), dtype=torch.uint8, device=DEV)
+    held = s.attn._ws.data_ptr()
+    s.check()
+    assert s.attn._ws.data_ptr() == held
