@@ -956,7 +956,7 @@ size_t moe_attn_ws_bytes(int head_dim, int group, int max_q, int max_kv, int nsm
 }
 
 cudaError_t moe_launch_attn(int head_dim, const MoeAttnArgs &a, int nsm, cudaStream_t st) {
-    if (moe_attn_prefill_fits(a.b.n_seqs, a.n_kv, a.group, a.b.max_q, a.b.max_kv, nsm))
+    if (moe_attn_prefill_fits(a.b.n_seqs, a.n_kv, a.group, a.b.max_q, a.b.max_kv))
         return moe_launch_attn_prefill(head_dim, a, nsm, st);
     const bool w = wide(a.group, a.b.max_q);
     if (head_dim == 64) return w ? launch<64, 2>(a, nsm, st) : launch<64, 1>(a, nsm, st);

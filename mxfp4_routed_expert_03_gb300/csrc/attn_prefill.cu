@@ -312,10 +312,31 @@ struct Column {
 
 // The r-th (sequence, column tile): the longest first, so that the last CTAs to
 // start are short. The order is by the whole steps of keys that a tile sees,
-// found by a search (32 lengths at a time, a lane each); for many sequences (whose CTAs
-// are many) by column tile alone. False if there are fewer. Warp-collective.
+// found by a search (32 lengths at a time, a lane each); for many sequences (whose
+// CTAs are many) by column tile alone, or, where that would number too many tiles
+// that do not exist (tiles_max 0), by sequence. False if there are fewer.
+// Warp-collective.
 __device__ __forceinline__ bool item_of(const MoeAttnArgs &a, int tiles_max, int r, int &b, int &ct) {
     const int lane = threadIdx.x & 31, B = a.b.n_seqs;
+    if (B > 32 && tiles_max == 0) {
+        for (int b0 = 0; b0 < B; b0 += 32) {
+            const int cts = b0 + lane < B ? seq_of<kCols>(a, b0 + lane).cts : 0;
+            int at = cts;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int o = __shfl_up_sync(kFull, at, off);
+                if (lane >= off) at += o;
+            }
+            const uint32_t m = __ballot_sync(kFull, at > r);
+            if (m != 0u) {
+                b = b0 + __ffs(m) - 1;
+                ct = __shfl_sync(kFull, at, b - b0) - 1 - r;  // the last tile first
+                return true;
+            }
+            r -= __shfl_sync(kFull, at, 31);
+        }
+        return false;
+    }
     if (B > 32) {
         b = r % B;
         ct = tiles_max - 1 - r / B;
@@ -872,17 +893,24 @@ constexpr int kSplitKeys = 4 * kN;   // keys of a split at least
 constexpr int kOneReadCols = 16;     // columns for which the split kernel reads the cache once
 
 struct Shape {
-    int tiles_max, splits;
+    int tiles_max, splits;  // (see item_of; column tiles of the longest sequence)
     int64_t ctas;
 };
 
-Shape shape_of(int n_seqs, int n_kv, int group, int max_q, int max_kv, int nsm) {
+Shape shape_of(const moe_attn_batch &q, int n_kv, int group, int nsm) {
     Shape r;
-    r.tiles_max = (int)(((int64_t)max_q * group + kCols - 1) / kCols);
-    const int64_t items = (int64_t)r.tiles_max * n_seqs * n_kv;
+    const int64_t tiles_max = ((int64_t)q.max_q * group + kCols - 1) / kCols;
+    // column tiles of all sequences, by either bound
+    const int64_t grid = tiles_max * q.n_seqs, most = (int64_t)q.n_tokens * group / kCols + q.n_seqs;
+    // 8 prompts of 2000 rows among 248 single rows, 64 / 8 heads: grid is 16128 and
+    // most 763 tiles a key/value head, and a CTA without a tile costs its start: 2.75
+    // and 1.95 ms
+    const bool ragged = q.n_seqs > 32 && grid > 4 * most;
+    r.tiles_max = ragged ? 0 : (int)tiles_max;
+    const int64_t items = (q.n_seqs > 32 && !ragged ? grid : std::min(grid, most)) * n_kv;
     // few items: split the keys so that the SMs are all used
-    const int64_t most = std::max(1, max_kv / kSplitKeys);
-    r.splits = (int)std::max<int64_t>(1, std::min<int64_t>(nsm / std::max<int64_t>(items, 1), most));
+    r.splits = (int)std::max<int64_t>(1, std::min<int64_t>(nsm / std::max<int64_t>(items, 1),
+                                                           std::max(1, q.max_kv / kSplitKeys)));
     r.ctas = items * r.splits;
     return r;
 }
@@ -890,7 +918,7 @@ Shape shape_of(int n_seqs, int n_kv, int group, int max_q, int max_kv, int nsm) 
 template <int D>
 cudaError_t launch(const MoeAttnArgs &a, int nsm, cudaStream_t st) {
     using C = PCfg<D>;
-    const Shape g = shape_of(a.b.n_seqs, a.n_kv, a.group, a.b.max_q, a.b.max_kv, nsm);
+    const Shape g = shape_of(a.b, a.n_kv, a.group, nsm);
     const cudaError_t err = launch_pdl_ready(moe_attn_prefill_kernel<D>, dim3((unsigned)g.ctas), dim3(kThreadsP), C::kSmem, st, a,
                      g.tiles_max, g.splits);
     if (err != cudaSuccess || g.splits == 1) return err;
@@ -911,7 +939,7 @@ cudaError_t moe_attn_prefill_setup() {
     return err != cudaSuccess ? err : setup<128>();
 }
 
-bool moe_attn_prefill_fits(int n_seqs, int n_kv, int group, int max_q, int max_kv, int nsm) {
+bool moe_attn_prefill_fits(int n_seqs, int n_kv, int group, int max_q, int max_kv) {
     // The split kernel reads the cache once for every 16 columns, this one once for
     // 256, but its CTAs take a while to start. 16 sequences of 4000 keys, 8
     // key/value heads: 49 us there and 65 here with 16 columns, 81 and 66 with 24,
@@ -922,7 +950,7 @@ bool moe_attn_prefill_fits(int n_seqs, int n_kv, int group, int max_q, int max_k
     if (cols < MOE_ATTN_PREFILL_COLS &&
         (double)cols * n_seqs * n_kv * max_kv < MOE_ATTN_PREFILL_LOGITS)
         return false;
-    return shape_of(n_seqs, n_kv, group, max_q, max_kv, nsm).ctas <= (1 << 24);
+    return true;
 }
 
 size_t moe_attn_prefill_ws_bytes(int head_dim, int group, int max_q, int max_kv, int nsm) {

@@ -312,6 +312,6 @@ cudaError_t moe_launch_attn(int head_dim, const MoeAttnArgs &a, int nsm, cudaStr
 #define MOE_ATTN_PREFILL_COLS 64
 #define MOE_ATTN_PREFILL_LOGITS 4e6
 cudaError_t moe_attn_prefill_setup();
-bool moe_attn_prefill_fits(int n_seqs, int n_kv, int group, int max_q, int max_kv, int nsm);
+bool moe_attn_prefill_fits(int n_seqs, int n_kv, int group, int max_q, int max_kv);
 size_t moe_attn_prefill_ws_bytes(int head_dim, int group, int max_q, int max_kv, int nsm);
 cudaError_t moe_launch_attn_prefill(int head_dim, const MoeAttnArgs &a, int nsm, cudaStream_t st);

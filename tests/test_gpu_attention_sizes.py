@@ -75,3 +75,15 @@ def test_workspace_of_the_bounds_serves_every_batch_within_them():
     held = s.attn._ws.data_ptr()
     s.check()
     assert s.attn._ws.data_ptr() == held
+
+
+def test_prompts_among_many_single_rows():
+    """More than 32 sequences, few of which have many rows (most tiles of the
+    longest sequence's number do not exist in the others)."""
+    nq, kv = [1] * 40, [33 + b for b in range(40)]
+    nq[3], kv[3] = 150, 333
+    nq[38], kv[38] = 300, 301
+    nq[39], kv[39] = 2, 0
+    Setup(8, 2, 64, 32, nq, kv, seed=61).check()
+    nq, kv = [33] * 34, [40 + 3 * b for b in range(34)]   # most tiles exist
+    Setup(16, 2, 64, 32, nq, kv, seed=62).check()
