@@ -26,7 +26,7 @@
 // 254 without).
 //
 // Bound: 4 D flops per column and key on the tensor cores (the prompts above:
-// 131 us of 239, their 256 columns and 128 keys in 2048 cycles); one exponential
+// 131 us of 236, their 256 columns and 128 keys in 2048 cycles); one exponential
 // per column and key (32 a cycle and SM) is next. A step takes about 3500 cycles:
 // a row warp's chain per unit (read, exponentials, write, two barriers) is longer
 // than its products.
@@ -212,7 +212,9 @@ __device__ __forceinline__ void convert(const MoeAttnArgs &a, bool v, int h, con
         }
     };
     // this lane's block in the first octet of a page, and its scale
-    codes += k * 128 + tl * 16;
+    const uint32_t page_scales = (uint32_t)a.n_kv * NB << a.page_shift;  // bytes of a page
+    codes += ((uint64_t)h * NB << a.page_shift) * 16 + k * 128 + tl * 16;
+    scales += (uint64_t)h * NB << a.page_shift;
     scales += v ? (tl & 6) * NB + 2 * k + (tl & 1) : tl * NB + k;
     auto load = [&](int j) {
         have = 0u;
@@ -223,10 +225,10 @@ __device__ __forceinline__ void convert(const MoeAttnArgs &a, bool v, int h, con
             // (nothing here may look at a loaded value: it would wait for it)
             if ((uint32_t)id[i] < (uint32_t)a.n_pages) {
                 have |= 1u << i;
-                const uint64_t row = (((uint64_t)(uint32_t)id[i] * (uint32_t)a.n_kv + (uint32_t)h) << a.page_shift) +
-                                     (uint32_t)((first + kN * j + row_of(i)) & in_page_mask & ~7);
-                cq[i] = *(const uint4 *)(codes + row * (NB * 16));
-                sb[i] = scales[row * NB];
+                const uint64_t at = (uint64_t)(uint32_t)id[i] * page_scales +
+                                    (uint32_t)((first + kN * j + row_of(i)) & in_page_mask & ~7) * NB;
+                cq[i] = *(const uint4 *)(codes + at * 16);
+                sb[i] = scales[at];
             }
         }
     };
