@@ -26,7 +26,7 @@
 // 254 without).
 //
 // Bound: 4 D flops per column and key on the tensor cores (the prompts above:
-// 131 us of 236, their 256 columns and 128 keys in 2048 cycles); one exponential
+// 131 us of 230, their 256 columns and 128 keys in 2048 cycles); one exponential
 // per column and key (32 a cycle and SM) is next. A step takes about 3500 cycles:
 // a row warp's chain per unit (read, exponentials, write, two barriers) is longer
 // than its products.
@@ -232,6 +232,10 @@ __device__ __forceinline__ void convert(const MoeAttnArgs &a, bool v, int h, con
             }
         }
     };
+    uint8_t *const base = ops + (k >> 1) * C::kHalf + (row0 >> 3) * 1024 + tl * 128;
+    int swz[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) swz[q] = ((4 * (k & 1) + q) ^ tl) << 4;
     page_ids(0);
     load(0);
     page_ids(1);
@@ -248,16 +252,18 @@ __device__ __forceinline__ void convert(const MoeAttnArgs &a, bool v, int h, con
                 const bool nan = sb[i] == 255u;
                 const uint32_t fac = nan ? (v ? 0u : 0x7E007E00u) : factor_of(sb[i], rmax);
                 if (v ? nan && first + kN * j + r >= lo_all : !((have >> i) & 1u)) odd |= 1u << i;
-                uint8_t *dst = ops + st * C::kOp + (k >> 1) * C::kHalf + (r >> 3) * 1024 + (r & 7) * 128;
+                uint8_t *dst = base + st * C::kOp + i * (kConv * OCT * 1024);
                 const uint32_t wd[4] = {cq[i].x, cq[i].y, cq[i].z, cq[i].w};
+                uint32_t x[4][4];  // (all conversions first: 16 in flight)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t x[4];
-                    codes_f16(wd[q], x);
+                for (int q = 0; q < 4; ++q) codes_f16(wd[q], x[q]);
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) x[z] = mul_f16x2(x[z], fac);
-                    *(uint4 *)(dst + (((4 * (k & 1) + q) ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
-                }
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) x[q][z] = mul_f16x2(x[q][z], fac);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *(uint4 *)(dst + swz[q]) = make_uint4(x[q][0], x[q][1], x[q][2], x[q][3]);
             }
         }
         StepInfo &f = info[j % kInfo];
