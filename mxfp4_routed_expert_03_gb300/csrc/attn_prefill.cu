@@ -720,7 +720,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 }
             }
             // ------------------------------------------------ output
-            if (ok && n > 0) ok = wait(&o_full[t], 0);
+            // (without keys nothing else says that all four warps are done with the tile's
+            // queries, which the output is staged over)
+            if (ok) ok = wait(n > 0 ? &o_full[t] : &q_full[t], 0);
             if (ok) {
                 tc::tc_fence_after();
                 if (n > 0) nan_blocks |= nan_seen(n - 1);
