@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
         p_full[2][2], o_part[2], o_full[2], q_full[2], drain[2];
     __shared__ StepInfo info[kInfo];
     __shared__ int s_rk, s_rv[NB], s_abort;
-    __shared__ uint32_t s_tmem;
+    __shared__ uint32_t s_tmem, s_bad[8];  // s_bad: rows of each row warp with a query that is not finite
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
 
     grid_dep_wait();
@@ -543,13 +543,17 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                                              __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
             }
             big = max(big & 0xFFFFu, big >> 16);
-            const bool bad = big >= 0x7F80u;  // the row is NaN: zero operand, NaN factor
+            // an infinity or NaN: the row goes through as zeros, so that keys that it does not
+            // see stay out of it, and becomes NaN at the end if it saw any
+            const bool bad = big >= 0x7F80u;
+            const uint32_t bad_rows = __ballot_sync(kFull, bad);
+            if (lane == 0) s_bad[wid] = bad_rows;  // (read behind the __syncwarp below)
             const int sh = min(141 - (int)(big >> 7), 127);
             // a negative scale's sign goes into the queries, so that the largest
             // product is the largest logit
             const float up = copysignf(pow2(sh), a.b.scale);
             // back from that power, |scale| log2(e)
-            const float mul = bad ? CUDART_NAN_F : pow2(-sh) * (fabsf(a.b.scale) * CUDART_L2E_F);
+            const float mul = bad ? 0.f : pow2(-sh) * (fabsf(a.b.scale) * CUDART_L2E_F);
             const uint32_t keep = bad ? 0u : kFull;
 #pragma unroll 4
             for (int i = 0; i < D / 8; ++i) {
@@ -729,6 +733,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 const bool live_row = c < s.ncol;
                 const int row = s.q0 + c / G, head = h * G + c % G;
                 float *rec = a.part + (int64_t)blockIdx.x * C::kRec + (int64_t)tid * (D + 2);
+                if (((s_bad[wid] >> lane) & 1u) && l != 0.f) l = CUDART_NAN_F;
                 const float r = l == 0.f ? 0.f : 1.f / l;  // (a row without keys: O is 0 too)
                 // rows of the output meet in the tile's queries, which no product reads
                 // any more, so that they leave in whole lines

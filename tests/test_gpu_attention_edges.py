@@ -35,3 +35,30 @@ def test_many_rows_without_keys_are_zero_whatever_the_timing(d):
         assert bool((s.out[dead] == 0).all()) and bool((s.lse[dead] == -math.inf).all())
         assert bool((s.lse[~dead] > -math.inf).all())
     assert s.attn.status() == 0
+
+
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("H,KV,nq,kv", [(4, 2, [6, 1], [2, 3]), (8, 2, [90, 40], [50, 0]), (8, 1, [200], [10]),
+                                        (8, 2, [1200], [1100])])
+def test_non_finite_query_that_sees_no_key_gives_zero(H, KV, nq, kv, bad):
+    """Few rows, many rows, and many rows with the keys split over CTAs. Rows that see a key
+    become NaN, all others stay within twice test_gpu_attention's bound of a run without."""
+    s = Setup(H, KV, 64, 16, nq, kv, seed=71)
+    clean, clean_lse = (t.double().clone() for t in s.run())
+    hit = torch.zeros(s.T, H, dtype=torch.bool, device=DEV)
+    empty = torch.zeros(s.T, H, dtype=torch.bool, device=DEV)
+    for b, (n, m) in enumerate(zip(nq, kv)):
+        first = s.cu[b] + max(n - m, 0)  # row that sees the first key
+        empty[s.cu[b]:first] = True
+        for r in {s.cu[b], max(first - 1, s.cu[b]), min(first, s.cu[b + 1] - 1), s.cu[b + 1] - 1}:
+            s.q[r, 64 * (r % H) + 7] = bad
+            hit[r, r % H] = True
+    out, lse = s.run()
+    assert s.attn.status() == 0
+    out = out.double().view(s.T, H, 64)
+    assert bool((out[empty] == 0).all()) and bool((lse[empty] == -math.inf).all())
+    assert bool(torch.isnan(out[hit & ~empty]).all()) and bool(torch.isnan(lse[hit & ~empty]).all())
+    rest = ~hit & ~empty
+    top = max([float(v.abs().max()) for v in s.v if v.numel()])
+    assert bool(((out - clean.view(s.T, H, 64))[rest].abs() <= 2 * top * (2.0 ** -8 + 2.0 ** -9)).all())
+    assert bool(((lse - clean_lse)[rest].abs() <= 2.0 ** -10).all())
