@@ -32,6 +32,8 @@
 // tile of each stage, each with its own m, l, o, and merge at an item's end;
 // items cut between CTAs leave partial results that a second kernel joins in
 // a fixed order.
+#include <limits.h>
+
 #include <algorithm>
 
 #include "attn.cuh"
@@ -336,10 +338,12 @@ __device__ __forceinline__ void fill_ring(const MoeAttnArgs &a, Walk walk, uint8
                     a.q + (int64_t)(it.s.q0 + c / a.group) * a.q_stride + (it.h * a.group + c % a.group) * D +
                     i % (D / 64) * 64));
         }
-        // the page of this lane's tile of the stage at tile x (-2: not needed)
+        // the page of this lane's tile of the stage at tile x (-2: not needed; the first
+        // of a tile's two pages may lie wholly before the window)
+        const int from = parts == 2 ? it.lo_min - 16 : INT_MIN;
         auto page_at = [&](int x) {
             const int tok = it.s.lo + kTile * (x + tile) + 16 * part;
-            if (part >= parts || x + tile >= it.x_hi || tok >= it.hi_max) return -2;
+            if (part >= parts || x + tile >= it.x_hi || tok >= it.hi_max || tok <= from) return -2;
             const int id = pages[tok >> a.page_shift];
             return id >= 0 && id < a.n_pages ? id : -1;
         };

@@ -62,3 +62,14 @@ def test_non_finite_query_that_sees_no_key_gives_zero(H, KV, nq, kv, bad):
     top = max([float(v.abs().max()) for v in s.v if v.numel()])
     assert bool(((out - clean.view(s.T, H, 64))[rest].abs() <= 2 * top * (2.0 ** -8 + 2.0 ** -9)).all())
     assert bool(((lse - clean_lse)[rest].abs() <= 2.0 ** -10).all())
+
+
+@pytest.mark.parametrize("page", [16, 32])
+@pytest.mark.parametrize("H,KV,nq", [(4, 2, 1), (8, 1, 3), (8, 1, 40)])
+def test_pages_before_the_window_are_not_looked_up(H, KV, nq, page):
+    """A cache manager may have given the pages back that lie wholly before the window."""
+    kv = [100 + i for i in range(0, 70, 3)]
+    s = Setup(H, KV, 64, page, [nq] * len(kv), kv, seed=72, window=20)
+    for b, n in enumerate(kv):
+        s.table[b, :(n - nq + 1 - 20) // page] = -1
+    s.check()
