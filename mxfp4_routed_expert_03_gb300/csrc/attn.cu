@@ -732,13 +732,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
 #pragma unroll
                     for (int k = 0; k < NB; ++k)
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            pv[n][q][k] = mul_f16x2(pt[n][q], f[k]);
-                            if (special) {  // a NaN value is none for the columns that give it no weight
-                                if ((pt[n][q] & 0xFFFFu) == 0u) pv[n][q][k] &= 0xFFFF0000u;
-                                if ((pt[n][q] >> 16) == 0u) pv[n][q][k] &= 0x0000FFFFu;
-                            }
+                        for (int n = 0; n < NT; ++n) pv[n][q][k] = mul_f16x2(pt[n][q], f[k]);
+                    if (special) {  // a NaN value is one for every column that sees it, however small its
+                                    // weight, and none for the others
+                        const int i = 16 * u + 8 * q + 2 * t;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {  // bounds of column g
+                            const int h0 = __shfl_sync(kFull, hi[n][0], g >> 1), h1 = __shfl_sync(kFull, hi[n][1], g >> 1);
+                            const int l0 = __shfl_sync(kFull, lo[n][0], g >> 1), l1 = __shfl_sync(kFull, lo[n][1], g >> 1);
+                            const int to = g & 1 ? h1 : h0, from = g & 1 ? l1 : l0;
+                            uint32_t keep = 0u;
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                if (tok0 + i + e < to && tok0 + i + e >= from && ((live >> (i + e)) & 1u))
+                                    keep |= 0xFFFFu << (16 * e);
+#pragma unroll
+                            for (int k = 0; k < NB; ++k) pv[n][q][k] &= keep;
                         }
+                    }
                 }
                 // --- O^T += V^T P^T
 #pragma unroll

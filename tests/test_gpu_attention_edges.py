@@ -6,7 +6,7 @@ import math
 import pytest
 import torch
 
-from test_gpu_attention import DEV, Setup
+from test_gpu_attention import DEV, Setup, _randn
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +73,34 @@ def test_pages_before_the_window_are_not_looked_up(H, KV, nq, page):
     for b, n in enumerate(kv):
         s.table[b, :(n - nq + 1 - 20) // page] = -1
     s.check()
+
+
+@pytest.mark.parametrize("nq", [1, 40])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nan_at,top_at", [(37, 250), (250, 37), (36, 37), (37, 36), (200, 201)])
+@pytest.mark.parametrize("window", [0, 150])
+def test_nan_value_reaches_rows_that_hardly_weigh_it(window, nan_at, top_at, d, nq):
+    """One key's logit far above the others' (whose weights are below 2^-40 of it), a NaN value
+    at another: every row that sees that key has it, and no other."""
+    from mxfp4_routed_expert_03_gb300 import check
+    n = 300
+    s = Setup(8, 1, d, 16, [nq], [n], seed=73, window=window)
+    s.q.copy_((3.0 * torch.sign(s.q)).bfloat16())
+    k = torch.zeros(n, d, dtype=torch.bfloat16, device=DEV)
+    v = _randn(n, d, seed=74)
+    v[nan_at, d - 7] = math.nan
+    j = torch.arange(n, device=DEV)
+    slots = (s.table[0, j // 16] * 16 + j % 16).int()
+    # head r % 8 of every row has the key of its own signs: 9 d scale
+    for head in (0, 5):
+        k[top_at] = s.q[nq - 1, head * d:(head + 1) * d]
+        check(s.attn.append(n, k, v, slots), "append")
+        out, lse = s.run()
+        assert s.attn.status() == 0
+        pos = n - nq + torch.arange(nq, device=DEV)
+        sees = (pos >= nan_at) & ((pos - window < nan_at) | (window == 0))
+        hit = torch.zeros(nq, 8, d, dtype=torch.bool, device=DEV)
+        hit[sees, :, d - 32:] = True
+        out = out.view(nq, 8, d)
+        assert bool(torch.isnan(out[hit]).all()) and bool(torch.isfinite(out[~hit]).all())
+        assert bool(torch.isfinite(lse).all())
