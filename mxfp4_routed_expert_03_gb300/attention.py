@@ -11,6 +11,7 @@ import torch
 from . import (moe_attn_batch, moe_attn_create, moe_attn_desc, moe_attn_destroy, moe_attn_forward,
                moe_attn_status, moe_attn_workspace_bytes, moe_kv_append, moe_kv_cache, moe_kv_read,
                moe_qk_norm_rope, moe_rope_desc)
+from .workspace import Workspace
 
 CACHE_NAMES = ("k_q", "k_s", "v_q", "v_s")
 
@@ -79,7 +80,7 @@ class Attention:
         self.h = None
         self.desc = moe_attn_desc(n_heads, n_kv_heads, head_dim, page_size, n_pages)
         self.h = moe_attn_create(self.desc, moe_kv_cache(*[cache[n].data_ptr() for n in CACHE_NAMES]))
-        self._ws = None
+        self._space = Workspace(cache["k_q"].device)
         self._need = (None, 0)  # the last batch bounds and their workspace bytes
 
     def close(self):
@@ -103,16 +104,32 @@ class Attention:
     def read(self, n, slots, k, v, stream=None) -> int:
         return moe_kv_read(self.h, n, slots, *_rows(k), *_rows(v), stream)
 
-    def workspace(self, batch: Batch) -> tuple:
+    @property
+    def _ws(self):
+        """The default stream's buffer."""
+        return self._space.bufs.get(0)
+
+    @_ws.setter
+    def _ws(self, buf):
+        self._space.bufs[0] = buf
+
+    def workspace_bytes(self, batch: Batch) -> int:
         if self._need[0] != batch.key:
             self._need = (batch.key, moe_attn_workspace_bytes(self.h, *batch.key))
-        n = self._need[1]
-        if self._ws is None or self._ws.numel() < n:
-            self._ws = torch.empty(max(n, 256), dtype=torch.uint8, device="cuda")
-        return self._ws, n
+        return self._need[1]
 
-    def forward(self, batch: Batch, q, out, lse=None, stream=None) -> int:
-        ws, n = self.workspace(batch)
+    def workspace(self, batch: Batch, stream=None) -> tuple:
+        """Scratch of a call on `stream` (each stream has its own; see Workspace) and the bytes it needs."""
+        n = self.workspace_bytes(batch)
+        return self._space.get(n, stream), n
+
+    def forward(self, batch: Batch, q, out, lse=None, stream=None, ws=None) -> int:
+        """ws: the call's own scratch (a tensor of workspace_bytes(batch) or more), for calls that may
+        overlap others of the same stream: graphs that were captured on one and run at a time."""
+        if ws is None:
+            ws, n = self.workspace(batch, stream)
+        else:
+            n = ws.numel() * ws.element_size()
         return moe_attn_forward(self.h, batch.desc, *_rows(q), *_rows(out), lse, ws, n, stream)
 
     def status(self, stream=None) -> int:

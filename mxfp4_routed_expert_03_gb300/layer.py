@@ -13,6 +13,7 @@ from . import (MOE_OP_DECODE, MOE_OP_FORWARD, MOE_OP_PLAN, MOE_ROUTER_XWR, check
                moe_prepared_bytes, moe_route_desc, moe_router_logits, moe_status, moe_store, moe_store_blob_bound, moe_store_encode,
                moe_store_tiles_per_expert, moe_stream_state_bytes, moe_stream_stats, moe_weights,
                moe_workspace_bytes)
+from .workspace import Workspace, empty_on
 
 WEIGHT_NAMES = ("gate_q", "gate_s", "up_q", "up_s", "down_q", "down_s")
 
@@ -77,14 +78,14 @@ class Layer:
                                  ptr(sh.get("sh_gate")), ptr(sh.get("sh_up")),
                                  ptr(sh.get("sh_down")))
         self.h = moe_create(self.desc, self.wdesc)
-        self._ws = None
+        self._space = Workspace()
         self.atoms = None
 
     def prepare(self, stream=None) -> None:
         """One-time weight-scale re-layout (and W_r split) for the tensor-core paths."""
         if self.atoms is None:
             n = moe_prepared_bytes(self.h)
-            self.atoms = torch.empty(n, dtype=torch.uint8, device="cuda")
+            self.atoms = empty_on(n, stream, "cuda")
             check(moe_prepare(self.h, self.atoms, n, stream), "moe_prepare")
 
     def close(self):
@@ -98,11 +99,10 @@ class Layer:
         except Exception:
             pass
 
-    def workspace(self, T: int, op: int) -> tuple:
+    def workspace(self, T: int, op: int, stream=None) -> tuple:
+        """Scratch of a call on `stream` (each stream has its own; see Workspace) and the bytes it needs."""
         n = moe_workspace_bytes(self.h, T, op)
-        if self._ws is None or self._ws.numel() < n:
-            self._ws = torch.empty(max(n, 256), dtype=torch.uint8, device="cuda")
-        return self._ws, n
+        return self._space.get(n, stream), n
 
     def router_logits(self, T, x, logits, stream=None) -> int:
         self.prepare(stream)
@@ -111,7 +111,7 @@ class Layer:
     def plan(self, T, logits, x, plan: Plan, stream=None) -> int:
         if self.router_mode == MOE_ROUTER_XWR:
             self.prepare(stream)
-        ws, n = self.workspace(T, MOE_OP_PLAN)
+        ws, n = self.workspace(T, MOE_OP_PLAN, stream)
         return moe_plan(self.h, T, logits, x, plan.buf, ws, ws.numel(), stream)
 
     def plan_scored(self, T, logits, x, plan: Plan, route: moe_route_desc, bias=None,
@@ -119,16 +119,16 @@ class Layer:
         """plan() with scored routing (softmax or sigmoid scores, a balance bias, groups)."""
         if self.router_mode == MOE_ROUTER_XWR:
             self.prepare(stream)
-        ws, n = self.workspace(T, MOE_OP_PLAN)
+        ws, n = self.workspace(T, MOE_OP_PLAN, stream)
         return moe_plan_scored(self.h, T, logits, x, route, bias, plan.buf, ws, ws.numel(), stream)
 
     def decode(self, T, x, plan: Plan, out, stream=None) -> int:
-        ws, n = self.workspace(T, MOE_OP_DECODE)
+        ws, n = self.workspace(T, MOE_OP_DECODE, stream)
         return moe_decode(self.h, T, x, plan.buf, out, ws, ws.numel(), stream)
 
     def forward(self, T, x, plan: Plan, out, stream=None) -> int:
         self.prepare(stream)
-        ws, n = self.workspace(T, MOE_OP_FORWARD)
+        ws, n = self.workspace(T, MOE_OP_FORWARD, stream)
         return moe_forward(self.h, T, x, plan.buf, out, ws, ws.numel(), stream)
 
     def status(self, stream=None) -> int:
@@ -206,7 +206,7 @@ class StreamingLayer(Layer):
             self.hdesc = moe_weights(*[host_weights[n].data_ptr() for n in WEIGHT_NAMES], None,
                                      None, None, None)
             self.h = moe_create_streaming(self.desc, self.hdesc, self.wdesc, n_slots, self.state)
-        self._ws = None
+        self._space = Workspace()
         self.atoms = None
 
     def stats(self, stream=None) -> tuple:
