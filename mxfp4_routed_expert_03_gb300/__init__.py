@@ -228,19 +228,11 @@ def lib() -> ctypes.CDLL:
 
 def _ptr(t) -> int | None:
     """Device pointer of a tensor (or an int pointer, or None)."""
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    return t if t is None or isinstance(t, int) else t.data_ptr()
 
 
 def _stream(s) -> int | None:
-    if s is None:
-        return None
-    if isinstance(s, int):
-        return s
-    return s.cuda_stream
+    return s if s is None or isinstance(s, int) else s.cuda_stream
 
 
 def moe_strerror(code: int) -> str:

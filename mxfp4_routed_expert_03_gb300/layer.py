@@ -13,6 +13,7 @@ from . import (MOE_OP_DECODE, MOE_OP_FORWARD, MOE_OP_PLAN, MOE_ROUTER_XWR, check
                moe_prepared_bytes, moe_route_desc, moe_router_logits, moe_status, moe_store, moe_store_blob_bound, moe_store_encode,
                moe_store_tiles_per_expert, moe_stream_state_bytes, moe_stream_stats, moe_weights,
                moe_workspace_bytes)
+from .checks import flat
 from .workspace import Workspace, empty_on
 
 WEIGHT_NAMES = ("gate_q", "gate_s", "up_q", "up_s", "down_q", "down_s")
@@ -116,9 +117,18 @@ class Layer:
 
     def plan_scored(self, T, logits, x, plan: Plan, route: moe_route_desc, bias=None,
                     stream=None) -> int:
-        """plan() with scored routing (softmax or sigmoid scores, a balance bias, groups)."""
+        """plan() with scored routing (softmax or sigmoid scores, a balance bias, groups). Tensors
+        shorter than T tokens, or of another type, are refused with a ValueError."""
+        if plan.T < T:
+            raise ValueError(f"plan: for {T} tokens")
+        bias = flat(bias, self.E, torch.float32, "bias")
         if self.router_mode == MOE_ROUTER_XWR:
+            if isinstance(x, torch.Tensor) and (x.element_size() != 2 or x.numel() < T * self.D or
+                                                not x.is_contiguous()):
+                raise ValueError(f"x: {T} contiguous rows of {self.D} bf16 elements")
             self.prepare(stream)
+        else:
+            logits = flat(logits, T * self.E, torch.float32, "logits")
         ws, n = self.workspace(T, MOE_OP_PLAN, stream)
         return moe_plan_scored(self.h, T, logits, x, route, bias, plan.buf, ws, ws.numel(), stream)
 

@@ -19,7 +19,7 @@ def _on(stream: int, device):
 
 def _capturing(stream: int) -> bool:
     """Whether a graph is being captured on the stream (which need not be the current one)."""
-    if stream in (0, 1):  # (the default stream cannot be captured)
+    if stream == 1:  # (the default stream by its other name)
         return False
     from . import lib
     status = ctypes.c_int(0)
@@ -53,6 +53,6 @@ class Workspace:
                 self._captured.discard(key)
                 self._kept.append(buf)
             buf = self.bufs[key] = empty_on(max(n, 256), key, self.device)
-        if _capturing(key):
+        if key and _capturing(key):  # (the default stream cannot be captured)
             self._captured.add(key)
         return buf

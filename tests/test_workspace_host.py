@@ -79,8 +79,11 @@ def test_layer_and_attention_ask_for_the_calls_stream(W, monkeypatch, T):
     L = layer.Layer.__new__(layer.Layer)
     L.h, L.router_mode, L.atoms, L._space = None, 0, object(), Space()
 
+    L.E = 8
+
     class P:
         buf = None
+    P.T = T
     L.plan(T, None, None, P, 3)
     L.plan_scored(T, None, None, P, None, None, 4)
     L.decode(T, None, P, None, 5)
@@ -89,12 +92,19 @@ def test_layer_and_attention_ask_for_the_calls_stream(W, monkeypatch, T):
     asked.clear()
     monkeypatch.setattr(attention, "moe_attn_workspace_bytes", lambda h, *key: sum(key))
     given = []
-    monkeypatch.setattr(attention, "moe_attn_forward", lambda *a: given.append(a[-3:]) or 0)
+
+    class Lib:
+        def moe_attn_forward(self, *a):
+            given.append(a[-3:])
+            return 0
+    monkeypatch.setattr(attention, "lib", Lib)
     A = attention.Attention.__new__(attention.Attention)
     A.h, A._need, A._space = None, (None, 0), Space()
+    A.n_heads, A.q_width = 1, 64
+    A.desc = attention.moe_attn_desc(1, 1, 64, 16, 1)
     b = attention.Batch(1, T, 1, 9, None, None, None, 1.0)
     A.forward(b, None, None, None, 8)
     assert asked == [(T + 11, 8)]
     own = W.empty_on(500, None, "cpu")
     A.forward(b, None, None, None, 8, own)
-    assert len(asked) == 1 and given[-1][0] is own and given[-1][1:] == (500, 8)
+    assert len(asked) == 1 and given[-1][0] == own.data_ptr() and given[-1][1:] == (500, 8)
