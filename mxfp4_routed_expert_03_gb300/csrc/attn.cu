@@ -20,7 +20,9 @@
 // multiplies the block's partial product in fp32, a value block's scale goes
 // into the weight p, as 2^(e - R) with R a running maximum of the block's
 // exponents (o carries 2^R), so p 2^(e - R) stays within fp16 (values over
-// 2^29 below the largest vanish). p itself is rounded to fp16 (11 bits).
+// 2^29 below the largest vanish). p itself is rounded to fp16 (11 bits) as
+// 2^10 p, so that a warp's sum loses 2^-35 of the largest weight a key at most,
+// and its factor is 2^(5 + e - R).
 // Queries are put into fp16 with one power of two per row, exact for elements
 // within 2^-29 of the row's largest.
 //
@@ -46,6 +48,7 @@ constexpr int kWarps = 4;              // that compute, a tile each; one more fi
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kStages = 3;
 constexpr int kMinTiles = kWarps;      // of a piece
+constexpr int kUp = 10;                // weights carry 2^10 (see above)
 constexpr int kItemCost = 12;          // an item's start and end in tiles (50 us for 64 ragged sequences, 53 with 8)
 
 template <int D, int NT>
@@ -107,6 +110,12 @@ __device__ __forceinline__ void bulk_g2s(void *dst, const void *src, uint32_t by
         : "memory");
 }
 
+// The factor 2^(15 - kUp + y) of a value scale 2^y times the largest (y <= 0; more counts as
+// 0) in fp16: subnormal below 2^-14, 0 below 2^-24.
+__device__ __forceinline__ uint32_t factor(int y) {
+    const int e = 15 - kUp + min(y, 0);
+    return e >= -14 ? (uint32_t)(e + 15) << 10 : e >= -24 ? 1u << (e + 24) : 0u;
+}
 // R of a stored (15 - R) x 65537.
 __device__ __forceinline__ int max_exp(uint32_t r15) { return 15 - (int)r15 / 65537; }
 
@@ -507,8 +516,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
             }
         }
 
-        // ms: the maximum that weights are taken against, 0 while there is none
-        float o[NB][2][NT][4], m[NT][2], ms[NT][2], l[NT][2];
+        // m: the running maximum less kUp; ms: the same as weights are taken against it, 0 while
+        // there is none
+        float o[NB][2][NT][4], m[NT][2], ms[NT][2], l[NT][2], lc[NT][2];  // (l: see add_to)
         // (15 - R) in both halves, as one product so that nothing carries between
         // them, of this lane's two blocks (see the scales below)
         uint32_t r15[2] = {15u * 65537u, 15u * 65537u};
@@ -522,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
                     for (int c = 0; c < 4; ++c) o[k][hh][n][c] = 0.f;
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = -INFINITY, ms[n][0] = ms[n][1] = l[n][0] = l[n][1] = 0.f;
+        for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = -INFINITY, ms[n][0] = ms[n][1] = l[n][0] = l[n][1] = lc[n][0] = lc[n][1] = 0.f;
 
         for (int x = it.x_lo; x < it.x_hi && !dead; x += kWarps) {
             const int st = use_st;
@@ -560,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
                 if constexpr (NB == 4) *(uint4 *)(kf + 4 * lane) = make_uint4(f[0], f[1], f[2], f[3]);
                 else *(uint2 *)(kf + 2 * lane) = make_uint2(f[0], f[1]);
             }
-            // Values: lane = token pair and pair of blocks, 2^(15 + e - R) of both
+            // Values: lane = token pair and pair of blocks, factor(e - R) of both
             // tokens as an fp16 pair. e - R + 15 is in 0 .. 15 for all but few tiles.
             bool special = false;  // a scale that is NaN
             {
@@ -594,9 +604,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
                         for (int off = NB / 2; off < 32; off <<= 1) top = max(top, __shfl_xor_sync(kFull, top, off));
                         back[j] = exp2f((float)((int)old - (int)top));
                         r15[j] = (15u - top) * 65537u;
-                        // clamped at a zero factor (exponent field 0)
-                        const int y0 = (int)(e2[j] & 0xFFFFu) - (int)top, y1 = (int)(e2[j] >> 16) - (int)top;
-                        const uint32_t d = (uint32_t)((max(min(y1, 0), -30) + 15) * 65536 + max(min(y0, 0), -30) + 15);
+                        const uint32_t d = factor((int)(e2[j] & 0xFFFFu) - (int)top) |
+                                           factor((int)(e2[j] >> 16) - (int)top) << 16;
                         if (j == 0) d0 = d;
                         else d1 = d;
                     }
@@ -611,9 +620,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
 #pragma unroll
                                 for (int c = 0; c < 4; ++c) o[k][hh][n][c] *= f;
                     }
+                } else {  // factor(e - R), both halves at once
+                    d0 = d0 * 1024u + (uint32_t)(15 - kUp) * 0x04000400u;
+                    d1 = d1 * 1024u + (uint32_t)(15 - kUp) * 0x04000400u;
                 }
-                d0 = d0 * 1024u + 0x3C003C00u;
-                d1 = d1 * 1024u + 0x3C003C00u;
                 if (special) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -689,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
                         v = fmaxf(v, __shfl_xor_sync(kFull, v, 4));
                         v = fmaxf(v, __shfl_xor_sync(kFull, v, 8));
                         v = fmaxf(v, __shfl_xor_sync(kFull, v, 16));
-                        mx[n][c] = fmaxf(m[n][c], v);
+                        mx[n][c] = fmaxf(m[n][c], v - (float)kUp);
                         grew |= mx[n][c] > m[n][c];
                     }
                 if (__any_sync(kFull, grew)) {
@@ -701,6 +711,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
                             m[n][c] = mx[n][c];
                             ms[n][c] = mx[n][c] == -INFINITY ? 0.f : mx[n][c];
                             l[n][c] *= f;
+                            lc[n][c] *= f;
 #pragma unroll
                             for (int k = 0; k < NB; ++k)
 #pragma unroll
@@ -716,10 +727,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
                 for (int n = 0; n < NT; ++n) {
                     float p[4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        p[c] = ex2(sc[n][c] - ms[n][c & 1]);
-                        l[n][c & 1] += p[c];
-                    }
+                    for (int c = 0; c < 4; ++c) p[c] = ex2(sc[n][c] - ms[n][c & 1]);
+                    add_to(l[n][0], lc[n][0], p[0] + p[2]);
+                    add_to(l[n][1], lc[n][1], p[1] + p[3]);
                     pt[n][0] = transpose8(pack_f16(p[0], p[1]));
                     pt[n][1] = transpose8(pack_f16(p[2], p[3]));
                 }
@@ -788,14 +798,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                float v = l[n][c];
+                float v = l[n][c] - lc[n][c];
                 v += __shfl_xor_sync(kFull, v, 4);
                 v += __shfl_xor_sync(kFull, v, 8);
                 v += __shfl_xor_sync(kFull, v, 16);
                 const int col = 8 * n + 2 * t + c;
                 if (g == 0) {
                     s_m[wid * NC + col] = m[n][c];
-                    s_l[wid * NC + col] = v;
+                    s_l[wid * NC + col] = v * (1.f / (1 << kUp));
                 }
                 float *dst = s_o + (wid * NC + col) * C::kOStride + 4 * g;
 #pragma unroll
@@ -840,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
                 }
             } else if (c0 + col < s.ncol) {
                 store_out(a, s.q0 + (c0 + col) / a.group, h * a.group + (c0 + col) % a.group, D, d, o0, o1,
-                          mt, lt);
+                          mt, lt, kUp);
             }
         }
         consumers_sync();  // the merge buffer is read before the next item's results come
@@ -920,7 +930,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) moe_attn_join_kernel(MoeAttnA
             o0 = fmaf(f, v.x, o0);
             o1 = fmaf(f, v.y, o1);
         }
-        store_out(a, cut.q0 + c / a.group, cut.head * a.group + c % a.group, D, d, o0, o1, m, l);
+        store_out(a, cut.q0 + c / a.group, cut.head * a.group + c % a.group, D, d, o0, o1, m, l, kUp);
     }
 }
 

@@ -35,6 +35,12 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     const __half2 r = __hmul2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
     return *reinterpret_cast<const uint32_t *>(&r);
 }
+// s += a, with c the part by which s is too large (Kahan's summation).
+__device__ __forceinline__ void add_to(float &s, float &c, float a) {
+    const float y = __fsub_rn(a, c), t = __fadd_rn(s, y);
+    c = __fsub_rn(__fsub_rn(t, s), y);
+    s = t;
+}
 __device__ __forceinline__ float pow2(int e) {  // 2^e for e in [-127, 127]
     return __uint_as_float(e == -127 ? 0x00400000u : (uint32_t)(e + 127) << 23);
 }
@@ -80,15 +86,16 @@ __device__ __forceinline__ Seq seq_of(const MoeAttnArgs &a, int b) {
     return s;
 }
 
-// Output of elements d, d + 1 of one row and head: o / l, or 0 where no key was seen.
+// Output of elements d, d + 1 of one row and head: o / l, or 0 where no key was seen. `up` is
+// what m is less than the maximum that l is taken against.
 __device__ __forceinline__ void store_out(const MoeAttnArgs &a, int row, int head, int D, int d,
-                                          float o0, float o1, float m, float l) {
+                                          float o0, float o1, float m, float l, int up) {
     const float r = l == 0.f ? 0.f : 1.f / l;
     *(__nv_bfloat162 *)(a.out + (int64_t)row * a.out_stride + head * D + d) =
         __floats2bfloat162_rn(l == 0.f ? 0.f : o0 * r, l == 0.f ? 0.f : o1 * r);
     if (d == 0 && a.lse)
         a.lse[(int64_t)row * a.n_kv * a.group + head] =
-            l == 0.f ? -INFINITY : (m + log2f(l)) * CUDART_LN2_F;
+            l == 0.f ? -INFINITY : (m + (log2f(l) + up)) * CUDART_LN2_F;
 }
 
 }  // namespace moe_attention

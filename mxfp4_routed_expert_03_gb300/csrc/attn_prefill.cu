@@ -19,7 +19,10 @@
 // with R the largest key exponent (or, per block of 32 dimensions, the largest
 // value exponent) that the CTA's rows can see, found in a pass over the scales
 // before the loop; a block whose scale lies over 2^26 below the largest counts
-// as 0. Queries as in the split kernel. The maximum in use moves only when a
+// as 0. Queries as in the split kernel. Weights are rounded to fp16 as 2^5 p, so
+// that a key loses 2^-30 of the maximum's weight at most (2^20 keys: half of the
+// output's rounding); with 2^8 the maximum in use has to move more often (243 us
+// against 230 for the prompts above). The maximum in use moves only when a
 // unit's weights add up to more than 2^10 with it (they stay far inside fp16's
 // range), so a unit is read once and no maximum of it is taken but for those
 // few, which also rescale O (267 us for the same prompts with a maximum first,
@@ -50,7 +53,8 @@ constexpr int kWarpK = 8, kWarpV = 11, kWarpMma = 14, kConv = 3;
 constexpr int kThreadsP = 32 * kWarpsP;
 constexpr int kInfo = 4;         // steps whose masks are kept
 constexpr int kHead = 12;        // operands carry 2^12
-constexpr float kLag = 1024.f;   // what a unit's weights may add up to (64 at most of the row's maximum)
+constexpr int kUp = 5;           // weights carry 2^5
+constexpr float kLag = 1024.f * (1 << kUp);  // what a unit's weights may add up to (64 x 2^5 at the row's maximum)
 
 template <int D>
 struct PCfg {
@@ -577,7 +581,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
             // logits: S x mul x 2^(R - 127 - 12); not 0, for masked columns are -inf
             float mr = mul * exp2f((float)(s_rk - 127 - kHead));
             if (mr == 0.f) mr = 1.17549435e-38f;
-            float m = -INFINITY, l = 0.f;  // m: the maximum in use
+            // m: the maximum in use, less kUp; l is summed with its rounding errors in lc, so that
+            // the weights of a long context count beside one that is far above them
+            float m = -INFINITY, l = 0.f, lc = 0.f;
             // tokens tok0 + 32 q .. + 31 that the row sees
             auto seen = [&](int tok0, int q) {
                 const int above = min(max(hi - (tok0 + 32 * q), 0), 32);
@@ -670,8 +676,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) mx = max3(mx, __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
                     }
-                    const float top = mx * mr;  // (-inf x 0 is NaN: no key seen)
-                    const bool rise = mx > -INFINITY && top > m;
+                    const float top = mx * mr - (float)kUp;
+                    const bool rise = top > m;
                     const float fac = rise && m > -INFINITY ? ex2(m - top) : 1.f;
                     if (u > 0) {  // O holds the units before, once S of unit u + 1, issued behind them, is there
                         if (!(u + 1 < 2 * n ? wait(&s_full[t][side ^ 1], (u + 1) >> 1) : wait(&o_part[t], 0))) {
@@ -691,6 +697,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                     }
                     if (rise) {
                         l *= fac;
+                        lc *= fac;
                         m = top;
                     }
                     sum = 0.f;
@@ -704,7 +711,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                         tmem_st16(sp + kU * side + 16 * q, p);
                     }
                 }
-                l += sum;
+                add_to(l, lc, sum);
                 // half of the next unit's logits, if there, over the wait for the weights' store
                 there = u + 1 < 2 * n &&
                         __all_sync(kFull, tc::mbar_try_wait(&s_full[t][side ^ 1], ((u + 1) >> 1) & 1));
@@ -733,6 +740,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 const bool live_row = c < s.ncol;
                 const int row = s.q0 + c / G, head = h * G + c % G;
                 float *rec = a.part + (int64_t)blockIdx.x * C::kRec + (int64_t)tid * (D + 2);
+                l = (l - lc) * (1.f / (1 << kUp));
                 if (((s_bad[wid] >> lane) & 1u) && l != 0.f) l = CUDART_NAN_F;
                 const float r = l == 0.f ? 0.f : 1.f / l;  // (a row without keys: O is 0 too)
                 // rows of the output meet in the tile's queries, which no product reads
@@ -741,7 +749,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
 #pragma unroll 1
                 for (int q = 0; q < D / 32; ++q) {
                     uint32_t x[32];
-                    const float back = exp2f((float)(s_rv[q] - 127 - kHead));
+                    const float back = exp2f((float)(s_rv[q] - 127 - kHead - kUp));
                     if (n > 0) {
                         tmem_ld32(op + 32 * q, x);
                         tc::tmem_ld_wait();
@@ -789,7 +797,7 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                     rec[D + 1] = l;
                 } else if (live_row && a.lse) {
                     a.lse[(int64_t)row * a.n_kv * G + head] =
-                        l == 0.f ? -INFINITY : (m + log2f(l)) * CUDART_LN2_F;
+                        l == 0.f ? -INFINITY : (m + (log2f(l) + kUp)) * CUDART_LN2_F;
                 }
             }
             tc::tc_fence_before();
@@ -901,7 +909,7 @@ __global__ void __launch_bounds__(256) moe_attn_prefill_join_kernel(MoeAttnArgs 
     }
 #pragma unroll
     for (int i = 0; i < D / 64; ++i)
-        store_out(a, s.q0 + c / a.group, h * a.group + c % a.group, D, 64 * i + 2 * lane, o[2 * i], o[2 * i + 1], m, l);
+        store_out(a, s.q0 + c / a.group, h * a.group + c % a.group, D, 64 * i + 2 * lane, o[2 * i], o[2 * i + 1], m, l, kUp);
 }
 
 constexpr int kSplitKeys = 4 * kN;   // keys of a split at least

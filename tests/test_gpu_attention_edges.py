@@ -104,3 +104,37 @@ def test_nan_value_reaches_rows_that_hardly_weigh_it(window, nan_at, top_at, d, 
         out = out.view(nq, 8, d)
         assert bool(torch.isnan(out[hit]).all()) and bool(torch.isfinite(out[~hit]).all())
         assert bool(torch.isfinite(lse).all())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nq,seqs", [(64, 80), (1, 912)])
+def test_small_weights_of_a_long_context_add_up(nq, seqs, d):
+    """One key far above 2^20 others, whose weights are 2^-25.5 of its own and 2^-5.5 in all.
+    Keys of 0 and 1, values of 0 (the one) and 1 (the others): out = W / (1 + W), with W the sum
+    of the others' weights. Weights are rounded to fp16 after a factor of 2^5 at least, so they
+    lose 2^-30 each; the bounds are otherwise test_gpu_attention's. Enough column tiles that the
+    keys of one are not split (many rows), or CTAs that take whole sequences (one row); all
+    sequences share the pages."""
+    from mxfp4_routed_expert_03_gb300 import check
+    from mxfp4_routed_expert_03_gb300.attention import Attention, Batch, alloc_kv_cache
+    n, page, H = 1 << 20, 256, 8 if nq > 1 else 1
+    a = Attention(H, 1, d, page, n // page, alloc_kv_cache(1, d, page, n // page))
+    k, v = torch.zeros(n, d, device=DEV).bfloat16(), torch.ones(n, d, device=DEV).bfloat16()
+    k[5], v[5] = 1.0, 0.0
+    slots = torch.randperm(n // page, device=DEV)[:, None] * page + torch.arange(page, device=DEV)
+    table = (slots[:, 0] // page).int().expand(seqs, -1).contiguous()
+    check(a.append(n, k, v, slots.flatten().int()), "append")
+    low = 25.5
+    q = torch.ones(seqs * nq, H * d, device=DEV).bfloat16()
+    cu = torch.arange(0, seqs * nq + 1, nq, device=DEV, dtype=torch.int32)
+    kv = torch.full((seqs,), n, dtype=torch.int32, device=DEV)
+    batch = Batch(seqs, seqs * nq, nq, n, cu, kv, table, low * math.log(2.0) / d)
+    out, lse = torch.empty_like(q), torch.empty(seqs * nq, H, device=DEV)
+    check(a.forward(batch, q, out, lse), "forward")
+    assert a.status() == 0
+    seen = (n - nq + 1 + torch.arange(nq, device=DEV, dtype=torch.float64)).repeat(seqs)
+    W = ((seen - 1) * 2.0 ** -low)[:, None]
+    want = W / (1 + W)
+    bound = 2.0 ** -8 * want + 2.0 ** -9 * want + n * 2.0 ** -30 / (1 + W)
+    assert bool(((out.double() - want).abs() <= bound).all())
+    assert bool(((lse.double() - (low * math.log(2.0) + torch.log1p(W))).abs() <= 2.0 ** -17 * (1 + low)).all())
