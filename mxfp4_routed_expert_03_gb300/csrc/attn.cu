@@ -559,14 +559,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
 
             // --- scales, once for the warp. Keys: lane = token, 2^(byte - 127) of its
             // blocks in fp32; the lowest bit set makes 255 a NaN (and is a 2^-23
-            // error otherwise).
+            // error otherwise), 2^-127 is a subnormal.
             {
                 const uint8_t *ks = buf + 2 * C::kCode + lane * NB;
                 const uint32_t w = NB == 4 ? *(const uint32_t *)ks : *(const uint16_t *)ks;
                 uint32_t f[NB];
 #pragma unroll
-                for (int k = 0; k < NB; ++k)
-                    f[k] = ((k == 0 ? w << 23 : k == 1 ? w << 15 : k == 2 ? w << 7 : w >> 1) & 0x7F800000u) | 1u;
+                for (int k = 0; k < NB; ++k) {
+                    f[k] = (k == 0 ? w << 23 : k == 1 ? w << 15 : k == 2 ? w << 7 : w >> 1) & 0x7F800000u;
+                    f[k] = f[k] == 0u ? 0x00400000u : f[k] | 1u;
+                }
                 if constexpr (NB == 4) *(uint4 *)(kf + 4 * lane) = make_uint4(f[0], f[1], f[2], f[3]);
                 else *(uint2 *)(kf + 2 * lane) = make_uint2(f[0], f[1]);
             }

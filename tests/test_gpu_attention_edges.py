@@ -6,7 +6,9 @@ import math
 import pytest
 import torch
 
+from oracle.act_study import round_to_format
 from test_gpu_attention import DEV, Setup, _randn
+from test_gpu_attention_sizes import _refill
 
 pytestmark = pytest.mark.gpu
 
@@ -138,3 +140,19 @@ def test_small_weights_of_a_long_context_add_up(nq, seqs, d):
     bound = 2.0 ** -8 * want + 2.0 ** -9 * want + n * 2.0 ** -30 / (1 + W)
     assert bool(((out.double() - want).abs() <= bound).all())
     assert bool(((lse.double() - (low * math.log(2.0) + torch.log1p(W))).abs() <= 2.0 ** -17 * (1 + low)).all())
+
+
+@pytest.mark.parametrize("nq", [1, 2, 40])
+@pytest.mark.parametrize("d", [64, 128])
+def test_keys_of_the_smallest_scale(d, nq):
+    """All keys have scale byte 0 (2^-127), and queries are so large that the logits are of
+    ordinary size: no key lies below another by enough to count as zero."""
+    s = Setup(8, 1, d, 32, [nq], [200], seed=75, q_scale=1e37, scale=1.0)
+    k = _randn(200, d, seed=76, scale=1e-38)
+    _refill(s, 0, k)
+    # (the reference's own quantisation has no smallest scale)
+    s.k[0] = torch.from_numpy(round_to_format(k.double().cpu().numpy() * 2.0 ** 127, "e2m1") * 2.0 ** -127).to(DEV)
+    s.k[0] = s.k[0].view(200, 1, d)
+    assert bool((s.attn.cache["k_s"].view(-1, 32, d // 32)[s.table[0, 0].long()] == 0).all())
+    assert float((s.q.double().view(-1, 8, d) @ s.k[0][:, 0].T).std()) > 0.3
+    s.check()
