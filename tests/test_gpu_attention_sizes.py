@@ -87,3 +87,18 @@ def test_prompts_among_many_single_rows():
     Setup(8, 2, 64, 32, nq, kv, seed=61).check()
     nq, kv = [33] * 34, [40 + 3 * b for b in range(34)]   # most tiles exist
     Setup(16, 2, 64, 32, nq, kv, seed=62).check()
+
+
+@pytest.mark.parametrize("B", [160, 161, 333, 500])
+@pytest.mark.parametrize("longest", [100, 129, 700])
+def test_more_sequences_than_threads(B, longest):
+    """Batches of one row and of a few rows a sequence that a block has to scan in rounds of
+    160 sequences: whole items (up to 128 keys), and pieces of the line of all tiles. Lengths
+    repeat irregularly, with empty sequences beside the rounds' ends."""
+    kv = [1 + (37 * b * b + 11 * b) % longest for b in range(B)]
+    for b in (0, 159, 160, 161, 319, 320, 332, 479, 480, B - 1):
+        if b < B and b != 1:
+            kv[b] = 0 if b % 2 else longest
+    Setup(4, 2, 64, 32, [1] * B, kv, seed=B, single=True).check()
+    nq = [1 + b % 3 for b in range(B)]
+    Setup(4, 2, 64, 32, nq, kv, seed=B + 1, window=50).check()
