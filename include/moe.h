@@ -625,9 +625,11 @@ int moe_profile_kernel(moe_handle *h, int32_t which, void *ev_start, void *ev_st
  * hook. Off by default; meant for tests only. */
 enum moe_inject {
     MOE_INJECT_NONE = 0,
-    MOE_INJECT_GEMM_STALL = 1  /* moe_forward's gate/up GEMM: in every CTA the first MMA issuer
+    MOE_INJECT_GEMM_STALL = 1, /* moe_forward's gate/up GEMM: in every CTA the first MMA issuer
                                   waits on a barrier that nothing signals, so that wait runs
                                   out with operand copies in flight */
+    MOE_INJECT_ATTN_STALL = 2  /* moe_attn_forward: the same for the warp that copies the cache
+                                  (few query rows) or the first MMA issuer (many) */
 };
 
 /* Host. Sets the handle's injection mode (enum moe_inject) and the limit of
@@ -636,6 +638,10 @@ enum moe_inject {
  * at least 1e5). Returns MOE_ERR_INVALID_ARG for an unknown mode or a limit
  * below 1e5. */
 int moe_set_fault_injection(moe_handle *h, int32_t mode, int64_t timeout_cycles);
+
+/* Host. The same for an attention handle (MOE_INJECT_NONE or
+ * MOE_INJECT_ATTN_STALL). */
+int moe_attn_set_fault_injection(moe_attn *a, int32_t mode, int64_t timeout_cycles);
 
 /* Host. Synchronises `stream`, returns the first device-side error recorded
  * since the last call (MOE_OK if none) and clears it. */

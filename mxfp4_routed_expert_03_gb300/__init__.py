@@ -42,10 +42,12 @@ EXPORTS = ("moe_create", "moe_destroy", "moe_expert_bytes", "moe_prepared_bytes"
            "moe_profile_kernel", "moe_set_fault_injection", "moe_status", "moe_strerror",
            "moe_plan_scored", "moe_kv_code_bytes", "moe_kv_scale_bytes", "moe_attn_create",
            "moe_attn_destroy", "moe_qk_norm_rope", "moe_kv_append", "moe_kv_read",
-           "moe_attn_workspace_bytes", "moe_attn_forward", "moe_attn_status")
+           "moe_attn_workspace_bytes", "moe_attn_forward", "moe_attn_status",
+           "moe_attn_set_fault_injection")
 
 MOE_INJECT_NONE = 0
 MOE_INJECT_GEMM_STALL = 1
+MOE_INJECT_ATTN_STALL = 2
 
 MOE_PROF_NONE = 0
 MOE_PROF_DECODE_GATEUP = 1
@@ -222,6 +224,8 @@ def lib() -> ctypes.CDLL:
         L.moe_attn_forward.restype = ctypes.c_int
         L.moe_attn_status.argtypes = [p, p]
         L.moe_attn_status.restype = ctypes.c_int
+        L.moe_attn_set_fault_injection.argtypes = [p, i32, i64]
+        L.moe_attn_set_fault_injection.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -427,6 +431,11 @@ def moe_attn_forward(a, batch: moe_attn_batch, q, q_stride, out, out_stride, lse
                      stream=None) -> int:
     return lib().moe_attn_forward(a, ctypes.byref(batch), _ptr(q), q_stride, _ptr(out), out_stride,
                                   _ptr(lse), _ptr(ws), ws_bytes, _stream(stream))
+
+
+def moe_attn_set_fault_injection(a, mode: int, timeout_cycles: int = 0) -> int:
+    """moe_set_fault_injection for an attention handle."""
+    return lib().moe_attn_set_fault_injection(a, mode, timeout_cycles)
 
 
 def moe_attn_status(a, stream=None) -> int:

@@ -336,6 +336,15 @@ __device__ __forceinline__ void fill_ring(const MoeAttnArgs &a, Walk walk, uint8
     int st = 0;
     uint32_t par = 1;  // of the empty barriers: a fresh one counts as passed
     int fills = 0;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {  // bounded; false: give up
+        const bool ok = tc::mbar_wait_sleep(bar, parity, a.timeout_cycles, abort_flag);
+        if (__all_sync(kFull, ok)) return true;
+        if (lane == 0) {
+            moe_flag(a.status, MOE_ERR_DEVICE_TIMEOUT);
+            *(volatile int *)abort_flag = 1;
+        }
+        return false;
+    };
     Item it;
     while (next_item<C::NC>(a, walk, it)) {
         const int32_t *pages = a.b.page_table + (int64_t)it.b * a.b.table_stride;
@@ -360,14 +369,7 @@ __device__ __forceinline__ void fill_ring(const MoeAttnArgs &a, Walk walk, uint8
         for (int x = it.x_lo; x < it.x_hi; x += kWarps) {
             if (id == -1) moe_flag(a.status, MOE_ERR_BAD_INDEX);
             const int next = page_at(x + kWarps);  // in flight over the wait
-            const bool ok = tc::mbar_wait_sleep(&empty[st], par, a.timeout_cycles, abort_flag);
-            if (!__all_sync(kFull, ok)) {
-                if (lane == 0) {
-                    moe_flag(a.status, MOE_ERR_DEVICE_TIMEOUT);
-                    *(volatile int *)abort_flag = 1;
-                }
-                goto wind_down;
-            }
+            if (!wait(&empty[st], par)) goto wind_down;
             const uint32_t have = __ballot_sync(kFull, which == 0 && id >= 0);
             if ((lane & 7) == 0) {
                 const uint32_t two = have >> lane;  // bit 0: first page, bit 1: second
@@ -386,10 +388,11 @@ __device__ __forceinline__ void fill_ring(const MoeAttnArgs &a, Walk walk, uint8
             id = next;
             ++fills;
             if (++st == kStages) st = 0, par ^= 1u;
+            // (test hook: nothing signals this barrier)
+            if (a.inject == MOE_INJECT_ATTN_STALL && !wait(&empty[kStages], 0u)) goto wind_down;
         }
     }
-    return;
-wind_down:  // copies still in flight land before the shared memory goes
+wind_down:  // copies in flight land before the shared memory goes, whether or not a warp waits for them
     int never = 0;
     for (int i = 0; i < kStages; ++i) {
         const int rounds = fills > i ? (fills - i + kStages - 1) / kStages : 0;
@@ -406,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ ScanSpace s_scan;
     __shared__ __align__(16) uint32_t s_scale[kWarps][kTile * NB + kTile / 2 * NB];
-    __shared__ __align__(8) uint64_t full[kStages], empty[kStages];
+    __shared__ __align__(8) uint64_t full[kStages], empty[kStages + 1];  // (empty: one more for the test hook)
     __shared__ uint32_t valid[kStages][kWarps];
     __shared__ float s_m[kWarps * NC], s_l[kWarps * NC];
     __shared__ int s_abort;
@@ -418,6 +421,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
             tc::mbar_init(&full[i], 1);
             tc::mbar_init(&empty[i], kWarps);
         }
+        tc::mbar_init(&empty[kStages], 1);
         s_abort = 0;
         tc::fence_mbar_init();
     }

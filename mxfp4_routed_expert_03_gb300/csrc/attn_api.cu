@@ -12,6 +12,8 @@ struct moe_attn {
     int page_shift;  // log2(page_size)
     int num_sms;
     int *status;     // device word: first error code recorded by a kernel
+    int inject;      // enum moe_inject (test hook; MOE_INJECT_NONE by default)
+    long long timeout;
 };
 
 static int page_shift_of(int page_size) {
@@ -67,6 +69,8 @@ MOE_API int moe_attn_create(const moe_attn_desc *d, const moe_kv_cache *c, moe_a
     a->cache = *c;
     a->page_shift = page_shift_of(d->page_size);
     a->num_sms = nsm;
+    a->inject = MOE_INJECT_NONE;
+    a->timeout = kTimeoutCycles;
     if (cudaMalloc(&a->status, sizeof(int)) != cudaSuccess) {
         free(a);
         return MOE_ERR_CUDA;
@@ -241,10 +245,19 @@ MOE_API int moe_attn_forward(moe_attn *a, const moe_attn_batch *b, const uint16_
     g.lse = lse;
     g.part = (float *)ws;
     g.status = a->status;
-    g.timeout_cycles = kTimeoutCycles;
+    g.timeout_cycles = a->timeout;
+    g.inject = a->inject;
     return moe_launch_attn(d.head_dim, g, a->num_sms, (cudaStream_t)stream) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
+}
+
+MOE_API int moe_attn_set_fault_injection(moe_attn *a, int32_t mode, int64_t timeout_cycles) {
+    if (!a || (mode != MOE_INJECT_NONE && mode != MOE_INJECT_ATTN_STALL)) return MOE_ERR_INVALID_ARG;
+    if (timeout_cycles > 0 && timeout_cycles < 100000) return MOE_ERR_INVALID_ARG;
+    a->inject = mode;
+    a->timeout = timeout_cycles > 0 ? (long long)timeout_cycles : kTimeoutCycles;
+    return MOE_OK;
 }
 
 MOE_API int moe_attn_status(moe_attn *a, void *stream) {

@@ -841,6 +841,8 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 }
                 __syncwarp();
             }
+            // (test hook: nothing signals this barrier)
+            if (a.inject == MOE_INJECT_ATTN_STALL && t == 0 && n > 0 && ok) ok = wait(&drain[t], 0);
             for (int u = 0; u < 2 * n && ok; ++u) {  // O += P V of unit u, then S of unit u + 2 over its P
                 const int j = u >> 1, st = j & 1, side = u & 1;
                 const bool more = j + 1 < n;
@@ -865,7 +867,9 @@ __global__ void __launch_bounds__(kThreadsP, 1)
                 }
                 __syncwarp();
             }
-            if (!ok && elect_one()) tc::drain_mmas(&drain[t], limit);  // MMAs in flight end before TMEM goes
+            // MMAs in flight end before TMEM goes, also where the rows give up on the last ones
+            if (n > 0 && ok) ok = wait(&o_full[t], 0);
+            if (!ok && elect_one()) tc::drain_mmas(&drain[t], limit);
         }
         __syncwarp();
     }

@@ -301,6 +301,7 @@ struct MoeAttnArgs {
     float *part;               // partial results (workspace)
     int *status;
     long long timeout_cycles;
+    int inject;                // MOE_INJECT_NONE, or a test hook (see moe_attn_set_fault_injection)
 };
 cudaError_t moe_attn_setup();  // attn_prefill.cu's too
 size_t moe_attn_ws_bytes(int head_dim, int group, int max_q, int max_kv, int nsm);
