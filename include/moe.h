@@ -591,7 +591,8 @@ size_t moe_attn_workspace_bytes(const moe_attn *a, int32_t n_seqs, int32_t n_tok
 /* Attention of a batch over the cache: out = softmax(scale q . k) v in bf16
  * and, when lse is not NULL, lse fp32 [n_tokens][n_heads] = log(sum(exp(scale
  * q . k))). The products of the codes are exact; sums and the softmax are fp32,
- * the weights of v are rounded to fp16. Scales over 2^26 below the largest that
+ * the weights of v are rounded to fp16 (2^-12 of a weight, or 2^-30 of the row's
+ * largest where that is more). Scales over 2^26 below the largest that
  * some row of the sequence sees may count as zero: a value's against the same
  * block of 32 dimensions, a key's against all of the head (such keys add less
  * than 2^-26 of the largest key's part to a logit). An infinity or NaN in a query, a key or a

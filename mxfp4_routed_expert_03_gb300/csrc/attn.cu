@@ -49,7 +49,10 @@ constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kStages = 3;
 constexpr int kMinTiles = kWarps;      // of a piece
 constexpr int kUp = 10;                // weights carry 2^10 (see above)
-constexpr int kItemCost = 12;          // an item's start and end in tiles (50 us for 64 ragged sequences, 53 with 8)
+// An item's start and end in tiles, at 8, 12 and 16: 64 ragged sequences to 8192 keys 52.2,
+// 48.4 and 48.0 us, 16 to 4000 keys 22.3, 21.3 and 21.4, 24 of 5 rows 19.6, 19.7 and 20.7, 32 equal ones
+// of 2000 keys 31.8, 32.1 and 32.7.
+constexpr int kItemCost = 12;
 
 template <int D, int NT>
 struct Cfg {
@@ -439,9 +442,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm)
     walk.parts = 1;
     walk.per = 1;
     // Parts of an item, if every CTA took one; at the finest. Equal parts where there
-    // are four of an item or all it can have: one sequence of 777 keys 9.4 us (on the
-    // line, where a CTA meets two items, 13.4), four of 5000 15.0 (15.7), two of
-    // 100000 67.5 (65.7).
+    // are four of an item or all it can have: one sequence of 777 keys 9.2 us (on the
+    // line, where a CTA meets two items, 13.4), four of 5000 14.5 (15.7). Where parts are
+    // long the line, which leaves no CTA idle, is 1 to 3 % faster: two of 100000 64.5
+    // (63.2), two of 262143 146 (141).
     const int cap = (int)((long long)gridDim.x / all.items), fine = (longest + kMinTiles - 1) / kMinTiles;
     walk.deal = whole ? DEAL_WHOLE : cap >= min(fine, 4) ? DEAL_PARTS : DEAL_LINE;
     if (walk.deal == DEAL_WHOLE) {
@@ -944,7 +948,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) moe_attn_join_kernel(MoeAttnA
 bool wide(int group, int max_q) { return (int64_t)group * max_q > 8; }
 
 // A CTA takes whole items where each has at most a tile per warp, and nothing is
-// left to join: 48 sequences of 128 keys 9.2 us, on the line 11.4.
+// left to join: 48 sequences of 128 keys 9.0 us, on the line 10.5.
 bool whole_items(int max_kv) { return max_kv <= kWarps * kTile; }
 
 template <int D, int NT>

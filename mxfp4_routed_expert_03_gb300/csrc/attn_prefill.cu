@@ -22,14 +22,14 @@
 // as 0. Queries as in the split kernel. Weights are rounded to fp16 as 2^5 p, so
 // that a key loses 2^-30 of the maximum's weight at most (2^20 keys: half of the
 // output's rounding); with 2^8 the maximum in use has to move more often (243 us
-// against 230 for the prompts above). The maximum in use moves only when a
+// against 230 for 3 prompts of 2000 rows). The maximum in use moves only when a
 // unit's weights add up to more than 2^10 with it (they stay far inside fp16's
 // range), so a unit is read once and no maximum of it is taken but for those
 // few, which also rescale O (267 us for the same prompts with a maximum first,
 // 254 without).
 //
 // Bound: 4 D flops per column and key on the tensor cores (the prompts above:
-// 131 us of 230, their 256 columns and 128 keys in 2048 cycles); one exponential
+// 131 us of 235, their 256 columns and 128 keys in 2048 cycles); one exponential
 // per column and key (32 a cycle and SM) is next. A step takes about 3500 cycles:
 // a row warp's chain per unit (read, exponentials, write, two barriers) is longer
 // than its products.
@@ -969,9 +969,9 @@ cudaError_t moe_attn_prefill_setup() {
 bool moe_attn_prefill_fits(int n_seqs, int n_kv, int group, int max_q, int max_kv) {
     // The split kernel reads the cache once for every 16 columns, this one once for
     // 256, but its CTAs take a while to start. 16 sequences of 4000 keys, 8
-    // key/value heads: 49 us there and 65 here with 16 columns, 81 and 66 with 24,
-    // 151 and 67 with 64; one such sequence: 18 and 25 with 32 columns, 22 and 27
-    // with 64, 31 and 29 with 128.
+    // key/value heads: 46 us there and 63 here with 16 columns, 76 and 63 with 24,
+    // 139 and 64 with 64; one such sequence: 18 and 25 with 32 columns, 22 and 26
+    // with 64 (from there on always here: longer batches gain), 29 and 29 with 128.
     const int64_t cols = (int64_t)group * max_q;
     if (cols <= kOneReadCols) return false;
     if (cols < MOE_ATTN_PREFILL_COLS &&

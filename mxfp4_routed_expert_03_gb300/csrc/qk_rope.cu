@@ -148,8 +148,9 @@ cudaError_t launch(int T, const MoeRopeArgs &a, cudaStream_t st) {
 template <int D>
 cudaError_t launch(int T, const MoeRopeArgs &a, int nsm, cudaStream_t st) {
     const int passes = (a.n_q + a.n_k + 32 / (D / 16) - 1) / (32 / (D / 16));
-    // few tokens: one pass per warp, so that the rows spread over the SMs (5 tokens of
-    // 64 heads 2.0 us, 2.6 with more passes; 2000 tokens 12.4 and 10.7); else
+    // few tokens: one pass per warp, so that the rows spread over the SMs (tokens of 64
+    // heads, one pass and more: 5 1.9 and 2.7 us, 76 2.1 and 2.9, 152 2.5 and 3.0, 300 3.3
+    // and 3.3, 600 5.0 and 5.2, 2000 12.3 and 10.7; the rule changes at 152); else
     // the largest of 4, 3 and 2 that wastes the fewest passes (more loads in
     // flight: 8191 tokens of 72 heads 73 us with 4 passes a warp of which a
     // quarter were empty, 56 us with 3)

@@ -491,6 +491,9 @@ cudaError_t moe_launch_plan_scored(int T, int E, int k, const float *logits,
                                    const moe_route_desc &r, const float *bias,
                                    const moe_plan_buf *p, void *ws, int *status, int nsm, cudaStream_t st) {
     const ScoreArgs a = {E, k, r, bias};
+    // Slots of a lane: 8, 28 or 32, three kinds of six kernels each. What lies between pays
+    // for empty slots: 16384 tokens of 384 experts 31 us (sigmoid) and 40 (softmax), with 16
+    // slots 26 and 31; of 512 experts 32 and 26.
     const bool sig = r.score == MOE_SCORE_SIGMOID;
     if (E <= 256)
         return sig ? launch<8, true>(T, a, logits, p, ws, status, nsm, st)
