@@ -1,0 +1,337 @@
+"""The dense half of a decoder layer in 8 bits, up to the cache, as workloads to time.
+
+Three operators: the norm with the residual's addition, its output in E4M3 with a scale per 128
+columns; the matrix product of such rows with E4M3 weights that have a scale per 128 x 128 block;
+and the norm and rotation of queries and keys that writes keys and values into the paged 4-bit cache
+on the way.
+
+`run` computes them from elementary torch operations, or, with `own` set, through the library's
+entry points. Head counts: 56 x 128 and 32 x 128 are the layer widths 7168 and 4096 of the
+repository's workloads; 896 experts are its router; the other sizes are generic.
+"""
+import math
+
+import torch
+
+own = False
+DEV = "cuda"
+E4M3, E5M2 = torch.float8_e4m3fn, torch.float8_e5m2
+
+
+def listed():
+    """The cases: for each operator the latency of a decode step, an odd batch, and a prefill."""
+    return [
+        # one token's residual stream before a projection: a decode step, bound by latency
+        dict(name="norm_one", op="norm", T=1, d=7168, residual=True, norm=True, y=False, y8=True),
+        # the norm before the router and the experts (bf16) and a projection, odd token count
+        dict(name="norm_both", op="norm", T=777, d=4096, residual=True, norm=True, y=True, y8=True),
+        # attention output to 8 bits for the output projection: no norm, no residual
+        dict(name="norm_quant", op="norm", T=4099, d=8192, residual=False, norm=False, y=False, y8=True),
+        # a prefill batch of the widest layer
+        dict(name="norm_prefill", op="norm", T=8191, d=7168, residual=True, norm=True, y=False, y8=True),
+        # one token through the fused query/key/value projection (56 + 16 heads): weights are everything
+        dict(name="linear_one", op="linear", T=1, K=7168, N=9216, f32=False),
+        # a decode batch through the output projection
+        dict(name="linear_batch", op="linear", T=64, K=7168, N=7168, f32=False),
+        # a chunk of odd length through a narrower layer's fused projection (32 + 8 heads)
+        dict(name="linear_chunk", op="linear", T=333, K=4096, N=5120, f32=False),
+        # fp32 logits of 1000 experts for a batch, ragged in tokens and columns
+        dict(name="linear_logits", op="linear", T=2049, K=4096, N=1000, f32=True),
+        # a prefill batch through the widest layer's fused projection
+        dict(name="linear_prefill", op="linear", T=8191, K=7168, N=9216, f32=False),
+        # queries, keys and values of a decode step, one token in each of 16 sequences
+        dict(name="append_step", op="append", T=16, H=56, KV=8, d=128, rot=128, pairs="halves", page=16,
+             n_pos=32768, pad=0),
+        # an odd chunk padded to the batch size (its last tokens have no slot), partial rotation
+        dict(name="append_chunk", op="append", T=1333, H=32, KV=4, d=64, rot=32, pairs="interleaved",
+             page=32, n_pos=4096, pad=21),
+        # a prefill batch of the widest layer
+        dict(name="append_prefill", op="append", T=8191, H=56, KV=8, d=128, rot=128, pairs="halves",
+             page=64, n_pos=16384, pad=0),
+    ]
+
+
+def _log(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    """One more case of the listed ones' ranges."""
+    op = rng.choice(["norm", "linear", "linear", "append"])
+    if op == "norm":
+        kind = rng.choice(["step", "both", "quant", "y"])
+        return dict(op=op, T=_log(rng, 1, 7000), d=rng.choice([7168, 4096, 2048, 1536, 5120, 8192, 1000, 136]),
+                    residual=kind in ("step", "both"), norm=kind != "quant", y=kind in ("both", "y"), y8=kind != "y")
+    if op == "linear":
+        K, N = rng.choice([(7168, 9216), (7168, 7168), (4096, 5120), (4096, 4096), (8192, 7168), (2048, 6144),
+                           (7168, 896), (4096, 1000), (1536, 7168), (1040, 776), (7168, 264)])
+        return dict(op=op, T=_log(rng, 1, 7000), K=K, N=N, f32=rng.random() < 0.2)
+    H, KV, d = rng.choice([(56, 8, 128), (32, 4, 128), (64, 8, 128), (40, 8, 64), (12, 1, 128), (32, 4, 64)])
+    T = _log(rng, 1, 7000)
+    return dict(op=op, T=T, H=H, KV=KV, d=d, rot=rng.choice([d, d, d // 2, 48]),
+                pairs=rng.choice(["halves", "interleaved"]), page=rng.choice([16, 32, 64, 128]),
+                n_pos=rng.choice([4096, 16384]), pad=rng.choice([0, 0, T // 9]))
+
+
+def work(case):
+    c = case
+    if c["op"] == "norm":
+        n = c["T"] * c["d"]
+        nbytes = n * (2 + 4 * c["residual"] + 2 * c["y"] + c["y8"]) + 2 * c["d"] * c["norm"]
+        return {"bytes": nbytes + 4 * c["T"] * -(-c["d"] // 128) * c["y8"], "flops": n * (5 + c["residual"])}
+    if c["op"] == "linear":
+        T, K, N = c["T"], c["K"], c["N"]
+        kb = -(-K // 128)
+        return {"bytes": T * K + N * K + 4 * kb * (T + -(-N // 128)) + T * N * (4 if c["f32"] else 2),
+                "flops": 2 * T * N * K}
+    T, d = c["T"], c["d"]
+    live = T - c["pad"]
+    # queries in and out, keys and values in, their codes and scales written, then read back
+    return {"bytes": T * c["H"] * d * 4 + live * c["KV"] * (2 * 2 * d + 2 * (d // 2 + d // 32) + 3 * d)
+            + 4 * T * (c["rot"] + 2) + 4 * d,
+            "flops": T * (c["H"] + c["KV"]) * (4 * d + 3 * c["rot"]) + 4 * live * c["KV"] * d}
+
+
+def _blocks(x):
+    """x [n][d] in blocks of 128 columns, the last one filled up with zeros: [n][blocks][128]."""
+    return torch.nn.functional.pad(x, (0, -x.shape[1] % 128)).unflatten(1, (-1, 128))
+
+
+def _stream_rows(T, d, g):
+    """Rows of a residual stream: channels of different size, a few of them far larger, rows too."""
+    channel = torch.exp(0.4 * torch.randn(d, device=DEV, generator=g))
+    channel[torch.randint(d, (4,), device=DEV, generator=g)] *= 20
+    row = torch.exp(0.3 * torch.randn(T, 1, device=DEV, generator=g))
+    return (torch.randn(T, d, device=DEV, generator=g) * channel * row).bfloat16()
+
+
+def _angles(n_pos, rot):
+    """cos then sin of position x frequency, made in 64 bits: fp32 [n_pos][rot]."""
+    f = 10000.0 ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=DEV) / rot)
+    a = torch.arange(n_pos, dtype=torch.float64, device=DEV)[:, None] * f
+    return torch.cat([a.cos(), a.sin()], 1).float()
+
+
+def _weights(N, K, g):
+    """E4M3 weights [N][K] and their fp32 scales per 128 x 128 block."""
+    nb, kb = -(-N // 128), -(-K // 128)
+    w = torch.randn(N, K, device=DEV, generator=g) * K ** -0.5
+    full = torch.nn.functional.pad(w, (0, -K % 128, 0, -N % 128)).view(nb, 128, kb, 128)
+    s = full.abs().amax((1, 3)) / 448
+    q = (full / s[:, None, :, None]).clamp(-448, 448).to(E4M3).view(nb * 128, kb * 128)[:N, :K]
+    return q.contiguous(), s.contiguous()
+
+
+def prepare(case, seed):
+    c = dict(case)
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    s = {"case": c}
+    T, d = c["T"], c.get("d")
+    if c["op"] == "norm":
+        s["x"] = _stream_rows(T, d, g)
+        s["r"] = _stream_rows(T, d, g) if c["residual"] else None
+        s["w"] = (1 + 0.2 * torch.randn(d, device=DEV, generator=g)).bfloat16() if c["norm"] else None
+        if own:  # the parameters and buffers that a program keeps
+            from mxfp4_routed_expert_03_gb300.linear import Fp8Rows, Norm
+            s["norm"] = Norm(d, 1e-6, s["w"])
+            s["total"] = torch.empty_like(s["x"]) if c["residual"] else None
+            s["y"] = torch.empty_like(s["x"]) if c["y"] else None
+            s["y8"] = Fp8Rows.empty(T, d) if c["y8"] else None
+        return s
+    if c["op"] == "linear":
+        K, N = c["K"], c["N"]
+        x = _blocks(torch.randn(T, K, device=DEV, generator=g) * torch.exp(0.4 * torch.randn(K, device=DEV, generator=g)))
+        s["xs"] = x.abs().amax(2) / 448
+        s["xq"] = (x / s["xs"][:, :, None]).clamp(-448, 448).to(E4M3).flatten(1)[:, :K].contiguous()
+        s["wq"], s["ws"] = _weights(N, K, g)
+        if own:
+            from mxfp4_routed_expert_03_gb300.linear import Fp8Rows, Linear
+            s["linear"] = Linear(K, N, s["wq"], s["ws"])
+            s["rows"] = Fp8Rows(s["xq"], s["xs"])
+            s["out"] = torch.empty(T, N, dtype=torch.float32 if c["f32"] else torch.bfloat16, device=DEV)
+        return s
+    H, KV, page = c["H"], c["KV"], c["page"]
+    # slices of one fused projection's output: strided rows, as a layer has them
+    x = torch.randn(T, (H + 2 * KV) * d, device=DEV, generator=g).bfloat16()
+    s["q"], s["k"], s["v"] = x.split([H * d, KV * d, KV * d], dim=1)
+    s["wq"], s["wk"] = ((1 + 0.2 * torch.randn(d, device=DEV, generator=g)).bfloat16() for _ in range(2))
+    s["pos"] = torch.randint(c["n_pos"], (T,), device=DEV, generator=g, dtype=torch.int32)
+    s["table"] = _angles(c["n_pos"], c["rot"])
+    s["pages"] = pages = -(-T // page) + 70
+    # whole pages in any order, filled from their start, as an allocator hands them out
+    order = torch.randperm(pages, device=DEV, generator=g)
+    at = torch.arange(T, device=DEV)
+    if T <= 64:  # one token in each of T sequences
+        slots = order[:T] * page + torch.randint(page, (T,), device=DEV, generator=g)
+    else:
+        slots = order[at // page] * page + at % page
+    s["slots"] = torch.where(at < T - c["pad"], slots, torch.full_like(slots, -1)).int()
+    if own:
+        from mxfp4_routed_expert_03_gb300.attention import Attention, Rope, alloc_kv_cache
+        s["attn"] = Attention(H, KV, d, page, pages, alloc_kv_cache(KV, d, page, pages))
+        s["rope"] = Rope(s["table"], c["rot"], interleaved=c["pairs"] == "interleaved", eps=1e-6,
+                         q_weight=s["wq"], k_weight=s["wk"])
+        s["q_out"] = torch.empty(T, H * d, dtype=torch.bfloat16, device=DEV)
+        s["k_out"], s["v_out"] = (torch.zeros(T, KV * d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    return s
+
+
+def _plain_norm(s):
+    c = s["case"]
+    h = s["x"]
+    if c["residual"]:
+        h = (s["x"].float() + s["r"].float()).bfloat16()
+    y = h.float()
+    if c["norm"]:
+        y = y / torch.sqrt((y * y).mean(1, keepdim=True) + 1e-6) * s["w"].float()
+    out = {"total": h} if c["residual"] else {}
+    if c["y"]:
+        out["y"] = y.bfloat16()
+    if c["y8"]:
+        b = _blocks(y)
+        scale = (b.abs().amax(2) / 448).clamp(min=2.0 ** -126)
+        out["scale"] = scale
+        out["q"] = (b / scale[:, :, None]).clamp(-448, 448).to(E4M3).flatten(1)[:, :c["d"]]
+    return out
+
+
+def _plain_linear(s):
+    c = s["case"]
+    x = (_blocks(s["xq"].float()) * s["xs"][:, :, None]).flatten(1)[:, :c["K"]]
+    by_row = s["ws"].repeat_interleave(128, 0)[:c["N"]]
+    w = (_blocks(s["wq"].float()) * by_row[:, :, None]).flatten(1)[:, :c["K"]]
+    out = x @ w.T
+    return out if c["f32"] else out.bfloat16()
+
+
+_VALUES = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0]
+
+
+def _plain_codes(x):
+    """Signed E2M1 codes and biased scale exponents of x [..., d] in blocks of 32; ties to the even code."""
+    b = x.float().unflatten(-1, (-1, 32))
+    top = b.abs().amax(-1, keepdim=True)
+    e = (torch.frexp(top)[1] - 3).clamp(min=-127)
+    e = torch.where(top == 0, torch.full_like(e, -127), e)
+    a = torch.ldexp(b, -e).abs()
+    n = (a > 0.25).to(torch.uint8)
+    for edge, tie in ((0.75, True), (1.25, False), (1.75, True), (2.5, False), (3.5, True), (5.0, False)):
+        n += (a >= edge) if tie else (a > edge)
+    code = n | (torch.signbit(b).to(torch.uint8) << 3)
+    return code.flatten(-2), (e.squeeze(-1) + 127).to(torch.uint8)
+
+
+def _plain_append(s):
+    c, d, rot, KV, T = s["case"], s["case"]["d"], s["case"]["rot"], s["case"]["KV"], s["case"]["T"]
+    cos, sin = s["table"][s["pos"].long()][:, None].chunk(2, -1)
+    turned = []
+    for x, w in ((s["q"], s["wq"]), (s["k"], s["wk"])):
+        x = x.float().unflatten(1, (-1, d))
+        y = x / torch.sqrt((x * x).mean(-1, keepdim=True) + 1e-6) * w.float()
+        r = y[..., :rot]
+        if c["pairs"] == "halves":
+            a, b = r.chunk(2, -1)
+            r = torch.cat([a * cos - b * sin, b * cos + a * sin], -1)
+        else:
+            a, b = r[..., 0::2], r[..., 1::2]
+            r = torch.stack([a * cos - b * sin, b * cos + a * sin], -1).flatten(-2)
+        turned.append(torch.cat([r, y[..., rot:]], -1).flatten(1).bfloat16())
+    # into the cache, and back: tokens without a slot are not there
+    n, value = T - c["pad"], torch.tensor(_VALUES + [-v for v in _VALUES], device=DEV)
+    slots, back = s["slots"][:n].long(), []
+    for x in (turned[1][:n], s["v"][:n]):
+        code, exp = _plain_codes(x.unflatten(1, (KV, d)))
+        q = torch.empty((s["pages"] * c["page"], KV, d // 2), dtype=torch.uint8, device=DEV)
+        e = torch.empty((s["pages"] * c["page"], KV, d // 32), dtype=torch.uint8, device=DEV)
+        q[slots] = code[..., 0::2] | (code[..., 1::2] << 4)
+        e[slots] = exp
+        byte = q[slots]
+        y = value[torch.stack([byte & 15, byte >> 4], -1).flatten(-2).int()]
+        y = torch.ldexp(y.unflatten(-1, (-1, 32)), e[slots].int()[..., None] - 127).flatten(1)
+        back.append(torch.nn.functional.pad(y, (0, 0, 0, c["pad"])).bfloat16())
+    return {"q": turned[0], "k": back[0].to(E5M2), "v": back[1]}
+
+
+def run(state):
+    s, c = state, state["case"]
+    if not own:
+        return {"norm": _plain_norm, "linear": _plain_linear, "append": _plain_append}[c["op"]](s)
+    from mxfp4_routed_expert_03_gb300 import check
+    st = torch.cuda.current_stream()
+    if c["op"] == "norm":
+        check(s["norm"].forward(c["T"], s["x"], s["r"], s["total"], s["y"], s["y8"], st), "moe_add_norm")
+        out = {"total": s["total"]} if c["residual"] else {}
+        if c["y"]:
+            out["y"] = s["y"]
+        if c["y8"]:
+            out["scale"], out["q"] = s["y8"].s, s["y8"].q
+        return out
+    if c["op"] == "linear":
+        check(s["linear"].forward(c["T"], s["rows"], s["out"], st), "moe_linear_forward")
+        return s["out"]
+    a = s["attn"]
+    check(a.rope_append(c["T"], s["q"], s["k"], s["v"], s["pos"], s["rope"], s["q_out"], s["slots"], st), "moe_rope_append")
+    # the cache's new tokens as the values that they stand for (4-bit keys fit 8 bits)
+    check(a.read(c["T"], s["slots"], s["k_out"], s["v_out"], st), "moe_kv_read")
+    return {"q": s["q_out"], "k": s["k_out"].to(E5M2), "v": s["v_out"]}
+
+
+def _exact_norm(s):
+    c = s["case"]
+    total = s["x"].double()
+    if c["residual"]:
+        total = total + s["r"].double()
+    y = total.float().bfloat16().double() if c["residual"] else total
+    if c["norm"]:
+        y = y * torch.rsqrt(y.pow(2).sum(1, keepdim=True) / c["d"] + 1e-6) * s["w"].double()
+    out = {"total": total} if c["residual"] else {}
+    if c["y"]:
+        out["y"] = y
+    if c["y8"]:
+        parts = [p.abs().amax(1) for p in y.split(128, 1)]
+        out["scale"] = (torch.stack(parts, 1) / 448).clamp(min=2.0 ** -126)
+        out["q"] = torch.cat([p / out["scale"][:, i:i + 1] for i, p in enumerate(y.split(128, 1))], 1)
+    return out
+
+
+def _exact_linear(s):
+    c = s["case"]
+    out = torch.zeros(c["T"], c["N"], dtype=torch.float64, device=DEV)
+    of = torch.arange(c["N"], device=DEV) // 128
+    for b in range(s["ws"].shape[1]):
+        k = slice(128 * b, min(128 * b + 128, c["K"]))
+        part = s["xq"][:, k].float().double() @ s["wq"][:, k].float().double().T
+        out += part * s["xs"][:, b].double()[:, None] * s["ws"][:, b].double()[of]
+    return out
+
+
+def _exact_append(s):
+    c, d, rot, T = s["case"], s["case"]["d"], s["case"]["rot"], s["case"]["T"]
+    angle = s["table"].double()[s["pos"].long()]
+    turn = torch.complex(angle[:, :rot // 2], angle[:, rot // 2:])[:, None]
+    rows = []
+    for x, w in ((s["q"], s["wq"]), (s["k"], s["wk"])):
+        x = x.double().reshape(T, -1, d)
+        y = x * torch.rsqrt(x.pow(2).sum(-1, keepdim=True) / d + 1e-6) * w.double()
+        first, second = (slice(0, rot // 2), slice(rot // 2, rot)) if c["pairs"] == "halves" else (slice(0, rot, 2), slice(1, rot, 2))
+        z = torch.complex(y[..., first], y[..., second]) * turn
+        y[..., first], y[..., second] = z.real, z.imag
+        rows.append(y.reshape(T, -1))
+    levels = torch.tensor(_VALUES, dtype=torch.float64, device=DEV)
+    odd = torch.arange(8, device=DEV) % 2 * 1e-12  # an odd level loses a tie
+    back = []
+    for x in (rows[1].bfloat16(), s["v"]):  # (keys are rounded to bf16 once before their codes)
+        y = torch.zeros(T, x.shape[1], dtype=torch.float64, device=DEV)
+        for t in range(0, T - c["pad"], 1024):
+            at = slice(t, min(t + 1024, T - c["pad"]))
+            b = x[at].double().reshape(-1, 32)
+            unit = torch.exp2((torch.floor(torch.log2(b.abs().amax(1, keepdim=True).clamp(min=1e-300))) - 2).clamp(min=-127))
+            near = ((b / unit).abs()[..., None] - levels).abs() + odd
+            y[at] = (torch.copysign(levels[near.argmin(-1)], b) * unit).reshape(at.stop - at.start, -1)
+        back.append(y)
+    return {"q": rows[0], "k": back[0], "v": back[1]}
+
+
+def exact(case, seed):
+    s = prepare(dict(case), seed)
+    return {"norm": _exact_norm, "linear": _exact_linear, "append": _exact_append}[case["op"]](s)
