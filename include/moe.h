@@ -565,6 +565,20 @@ int moe_kv_append(moe_attn *a, int32_t T, const uint16_t *k, int64_t k_stride, c
 int moe_kv_read(moe_attn *a, int32_t n, const int32_t *slots, uint16_t *k, int64_t k_stride,
                 uint16_t *v, int64_t v_stride, void *stream);
 
+/* moe_qk_norm_rope and moe_kv_append in one pass, for tokens whose keys are
+ * wanted in the cache only: the queries are normed and rotated into q_out, the
+ * keys normed, rotated, rounded once to bf16 and written with the values into
+ * the slots in MXFP4; the same bits as the two calls give. Arguments as there
+ * (k and v are needed; q may be NULL with q_out: that part is left out).
+ * Slots must be distinct; a slot of -1 skips the token's key and value, not its
+ * query; any other slot outside the cache is reported as MOE_ERR_BAD_INDEX and
+ * treated the same way. A token whose position is outside [0, n_pos) is
+ * reported as MOE_ERR_BAD_INDEX, and nothing of it is written. */
+int moe_rope_append(moe_attn *a, int32_t T, const moe_rope_desc *rope, const int32_t *positions,
+                    const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                    const uint16_t *v, int64_t v_stride, const int32_t *slots, uint16_t *q_out,
+                    int64_t q_out_stride, void *stream);
+
 /* A batch of sequences. Sequence b has the query rows cu_q[b] .. cu_q[b+1]-1
  * and kv_len[b] cached tokens, of which its queries are the last: query i of n
  * sits at position p = kv_len[b] - n + i and sees the keys j <= p, with
@@ -608,6 +622,97 @@ int moe_attn_forward(moe_attn *a, const moe_attn_batch *batch, const uint16_t *q
 /* Host. As moe_status, for an attention handle. */
 int moe_attn_status(moe_attn *a, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * The dense half of a decoder layer in 8 bits: the norm with the residual's
+ * addition, whose output can be E4M3 rows with a scale per 128 columns, and the
+ * product of such rows with an E4M3 weight matrix that has a scale per 128 x 128
+ * block (the projections around the attention, a router's logits).
+ * The calls below run on the device that was current when their handle was
+ * created; MOE_ERR_INVALID_ARG when another one is current.
+ * ------------------------------------------------------------------------- */
+
+/* Rows of E4M3FN codes with fp32 scales: element x of row t stands for
+ * q[t * q_stride + x] * s[t * s_stride + x / 128]. */
+typedef struct moe_fp8_rows {
+    uint8_t *q;
+    int64_t q_stride;  /* bytes; a multiple of 16, at least the row length; q 16-byte aligned */
+    float *s;
+    int64_t s_stride;  /* elements; at least ceil(row length / 128); s 4-byte aligned */
+} moe_fp8_rows;
+
+typedef struct moe_norm_desc {
+    int32_t d_model;         /* row length: a multiple of 8, up to 16384 */
+    float eps;               /* >= 0, finite */
+    const uint16_t *weight;  /* bf16 [d_model], 16-byte aligned; NULL: no norm */
+} moe_norm_desc;
+
+typedef struct moe_norm moe_norm;
+
+/* Host. Validates the parameters and the device as moe_create does and records
+ * the weight pointer (caller-owned, it must outlive the handle). *out is NULL
+ * on failure. */
+int moe_norm_create(const moe_norm_desc *desc, moe_norm **out);
+
+/* Host. Frees the handle. NULL is a no-op. */
+void moe_norm_destroy(moe_norm *n);
+
+/* For each of T rows of d_model elements
+ *   h = x + residual, rounded once to bf16 (h = x where residual is NULL)
+ *   y = h / sqrt(mean(h^2) + eps) * weight in fp32 (y = h where weight is NULL)
+ * and, each where it is not NULL: h into total, y rounded to bf16 into y, y
+ * into y8: per 128 columns (the last block may be shorter) the scale
+ * s = max(max|y| / 448, 2^-126), codes y / s rounded to the nearest E4M3 value,
+ * ties to even. A block holding an infinity or NaN gets a NaN scale: all of it
+ * reads as NaN. total needs a residual. bf16 rows may be strided (elements,
+ * multiples of 8; bases 16-byte aligned); for y8 d_model is a multiple of 16.
+ * A bf16 output may be an input (same pointer and stride) but must not overlap
+ * one otherwise. Asynchronous on `stream`, no workspace. */
+int moe_add_norm(moe_norm *n, int32_t T, const uint16_t *x, int64_t x_stride,
+                 const uint16_t *residual, int64_t residual_stride, uint16_t *total,
+                 int64_t total_stride, uint16_t *y, int64_t y_stride, const moe_fp8_rows *y8,
+                 void *stream);
+
+/* d_in: a multiple of 16 up to 65536; d_out: a multiple of 8 up to 2^20. */
+typedef struct moe_linear_desc {
+    int32_t d_in;
+    int32_t d_out;
+} moe_linear_desc;
+
+/* Element type of moe_linear_forward's output. */
+enum moe_linear_out {
+    MOE_LINEAR_BF16 = 0,
+    MOE_LINEAR_F32 = 1
+};
+
+typedef struct moe_linear moe_linear;
+
+/* Host. Validates the shape and the device as moe_create does, records the
+ * weight pointers (caller-owned, they must outlive the handle; their contents
+ * may change between calls) and allocates the 4-byte device status word. *out
+ * is NULL on failure.
+ *   w_q  E4M3FN codes [d_out][d_in], 16-byte aligned
+ *   w_s  fp32 [ceil(d_out/128)][ceil(d_in/128)], 4-byte aligned (the layout of
+ *        MOE_W_FP8's matrices) */
+int moe_linear_create(const moe_linear_desc *desc, const uint8_t *w_q, const float *w_s,
+                      moe_linear **out);
+
+/* Host. Frees the status word and the handle. NULL is a no-op. */
+void moe_linear_destroy(moe_linear *l);
+
+/* out[t][n] = sum_b x_s[t][b] w_s[n/128][b] sum_{k in block b} x_q[t][k] w_q[n][k]
+ * for T rows x of d_in codes. The products of the codes are exact; a block's 128
+ * are summed by the tensor cores in fp32, the blocks in fp32 with their scales,
+ * in an order fixed by the shape; rounded once to out_type (enum
+ * moe_linear_out). out: rows of d_out elements, 16-byte aligned, out_stride in
+ * elements with 16-byte rows; nothing behind the T rows or between them is
+ * written. NaN codes and scales reach the rows and columns that they belong to.
+ * Asynchronous on `stream`, no workspace: calls on any streams may overlap. */
+int moe_linear_forward(moe_linear *l, int32_t T, const moe_fp8_rows *x, void *out,
+                       int64_t out_stride, int32_t out_type, void *stream);
+
+/* Host. As moe_status, for a linear handle. */
+int moe_linear_status(moe_linear *l, void *stream);
+
 /* Host. Instrumentation for timing one kernel on the library's own stream:
  * while `which` names a kernel (enum moe_prof_kernel), every later call that
  * launches it records ev_start (a cudaEvent_t) immediately before that launch
@@ -629,8 +734,9 @@ enum moe_inject {
     MOE_INJECT_GEMM_STALL = 1, /* moe_forward's gate/up GEMM: in every CTA the first MMA issuer
                                   waits on a barrier that nothing signals, so that wait runs
                                   out with operand copies in flight */
-    MOE_INJECT_ATTN_STALL = 2  /* moe_attn_forward: the same for the warp that copies the cache
+    MOE_INJECT_ATTN_STALL = 2, /* moe_attn_forward: the same for the warp that copies the cache
                                   (few query rows) or the first MMA issuer (many) */
+    MOE_INJECT_LINEAR_STALL = 3 /* moe_linear_forward: the same for every MMA issuer */
 };
 
 /* Host. Sets the handle's injection mode (enum moe_inject) and the limit of
@@ -643,6 +749,10 @@ int moe_set_fault_injection(moe_handle *h, int32_t mode, int64_t timeout_cycles)
 /* Host. The same for an attention handle (MOE_INJECT_NONE or
  * MOE_INJECT_ATTN_STALL). */
 int moe_attn_set_fault_injection(moe_attn *a, int32_t mode, int64_t timeout_cycles);
+
+/* Host. The same for a linear handle (MOE_INJECT_NONE or
+ * MOE_INJECT_LINEAR_STALL). */
+int moe_linear_set_fault_injection(moe_linear *l, int32_t mode, int64_t timeout_cycles);
 
 /* Host. Synchronises `stream`, returns the first device-side error recorded
  * since the last call (MOE_OK if none) and clears it. */

@@ -43,11 +43,14 @@ EXPORTS = ("moe_create", "moe_destroy", "moe_expert_bytes", "moe_prepared_bytes"
            "moe_plan_scored", "moe_kv_code_bytes", "moe_kv_scale_bytes", "moe_attn_create",
            "moe_attn_destroy", "moe_qk_norm_rope", "moe_kv_append", "moe_kv_read",
            "moe_attn_workspace_bytes", "moe_attn_forward", "moe_attn_status",
-           "moe_attn_set_fault_injection")
+           "moe_attn_set_fault_injection", "moe_rope_append", "moe_norm_create",
+           "moe_norm_destroy", "moe_add_norm", "moe_linear_create", "moe_linear_destroy",
+           "moe_linear_forward", "moe_linear_status", "moe_linear_set_fault_injection")
 
 MOE_INJECT_NONE = 0
 MOE_INJECT_GEMM_STALL = 1
 MOE_INJECT_ATTN_STALL = 2
+MOE_INJECT_LINEAR_STALL = 3
 
 MOE_PROF_NONE = 0
 MOE_PROF_DECODE_GATEUP = 1
@@ -68,6 +71,9 @@ MOE_W_FP8 = 1
 
 MOE_SCORE_SOFTMAX = 0
 MOE_SCORE_SIGMOID = 1
+
+MOE_LINEAR_BF16 = 0
+MOE_LINEAR_F32 = 1
 
 
 class moe_desc(ctypes.Structure):
@@ -127,6 +133,19 @@ class moe_attn_batch(ctypes.Structure):
                 ("table_stride", ctypes.c_int32), ("window", ctypes.c_int32),
                 ("scale", ctypes.c_float), ("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
                 ("page_table", ctypes.c_void_p)]
+
+
+class moe_fp8_rows(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("s", ctypes.c_void_p),
+                ("s_stride", ctypes.c_int64)]
+
+
+class moe_norm_desc(ctypes.Structure):
+    _fields_ = [("d_model", ctypes.c_int32), ("eps", ctypes.c_float), ("weight", ctypes.c_void_p)]
+
+
+class moe_linear_desc(ctypes.Structure):
+    _fields_ = [("d_in", ctypes.c_int32), ("d_out", ctypes.c_int32)]
 
 
 class MoeError(RuntimeError):
@@ -226,6 +245,26 @@ def lib() -> ctypes.CDLL:
         L.moe_attn_status.restype = ctypes.c_int
         L.moe_attn_set_fault_injection.argtypes = [p, i32, i64]
         L.moe_attn_set_fault_injection.restype = ctypes.c_int
+        L.moe_rope_append.argtypes = [p, i32, ctypes.POINTER(moe_rope_desc), p, p, i64, p, i64, p,
+                                      i64, p, p, i64, p]
+        L.moe_rope_append.restype = ctypes.c_int
+        L.moe_norm_create.argtypes = [ctypes.POINTER(moe_norm_desc), ctypes.POINTER(p)]
+        L.moe_norm_create.restype = ctypes.c_int
+        L.moe_norm_destroy.argtypes = [p]
+        L.moe_norm_destroy.restype = None
+        L.moe_add_norm.argtypes = [p, i32, p, i64, p, i64, p, i64, p, i64,
+                                   ctypes.POINTER(moe_fp8_rows), p]
+        L.moe_add_norm.restype = ctypes.c_int
+        L.moe_linear_create.argtypes = [ctypes.POINTER(moe_linear_desc), p, p, ctypes.POINTER(p)]
+        L.moe_linear_create.restype = ctypes.c_int
+        L.moe_linear_destroy.argtypes = [p]
+        L.moe_linear_destroy.restype = None
+        L.moe_linear_forward.argtypes = [p, i32, ctypes.POINTER(moe_fp8_rows), p, i64, i32, p]
+        L.moe_linear_forward.restype = ctypes.c_int
+        L.moe_linear_status.argtypes = [p, p]
+        L.moe_linear_status.restype = ctypes.c_int
+        L.moe_linear_set_fault_injection.argtypes = [p, i32, i64]
+        L.moe_linear_set_fault_injection.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -440,6 +479,58 @@ def moe_attn_set_fault_injection(a, mode: int, timeout_cycles: int = 0) -> int:
 
 def moe_attn_status(a, stream=None) -> int:
     return lib().moe_attn_status(a, _stream(stream))
+
+
+def moe_rope_append(a, T, rope: moe_rope_desc, positions, q, q_stride, k, k_stride, v, v_stride,
+                    slots, q_out, q_out_stride, stream=None) -> int:
+    return lib().moe_rope_append(a, T, ctypes.byref(rope), _ptr(positions), _ptr(q), q_stride,
+                                 _ptr(k), k_stride, _ptr(v), v_stride, _ptr(slots), _ptr(q_out),
+                                 q_out_stride, _stream(stream))
+
+
+def moe_norm_create(desc: moe_norm_desc) -> int:
+    h = ctypes.c_void_p()
+    rc = lib().moe_norm_create(ctypes.byref(desc), ctypes.byref(h))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_norm_create")
+    return h.value
+
+
+def moe_norm_destroy(n: int) -> None:
+    lib().moe_norm_destroy(n)
+
+
+def moe_add_norm(n, T, x, x_stride, residual, residual_stride, total, total_stride, y, y_stride,
+                 y8: moe_fp8_rows | None, stream=None) -> int:
+    return lib().moe_add_norm(n, T, _ptr(x), x_stride, _ptr(residual), residual_stride,
+                              _ptr(total), total_stride, _ptr(y), y_stride,
+                              None if y8 is None else ctypes.byref(y8), _stream(stream))
+
+
+def moe_linear_create(desc: moe_linear_desc, w_q, w_s) -> int:
+    h = ctypes.c_void_p()
+    rc = lib().moe_linear_create(ctypes.byref(desc), _ptr(w_q), _ptr(w_s), ctypes.byref(h))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_linear_create")
+    return h.value
+
+
+def moe_linear_destroy(l: int) -> None:
+    lib().moe_linear_destroy(l)
+
+
+def moe_linear_forward(l, T, x: moe_fp8_rows, out, out_stride, out_type, stream=None) -> int:
+    return lib().moe_linear_forward(l, T, ctypes.byref(x), _ptr(out), out_stride, out_type,
+                                    _stream(stream))
+
+
+def moe_linear_set_fault_injection(l, mode: int, timeout_cycles: int = 0) -> int:
+    """moe_set_fault_injection for a linear handle."""
+    return lib().moe_linear_set_fault_injection(l, mode, timeout_cycles)
+
+
+def moe_linear_status(l, stream=None) -> int:
+    return lib().moe_linear_status(l, _stream(stream))
 
 
 def check(rc: int, where: str = "") -> None:

@@ -17,7 +17,7 @@ OBJDIR = os.path.join(HERE, "_build")
 SOURCES = ["api.cu", "route.cu", "decode.cu", "quant.cu", "grouped_gemm.cu", "dense_gemm.cu", "fp8.cu",
            "noalloc.cu", "stream.cu", "store.cu", "store_enc.cu", "route_scored.cu", "qk_rope.cu",
            "kv_cache.cu", "attn.cu", "attn_prefill.cu",
-           "attn_api.cu"]
+           "attn_api.cu", "rope_append.cu", "norm.cu", "linear.cu", "linear_api.cu"]
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo", "-O3", "-std=c++17",
               "-Xcompiler", "-fPIC,-fvisibility=hidden", "-I", os.path.join(ROOT, "include")]
 

@@ -26,3 +26,10 @@ def flat(t, n: int, dtype, what: str):
     if t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{what}: {n} contiguous elements of {dtype}")
     return t.data_ptr()
+
+
+def on_device(index: int, *tensors) -> None:
+    """Refuses tensors that are not on CUDA device `index` (pointers and None are left alone)."""
+    for t in tensors:
+        if t is not None and t.__class__ is not int and t.get_device() != index:
+            raise ValueError(f"a tensor on {t.device}: not on the handle's device cuda:{index}")

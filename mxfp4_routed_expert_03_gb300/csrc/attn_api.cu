@@ -61,7 +61,7 @@ MOE_API int moe_attn_create(const moe_attn_desc *d, const moe_kv_cache *c, moe_a
         return MOE_ERR_CUDA;
     if (major != 10 || minor != 3) return MOE_ERR_UNSUPPORTED;
     if (moe_qk_norm_rope_setup() != cudaSuccess || moe_kv_setup() != cudaSuccess ||
-        moe_attn_setup() != cudaSuccess)
+        moe_rope_append_setup() != cudaSuccess || moe_attn_setup() != cudaSuccess)
         return MOE_ERR_CUDA;
     moe_attn *a = (moe_attn *)calloc(1, sizeof(moe_attn));
     if (!a) return MOE_ERR_INVALID_ARG;
@@ -95,32 +95,25 @@ static bool rows_ok(const void *p, int64_t stride, int64_t width) {
     return p && aligned16(p) && stride % 8 == 0 && stride >= width;
 }
 
-MOE_API int moe_qk_norm_rope(moe_attn *a, int32_t T, const moe_rope_desc *r,
-                             const int32_t *positions, const uint16_t *q, int64_t q_stride,
-                             const uint16_t *k, int64_t k_stride, uint16_t *q_out,
-                             int64_t q_out_stride, uint16_t *k_out, int64_t k_out_stride,
-                             void *stream) {
-    NvtxRange nvtx_range("moe_qk_norm_rope");
-    if (!a || T < 0 || !r) return MOE_ERR_INVALID_ARG;
-    const moe_attn_desc &d = a->desc;
-    if (r->rope_dim < 0 || r->rope_dim > d.head_dim || r->rope_dim % 16 || r->n_pos < 0 ||
-        (r->interleaved != 0 && r->interleaved != 1) || !finite_f32(r->eps) || r->eps < 0.f)
-        return MOE_ERR_INVALID_ARG;
-    if (!aligned16(r->q_weight) || !aligned16(r->k_weight)) return MOE_ERR_INVALID_ARG;
-    if ((!q) != (!q_out) || (!k) != (!k_out)) return MOE_ERR_INVALID_ARG;
-    if (T == 0 || (!q && !k)) return MOE_OK;
-    if (r->rope_dim > 0 &&
-        (!r->cos_sin || !aligned16(r->cos_sin) || !positions || ((uintptr_t)positions & 3u)))
-        return MOE_ERR_INVALID_ARG;
-    const int64_t qw = (int64_t)d.n_heads * d.head_dim, kw = (int64_t)d.n_kv_heads * d.head_dim;
-    if (q && (!rows_ok(q, q_stride, qw) || !rows_ok(q_out, q_out_stride, qw)))
-        return MOE_ERR_INVALID_ARG;
-    if (k && (!rows_ok(k, k_stride, kw) || !rows_ok(k_out, k_out_stride, kw)))
-        return MOE_ERR_INVALID_ARG;
-    if ((int64_t)T * (d.n_heads + d.n_kv_heads) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+// Whether norm and rotation parameters make sense, tokens or not.
+static bool rope_desc_ok(const moe_attn_desc &d, const moe_rope_desc *r) {
+    return r->rope_dim >= 0 && r->rope_dim <= d.head_dim && r->rope_dim % 16 == 0 && r->n_pos >= 0 &&
+           (r->interleaved == 0 || r->interleaved == 1) && finite_f32(r->eps) && r->eps >= 0.f &&
+           aligned16(r->q_weight) && aligned16(r->k_weight);
+}
+
+// Whether a rotation has its table and positions.
+static bool rope_arrays_ok(const moe_rope_desc *r, const int32_t *positions) {
+    return r->rope_dim == 0 ||
+           (r->cos_sin && aligned16(r->cos_sin) && positions && !((uintptr_t)positions & 3u));
+}
+
+static MoeRopeArgs rope_args(const moe_attn *a, const moe_rope_desc *r, const int32_t *positions,
+                             const uint16_t *q, int64_t q_stride, const uint16_t *k, int64_t k_stride,
+                             uint16_t *q_out, int64_t q_out_stride) {
     MoeRopeArgs g = {};
-    g.n_q = q ? d.n_heads : 0;
-    g.n_k = k ? d.n_kv_heads : 0;
+    g.n_q = q ? a->desc.n_heads : 0;
+    g.n_k = k ? a->desc.n_kv_heads : 0;
     g.rope_dim = r->rope_dim;
     g.interleaved = r->interleaved;
     g.n_pos = r->n_pos;
@@ -132,12 +125,34 @@ MOE_API int moe_qk_norm_rope(moe_attn *a, int32_t T, const moe_rope_desc *r,
     g.q = q;
     g.k = k;
     g.q_out = q_out;
-    g.k_out = k_out;
     g.q_stride = q_stride;
     g.k_stride = k_stride;
     g.q_out_stride = q_out_stride;
-    g.k_out_stride = k_out_stride;
     g.status = a->status;
+    return g;
+}
+
+MOE_API int moe_qk_norm_rope(moe_attn *a, int32_t T, const moe_rope_desc *r,
+                             const int32_t *positions, const uint16_t *q, int64_t q_stride,
+                             const uint16_t *k, int64_t k_stride, uint16_t *q_out,
+                             int64_t q_out_stride, uint16_t *k_out, int64_t k_out_stride,
+                             void *stream) {
+    NvtxRange nvtx_range("moe_qk_norm_rope");
+    if (!a || T < 0 || !r) return MOE_ERR_INVALID_ARG;
+    const moe_attn_desc &d = a->desc;
+    if (!rope_desc_ok(d, r)) return MOE_ERR_INVALID_ARG;
+    if ((!q) != (!q_out) || (!k) != (!k_out)) return MOE_ERR_INVALID_ARG;
+    if (T == 0 || (!q && !k)) return MOE_OK;
+    if (!rope_arrays_ok(r, positions)) return MOE_ERR_INVALID_ARG;
+    const int64_t qw = (int64_t)d.n_heads * d.head_dim, kw = (int64_t)d.n_kv_heads * d.head_dim;
+    if (q && (!rows_ok(q, q_stride, qw) || !rows_ok(q_out, q_out_stride, qw)))
+        return MOE_ERR_INVALID_ARG;
+    if (k && (!rows_ok(k, k_stride, kw) || !rows_ok(k_out, k_out_stride, kw)))
+        return MOE_ERR_INVALID_ARG;
+    if ((int64_t)T * (d.n_heads + d.n_kv_heads) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    MoeRopeArgs g = rope_args(a, r, positions, q, q_stride, k, k_stride, q_out, q_out_stride);
+    g.k_out = k_out;
+    g.k_out_stride = k_out_stride;
     return moe_launch_qk_norm_rope(T, d.head_dim, g, a->num_sms, (cudaStream_t)stream) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
@@ -170,6 +185,29 @@ MOE_API int moe_kv_append(moe_attn *a, int32_t T, const uint16_t *k, int64_t k_s
     g.k_stride = k_stride;
     g.v_stride = v_stride;
     return moe_launch_kv_append(a->desc.head_dim, g, (cudaStream_t)stream) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+
+MOE_API int moe_rope_append(moe_attn *a, int32_t T, const moe_rope_desc *r,
+                            const int32_t *positions, const uint16_t *q, int64_t q_stride,
+                            const uint16_t *k, int64_t k_stride, const uint16_t *v,
+                            int64_t v_stride, const int32_t *slots, uint16_t *q_out,
+                            int64_t q_out_stride, void *stream) {
+    NvtxRange nvtx_range("moe_rope_append");
+    if (!a || T < 0 || !r || !rope_desc_ok(a->desc, r) || (!q) != (!q_out)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    const moe_attn_desc &d = a->desc;
+    const int64_t qw = (int64_t)d.n_heads * d.head_dim, kw = (int64_t)d.n_kv_heads * d.head_dim;
+    if (!rope_arrays_ok(r, positions) || !rows_ok(k, k_stride, kw) || !rows_ok(v, v_stride, kw) || !slots ||
+        ((uintptr_t)slots & 3u) || (q && (!rows_ok(q, q_stride, qw) || !rows_ok(q_out, q_out_stride, qw))))
+        return MOE_ERR_INVALID_ARG;
+    if ((int64_t)T * (d.n_heads + 2 * d.n_kv_heads) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    MoeKvArgs c = kv_args(a, T, slots);
+    c.v = v;
+    c.v_stride = v_stride;
+    const MoeRopeArgs g = rope_args(a, r, positions, q, q_stride, k, k_stride, q_out, q_out_stride);
+    return moe_launch_rope_append(d.head_dim, g, c, a->num_sms, (cudaStream_t)stream) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
 }

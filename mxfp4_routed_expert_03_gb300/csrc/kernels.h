@@ -287,6 +287,12 @@ cudaError_t moe_kv_setup();
 cudaError_t moe_launch_kv_append(int head_dim, const MoeKvArgs &a, cudaStream_t st);
 cudaError_t moe_launch_kv_read(int head_dim, const MoeKvArgs &a, cudaStream_t st);
 
+// rope_append.cu: norm and rotation with the keys and values going into the
+// cache (moe_rope_append); the keys are r.k (r.k_out and kv.k are not used).
+cudaError_t moe_rope_append_setup();
+cudaError_t moe_launch_rope_append(int head_dim, const MoeRopeArgs &r, const MoeKvArgs &kv, int nsm,
+                                   cudaStream_t st);
+
 // attn.cu: attention over the cache
 struct MoeAttnArgs {
     int n_kv, group;           // key/value heads, query heads of each
@@ -316,3 +322,37 @@ cudaError_t moe_attn_prefill_setup();
 bool moe_attn_prefill_fits(int n_seqs, int n_kv, int group, int max_q, int max_kv);
 size_t moe_attn_prefill_ws_bytes(int head_dim, int group, int max_q, int max_kv, int nsm);
 cudaError_t moe_launch_attn_prefill(int head_dim, const MoeAttnArgs &a, int nsm, cudaStream_t st);
+
+// norm.cu: residual addition, norm, rows in E4M3 (moe_add_norm)
+#define MOE_NORM_MAX_D 16384
+struct MoeNormArgs {
+    int T, d;
+    float eps;
+    const uint16_t *weight;       // or NULL: no norm
+    const uint16_t *x, *residual;  // residual or NULL
+    uint16_t *total, *y;          // each or NULL
+    uint8_t *q;                   // E4M3 codes and scales, or NULL
+    float *s;
+    int64_t x_stride, residual_stride, total_stride, y_stride, q_stride, s_stride;
+};
+cudaError_t moe_norm_setup();
+cudaError_t moe_launch_norm(const MoeNormArgs &a, int nsm, cudaStream_t st);
+
+// linear.cu: E4M3 rows times E4M3 weights with block scales (moe_linear_forward)
+struct MoeLinearArgs {
+    int T, K, N;       // rows, d_in, d_out
+    const float *x_s;  // [T][x_s_stride]
+    int64_t x_s_stride;
+    const float *w_s;  // [ceil(N/128)][ceil(K/128)]
+    void *out;
+    int64_t out_stride;
+    int out_f32;
+    int *status;
+    long long timeout_cycles;
+    int inject;
+};
+cudaError_t moe_linear_setup();
+// Rows of x that one box of its tensor map holds, for T rows.
+int moe_linear_box_rows(int T, int K, int N, int nsm);
+cudaError_t moe_launch_linear(const CUtensorMap &map_w, const CUtensorMap &map_x,
+                              const MoeLinearArgs &a, int nsm, cudaStream_t st);

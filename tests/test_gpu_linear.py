@@ -1,0 +1,241 @@
+"""moe_linear_forward: E4M3 rows times E4M3 weights with block scales, against 64 bits."""
+import pytest
+import torch
+
+from linear_ref import bound, product, quantised, weights
+
+pytestmark = pytest.mark.gpu
+
+E4M3 = torch.float8_e4m3fn
+
+
+class Setup:
+    def __init__(self, T, K, N, seed=0, dtype=torch.bfloat16):
+        from mxfp4_routed_expert_03_gb300.linear import Fp8Rows, Linear
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.T, self.K, self.N, self.dtype = T, K, N, dtype
+        self.wq, self.ws = weights(N, K, g)
+        self.xq, self.xs = quantised(T, K, g)
+        self.linear = Linear(K, N, self.wq, self.ws)
+        self.rows = Fp8Rows(self.xq, self.xs)
+        self.out = torch.full((T, N), 7.0, dtype=dtype, device="cuda")
+
+    def run(self, stream=None):
+        from mxfp4_routed_expert_03_gb300 import check
+        check(self.linear.forward(self.T, self.rows, self.out, stream), "moe_linear_forward")
+
+    def verify(self, out=None):
+        assert self.linear.status() == 0
+        ref, mag = product(self.xq, self.xs, self.wq, self.ws)
+        off = ((self.out if out is None else out).double() - ref).abs()
+        assert bool((off <= bound(ref, mag, self.K, self.dtype)).all()), float((off / bound(ref, mag, self.K, self.dtype)).max())
+
+
+# tokens around every tile's edge, from one to several tiles
+TOKENS = [1, 2, 7, 8, 9, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 191, 255, 256, 257, 300, 511, 513, 1000]
+
+
+@pytest.mark.parametrize("T", TOKENS)
+@pytest.mark.parametrize("K,N", [(256, 384), (1040, 776)])
+def test_tokens(T, K, N):
+    s = Setup(T, K, N, seed=T)
+    s.run()
+    s.verify()
+
+
+@pytest.mark.parametrize("K,N", [(16, 8), (32, 16), (112, 120), (128, 128), (144, 136), (2048, 8), (16, 2000),
+                                 (7168, 264), (4096, 1000), (1536, 4096), (7168, 7168), (65536, 128), (128, 20000)])
+@pytest.mark.parametrize("T,dtype", [(1, torch.bfloat16), (5, torch.float32), (40, torch.bfloat16),
+                                     (140, torch.float32), (600, torch.bfloat16)])
+def test_shapes(T, K, N, dtype):
+    s = Setup(T, K, N, seed=1, dtype=dtype)
+    s.run()
+    s.verify()
+
+
+@pytest.mark.parametrize("T,K,N", [(3000, 7168, 9216), (2049, 4096, 1000), (4100, 512, 2560)])
+def test_prefill(T, K, N):
+    s = Setup(T, K, N, seed=2, dtype=torch.float32)
+    s.run()
+    s.verify()
+
+
+@pytest.mark.parametrize("T", [1, 20, 70, 200, 700])
+def test_whole_numbers_are_exact(T):
+    """Small whole codes and scales that are powers of two: every sum is a whole number of at most 24
+    bits, so nothing is rounded, wherever a row, a column or a block of 128 lies."""
+    from mxfp4_routed_expert_03_gb300 import check
+    from mxfp4_routed_expert_03_gb300.linear import Fp8Rows, Linear
+    K, N = 1296, 392
+    g = torch.Generator(device="cuda").manual_seed(T)
+    whole = lambda *s: torch.randint(-3, 4, s, device="cuda", generator=g).float()  # noqa: E731
+    pow2 = lambda *s: torch.randint(0, 3, s, device="cuda", generator=g).float().exp2()  # noqa: E731
+    xq, wq, kb = whole(T, K).to(E4M3), whole(N, K).to(E4M3), -(-K // 128)
+    xs, ws = pow2(T, kb), pow2(-(-N // 128), kb)
+    out = torch.empty(T, N, device="cuda")
+    linear = Linear(K, N, wq, ws)
+    check(linear.forward(T, Fp8Rows(xq, xs), out), "moe_linear_forward")
+    assert torch.equal(out.double(), product(xq, xs, wq, ws)[0])
+
+
+@pytest.mark.parametrize("T", [1, 6, 50, 130, 400])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_strided_rows_and_untouched_memory(T, dtype):
+    """Rows cut out of wider ones, more rows than tokens: what lies around the output stays."""
+    from mxfp4_routed_expert_03_gb300 import check
+    from mxfp4_routed_expert_03_gb300.linear import Fp8Rows
+    s = Setup(T, 400, 264, seed=3, dtype=dtype)
+    codes = torch.full((T + 3, 512), 0x7F, dtype=torch.uint8, device="cuda")  # NaN wherever it is not a row
+    codes[:T, 16:416] = s.xq.view(torch.uint8)
+    scales = torch.full((T + 3, 9), float("nan"), device="cuda")
+    scales[:T, 2:6] = s.xs
+    out = torch.full((T + 2, 296), 7.0, dtype=dtype, device="cuda")
+    rows = Fp8Rows(codes.view(E4M3)[:, 16:416], scales[:, 2:6])
+    check(s.linear.forward(T, rows, out[:, 16:280]), "moe_linear_forward")
+    s.verify(out[:T, 16:280])
+    out[:T, 16:280] = 7.0
+    assert bool((out == 7.0).all())
+
+
+@pytest.mark.parametrize("T", [1, 12, 60, 150, 500])
+def test_what_is_not_finite_stays_where_it_belongs(T):
+    s = Setup(T, 640, 520, seed=4, dtype=torch.float32)
+    t, n = T // 2, 300
+    s.xq.view(torch.uint8)[t, 77] = 0x7F
+    s.wq.view(torch.uint8)[n, 130] = 0xFF
+    s.xs[T - 1, 4] = float("inf")
+    s.ws[3, 2] = float("nan")  # columns 384 .. 511
+    s.run()
+    ref, mag = product(s.xq, s.xs, s.wq, s.ws)
+    assert torch.equal(s.out.isfinite(), ref.isfinite())
+    fine = ref.isfinite()
+    assert bool(((s.out.double() - ref).abs() <= bound(ref, mag, 640, s.dtype))[fine].all())
+
+
+@pytest.mark.parametrize("T", [1, 16, 64, 333])
+def test_zero_scales_and_zero_codes(T):
+    s = Setup(T, 384, 256, seed=5)
+    s.xs.zero_()
+    s.run()
+    assert bool((s.out == 0).all())
+    s.xs.fill_(1.0)
+    s.xq.view(torch.uint8).fill_(0x80)  # negative zeros
+    s.run()
+    assert bool((s.out == 0).all())
+
+
+@pytest.mark.parametrize("T", [1, 8, 48, 100, 260, 900])
+def test_same_bits_again_and_in_any_batch(T):
+    """Repeated calls give the same bits; so do calls on two streams at a time."""
+    a = Setup(T, 2048, 1024, seed=6)
+    a.run()
+    first = a.out.clone()
+    other = Setup(T, 2048, 1024, seed=7)
+    other.run()
+    want = other.out.clone()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        a.out.fill_(0)
+        other.out.fill_(0)
+        torch.cuda.synchronize()
+        for _ in range(4):
+            a.run(streams[0])
+            other.run(streams[1])
+        torch.cuda.synchronize()
+        assert torch.equal(a.out, first) and torch.equal(other.out, want)
+
+
+@pytest.mark.parametrize("T", [1, 33, 300])
+def test_captured_and_replayed_with_changed_inputs(T):
+    """A graph reads the codes, scales and weights of the time of its replay."""
+    s = Setup(T, 1152, 640, seed=8)
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        s.run(st)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        s.run(torch.cuda.current_stream())
+    new = Setup(T, 1152, 640, seed=9)
+    for mine, fresh in ((s.xq, new.xq), (s.xs, new.xs), (s.wq, new.wq), (s.ws, new.ws)):
+        mine.view(torch.uint8).copy_(fresh.view(torch.uint8))
+    s.out.fill_(0)
+    graph.replay()
+    torch.cuda.synchronize()
+    s.verify()
+
+
+def test_weights_written_right_before_the_call_count():
+    """The weights' last writer may be the call before in the same stream."""
+    T, K, N = 4, 7168, 7168
+    s = Setup(T, K, N, seed=10)
+    new = Setup(T, K, N, seed=11)
+    new.run()
+    for _ in range(3):
+        s.wq.view(torch.uint8).zero_()
+        s.run()
+        assert bool((s.out == 0).all())
+        s.wq.view(torch.uint8).copy_(new.wq.view(torch.uint8))
+        s.ws.copy_(new.ws)
+        s.xq.view(torch.uint8).copy_(new.xq.view(torch.uint8))
+        s.xs.copy_(new.xs)
+        s.run()
+        torch.cuda.synchronize()
+        assert torch.equal(s.out, new.out)
+
+
+def test_no_tokens_and_refusals():
+    from mxfp4_routed_expert_03_gb300 import MOE_ERR_INVALID_ARG, moe_linear_forward
+    from mxfp4_routed_expert_03_gb300.linear import Fp8Rows, Linear
+    s = Setup(4, 256, 128, seed=12)
+    assert s.linear.forward(0, s.rows, s.out) == 0
+    assert bool((s.out == 7.0).all())
+    for bad in (s.out[:3], s.out[:, :64], s.out.half(), s.out.double(), s.out.cpu(), s.out.t()):
+        with pytest.raises(ValueError):
+            s.linear.forward(4, s.rows, bad)
+    with pytest.raises(ValueError):
+        s.linear.forward(5, s.rows, torch.empty(5, 128, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError):
+        s.linear.forward(4, Fp8Rows.empty(4, 240), s.out)
+    with pytest.raises(ValueError):
+        Fp8Rows(s.xq, s.xs[:, :1])
+    with pytest.raises(ValueError):
+        Fp8Rows(s.xq, s.xs.double())
+    with pytest.raises(ValueError):
+        Fp8Rows(s.xq.float(), s.xs)
+    with pytest.raises(ValueError):
+        Fp8Rows(s.xq, s.xs.cpu())
+    with pytest.raises(ValueError):
+        Linear(256, 128, s.wq[:, :128], s.ws)
+    with pytest.raises(ValueError):
+        Linear(256, 128, s.wq.cpu(), s.ws.cpu())
+    wide = torch.empty(4, 300, dtype=torch.bfloat16, device="cuda")
+    for out in (wide[:, 1:129], wide[:, :128]):  # unaligned base, row stride 300
+        assert s.linear.forward(4, s.rows, out) == MOE_ERR_INVALID_ARG
+    assert moe_linear_forward(s.linear.h, 4, s.rows.desc, s.out, 128, 2) == MOE_ERR_INVALID_ARG
+    s.run()
+    s.verify()
+
+
+@pytest.mark.parametrize("T", [1, 40, 100, 200, 600])
+def test_stall_times_out_then_recovers(T):
+    """With the test hook an MMA issuer waits, under a limit of 2e6 SM cycles, on a barrier that
+    nothing signals: the status is recorded, copies and products in flight end, tensor memory is
+    freed, and the next call is right. No GPU fault is involved."""
+    from mxfp4_routed_expert_03_gb300 import (MOE_ERR_DEVICE_TIMEOUT, MOE_ERR_INVALID_ARG, MOE_INJECT_ATTN_STALL,
+                                              MOE_INJECT_LINEAR_STALL, MOE_INJECT_NONE, check, moe_linear_set_fault_injection)
+    s = Setup(T, 2048, 1400, seed=13)
+    s.run()
+    clean = s.out.clone()
+    for mode, limit in ((7, 0), (MOE_INJECT_ATTN_STALL, 0), (MOE_INJECT_LINEAR_STALL, 1000)):
+        assert moe_linear_set_fault_injection(s.linear.h, mode, limit) == MOE_ERR_INVALID_ARG
+    check(moe_linear_set_fault_injection(s.linear.h, MOE_INJECT_LINEAR_STALL, 2_000_000), "inject")
+    for _ in range(2):
+        s.run()
+        assert s.linear.status() == MOE_ERR_DEVICE_TIMEOUT
+    check(moe_linear_set_fault_injection(s.linear.h, MOE_INJECT_NONE, 0), "inject off")
+    s.out.fill_(7.0)
+    s.run()
+    s.verify()
+    assert torch.equal(s.out, clean)
