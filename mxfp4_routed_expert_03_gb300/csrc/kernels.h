@@ -352,7 +352,12 @@ struct MoeLinearArgs {
     int inject;
 };
 cudaError_t moe_linear_setup();
-// Rows of x that one box of its tensor map holds, for T rows.
-int moe_linear_box_rows(int T, int K, int N, int nsm);
+// What a call's tensor maps hold: rows of x in a box of map_x, and whether map_w is the one with boxes of 64
+// weight rows (else 128).
+struct MoeLinearBox {
+    int x_rows;
+    bool w64;
+};
+MoeLinearBox moe_linear_box(int T, int K, int N, int nsm);
 cudaError_t moe_launch_linear(const CUtensorMap &map_w, const CUtensorMap &map_x,
                               const MoeLinearArgs &a, int nsm, cudaStream_t st);

@@ -16,7 +16,7 @@ struct moe_norm {
 struct moe_linear {
     moe_linear_desc desc;
     const float *w_s;
-    CUtensorMap map_w;
+    CUtensorMap map_w, map_w64;  // boxes of 128 and of 64 weight rows
     int device;
     int num_sms;
     int *status;  // device word: first error code recorded by a kernel
@@ -128,6 +128,8 @@ MOE_API int moe_linear_create(const moe_linear_desc *d, const uint8_t *w_q, cons
     l->timeout = kTimeoutCycles;
     if (!make_map_2d(&l->map_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_q, d->d_in, d->d_out, d->d_in, 128,
                      128) ||
+        !make_map_2d(&l->map_w64, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_q, d->d_in, d->d_out, d->d_in, 128,
+                     64) ||
         cudaMalloc(&l->status, sizeof(int)) != cudaSuccess) {
         free(l);
         return MOE_ERR_CUDA;
@@ -170,11 +172,12 @@ MOE_API int moe_linear_forward(moe_linear *l, int32_t T, const moe_fp8_rows *x, 
     g.status = l->status;
     g.timeout_cycles = l->timeout;
     g.inject = l->inject;
+    const MoeLinearBox box = moe_linear_box(T, d.d_in, d.d_out, l->num_sms);
     CUtensorMap map_x;
-    if (!make_map_2d(&map_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, x->q, d.d_in, T, x->q_stride, 128,
-                     moe_linear_box_rows(T, d.d_in, d.d_out, l->num_sms)))
+    if (!make_map_2d(&map_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, x->q, d.d_in, T, x->q_stride, 128, box.x_rows))
         return MOE_ERR_CUDA;
-    return moe_launch_linear(l->map_w, map_x, g, l->num_sms, (cudaStream_t)stream) == cudaSuccess
+    return moe_launch_linear(box.w64 ? l->map_w64 : l->map_w, map_x, g, l->num_sms, (cudaStream_t)stream) ==
+                   cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
 }
