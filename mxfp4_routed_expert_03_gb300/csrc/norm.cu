@@ -3,10 +3,13 @@
 //   h = bf16(x + r),  y = h / sqrt(mean(h^2) + eps) * w,
 //   per 128 columns s = max(max|y| / 448, 2^-126), code = e4m3(y / s)
 //
-// fp32 throughout. Bound: each of x, r, h, y moves 2 bytes an element, the codes 1.
-// A block owns a row and holds it in registers between the sum and the output: a
-// thread has chunks of 8 columns, a block's width apart, so that 16 neighbouring
-// lanes have a scale's 128 columns.
+// h exactly rounded, the rest in fp32. Bound: each of x, r, h, y moves 2 bytes an
+// element, the codes 1; beside that the instructions (about 10 an element).
+// Some warps of a block own a row and hold it in registers between the sum and the
+// output: a thread has CH chunks of 8 columns, the row's threads apart, so that 16
+// neighbouring lanes have a scale's 128 columns.
+// 8191 rows of 7168 with residual and codes: 65 us (6.3 TB/s of the 412 MB that have
+// to move); 4099 rows of 8192, codes alone: 20 us (5.1 TB/s).
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -15,8 +18,6 @@
 
 namespace {
 
-constexpr int kThreads = 256;
-
 // Two fp32 values to E4M3 (round to nearest even, saturating), the first in the low byte.
 __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
     uint16_t r;
@@ -24,93 +25,213 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
     return r;
 }
 
+// The larger of two values, NaN if one is.
+__device__ __forceinline__ float max_nan(float x, float y) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+
+// Sums of eight pairs of bf16 values, each rounded once.
+__device__ __forceinline__ uint4 add8(const uint4 &x, const uint4 &y) {
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&u[i]), *reinterpret_cast<const __nv_bfloat162 *>(&v[i]));
+        r[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// What a thread has of its row: chunk i is chunk tid + i * threads.
+struct Place {
+    int warps, tid, threads, sub, rows;  // warps of a row, this thread in it, the row of the block's `rows`
+    __device__ __forceinline__ explicit Place(int warps_) : warps(warps_) {
+        const int wid = threadIdx.x >> 5;
+        sub = wid / warps;
+        threads = 32 * warps;
+        tid = (wid - sub * warps) * 32 + (threadIdx.x & 31);
+        rows = blockDim.x / threads;
+    }
+};
+
+// Row t (none if chunks is 0) from its loaded chunks to its outputs. `part`: a word of shared memory per warp.
 template <int CH>
-__global__ void __launch_bounds__(kThreads) moe_norm_kernel(MoeNormArgs a) {
-    __shared__ float part[kThreads / 32];
-    const int64_t t = blockIdx.x;
-    const int tid = threadIdx.x, chunks = a.d / 8;
-    grid_dep_wait();
-    grid_dep_launch();
+__device__ __forceinline__ void row_out(const MoeNormArgs &a, const Place &p, int64_t t, int chunks, uint4 (&x)[CH],
+                                        const uint4 (&r)[CH], const uint4 (&w)[CH], float *part) {
+    const int lane = threadIdx.x & 31;
     float v[CH][8];
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-        const int c = tid + i * kThreads;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-        if (c >= chunks) continue;
-        rope::unpack8(*(const uint4 *)(a.x + t * a.x_stride + 8 * c), v[i]);
+        const int c = p.tid + i * p.threads;
         if (a.residual) {
-            float r[8];
-            rope::unpack8(*(const uint4 *)(a.residual + t * a.residual_stride + 8 * c), r);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] += r[j];
-            const uint4 h = rope::pack8(v[i]);
-            if (a.total) *(uint4 *)(a.total + t * a.total_stride + 8 * c) = h;
-            rope::unpack8(h, v[i]);  // the norm reads what is stored
+            x[i] = add8(x[i], r[i]);
+            if (a.total && c < chunks) *(uint4 *)(a.total + t * a.total_stride + 8 * c) = x[i];
         }
+        rope::unpack8(x[i], v[i]);  // (the norm reads what is stored)
+        if (a.weight) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+            for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+        }
     }
-    float inv = 1.f;
     if (a.weight) {
 #pragma unroll
         for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-        if ((tid & 31) == 0) part[tid >> 5] = ss;
-        __syncthreads();
-        ss = 0.f;
+        if (p.warps > 1) {
+            if (lane == 0) part[threadIdx.x >> 5] = ss;
+            __syncthreads();
+            ss = lane < p.warps ? part[p.sub * p.warps + lane] : 0.f;
 #pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) ss += part[i];
-        inv = rsqrtf(ss / (float)a.d + a.eps);
+            for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+        }
+        const float inv = rsqrtf(ss / (float)a.d + a.eps);
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            float u[8];
+            rope::unpack8(w[i], u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * inv * u[j];
+        }
     }
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-        const int c = tid + i * kThreads;
-        if (a.weight && c < chunks) {
-            float w[8];
-            rope::unpack8(*(const uint4 *)(a.weight + 8 * c), w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * inv * w[j];
-        }
+        const int c = p.tid + i * p.threads;
         if (a.y && c < chunks) *(uint4 *)(a.y + t * a.y_stride + 8 * c) = rope::pack8(v[i]);
         if (!a.q) continue;
-        // the block's largest magnitude by its bits: NaN is above infinity, and both above all else
-        uint32_t m = 0u;
+        float m = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[i][j]) & 0x7FFFFFFFu);
+        for (int j = 0; j < 8; ++j) m = max_nan(m, fabsf(v[i][j]));
 #pragma unroll
-        for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        for (int o = 8; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
         if (c >= chunks) continue;
-        const float s = fmaxf(__uint_as_float(m) / 448.f, 1.17549435e-38f), r = 1.f / s;
+        // (a reciprocal within an ulp: of the quotient's rounding to 4 bits that is 2^-19)
+        const float s = fmaxf(m * (1.f / 448.f), 1.17549435e-38f);
+        float f;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(s));
         uint32_t q[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-            q[k] = to_e4m3x2(v[i][4 * k] * r, v[i][4 * k + 1] * r) |
-                   to_e4m3x2(v[i][4 * k + 2] * r, v[i][4 * k + 3] * r) << 16;
+            q[k] = to_e4m3x2(v[i][4 * k] * f, v[i][4 * k + 1] * f) | to_e4m3x2(v[i][4 * k + 2] * f, v[i][4 * k + 3] * f) << 16;
         *(uint2 *)(a.q + t * a.q_stride + 8 * c) = make_uint2(q[0], q[1]);
-        if ((c & 15) == 0)
-            a.s[t * a.s_stride + c / 16] = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : s;
+        if ((c & 15) == 0)  // (m is not below infinity: it is that, or NaN)
+            a.s[t * a.s_stride + c / 16] = m < __uint_as_float(0x7F800000u) ? s : __uint_as_float(0x7FC00000u);
     }
 }
 
+// Few rows: a block has each of its rows once.
+template <int CH>
+__global__ void __launch_bounds__(1024) moe_norm_kernel(MoeNormArgs a, int warps) {
+    __shared__ float part[32];
+    const Place p(warps);
+    const int64_t t = (int64_t)blockIdx.x * p.rows + p.sub;
+    const int chunks = t < a.T ? a.d / 8 : 0;
+    grid_dep_wait();
+    grid_dep_launch();
+    uint4 x[CH], r[CH], w[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int c = p.tid + i * p.threads;
+        x[i] = r[i] = w[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (c >= chunks) continue;
+        x[i] = *(const uint4 *)(a.x + t * a.x_stride + 8 * c);
+        if (a.residual) r[i] = *(const uint4 *)(a.residual + t * a.residual_stride + 8 * c);
+        if (a.weight) w[i] = *(const uint4 *)(a.weight + 8 * c);
+    }
+    row_out<CH>(a, p, t, chunks, x, r, w, part);
+}
+
+__device__ __forceinline__ void cp_async_16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+                 : "memory");
+}
+
+// Many rows: a block goes through rows with the next one on its way (two: 72 us instead of 65 for the 8191 rows
+// above; four chunks a thread: 87, half as many warps fit). A thread copies what it will read itself, so
+// nothing has to be waited for but its own copies.
+constexpr int CH_STREAM = 2, STAGES = 2;
+
+__global__ void __launch_bounds__(1024) moe_norm_stream_kernel(MoeNormArgs a, int warps) {
+    constexpr int CH = CH_STREAM;
+    extern __shared__ uint4 ring[];  // [STAGES][CH][x, residual][thread]
+    __shared__ float part[2][32];
+    const Place p(warps);
+    const int64_t step = (int64_t)gridDim.x * p.rows;
+    const int chunks = a.d / 8, per = a.residual ? 2 : 1, n = blockDim.x;
+    uint4 *mine = ring + threadIdx.x;
+    grid_dep_wait();
+    grid_dep_launch();
+    uint4 w[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int c = p.tid + i * p.threads;
+        w[i] = a.weight && c < chunks ? *(const uint4 *)(a.weight + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    auto fetch = [&](int64_t t, int s) {
+        if (t < a.T) {
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                const int c = p.tid + i * p.threads;
+                if (c >= chunks) continue;
+                cp_async_16(mine + (s * CH + i) * per * n, a.x + t * a.x_stride + 8 * c);
+                if (a.residual) cp_async_16(mine + ((s * CH + i) * per + 1) * n, a.residual + t * a.residual_stride + 8 * c);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int64_t t = (int64_t)blockIdx.x * p.rows + p.sub;
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) fetch(t + s * step, s);
+    // (all rows of a block in as many turns, so that its threads meet at the sums)
+    const int64_t turns = (a.T - (int64_t)blockIdx.x * p.rows + step - 1) / step;
+    int s = 0, into = STAGES - 1;
+    for (int64_t k = 0; k < turns; ++k, t += step) {
+        fetch(t + (STAGES - 1) * step, into);
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+        const int live = t < a.T ? chunks : 0;
+        uint4 x[CH], r[CH];
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            x[i] = r[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (p.tid + i * p.threads >= live) continue;
+            x[i] = mine[(s * CH + i) * per * n];
+            if (a.residual) r[i] = mine[((s * CH + i) * per + 1) * n];
+        }
+        row_out<CH>(a, p, t, live, x, r, w, part[k & 1]);
+        s = s + 1 == STAGES ? 0 : s + 1;
+        into = into + 1 == STAGES ? 0 : into + 1;
+    }
+}
+
+int warps_of(int d, int ch) { return (d / 8 + 32 * ch - 1) / (32 * ch); }
+
 template <int CH>
 cudaError_t launch(const MoeNormArgs &a, cudaStream_t st) {
-    return launch_pdl_ready(moe_norm_kernel<CH>, dim3((unsigned)a.T), dim3(kThreads), 0, st, a);
+    const int warps = warps_of(a.d, CH), rows = a.T > 1 && warps < 8 ? 8 / warps : 1;
+    return launch_pdl_ready(moe_norm_kernel<CH>, dim3((unsigned)((a.T + rows - 1) / rows)), dim3(32 * warps * rows), 0, st, a, warps);
+}
+
+cudaError_t launch_stream(const MoeNormArgs &a, int nsm, cudaStream_t st) {
+    const int warps = warps_of(a.d, CH_STREAM), rows = warps < 8 ? 8 / warps : 1, threads = 32 * warps * rows;
+    const int smem = STAGES * CH_STREAM * (a.residual ? 2 : 1) * threads * 16;
+    // (the registers of 1024 threads on an SM, and at most 128 KB of rows)
+    const int64_t blocks = (a.T + rows - 1) / rows, most = (int64_t)nsm * (1024 / threads);
+    return launch_pdl_ready(moe_norm_stream_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(threads), smem, st, a, warps);
 }
 
 }  // namespace
 
 cudaError_t moe_norm_setup() {
-    const void *kernels[] = {(const void *)moe_norm_kernel<1>, (const void *)moe_norm_kernel<2>,
-                             (const void *)moe_norm_kernel<4>, (const void *)moe_norm_kernel<8>};
-    for (const void *k : kernels) {
-        const cudaError_t err = set_kernel(k);
-        if (err != cudaSuccess) return err;
-    }
-    return cudaSuccess;
+    cudaError_t err = set_kernel((const void *)moe_norm_kernel<1>);
+    if (err == cudaSuccess) err = set_kernel((const void *)moe_norm_kernel<2>);
+    if (err == cudaSuccess) err = set_kernel((const void *)moe_norm_stream_kernel, STAGES * CH_STREAM * 2 * 1024 * 16);
+    return err;
 }
 
 cudaError_t moe_launch_norm(const MoeNormArgs &a, int nsm, cudaStream_t st) {
-    const int per = (a.d / 8 + kThreads - 1) / kThreads;
-    return per <= 1 ? launch<1>(a, st) : per <= 2 ? launch<2>(a, st) : per <= 4 ? launch<4>(a, st) : launch<8>(a, st);
+    // few rows: latency counts (16 rows of 7168 2.8 and 2.9 us, 300 of 1024 2.0 and 2.5, 1216 of 1024 3.7 and 4.0;
+    // the rule changes at 8 K elements an SM; 304 of 7168 5.6 and 5.2)
+    if ((int64_t)a.T * a.d > (int64_t)nsm * 8192) return launch_stream(a, nsm, st);
+    return a.d <= 8192 ? launch<1>(a, st) : launch<2>(a, st);
 }
