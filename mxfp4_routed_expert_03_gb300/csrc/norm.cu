@@ -142,11 +142,6 @@ __global__ void __launch_bounds__(1024) moe_norm_kernel(MoeNormArgs a, int warps
     row_out<CH>(a, p, t, chunks, x, r, w, part);
 }
 
-__device__ __forceinline__ void cp_async_16(void *dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
-                 : "memory");
-}
-
 // Many rows: a block goes through rows with the next one on its way (two: 72 us instead of 65 for the 8191 rows
 // above; four chunks a thread: 87, half as many warps fit). A thread copies what it will read itself, so
 // nothing has to be waited for but its own copies.
@@ -178,7 +173,7 @@ __global__ void __launch_bounds__(1024) moe_norm_stream_kernel(MoeNormArgs a, in
                 if (a.residual) cp_async_16(mine + ((s * CH + i) * per + 1) * n, a.residual + t * a.residual_stride + 8 * c);
             }
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        cp_async_commit();
     };
     int64_t t = (int64_t)blockIdx.x * p.rows + p.sub;
 #pragma unroll
@@ -188,7 +183,7 @@ __global__ void __launch_bounds__(1024) moe_norm_stream_kernel(MoeNormArgs a, in
     int s = 0, into = STAGES - 1;
     for (int64_t k = 0; k < turns; ++k, t += step) {
         fetch(t + (STAGES - 1) * step, into);
-        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+        cp_async_wait<STAGES - 1>();
         const int live = t < a.T ? chunks : 0;
         uint4 x[CH], r[CH];
 #pragma unroll

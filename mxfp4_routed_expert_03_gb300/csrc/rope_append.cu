@@ -5,7 +5,8 @@
 // bf16, then per 32 elements that of kv_cache.cu (kv_block.cuh): the same bits as
 // the two calls, without the keys' way through memory. Bound: 2 bytes read per
 // element, 2 written for queries and 17/32 for keys and values; 8191 tokens of 56
-// query and 8 + 8 key and value heads of 128 52 us (5.3 TB/s of the 277 MB).
+// query and 8 + 8 key and value heads of 128 49 us (5.7 TB/s of the 277 MB; 56.6
+// with ordinary loads, see cp_async_16).
 //
 // A warp has one of three kinds of task: TOK tokens' keys of one head (normed and
 // rotated in two passes of the row layout, exchanged through 2 KB of shared memory
@@ -20,6 +21,8 @@ namespace {
 
 constexpr int kWarps = 4;
 
+// A warp's query rows: P passes of 32 / (D / 16) of them, all on their way to shared memory at once, each
+// lane copying the chunks that it reads itself.
 template <int D, int P>
 __global__ void __launch_bounds__(32 * kWarps)
     moe_rope_append_kernel(MoeRopeArgs a, MoeKvArgs c, int groups, uint32_t kv_tasks) {
@@ -27,10 +30,12 @@ __global__ void __launch_bounds__(32 * kWarps)
     constexpr int HP = 32 / TPH;           // head rows per warp and pass
     constexpr int NB = D / 32;             // blocks of a head row
     constexpr int TOK = 32 / NB;           // tokens of a key or value task
-    static_assert(TOK == 2 * HP, "two passes per key task");
-    __shared__ uint4 stage[kWarps][TOK * D / 8];
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    uint32_t task = blockIdx.x * kWarps + wid;
+    static_assert(TOK == 2 * HP && TOK * D / 8 == 128, "two passes per key task");
+    static_assert(P * 64 <= 256, "room for the rows");
+    __shared__ uint4 space[kWarps][256];
+    const int lane = threadIdx.x & 31;
+    uint4 *mine = space[threadIdx.x >> 5] + lane;
+    uint32_t task = blockIdx.x * kWarps + (threadIdx.x >> 5);
     const rope::Lane l(lane % TPH, a.rope_dim);
     grid_dep_wait();
     grid_dep_launch();
@@ -41,41 +46,48 @@ __global__ void __launch_bounds__(32 * kWarps)
         // the block that this lane writes: block b of token `tok`
         const int b = lane / 8 % NB, to = lane / (8 * NB) * 8 + lane % 8, tok = first + to;
         int slot = -1, at = 0;
-        if (tok < c.n) {
-            slot = c.slots[tok];
-            if (a.rope_dim > 0) at = a.positions[tok];
-        }
         uint32_t w[16];
         if (is_v) {
             if (tok >= c.n) return;
-            const uint4 *src = (const uint4 *)(c.v + (int64_t)tok * c.v_stride + head * D + 32 * b);
+            const uint16_t *src = c.v + (int64_t)tok * c.v_stride + head * D + 32 * b;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) cp_async_16(mine + 32 * i, src + 8 * i);
+            cp_async_commit();
+            slot = c.slots[tok];
+            if (a.rope_dim > 0) at = a.positions[tok];
+            cp_async_wait<0>();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint4 x = src[i];
+                const uint4 x = mine[32 * i];
                 w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
             }
         } else {
-            uint4 raw[2][2];
             int pos[2];
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 const int t = first + p * HP + lane / TPH;
-                raw[p][0] = raw[p][1] = make_uint4(0u, 0u, 0u, 0u);
                 pos[p] = 0;
+                mine[64 * p] = mine[64 * p + 32] = make_uint4(0u, 0u, 0u, 0u);
                 if (t < c.n) {
                     const uint16_t *src = a.k + (int64_t)t * a.k_stride + head * D;
-                    raw[p][0] = *(const uint4 *)(src + 8 * l.c0);
-                    raw[p][1] = *(const uint4 *)(src + 8 * l.c1);
+                    cp_async_16(mine + 64 * p, src + 8 * l.c0);
+                    cp_async_16(mine + 64 * p + 32, src + 8 * l.c1);
                     if (a.rope_dim > 0) pos[p] = a.positions[t];
                 }
             }
-            uint4 *mine = stage[wid];
+            cp_async_commit();
+            if (tok < c.n) {
+                slot = c.slots[tok];
+                if (a.rope_dim > 0) at = a.positions[tok];
+            }
+            cp_async_wait<0>();
+            uint4 *stage = space[threadIdx.x >> 5] + 128;  // [TOK rows][D / 8 chunks]
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 const int r = p * HP + lane / TPH;
                 float x[8], y[8], cs[8], sn[8];
-                rope::unpack8(raw[p][0], x);
-                rope::unpack8(raw[p][1], y);
+                rope::unpack8(mine[64 * p], x);
+                rope::unpack8(mine[64 * p + 32], y);
                 const float ss = rope::row_squares<D>(x, y);
                 // (rows of a bad position turn by position 0 and are not written below)
                 const bool ok = pos[p] >= 0 && pos[p] < a.n_pos;
@@ -84,13 +96,13 @@ __global__ void __launch_bounds__(32 * kWarps)
                 if (turned.turn) rope::load_angles(a, l, pos[p], cs, sn);
                 rope::norm_turn<D>(a, turned, a.k_weight, ss, cs, sn, x, y);
                 // 16-byte chunks permuted by the row, so that neither side's accesses collide
-                mine[r * (D / 8) + (l.c0 ^ (r & 7))] = rope::pack8(x);
-                mine[r * (D / 8) + (l.c1 ^ (r & 7))] = rope::pack8(y);
+                stage[r * (D / 8) + (l.c0 ^ (r & 7))] = rope::pack8(x);
+                stage[r * (D / 8) + (l.c1 ^ (r & 7))] = rope::pack8(y);
             }
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint4 x = mine[to * (D / 8) + ((4 * b + i) ^ (to & 7))];
+                const uint4 x = stage[to * (D / 8) + ((4 * b + i) ^ (to & 7))];
                 w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
             }
             if (tok >= c.n) return;
@@ -108,29 +120,31 @@ __global__ void __launch_bounds__(32 * kWarps)
     const int64_t t = token;
     const int row0 = group * P * HP + lane / TPH;
     const int pos = a.rope_dim > 0 ? a.positions[t] : 0;  // (in flight beside the rows)
-    uint4 raw[P][2];
 #pragma unroll
     for (int p = 0; p < P; ++p) {
         const int r = row0 + p * HP;
-        raw[p][0] = raw[p][1] = make_uint4(0u, 0u, 0u, 0u);
         if (r < a.n_q) {
             const uint16_t *src = a.q + t * a.q_stride + (int64_t)r * D;
-            raw[p][0] = *(const uint4 *)(src + 8 * l.c0);
-            raw[p][1] = *(const uint4 *)(src + 8 * l.c1);
+            cp_async_16(mine + 64 * p, src + 8 * l.c0);
+            cp_async_16(mine + 64 * p + 32, src + 8 * l.c1);
         }
     }
+    cp_async_commit();
     if (a.rope_dim > 0 && (pos < 0 || pos >= a.n_pos)) {
         if (lane == 0 && group == 0) moe_flag(a.status, MOE_ERR_BAD_INDEX);
+        cp_async_wait<0>();
         return;
     }
     float cs[8], sn[8];
     if (l.turn) rope::load_angles(a, l, pos, cs, sn);
+    cp_async_wait<0>();
 #pragma unroll
     for (int p = 0; p < P; ++p) {
         const int r = row0 + p * HP;
         float x[8], y[8];
-        rope::unpack8(raw[p][0], x);
-        rope::unpack8(raw[p][1], y);
+        // (rows that are not there hold what was in shared memory, and end here)
+        rope::unpack8(mine[64 * p], x);
+        rope::unpack8(mine[64 * p + 32], y);
         const float ss = rope::row_squares<D>(x, y);
         if (r >= a.n_q) continue;
         rope::norm_turn<D>(a, l, a.q_weight, ss, cs, sn, x, y);
@@ -150,20 +164,19 @@ cudaError_t launch(const MoeRopeArgs &a, const MoeKvArgs &c, cudaStream_t st) {
                             dim3(32 * kWarps), 0, st, a, c, groups > 0 ? groups : 1, kv_tasks);
 }
 
-// Query rows of a warp: one pass for few tokens (as qk_rope.cu), else five: a warp's loads are what is in flight,
-// and its cosines and sines serve them all (8191 tokens of 56 + 16 heads of 128: 2 passes 56.6 us, 4 60.8, 5 52.1,
-// 7 59.3; 7000 of 64 + 16: 54.4, 58.0, 51.9, 58.2).
+// Query rows of a warp: one pass for few tokens (as qk_rope.cu), else four (8191 tokens of 56 + 16 heads of 128: 2
+// passes 50.9 us, 4 48.9, 8 51.4; 7000 of 64 + 16 53.8, 54.5, 59.5; 400 of 56 + 16 5.2, 4.9, 6.1).
 template <int D>
 cudaError_t launch(const MoeRopeArgs &a, const MoeKvArgs &c, int nsm, cudaStream_t st) {
-    return (int64_t)c.n * a.n_q < (int64_t)nsm * 64 ? launch<D, 1>(a, c, st) : launch<D, 5>(a, c, st);
+    return (int64_t)c.n * a.n_q < (int64_t)nsm * 64 ? launch<D, 1>(a, c, st) : launch<D, 4>(a, c, st);
 }
 
 }  // namespace
 
 cudaError_t moe_rope_append_setup() {
     const void *kernels[] = {
-        (const void *)moe_rope_append_kernel<64, 1>, (const void *)moe_rope_append_kernel<64, 5>,
-        (const void *)moe_rope_append_kernel<128, 1>, (const void *)moe_rope_append_kernel<128, 5>};
+        (const void *)moe_rope_append_kernel<64, 1>, (const void *)moe_rope_append_kernel<64, 4>,
+        (const void *)moe_rope_append_kernel<128, 1>, (const void *)moe_rope_append_kernel<128, 4>};
     for (const void *k : kernels) {
         const cudaError_t err = set_kernel(k);
         if (err != cudaSuccess) return err;
