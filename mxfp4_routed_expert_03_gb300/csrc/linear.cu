@@ -94,15 +94,15 @@ __device__ __forceinline__ Ring after(Ring r, int n) {
     return r;
 }
 
-// A CTA's part of a tile, [128 rows][pitch] fp32 in `stage`, goes to the CTAs that join 128 / S of its rows
-// each: into their `recv` area [S][128 / S][pitch], counted on their `bar`. For one thread, once every CTA of the
-// cluster has its barriers ready.
-__device__ __forceinline__ void send_parts(const float *stage, float *recv, uint64_t *bar, int S, int rank, int pitch) {
-    const int n = 128 / S * pitch;
-    for (int i = 0; i < S; ++i) {
-        const int to = (rank + i) % S;
-        tc::bulk_copy_s2peer(tc::peer_addr(recv + rank * n, to), stage + to * n, n * 4, tc::peer_addr(bar, to));
-    }
+// A CTA's part of a tile, [rows][pitch] fp32 in `stage`, goes to the CTAs of the cluster that join `per` of its
+// rows each, rank 0 the first: into their `recv` area [S][per][pitch], counted on their `bar`. By one warp, once
+// every CTA of the cluster has its barriers ready.
+__device__ __forceinline__ void send_parts(const float *stage, float *recv, uint64_t *bar, int S, int rank, int rows, int per,
+                                           int pitch, int lane) {
+    const int to = (rank + lane) % S, n = min(per, rows - to * per);
+    if (lane < S && n > 0)
+        tc::bulk_copy_s2peer(tc::peer_addr(recv + rank * per * pitch, to), stage + to * per * pitch, n * pitch * 4, tc::peer_addr(bar, to));
+    __syncwarp();
 }
 
 // Four sums of S received parts, `step` apart, in the order of the ranks.
@@ -452,8 +452,7 @@ __global__ void __launch_bounds__(Wide::THREADS, 1)
             tc::fence_proxy_async_smem();
             ok = tc::bar_and(1, 256, ok);
             tc::cluster_wait();  // (1)
-            if (ok && warp == 4 && tc::elect_one()) send_parts((const float *)smem, parts, recv, S, rank, C::PITCH);
-            __syncwarp();
+            if (ok && warp == 4) send_parts((const float *)smem, parts, recv, S, rank, 128, 128 / S, C::PITCH, lane);
             ok = ok && tc::mbar_wait_warp(recv, 0, LIMIT, abort_p);
             if (!ok && lane == 0) fail();
         }
@@ -737,15 +736,15 @@ struct Narrow {
     static constexpr int STAGES = NT <= 16 ? 5 : NT <= 32 ? 4 : 3;  // and TMEM accumulators
     static constexpr int TMEM_COLS = STAGES * NT <= 128 ? 128 : 256;
     static constexpr int G = 32 * EW / NT;                 // blocks whose scales are fetched at a time, one per thread
-    static constexpr int PITCH = NT + 4;                   // row of a part (banks)
+    static constexpr int PITCH = 132;                      // row of a part: 128 weight rows and a gap (banks)
     static constexpr int SC_BASE = STAGES * STAGE_BYTES;   // scales [2][G][NT]
-    static constexpr int RECV = SC_BASE + 2 * G * NT * 4;  // parts [split][128 / split][PITCH]
-    static constexpr int BAR = RECV + 128 * PITCH * 4;
+    static constexpr int RECV = SC_BASE + 2 * G * NT * 4;  // parts [split][NT / split][PITCH]
+    static constexpr int BAR = RECV + NT * PITCH * 4;
     static constexpr int BYTES = 1024 + BAR + 256;
     static_assert(NT * G == 32 * EW && STAGES * NT <= TMEM_COLS, "scale loads, accumulators");
     static_assert((2 * STAGES + 3) * 8 + 12 <= 256, "barrier area");
     static_assert(2 * (BYTES + 1024) <= 233472, "two CTAs on an SM");
-    static_assert(128 * PITCH * 4 <= SC_BASE && RECV % 16 == 0, "a part fits over the ring");
+    static_assert(NT * PITCH * 4 <= SC_BASE && RECV % 16 == 0, "a part fits over the ring");
 };
 
 }  // namespace
@@ -772,6 +771,7 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, 2)
     const int n0 = tile % NTILES * 128, t0 = tile / NTILES * NT;
     const int kb0 = KB * rank / S, nkb = KB * (rank + 1) / S - kb0;
     const int rows = min(NT, args.T - t0);
+    const int per = NT / S, mine = min(per, rows - rank * per);  // rows of x that a CTA joins, that this one does
     if (tid == 0) {
         *abort_flag = 0;
         *s_issued = 0;
@@ -783,7 +783,7 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, 2)
         tc::mbar_init(drain, 1);
         tc::mbar_init(never, 1);
         tc::fence_mbar_init();
-        if (S > 1) tc::mbar_arrive_expect_tx(recv, 128 * C::PITCH * 4);
+        if (S > 1 && mine > 0) tc::mbar_arrive_expect_tx(recv, S * mine * C::PITCH * 4);
         tc::prefetch_map(&mW);
         tc::prefetch_map(&mX);
         // the first stages' weights on their way to L2 while the kernel before ends
@@ -896,10 +896,10 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, 2)
         }
         if (S > 1) {
             if (ok) {  // over the ring, all of whose copies and MMAs are done
-                float *o = (float *)smem + row * C::PITCH + col0;
+                float *o = (float *)smem + col0 * C::PITCH + row;
 #pragma unroll
-                for (int j = 0; j < C::COLS / 2; j += 2)
-                    *(float4 *)(o + 2 * j) = make_float4(sum[j].x, sum[j].y, sum[j + 1].x, sum[j + 1].y);
+                for (int j = 0; j < C::COLS; ++j)
+                    if (col0 + j < rows) o[j * C::PITCH] = j & 1 ? sum[j / 2].y : sum[j / 2].x;
             }
             tc::fence_proxy_async_smem();
             ok = tc::bar_and(1, 32 * C::EW, ok);
@@ -915,25 +915,18 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, 2)
     if (S > 1) {
         tc::cluster_wait();  // (1)
         if (warp >= 2) {
-            if (ok && warp == 2 && tc::elect_one()) send_parts((const float *)smem, parts, recv, S, rank, C::PITCH);
-            __syncwarp();
-            ok = ok && tc::mbar_wait_warp(recv, 0, LIMIT, abort_p);
+            if (ok && warp == 2) send_parts((const float *)smem, parts, recv, S, rank, rows, per, C::PITCH, lane);
+            ok = ok && (mine <= 0 || tc::mbar_wait_warp(recv, 0, LIMIT, abort_p));
             if (!ok && lane == 0) fail();
             __syncwarp();
         }
         tc::cluster_arrive();  // (2: this CTA has the parts of its rows)
         if (warp >= 2 && ok) {
-            // lanes along the weight rows, four rows of x each
-            const int R = 128 / S, lg = 31 - __clz(R);
-            for (int u = tid - 64; u < R * ((rows + 3) / 4); u += 32 * C::EW) {
-                const int r = u & (R - 1), j = (u >> lg) * 4, n = n0 + rank * R + r;
-                const float4 v = join(parts + r * C::PITCH + j, R * C::PITCH, S);
-                const int64_t to = (t0 + j) * args.out_stride + n;
-                if (n >= args.N) continue;
-                store1(args, to, v.x);
-                if (j + 1 < rows) store1(args, to + args.out_stride, v.y);
-                if (j + 2 < rows) store1(args, to + 2 * args.out_stride, v.z);
-                if (j + 3 < rows) store1(args, to + 3 * args.out_stride, v.w);
+            for (int u = tid - 64; u < mine * 32; u += 32 * C::EW) {
+                const int j = u / 32, n = n0 + u % 32 * 4;
+                if (n < args.N)
+                    store4(args, (int64_t)(t0 + rank * per + j) * args.out_stride + n,
+                           join(parts + j * C::PITCH + u % 32 * 4, per * C::PITCH, S));
             }
         }
         __syncwarp();
