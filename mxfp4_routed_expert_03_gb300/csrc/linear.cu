@@ -89,11 +89,6 @@ struct Ring {
     }
 };
 
-__device__ __forceinline__ Ring after(Ring r, int n) {
-    r.next(n);
-    return r;
-}
-
 // A CTA's part of a tile, [rows][pitch] fp32 in `stage`, goes to the CTAs of the cluster that join `per` of its
 // rows each, rank 0 the first: into their `recv` area [S][per][pitch], counted on their `bar`. By one warp, once
 // every CTA of the cluster has its barriers ready.
@@ -183,44 +178,59 @@ __device__ __forceinline__ bool load_scales(const MoeLinearArgs &args, float *xs
 }
 
 // A warp's sums over nkb blocks of 32 rows x 2 N2 columns: sum += accumulator * scale, block by block. TMEM is
-// read 32 columns ahead of the additions, the next block's barrier is tested and its scale read ahead of
-// their use (all of these in turn: 8191 rows of 7168 x 9216 467 us instead of 432).
+// read 64 columns ahead of the additions, the next block's barrier is tested and its scale read ahead of
+// their use (all of these in turn: 8191 rows of 7168 x 9216 467 us instead of 421; 32 columns ahead: 434).
 //   acc()           the current block's columns in TMEM
-//   wait(), test()  waits for the current block's MMAs, false: given up; whether the next block's are finished
+//   wait(), test()  waits for the current block's MMAs, false: given up; whether they are finished
 //   drained()       its accumulator has been read: on to the next block
 //   scale(kb, f)    block kb's factors of the thread's row and of the columns; false: given up
 template <int N2, typename Acc, typename Test, typename Wait, typename Drained, typename Scale>
 __device__ __forceinline__ bool add_blocks(float2 (&sum)[N2], int nkb, Acc acc, Test test, Wait wait, Drained drained,
                                            Scale scale) {
-    constexpr int P = N2 / 16;
+    constexpr int P = N2 / 16;  // pieces of 32 columns, in pairs
     uint32_t r[2][32];
     float2 f, next;
     if (!scale(0, f) || !wait()) return false;
     tc::tc_fence_after();
     tc::tmem_ld_32x32b_x32(acc(), r[0]);
+    tc::tmem_ld_32x32b_x32(acc() + 32, r[1]);
     for (int kb = 0; kb < nkb; ++kb) {
         const bool more = kb + 1 < nkb;
-        bool ready = false;
         if (more && !scale(kb + 1, next)) return false;
         const float factor = f.x * f.y;
+        const auto add = [&](int p) {
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
+            for (int j = 0; j < 16; ++j) fma2(sum[16 * p + j], r[p & 1][2 * j], r[p & 1][2 * j + 1], factor, factor);
+        };
+#pragma unroll
+        for (int p = 0; p < P; p += 2) {
             tc::tmem_ld_wait();
-            if (p + 1 < P) {
-                tc::tmem_ld_32x32b_x32(acc() + 32 * (p + 1), r[(p + 1) & 1]);
+            if (p + 2 < P) {
+                add(p);
+                tc::tmem_ld_32x32b_x32(acc() + 32 * (p + 2), r[0]);
+                add(p + 1);
+                tc::tmem_ld_32x32b_x32(acc() + 32 * (p + 3), r[1]);
             } else {
                 tc::tc_fence_before();
                 __syncwarp();
                 drained();
-                if (more) {
-                    if (!__all_sync(0xFFFFFFFFu, ready) && !wait()) return false;
+                const bool ready = more && test();
+                add(p);
+                if (__all_sync(0xFFFFFFFFu, ready)) {
                     tc::tc_fence_after();
                     tc::tmem_ld_32x32b_x32(acc(), r[0]);
+                    add(p + 1);
+                    tc::tmem_ld_32x32b_x32(acc() + 32, r[1]);
+                } else {
+                    add(p + 1);
+                    if (more) {
+                        if (!wait()) return false;
+                        tc::tc_fence_after();
+                        tc::tmem_ld_32x32b_x32(acc(), r[0]);
+                        tc::tmem_ld_32x32b_x32(acc() + 32, r[1]);
+                    }
                 }
             }
-            if (p == P - 2 && more) ready = test();
-#pragma unroll
-            for (int j = 0; j < 16; ++j) fma2(sum[16 * p + j], r[p & 1][2 * j], r[p & 1][2 * j + 1], factor, factor);
         }
         f = next;
     }
@@ -417,7 +427,7 @@ __global__ void __launch_bounds__(Wide::THREADS, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) sum[j] = make_float2(0.f, 0.f);
             ok = add_blocks(
-                sum, nkb, [&] { return acc + at.s * BN; }, [&] { return tc::mbar_test_wait(&done[after(at, C::STAGES).s], after(at, C::STAGES).par); },
+                sum, nkb, [&] { return acc + at.s * BN; }, [&] { return tc::mbar_test_wait(&done[at.s], at.par); },
                 [&] { return tc::mbar_wait_warp(&done[at.s], at.par, LIMIT, abort_p); },
                 [&] {
                     if (lane == 0) tc::mbar_arrive(&full[at.s]);
@@ -676,7 +686,7 @@ __global__ void __launch_bounds__(Pair::THREADS, 1)
 #pragma unroll
             for (int j = 0; j < 64; ++j) sum[j] = make_float2(0.f, 0.f);
             ok = add_blocks(
-                sum, KB, [&] { return acc + (i & 1) * 256; }, [&] { return tc::mbar_test_wait(&mine[after(at, C::STAGES).s], after(at, C::STAGES).par); },
+                sum, KB, [&] { return acc + (i & 1) * 256; }, [&] { return tc::mbar_test_wait(&mine[at.s], at.par); },
                 [&] { return tc::mbar_wait_warp(&mine[at.s], at.par, LIMIT, abort_p); },
                 [&] {
                     if (lane == 0) tc::peer_arrive(told + 8 * (half ? i & 1 : ahead.s));
@@ -951,7 +961,7 @@ namespace {
 //   4096 x 5120 13.4 and 12.5, but of 2048 x 6144 8.8 and 10.2), and by 8 and 4 only where the clusters fit beside
 //   each other (1000 columns of 4096: 128 rows by 8 8.2, by 4 9.3; 200 rows by 8 14.1, by 4 9.4).
 //   Very many: a wave of pairs takes about 1.5 times a wave of the others (512 rows of 7168 x 9216: 1 wave 32, the
-//   others 2 waves 37; 768 rows: 2 waves 57, 3 waves 53; 8191 rows: 432 and 500).
+//   others 2 waves 37; 768 rows: 2 waves 57, 3 waves 53; 8191 rows: 421 and 500).
 struct Plan {
     int nt;     // rows of x per tile of the few-row kernel; 0: the others
     bool pair;  // the CTA pairs' kernel
