@@ -179,7 +179,7 @@ __device__ __forceinline__ bool load_scales(const MoeLinearArgs &args, float *xs
 
 // A warp's sums over nkb blocks of 32 rows x 2 N2 columns: sum += accumulator * scale, block by block. TMEM is
 // read 64 columns ahead of the additions, the next block's barrier is tested and its scale read ahead of
-// their use (all of these in turn: 8191 rows of 7168 x 9216 467 us instead of 421; 32 columns ahead: 434).
+// their use (all of these in turn: 8191 rows of 7168 x 9216 467 us instead of 367; 32 columns ahead: 434).
 //   acc()           the current block's columns in TMEM
 //   wait(), test()  waits for the current block's MMAs, false: given up; whether they are finished
 //   drained()       its accumulator has been read: on to the next block
@@ -196,7 +196,6 @@ __device__ __forceinline__ bool add_blocks(float2 (&sum)[N2], int nkb, Acc acc, 
     tc::tmem_ld_32x32b_x32(acc() + 32, r[1]);
     for (int kb = 0; kb < nkb; ++kb) {
         const bool more = kb + 1 < nkb;
-        if (more && !scale(kb + 1, next)) return false;
         const float factor = f.x * f.y;
         const auto add = [&](int p) {
 #pragma unroll
@@ -215,6 +214,9 @@ __device__ __forceinline__ bool add_blocks(float2 (&sum)[N2], int nkb, Acc acc, 
                 __syncwarp();
                 drained();
                 const bool ready = more && test();
+                // (here, where the other warp of the scheduler can add: ahead of the block 421 us, behind add(p)
+                // 404, behind the next block's first load 438)
+                if (more && !scale(kb + 1, next)) return false;
                 add(p);
                 if (__all_sync(0xFFFFFFFFu, ready)) {
                     tc::tc_fence_after();
@@ -961,7 +963,7 @@ namespace {
 //   4096 x 5120 13.4 and 12.5, but of 2048 x 6144 8.8 and 10.2), and by 8 and 4 only where the clusters fit beside
 //   each other (1000 columns of 4096: 128 rows by 8 8.2, by 4 9.3; 200 rows by 8 14.1, by 4 9.4).
 //   Very many: a wave of pairs takes about 1.5 times a wave of the others (512 rows of 7168 x 9216: 1 wave 32, the
-//   others 2 waves 37; 768 rows: 2 waves 57, 3 waves 53; 8191 rows: 421 and 500).
+//   others 2 waves 37; 768 rows: 2 waves 57, 3 waves 53; 8191 rows: 367 and 500).
 struct Plan {
     int nt;     // rows of x per tile of the few-row kernel; 0: the others
     bool pair;  // the CTA pairs' kernel
