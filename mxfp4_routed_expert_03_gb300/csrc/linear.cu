@@ -962,8 +962,10 @@ namespace {
 //   Many rows: the exchange of a 128 x 128 part costs about 2 us, so K is split where that saves more (128 rows of
 //   4096 x 5120 13.4 and 12.5, but of 2048 x 6144 8.8 and 10.2), and by 8 and 4 only where the clusters fit beside
 //   each other (1000 columns of 4096: 128 rows by 8 8.2, by 4 9.3; 200 rows by 8 14.1, by 4 9.4).
-//   Very many: a wave of pairs takes about 1.5 times a wave of the others (512 rows of 7168 x 9216: 1 wave 32, the
-//   others 2 waves 37; 768 rows: 2 waves 57, 3 waves 53; 8191 rows: 367 and 500).
+//   Very many: by the times that the two kernels' waves take, which these sizes gave (waves of the many-row kernel
+//   and of pairs, times of both): 512 rows of 7168 x 9216 2, 1, 37.3, 28.0; 600 rows 3, 2, 50.7, 48.3; 8191 rows
+//   31, 16, 477, 382; 900 rows of 4096 x 5120 3, 2, 29.8, 31.1; 2049 rows 5, 3, 48.0, 45.7; 768 rows of 1536 x 7168
+//   3, 2, 14.7, 16.9; 4096 rows 12, 6, 48.0, 43.3.
 struct Plan {
     int nt;     // rows of x per tile of the few-row kernel; 0: the others
     bool pair;  // the CTA pairs' kernel
@@ -986,7 +988,7 @@ Plan plan_of(int T, int K, int N, int nsm) {
     else if (KB >= 16 && tiles * 4 <= nsm * 7 / 8) s = 4;
     else if (KB >= 24 && tiles * 2 <= nsm) s = 2;
     const int64_t waves = (tiles + nsm - 1) / nsm, pair_waves = (pairs + nsm / 2 - 1) / (nsm / 2);
-    const bool pair = 3 * pair_waves < 2 * waves;
+    const bool pair = 5500 + pair_waves * (365 * KB + 1100) < 4000 + waves * (265 * KB + 400);  // ns
     return {0, pair, pair ? 1 : s};
 }
 
