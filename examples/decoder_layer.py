@@ -1,14 +1,16 @@
-"""One decoder layer served by the library: attention over a 4-bit cache, then routed experts.
+"""One decoder layer served by the library: projections in 8 bits, attention over a 4-bit cache,
+then routed experts.
 
 A batch of prompts is taken in (many rows per sequence), then decoded token by token (one row
 per sequence), every step through the same calls:
 
-  fused q/k/v projection (torch) -> moe_qk_norm_rope -> moe_kv_append -> moe_attn_forward ->
-  output projection (torch) -> moe_plan_scored -> moe_forward
+  moe_add_norm (8-bit rows) -> moe_linear_forward (fused q/k/v) -> moe_rope_append ->
+  moe_attn_forward -> moe_add_norm (8-bit rows, no norm) -> moe_linear_forward (output) ->
+  moe_add_norm (residual, norm) -> moe_plan_scored -> moe_forward
 
     python examples/decoder_layer.py [--seqs 8] [--prompt 512] [--steps 64]
 
-Weights are random; the layer's own norms are left out to keep the calls in view.
+Weights are random.
 """
 from __future__ import annotations
 
@@ -23,6 +25,7 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 from mxfp4_routed_expert_03_gb300 import MOE_ROUTER_XWR, MOE_SCORE_SIGMOID, check, moe_route_desc
 from mxfp4_routed_expert_03_gb300.attention import Attention, Batch, Rope, alloc_kv_cache
 from mxfp4_routed_expert_03_gb300.layer import Layer, Plan, alloc_weights
+from mxfp4_routed_expert_03_gb300.linear import Fp8Rows, Linear, Norm
 
 
 def rope_table(n_pos: int, dim: int, base: float = 10000.0) -> torch.Tensor:
@@ -30,6 +33,15 @@ def rope_table(n_pos: int, dim: int, base: float = 10000.0) -> torch.Tensor:
     f = base ** (-torch.arange(0, dim, 2, dtype=torch.float64, device="cuda") / dim)
     a = torch.arange(n_pos, dtype=torch.float64, device="cuda")[:, None] * f
     return torch.cat([a.cos(), a.sin()], 1).float()
+
+
+def fp8_linear(w: torch.Tensor) -> Linear:
+    """A projection of w [d_out][d_in], quantised to E4M3 with a scale per 128 x 128 block."""
+    n, k = w.shape
+    full = torch.nn.functional.pad(w.float(), (0, -k % 128, 0, -n % 128)).view(-(-n // 128), 128, -(-k // 128), 128)
+    scale = (full.abs().amax((1, 3)) / 448).clamp(min=2.0 ** -126)
+    codes = (full / scale[:, None, :, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(-(-n // 128) * 128, -1)[:n, :k]
+    return Linear(k, n, codes.contiguous(), scale.contiguous())
 
 
 class DecoderLayer:
@@ -40,8 +52,10 @@ class DecoderLayer:
         g = torch.Generator(device="cuda").manual_seed(seed)
         rand = lambda *s, std: (std * torch.randn(*s, device="cuda", generator=g)).bfloat16()  # noqa: E731
         self.d, self.H, self.KV, self.hd, self.n_seqs, self.page = d_model, heads, kv_heads, head_dim, n_seqs, page
-        self.w_qkv = rand(d_model, (heads + 2 * kv_heads) * head_dim, std=d_model ** -0.5)
-        self.w_out = rand(heads * head_dim, d_model, std=(heads * head_dim) ** -0.5)
+        self.qkv = fp8_linear(rand((heads + 2 * kv_heads) * head_dim, d_model, std=d_model ** -0.5))
+        self.out = fp8_linear(rand(d_model, heads * head_dim, std=(heads * head_dim) ** -0.5))
+        self.norm_attn, self.norm_ffn = (Norm(d_model, weight=1 + rand(d_model, std=0.1)) for _ in range(2))
+        self.to_8bit = Norm(heads * head_dim)  # (no weight: no norm)
         self.rope = Rope(rope_table(max_len, head_dim), head_dim, q_weight=1 + rand(head_dim, std=0.1),
                          k_weight=1 + rand(head_dim, std=0.1))
         self.pages = -(-max_len // page)
@@ -66,29 +80,36 @@ class DecoderLayer:
         T, W = B * n, self.hd
         rows = x.reshape(T, self.d)
         st = torch.cuda.current_stream()
-        qkv = rows @ self.w_qkv
+        y8, qkv = Fp8Rows.empty(T, self.d), torch.empty(T, (self.H + 2 * self.KV) * W, dtype=torch.bfloat16, device="cuda")
+        check(self.norm_attn.forward(T, rows, y8=y8, stream=st), "moe_add_norm")
+        check(self.qkv.forward(T, y8, qkv, st), "moe_linear_forward")
         q, k, v = qkv.split([self.H * W, self.KV * W, self.KV * W], dim=1)
         pos = (self.length + torch.arange(n, device="cuda", dtype=torch.int32)).repeat(B)
-        check(self.attn.norm_rope(T, q, k, pos, self.rope, q, k, st), "moe_qk_norm_rope")  # in place
         seq = torch.arange(B, device="cuda").repeat_interleave(n)
         slots = (self.table[seq, (pos // self.page).long()] * self.page + pos % self.page).int()
-        check(self.attn.append(T, k, v, slots, st), "moe_kv_append")
+        check(self.attn.rope_append(T, q, k, v, pos, self.rope, q, slots, st), "moe_rope_append")  # q in place
         self.length += n
         self.k_len.fill_(self.length)
         cu = None if n == 1 else torch.arange(0, T + 1, n, device="cuda", dtype=torch.int32)
         batch = Batch(B, T, n, self.length, cu, self.k_len, self.table, W ** -0.5)
         out = torch.empty(T, self.H * W, dtype=torch.bfloat16, device="cuda")
         check(self.attn.forward(batch, q, out, None, st), "moe_attn_forward")
-        h = rows + out @ self.w_out
+        o8, proj = Fp8Rows.empty(T, self.H * W), torch.empty_like(rows)
+        check(self.to_8bit.forward(T, out, y8=o8, stream=st), "moe_add_norm")
+        check(self.out.forward(T, o8, proj, st), "moe_linear_forward")
+        h, z = torch.empty_like(rows), torch.empty_like(rows)
+        check(self.norm_ffn.forward(T, proj, rows, total=h, y=z, stream=st), "moe_add_norm")
         plan = Plan(T, self.moe.E, self.moe.k)
-        check(self.moe.plan_scored(T, None, h, plan, self.route, self.bias, st), "moe_plan_scored")
+        check(self.moe.plan_scored(T, None, z, plan, self.route, self.bias, st), "moe_plan_scored")
         y = torch.empty_like(h)
-        check(self.moe.forward(T, h, plan, y, st), "moe_forward")
+        check(self.moe.forward(T, z, plan, y, st), "moe_forward")
         return (h + y).view(B, n, self.d)
 
     def status(self) -> None:
         check(self.attn.status(torch.cuda.current_stream()), "attention")
         check(self.moe.status(torch.cuda.current_stream()), "experts")
+        for linear in (self.qkv, self.out):
+            check(linear.status(torch.cuda.current_stream()), "projections")
 
 
 def main() -> None:

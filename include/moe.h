@@ -627,8 +627,8 @@ int moe_attn_status(moe_attn *a, void *stream);
  * addition, whose output can be E4M3 rows with a scale per 128 columns, and the
  * product of such rows with an E4M3 weight matrix that has a scale per 128 x 128
  * block (the projections around the attention, a router's logits).
- * The calls below run on the device that was current when their handle was
- * created; MOE_ERR_INVALID_ARG when another one is current.
+ * The calls below, and moe_rope_append, run on the device that was current when
+ * their handle was created; MOE_ERR_INVALID_ARG when another one is current.
  * ------------------------------------------------------------------------- */
 
 /* Rows of E4M3FN codes with fp32 scales: element x of row t stands for
@@ -666,7 +666,9 @@ void moe_norm_destroy(moe_norm *n);
  * reads as NaN. total needs a residual. bf16 rows may be strided (elements,
  * multiples of 8; bases 16-byte aligned); for y8 d_model is a multiple of 16.
  * A bf16 output may be an input (same pointer and stride) but must not overlap
- * one otherwise. Asynchronous on `stream`, no workspace. */
+ * one otherwise. The squares are summed in fp32: a row whose sum passes its range
+ * gives zeros. An infinity or NaN spreads over its row by the norm, and no
+ * further. Asynchronous on `stream`, no workspace. */
 int moe_add_norm(moe_norm *n, int32_t T, const uint16_t *x, int64_t x_stride,
                  const uint16_t *residual, int64_t residual_stride, uint16_t *total,
                  int64_t total_stride, uint16_t *y, int64_t y_stride, const moe_fp8_rows *y8,

@@ -10,6 +10,7 @@ struct moe_attn {
     moe_attn_desc desc;
     moe_kv_cache cache;
     int page_shift;  // log2(page_size)
+    int device;
     int num_sms;
     int *status;     // device word: first error code recorded by a kernel
     int inject;      // enum moe_inject (test hook; MOE_INJECT_NONE by default)
@@ -68,6 +69,7 @@ MOE_API int moe_attn_create(const moe_attn_desc *d, const moe_kv_cache *c, moe_a
     a->desc = *d;
     a->cache = *c;
     a->page_shift = page_shift_of(d->page_size);
+    a->device = dev;
     a->num_sms = nsm;
     a->inject = MOE_INJECT_NONE;
     a->timeout = kTimeoutCycles;
@@ -199,6 +201,8 @@ MOE_API int moe_rope_append(moe_attn *a, int32_t T, const moe_rope_desc *r,
     if (T == 0) return MOE_OK;
     const moe_attn_desc &d = a->desc;
     const int64_t qw = (int64_t)d.n_heads * d.head_dim, kw = (int64_t)d.n_kv_heads * d.head_dim;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev != a->device) return MOE_ERR_INVALID_ARG;
     if (!rope_arrays_ok(r, positions) || !rows_ok(k, k_stride, kw) || !rows_ok(v, v_stride, kw) || !slots ||
         ((uintptr_t)slots & 3u) || (q && (!rows_ok(q, q_stride, qw) || !rows_ok(q_out, q_out_stride, qw))))
         return MOE_ERR_INVALID_ARG;

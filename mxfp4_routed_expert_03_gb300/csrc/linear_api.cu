@@ -159,6 +159,7 @@ MOE_API int moe_linear_forward(moe_linear *l, int32_t T, const moe_fp8_rows *x, 
     if (!x || !rows8_ok(x, d.d_in) || !out || !aligned16(out) || out_stride < d.d_out ||
         out_stride % (out_type == MOE_LINEAR_F32 ? 4 : 8) || !current(l->device))
         return MOE_ERR_INVALID_ARG;
+    if (T > INT32_MAX - 512) return MOE_ERR_UNSUPPORTED;  // 32-bit rows with room for a tile
     MoeLinearArgs g = {};
     g.T = T;
     g.K = d.d_in;

@@ -151,6 +151,40 @@ def test_strided_rows_in_place_and_untouched_memory(T):
     assert bool((wide == 7.0).all()) and bool((codes == 9).all()) and bool((scales == 9.0).all())
 
 
+def test_many_rows_in_place_on_a_stream_and_in_a_graph():
+    """Rows on their way while others are written: outputs over the inputs of the same rows."""
+    from mxfp4_routed_expert_03_gb300 import check
+    from mxfp4_routed_expert_03_gb300.linear import Fp8Rows, Norm
+    T, d = 3001, 1008
+    x, r, w = make(T, d, seed=10)
+    norm, rows = Norm(d, 1e-6, w), Fp8Rows.empty(T, d)
+    wide = torch.full((T + 1, 2 * d + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    a, b = wide[:, :d], wide[:, d + 8:]
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        check(norm.forward(T, a, b, b, a, rows, torch.cuda.current_stream()), "moe_add_norm")
+    for _ in range(3):
+        a[:T], b[:T] = x, r
+        graph.replay()
+        torch.cuda.synchronize()
+        verify(x, r, w, (b[:T].contiguous(), a[:T].contiguous(), rows))
+    assert bool((wide[T] == 7.0).all()) and bool((wide[:, d:d + 8] == 7.0).all())
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_many_rows_not_finite(bad):
+    T, d = 2000, 1024
+    x, r, w = make(T, d, seed=11)
+    x[77, 500], r[1999, 3] = bad, bad
+    total, y, rows = run(x, r, w)
+    others = torch.ones(T, dtype=torch.bool, device="cuda")
+    others[[77, 1999]] = False
+    verify(x[others], r[others], w, (total[others], y[others], type(rows)(rows.q.view(torch.uint8)[others].view(rows.q.dtype), rows.s[others])))
+    assert bool(rows.s[77, 3].isnan()) and bool(rows.s[1999, 0].isnan())
+
+
 def test_streams_and_graphs():
     from mxfp4_routed_expert_03_gb300 import check
     from mxfp4_routed_expert_03_gb300.linear import Fp8Rows, Norm

@@ -166,6 +166,79 @@ def test_captured_and_replayed_with_changed_inputs(T):
     s.verify()
 
 
+# several waves of tiles: a pair of CTAs on 256 x 256, one and several tiles a pair, ragged in both directions
+LARGE = [(400, 2064, 6000), (512, 2048, 5120), (1500, 2048, 7000), (3000, 1552, 5008)]
+
+
+@pytest.mark.parametrize("T,K,N", LARGE)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_large(T, K, N, dtype):
+    s = Setup(T, K, N, seed=20, dtype=dtype)
+    s.run()
+    s.verify()
+    first = s.out.clone()
+    s.out.fill_(0)
+    s.run()
+    assert torch.equal(s.out, first)
+
+
+@pytest.mark.parametrize("T,K,N", LARGE)
+def test_large_whole_numbers_are_exact(T, K, N):
+    from mxfp4_routed_expert_03_gb300 import check
+    from mxfp4_routed_expert_03_gb300.linear import Fp8Rows, Linear
+    g = torch.Generator(device="cuda").manual_seed(T)
+    xq = torch.randint(-3, 4, (T, K), device="cuda", generator=g).float().to(E4M3)
+    wq = torch.randint(-3, 4, (N, K), device="cuda", generator=g).float().to(E4M3)
+    xs = torch.randint(0, 3, (T, -(-K // 128)), device="cuda", generator=g).float().exp2()
+    ws = torch.randint(0, 3, (-(-N // 128), -(-K // 128)), device="cuda", generator=g).float().exp2()
+    out = torch.empty(T, N, device="cuda")
+    linear = Linear(K, N, wq, ws)
+    check(linear.forward(T, Fp8Rows(xq, xs), out), "moe_linear_forward")
+    assert torch.equal(out.double(), product(xq, xs, wq, ws)[0])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_large_strided_and_not_finite(dtype):
+    from mxfp4_routed_expert_03_gb300 import check
+    T, K, N = 700, 2064, 6008
+    s = Setup(T, K, N, seed=21, dtype=dtype)
+    s.xq.view(torch.uint8)[333, 77] = 0x7F
+    s.wq.view(torch.uint8)[5000, 130] = 0xFF
+    s.xs[T - 1, 4] = float("inf")
+    s.ws[3, 2] = float("nan")
+    out = torch.full((T + 2, N + 40), 7.0, dtype=dtype, device="cuda")
+    check(s.linear.forward(T, s.rows, out[:, 16:16 + N]), "moe_linear_forward")
+    got = out[:T, 16:16 + N].clone()
+    ref, mag = product(s.xq, s.xs, s.wq, s.ws)
+    fine = ref.isfinite()
+    assert torch.equal(got.isfinite(), fine)
+    assert bool(((got.double() - ref).abs() <= bound(ref, mag, K, dtype))[fine].all())
+    out[:T, 16:16 + N] = 7.0
+    assert bool((out == 7.0).all())
+
+
+def test_large_on_two_streams_and_in_a_graph():
+    a, b = Setup(600, 2048, 6000, seed=22), Setup(600, 2048, 6000, seed=23)
+    a.run()
+    b.run()
+    want = a.out.clone(), b.out.clone()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=streams[1]):
+        b.run(torch.cuda.current_stream())
+    for _ in range(5):
+        a.out.fill_(0)
+        b.out.fill_(0)
+        torch.cuda.synchronize()
+        for _ in range(3):
+            a.run(streams[0])
+            with torch.cuda.stream(streams[1]):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a.out, want[0]) and torch.equal(b.out, want[1])
+
+
 def test_weights_written_right_before_the_call_count():
     """The weights' last writer may be the call before in the same stream."""
     T, K, N = 4, 7168, 7168
@@ -218,14 +291,14 @@ def test_no_tokens_and_refusals():
     s.verify()
 
 
-@pytest.mark.parametrize("T", [1, 40, 100, 200, 600])
-def test_stall_times_out_then_recovers(T):
+@pytest.mark.parametrize("T,N", [(1, 1400), (40, 1400), (100, 1400), (200, 1400), (600, 1400), (500, 5120), (1500, 7000)])
+def test_stall_times_out_then_recovers(T, N):
     """With the test hook an MMA issuer waits, under a limit of 2e6 SM cycles, on a barrier that
     nothing signals: the status is recorded, copies and products in flight end, tensor memory is
     freed, and the next call is right. No GPU fault is involved."""
     from mxfp4_routed_expert_03_gb300 import (MOE_ERR_DEVICE_TIMEOUT, MOE_ERR_INVALID_ARG, MOE_INJECT_ATTN_STALL,
                                               MOE_INJECT_LINEAR_STALL, MOE_INJECT_NONE, check, moe_linear_set_fault_injection)
-    s = Setup(T, 2048, 1400, seed=13)
+    s = Setup(T, 2048, N, seed=13)
     s.run()
     clean = s.out.clone()
     for mode, limit in ((7, 0), (MOE_INJECT_ATTN_STALL, 0), (MOE_INJECT_LINEAR_STALL, 1000)):

@@ -110,35 +110,40 @@ def test_against_64_bits(d, interleaved):
         assert bool(((got.double() - y).abs() <= tol).all())
 
 
-def test_skipped_and_bad_tokens():
-    from mxfp4_routed_expert_03_gb300 import MOE_ERR_BAD_INDEX
-    s = Setup(200, 8, 2, 128, 16, 128, seed=3)
-    s.slots[[0, 5, 77, 199]] = -1  # padding: the query is still turned
+@pytest.mark.parametrize("T", [200, 1300])
+def test_skipped_tokens(T):
+    s = Setup(T, 8, 2, 128, 16, 128, seed=3)
+    s.slots[[0, 5, 77, T - 1]] = -1  # padding: the query is still turned
     live = s.slots >= 0
     s.two_calls(live)
-    want = torch.empty(200, 8 * 128, dtype=torch.bfloat16, device="cuda")
-    s.other.norm_rope(200, s.q, None, s.pos, s.rope, want, None)
+    want = torch.empty(T, 8 * 128, dtype=torch.bfloat16, device="cuda")
+    s.other.norm_rope(T, s.q, None, s.pos, s.rope, want, None)
     q_out = torch.full_like(want, 7.0)
     assert s.one(q_out) == 0 and s.attn.status() == 0
     assert torch.equal(q_out, want) and s.same_cache()
-    # slots outside the cache and positions outside the table: reported, left out
-    for bad_slot in (-2, s.pages * 16, 2 ** 31 - 1, -2 ** 31):
-        t = Setup(60, 8, 2, 128, 16, 128, seed=4)
+
+
+@pytest.mark.parametrize("T", [60, 1300])
+def test_bad_slots_and_positions(T):
+    """Slots outside the cache and positions outside the table: reported, left out."""
+    from mxfp4_routed_expert_03_gb300 import MOE_ERR_BAD_INDEX
+    for bad_slot in (-2, (-(-T // 16) + 3) * 16, 2 ** 31 - 1, -2 ** 31):
+        t = Setup(T, 8, 2, 128, 16, 128, seed=4)
         t.slots[[3, 40]] = bad_slot
-        ok = torch.ones(60, dtype=torch.bool, device="cuda")
+        ok = torch.ones(T, dtype=torch.bool, device="cuda")
         ok[[3, 40]] = False
-        want = torch.empty(60, 8 * 128, dtype=torch.bfloat16, device="cuda")
-        t.other.norm_rope(60, t.q, None, t.pos, t.rope, want, None)
+        want = torch.empty(T, 8 * 128, dtype=torch.bfloat16, device="cuda")
+        t.other.norm_rope(T, t.q, None, t.pos, t.rope, want, None)
         t.two_calls(ok)
         q_out = torch.full_like(want, 7.0)
         assert t.one(q_out) == 0 and t.attn.status() == MOE_ERR_BAD_INDEX and t.attn.status() == 0
         assert torch.equal(q_out, want) and t.same_cache()
     for bad_pos in (-1, 500, 2 ** 31 - 1, -2 ** 31):
-        t = Setup(60, 8, 2, 64, 16, 64, seed=5)
-        t.pos[[0, 33, 59]] = bad_pos
-        ok = torch.ones(60, dtype=torch.bool, device="cuda")
-        ok[[0, 33, 59]] = False
-        want = torch.full((60, 8 * 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        t = Setup(T, 8, 2, 64, 16, 64, seed=5)
+        t.pos[[0, 33, T - 1]] = bad_pos
+        ok = torch.ones(T, dtype=torch.bool, device="cuda")
+        ok[[0, 33, T - 1]] = False
+        want = torch.full((T, 8 * 64), 7.0, dtype=torch.bfloat16, device="cuda")
         want[ok] = t.two_calls(ok)
         q_out = torch.full_like(want, 7.0)
         assert t.one(q_out) == 0 and t.attn.status() == MOE_ERR_BAD_INDEX
@@ -154,8 +159,9 @@ def test_not_finite_values_stay_in_their_blocks():
     assert torch.equal(q_out, want) and s.same_cache()
 
 
-def test_in_place_keys_alone_streams_and_graphs():
-    s = Setup(90, 8, 2, 128, 32, 64, True, seed=7)
+@pytest.mark.parametrize("T", [90, 1300])
+def test_in_place_keys_alone_streams_and_graphs(T):
+    s = Setup(T, 8, 2, 128, 32, 64, True, seed=7)
     s.two_calls()
     assert s.one(None, q=None) == 0 and s.same_cache()  # keys and values alone
     want = s.two_calls()
