@@ -90,28 +90,28 @@ struct Ring {
 };
 
 // A CTA's part of a tile, [rows][pitch] fp32 in `stage`, goes to the CTAs of the cluster that join `per` of its
-// rows each, rank 0 the first: into their `recv` area [S][per][pitch], counted on their `bar`. By one warp, once
-// every CTA of the cluster has its barriers ready.
+// rows each, rank 0 the first: into their `recv` area [S][per][pitch], counted on their `bar`; its own rows stay.
+// By one warp, once every CTA of the cluster has its barriers ready.
 __device__ __forceinline__ void send_parts(const float *stage, float *recv, uint64_t *bar, int S, int rank, int rows, int per,
                                            int pitch, int lane) {
     const int to = (rank + lane) % S, n = min(per, rows - to * per);
-    if (lane < S && n > 0)
+    if (lane > 0 && lane < S && n > 0)
         tc::bulk_copy_s2peer(tc::peer_addr(recv + rank * per * pitch, to), stage + to * per * pitch, n * pitch * 4, tc::peer_addr(bar, to));
     __syncwarp();
 }
 
-// Four sums of S received parts, `step` apart, in the order of the ranks.
+// Four sums of S parts, this CTA's at `own`, the others' `step` apart at `recv`, in the order of the ranks.
 template <int S>
-__device__ __forceinline__ float4 join(const float *p, int step) {
+__device__ __forceinline__ float4 join(const float *own, const float *recv, int step, int rank) {
     float4 w[S];
 #pragma unroll
-    for (int k = 0; k < S; ++k) w[k] = *(const float4 *)(p + k * step);
+    for (int k = 0; k < S; ++k) w[k] = *(const float4 *)(k == rank ? own : recv + k * step);
 #pragma unroll
     for (int k = 1; k < S; ++k) w[0].x += w[k].x, w[0].y += w[k].y, w[0].z += w[k].z, w[0].w += w[k].w;
     return w[0];
 }
-__device__ __forceinline__ float4 join(const float *p, int step, int S) {
-    return S == 2 ? join<2>(p, step) : S == 4 ? join<4>(p, step) : join<8>(p, step);
+__device__ __forceinline__ float4 join(const float *own, const float *recv, int step, int rank, int S) {
+    return S == 2 ? join<2>(own, recv, step, rank) : S == 4 ? join<4>(own, recv, step, rank) : join<8>(own, recv, step, rank);
 }
 
 // After a timeout, by all threads: the copies and MMAs in flight end before the CTA leaves. A stage's last
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(Wide::THREADS, 1)
         tc::mbar_init(drain, 1);
         tc::mbar_init(never, 1);
         tc::fence_mbar_init();
-        if (S > 1) tc::mbar_arrive_expect_tx(recv, 128 * C::PITCH * 4);
+        if (S > 1) tc::mbar_arrive_expect_tx(recv, (S - 1) * (128 / S) * C::PITCH * 4);
         tc::prefetch_map(&mW);
         tc::prefetch_map(&mX);
     }
@@ -476,7 +476,8 @@ __global__ void __launch_bounds__(Wide::THREADS, 1)
             for (int u = tid - 128; u < R * BN / 4; u += 256) {
                 const int r = u / (BN / 4), c = u % (BN / 4) * 4;
                 if (t0 + r >= args.T || n0 + c >= args.N) continue;
-                store4(args, (t0 + r) * args.out_stride + n0 + c, join(parts + r * C::PITCH + c, R * C::PITCH, S));
+                store4(args, (t0 + r) * args.out_stride + n0 + c,
+                       join((const float *)smem + (rank * R + r) * C::PITCH + c, parts + r * C::PITCH + c, R * C::PITCH, rank, S));
             }
         }
         __syncwarp();
@@ -795,7 +796,7 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, 2)
         tc::mbar_init(drain, 1);
         tc::mbar_init(never, 1);
         tc::fence_mbar_init();
-        if (S > 1 && mine > 0) tc::mbar_arrive_expect_tx(recv, S * mine * C::PITCH * 4);
+        if (S > 1 && mine > 0) tc::mbar_arrive_expect_tx(recv, (S - 1) * mine * C::PITCH * 4);
         tc::prefetch_map(&mW);
         tc::prefetch_map(&mX);
         // the first stages' weights on their way to L2 while the kernel before ends
@@ -938,7 +939,8 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, 2)
                 const int j = u / 32, n = n0 + u % 32 * 4;
                 if (n < args.N)
                     store4(args, (int64_t)(t0 + rank * per + j) * args.out_stride + n,
-                           join(parts + j * C::PITCH + u % 32 * 4, per * C::PITCH, S));
+                           join((const float *)smem + (rank * per + j) * C::PITCH + u % 32 * 4, parts + j * C::PITCH + u % 32 * 4,
+                                per * C::PITCH, rank, S));
             }
         }
         __syncwarp();

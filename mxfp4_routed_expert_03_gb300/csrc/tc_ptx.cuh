@@ -209,9 +209,11 @@ __device__ __forceinline__ uint32_t cluster_size() {
     return r;
 }
 
-// The two halves of a barrier over all threads of the cluster.
+// The two halves of a barrier over all threads of the cluster. The arrival orders no memory (one that
+// does waits for the CTA's stores): barriers made ready by fence_mbar_init and copies whose completion was
+// waited for need no more.
 __device__ __forceinline__ void cluster_arrive() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
