@@ -4,12 +4,12 @@
 //   per 128 columns s = max(max|y| / 448, 2^-126), code = e4m3(y / s)
 //
 // h exactly rounded, the rest in fp32. Bound: each of x, r, h, y moves 2 bytes an
-// element, the codes 1; beside that the instructions (about 10 an element).
+// element, the codes 1; beside that the instructions.
 // Some warps of a block own a row and hold it in registers between the sum and the
 // output: a thread has CH chunks of 8 columns, the row's threads apart, so that 16
 // neighbouring lanes have a scale's 128 columns.
 // 8191 rows of 7168 with residual and codes: 65 us (6.3 TB/s of the 412 MB that have
-// to move); 4099 rows of 8192, codes alone: 20 us (5.1 TB/s).
+// to move); 4099 rows of 8192, codes alone: 17 us (6.0 TB/s).
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -25,7 +25,12 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
     return r;
 }
 
-// The larger of two values, NaN if one is.
+// The largest magnitude of three values, NaN if one is.
+__device__ __forceinline__ float max_abs(float x, float y, float z) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
 __device__ __forceinline__ float max_nan(float x, float y) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
@@ -56,27 +61,28 @@ struct Place {
     }
 };
 
-// Row t (none if chunks is 0) from its loaded chunks to its outputs. `part`: a word of shared memory per warp.
-template <int CH>
-__device__ __forceinline__ void row_out(const MoeNormArgs &a, const Place &p, int64_t t, int chunks, uint4 (&x)[CH],
-                                        const uint4 (&r)[CH], const uint4 (&w)[CH], float *part) {
+// Row t (of which this thread has the chunks with live[i]) from its loaded chunks to its outputs; `inv_d` = 1 / d.
+// `part`: a word of shared memory per warp.
+template <int CH, bool RES, bool NORM>
+__device__ __forceinline__ void row_out(const MoeNormArgs &a, const Place &p, int64_t t, const bool (&live)[CH], float inv_d,
+                                        uint4 (&x)[CH], const uint4 (&r)[CH], const uint4 (&w)[CH], float *part) {
     const int lane = threadIdx.x & 31;
     float v[CH][8];
     float ss = 0.f;
+    uint16_t *total = RES && a.total ? a.total + t * a.total_stride + 8 * p.tid : nullptr;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-        const int c = p.tid + i * p.threads;
-        if (a.residual) {
+        if (RES) {
             x[i] = add8(x[i], r[i]);
-            if (a.total && c < chunks) *(uint4 *)(a.total + t * a.total_stride + 8 * c) = x[i];
+            if (total && live[i]) *(uint4 *)(total + 8 * i * p.threads) = x[i];
         }
         rope::unpack8(x[i], v[i]);  // (the norm reads what is stored)
-        if (a.weight) {
+        if (NORM) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
         }
     }
-    if (a.weight) {
+    if (NORM) {
 #pragma unroll
         for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
         if (p.warps > 1) {
@@ -86,7 +92,7 @@ __device__ __forceinline__ void row_out(const MoeNormArgs &a, const Place &p, in
 #pragma unroll
             for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
         }
-        const float inv = rsqrtf(ss / (float)a.d + a.eps);
+        const float inv = rsqrtf(fmaf(ss, inv_d, a.eps));
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             float u[8];
@@ -95,17 +101,21 @@ __device__ __forceinline__ void row_out(const MoeNormArgs &a, const Place &p, in
             for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * inv * u[j];
         }
     }
+    if (a.y) {
+        uint16_t *y = a.y + t * a.y_stride + 8 * p.tid;
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+            if (live[i]) *(uint4 *)(y + 8 * i * p.threads) = rope::pack8(v[i]);
+    }
+    if (!a.q) return;
+    uint8_t *code = a.q + t * a.q_stride + 8 * p.tid;
+    float *scale = a.s + t * a.s_stride + p.tid / 16;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-        const int c = p.tid + i * p.threads;
-        if (a.y && c < chunks) *(uint4 *)(a.y + t * a.y_stride + 8 * c) = rope::pack8(v[i]);
-        if (!a.q) continue;
-        float m = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = max_nan(m, fabsf(v[i][j]));
+        float m = max_abs(max_abs(v[i][0], v[i][1], v[i][2]), max_abs(v[i][3], v[i][4], v[i][5]),
+                          max_abs(v[i][6], v[i][7], 0.f));
 #pragma unroll
         for (int o = 8; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        if (c >= chunks) continue;
         // (a reciprocal within an ulp: of the quotient's rounding to 4 bits that is 2^-19)
         const float s = fmaxf(m * (1.f / 448.f), 1.17549435e-38f);
         float f;
@@ -114,119 +124,141 @@ __device__ __forceinline__ void row_out(const MoeNormArgs &a, const Place &p, in
 #pragma unroll
         for (int k = 0; k < 2; ++k)
             q[k] = to_e4m3x2(v[i][4 * k] * f, v[i][4 * k + 1] * f) | to_e4m3x2(v[i][4 * k + 2] * f, v[i][4 * k + 3] * f) << 16;
-        *(uint2 *)(a.q + t * a.q_stride + 8 * c) = make_uint2(q[0], q[1]);
-        if ((c & 15) == 0)  // (m is not below infinity: it is that, or NaN)
-            a.s[t * a.s_stride + c / 16] = m < __uint_as_float(0x7F800000u) ? s : __uint_as_float(0x7FC00000u);
+        if (!live[i]) continue;
+        *(uint2 *)(code + 8 * i * p.threads) = make_uint2(q[0], q[1]);
+        if ((p.tid & 15) == 0)  // (m is not below infinity: it is that, or NaN)
+            scale[i * p.threads / 16] = m < __uint_as_float(0x7F800000u) ? s : __uint_as_float(0x7FC00000u);
     }
 }
 
 // Few rows: a block has each of its rows once.
-template <int CH>
+template <int CH, bool RES, bool NORM>
 __global__ void __launch_bounds__(1024) moe_norm_kernel(MoeNormArgs a, int warps) {
     __shared__ float part[32];
     const Place p(warps);
     const int64_t t = (int64_t)blockIdx.x * p.rows + p.sub;
-    const int chunks = t < a.T ? a.d / 8 : 0;
     grid_dep_wait();
     grid_dep_launch();
     uint4 x[CH], r[CH], w[CH];
+    bool live[CH];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         const int c = p.tid + i * p.threads;
+        live[i] = t < a.T && c < a.d / 8;
         x[i] = r[i] = w[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (c >= chunks) continue;
+        if (!live[i]) continue;
         x[i] = *(const uint4 *)(a.x + t * a.x_stride + 8 * c);
-        if (a.residual) r[i] = *(const uint4 *)(a.residual + t * a.residual_stride + 8 * c);
-        if (a.weight) w[i] = *(const uint4 *)(a.weight + 8 * c);
+        if (RES) r[i] = *(const uint4 *)(a.residual + t * a.residual_stride + 8 * c);
+        if (NORM) w[i] = *(const uint4 *)(a.weight + 8 * c);
     }
-    row_out<CH>(a, p, t, chunks, x, r, w, part);
+    row_out<CH, RES, NORM>(a, p, t, live, 1.f / (float)a.d, x, r, w, part);
 }
 
-// Many rows: a block goes through rows with the next one on its way (two: 72 us instead of 65 for the 8191 rows
-// above; four chunks a thread: 87, half as many warps fit). A thread copies what it will read itself, so
+// Many rows: a block goes through rows with the next one on its way (two of them, or four chunks a thread, so
+// that half as many warps fit: slower). A thread copies what it will read itself, so
 // nothing has to be waited for but its own copies.
-constexpr int CH_STREAM = 2, STAGES = 2;
+constexpr int CH_STREAM = 2;
 
+template <bool RES, bool NORM>
 __global__ void __launch_bounds__(1024) moe_norm_stream_kernel(MoeNormArgs a, int warps) {
-    constexpr int CH = CH_STREAM;
-    extern __shared__ uint4 ring[];  // [STAGES][CH][x, residual][thread]
+    constexpr int CH = CH_STREAM, PER = RES ? 2 : 1;
+    extern __shared__ uint4 ring[];  // [2][CH][x, residual][thread]
     __shared__ float part[2][32];
     const Place p(warps);
     const int64_t step = (int64_t)gridDim.x * p.rows;
-    const int chunks = a.d / 8, per = a.residual ? 2 : 1, n = blockDim.x;
+    const int n = blockDim.x;
     uint4 *mine = ring + threadIdx.x;
     grid_dep_wait();
     grid_dep_launch();
     uint4 w[CH];
+    bool live[CH];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         const int c = p.tid + i * p.threads;
-        w[i] = a.weight && c < chunks ? *(const uint4 *)(a.weight + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+        live[i] = c < a.d / 8;
+        w[i] = NORM && live[i] ? *(const uint4 *)(a.weight + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int s = 0; s < 2 * PER; ++s) mine[(s * CH + i) * n] = make_uint4(0u, 0u, 0u, 0u);  // (chunks that are not there)
     }
-    auto fetch = [&](int64_t t, int s) {
-        if (t < a.T) {
+    int64_t t = (int64_t)blockIdx.x * p.rows + p.sub;
+    auto fetch = [&](int64_t row, int s) {
+        if (row < a.T) {
+            const uint16_t *x = a.x + row * a.x_stride + 8 * p.tid;
+            const uint16_t *r = RES ? a.residual + row * a.residual_stride + 8 * p.tid : nullptr;
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
-                const int c = p.tid + i * p.threads;
-                if (c >= chunks) continue;
-                cp_async_16(mine + (s * CH + i) * per * n, a.x + t * a.x_stride + 8 * c);
-                if (a.residual) cp_async_16(mine + ((s * CH + i) * per + 1) * n, a.residual + t * a.residual_stride + 8 * c);
+                if (!live[i]) continue;
+                cp_async_16(mine + (s * CH + i) * PER * n, x + 8 * i * p.threads);
+                if (RES) cp_async_16(mine + ((s * CH + i) * PER + 1) * n, r + 8 * i * p.threads);
             }
         }
         cp_async_commit();
     };
-    int64_t t = (int64_t)blockIdx.x * p.rows + p.sub;
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) fetch(t + s * step, s);
+    const float inv_d = 1.f / (float)a.d;
+    fetch(t, 0);
     // (all rows of a block in as many turns, so that its threads meet at the sums)
-    const int64_t turns = (a.T - (int64_t)blockIdx.x * p.rows + step - 1) / step;
-    int s = 0, into = STAGES - 1;
-    for (int64_t k = 0; k < turns; ++k, t += step) {
-        fetch(t + (STAGES - 1) * step, into);
-        cp_async_wait<STAGES - 1>();
-        const int live = t < a.T ? chunks : 0;
+    const int turns = (int)((a.T - (int64_t)blockIdx.x * p.rows + step - 1) / step);
+    for (int k = 0; k < turns; ++k, t += step) {
+        const int s = k & 1;
+        // (the next row ahead of this one's arrival, or behind it: with a residual's four streams of rows the
+        // latter keeps the memory busier, 8191 rows of 7168 65 us against 69, without 4099 rows of 8192 18.8 and 17.1)
+        if (!RES) fetch(t + step, s ^ 1);
+        cp_async_wait<RES ? 0 : 1>();
         uint4 x[CH], r[CH];
+        bool here[CH];
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            x[i] = r[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (p.tid + i * p.threads >= live) continue;
-            x[i] = mine[(s * CH + i) * per * n];
-            if (a.residual) r[i] = mine[((s * CH + i) * per + 1) * n];
+            here[i] = live[i] && t < a.T;
+            x[i] = mine[(s * CH + i) * PER * n];
+            r[i] = RES ? mine[((s * CH + i) * PER + 1) * n] : make_uint4(0u, 0u, 0u, 0u);
         }
-        row_out<CH>(a, p, t, live, x, r, w, part[k & 1]);
-        s = s + 1 == STAGES ? 0 : s + 1;
-        into = into + 1 == STAGES ? 0 : into + 1;
+        if (RES) fetch(t + step, s ^ 1);
+        row_out<CH, RES, NORM>(a, p, t, here, inv_d, x, r, w, part[s]);
     }
 }
 
 int warps_of(int d, int ch) { return (d / 8 + 32 * ch - 1) / (32 * ch); }
 
-template <int CH>
+template <int CH, bool RES, bool NORM>
 cudaError_t launch(const MoeNormArgs &a, cudaStream_t st) {
     const int warps = warps_of(a.d, CH), rows = a.T > 1 && warps < 8 ? 8 / warps : 1;
-    return launch_pdl_ready(moe_norm_kernel<CH>, dim3((unsigned)((a.T + rows - 1) / rows)), dim3(32 * warps * rows), 0, st, a, warps);
+    return launch_pdl_ready(moe_norm_kernel<CH, RES, NORM>, dim3((unsigned)((a.T + rows - 1) / rows)), dim3(32 * warps * rows), 0,
+                            st, a, warps);
 }
 
-cudaError_t launch_stream(const MoeNormArgs &a, int nsm, cudaStream_t st) {
+template <bool RES, bool NORM>
+cudaError_t launch(const MoeNormArgs &a, int nsm, cudaStream_t st) {
+    // few rows: latency counts (16 rows of 7168 2.8 and 2.9 us, 300 of 1024 2.0 and 2.5, 1216 of 1024 3.7 and 4.0;
+    // the rule changes at 8 K elements an SM; 304 of 7168 5.6 and 5.2)
+    if ((int64_t)a.T * a.d <= (int64_t)nsm * 8192)
+        return a.d <= 8192 ? launch<1, RES, NORM>(a, st) : launch<2, RES, NORM>(a, st);
     const int warps = warps_of(a.d, CH_STREAM), rows = warps < 8 ? 8 / warps : 1, threads = 32 * warps * rows;
-    const int smem = STAGES * CH_STREAM * (a.residual ? 2 : 1) * threads * 16;
+    const int smem = 2 * CH_STREAM * (RES ? 2 : 1) * threads * 16;
     // (the registers of 1024 threads on an SM, and at most 128 KB of rows)
     const int64_t blocks = (a.T + rows - 1) / rows, most = (int64_t)nsm * (1024 / threads);
-    return launch_pdl_ready(moe_norm_stream_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(threads), smem, st, a, warps);
+    return launch_pdl_ready(moe_norm_stream_kernel<RES, NORM>, dim3((unsigned)(blocks < most ? blocks : most)), dim3(threads), smem,
+                            st, a, warps);
+}
+
+template <bool RES, bool NORM>
+cudaError_t setup() {
+    cudaError_t err = set_kernel((const void *)moe_norm_kernel<1, RES, NORM>);
+    if (err == cudaSuccess) err = set_kernel((const void *)moe_norm_kernel<2, RES, NORM>);
+    if (err == cudaSuccess)
+        err = set_kernel((const void *)moe_norm_stream_kernel<RES, NORM>, 2 * CH_STREAM * (RES ? 2 : 1) * 1024 * 16);
+    return err;
 }
 
 }  // namespace
 
 cudaError_t moe_norm_setup() {
-    cudaError_t err = set_kernel((const void *)moe_norm_kernel<1>);
-    if (err == cudaSuccess) err = set_kernel((const void *)moe_norm_kernel<2>);
-    if (err == cudaSuccess) err = set_kernel((const void *)moe_norm_stream_kernel, STAGES * CH_STREAM * 2 * 1024 * 16);
-    return err;
+    cudaError_t err = setup<false, false>();
+    if (err == cudaSuccess) err = setup<false, true>();
+    if (err == cudaSuccess) err = setup<true, false>();
+    return err == cudaSuccess ? setup<true, true>() : err;
 }
 
 cudaError_t moe_launch_norm(const MoeNormArgs &a, int nsm, cudaStream_t st) {
-    // few rows: latency counts (16 rows of 7168 2.8 and 2.9 us, 300 of 1024 2.0 and 2.5, 1216 of 1024 3.7 and 4.0;
-    // the rule changes at 8 K elements an SM; 304 of 7168 5.6 and 5.2)
-    if ((int64_t)a.T * a.d > (int64_t)nsm * 8192) return launch_stream(a, nsm, st);
-    return a.d <= 8192 ? launch<1>(a, st) : launch<2>(a, st);
+    if (a.residual) return a.weight ? launch<true, true>(a, nsm, st) : launch<true, false>(a, nsm, st);
+    return a.weight ? launch<false, true>(a, nsm, st) : launch<false, false>(a, nsm, st);
 }
