@@ -177,8 +177,11 @@ __global__ void __launch_bounds__(1024) moe_norm_stream_kernel(MoeNormArgs a, in
         const int c = p.tid + i * p.threads;
         live[i] = c < a.d / 8;
         w[i] = NORM && live[i] ? *(const uint4 *)(a.weight + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+        if (live[i]) continue;
 #pragma unroll
-        for (int s = 0; s < 2 * PER; ++s) mine[(s * CH + i) * n] = make_uint4(0u, 0u, 0u, 0u);  // (chunks that are not there)
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int k = 0; k < PER; ++k) mine[((s * CH + i) * PER + k) * n] = make_uint4(0u, 0u, 0u, 0u);
     }
     int64_t t = (int64_t)blockIdx.x * p.rows + p.sub;
     auto fetch = [&](int64_t row, int s) {

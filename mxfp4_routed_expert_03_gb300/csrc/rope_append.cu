@@ -67,8 +67,9 @@ __global__ void __launch_bounds__(32 * kWarps)
             for (int p = 0; p < 2; ++p) {
                 const int t = first + p * HP + lane / TPH;
                 pos[p] = 0;
-                mine[64 * p] = mine[64 * p + 32] = make_uint4(0u, 0u, 0u, 0u);
-                if (t < c.n) {
+                if (t >= c.n) {
+                    mine[64 * p] = mine[64 * p + 32] = make_uint4(0u, 0u, 0u, 0u);
+                } else {
                     const uint16_t *src = a.k + (int64_t)t * a.k_stride + head * D;
                     cp_async_16(mine + 64 * p, src + 8 * l.c0);
                     cp_async_16(mine + 64 * p + 32, src + 8 * l.c1);
