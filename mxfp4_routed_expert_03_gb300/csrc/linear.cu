@@ -288,6 +288,8 @@ __device__ __forceinline__ void store_rows(const MoeLinearArgs &args, int64_t t0
 // Barriers of a stage: `full` completes when its copies have come and the accumulator that its block goes to
 // has been read (an arrival of every adding warp), so the issuer has one wait per block; `done` when its MMAs
 // are finished: its memory is free, its accumulator is full.
+// Bound: an SM takes in about 62 bytes a cycle from L2, 276 ns for the 32 KB of a block (MMAs alone 178 ns, all
+// together 306). 333 rows of 4096 x 5120 12.0 us, 2049 of 4096 x 1000 to fp32 12.1: 32 of these blocks, then start and end.
 __global__ void __launch_bounds__(Wide::THREADS, 1)
     moe_linear_wide_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX,
                            const MoeLinearArgs args) {
@@ -535,6 +537,8 @@ __device__ __forceinline__ void mma_block_pair(uint32_t d, uint32_t a_s, uint32_
 // Barriers: `come` in each CTA, its copies; `full` in the first CTA, the copies of both and the first half's
 // accumulator read by both; `free1` in the first CTA, the second half's accumulator read by both; `done` in
 // each CTA, the MMAs of a half.
+// Bound: a block takes 375 ns; its copies alone 306, its additions alone 300, its MMAs alone 274. 8191 rows of 7168 x
+// 9216 374 to 382 us (2.85 PFLOP/s), 432 when it runs for seconds at the power limit.
 __global__ void __launch_bounds__(Pair::THREADS, 1)
     moe_linear_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX,
                            const MoeLinearArgs args) {
@@ -762,6 +766,9 @@ struct Narrow {
 
 }  // namespace
 
+// Bound: the weights, once through HBM; from 32 rows on also what an SM takes in from L2, and the exchange. 1 row of
+// 7168 x 9216 10.6 us (6.2 TB/s), 64 rows of 7168 x 7168 13.1 (3.9 TB/s). Two CTAs an SM: with 16 rows ten
+// stages, 180 KB, on their way on each.
 template <int NT>
 __global__ void __launch_bounds__(Narrow<NT>::THREADS, 2)
     moe_linear_narrow_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX,
@@ -960,14 +967,14 @@ namespace {
 
 // Which kernel, and the CTAs that share a tile's K (a power of two up to 8). Times of both sides in us.
 //   Few rows: as many CTAs per tile as fit on the SMs, two each, with two blocks of K at least (1 row of 7168 x
-//   9216: 1 CTA 14.9, 2 13.1, 4 11.8, 8 (which do not all fit) 15.3; of 7168 x 896: 1 12.9, 8 4.7).
+//   9216: 1 CTA 15.0, 2 12.6, 4 10.8, 8 (which do not all fit) 12.6; of 7168 x 896: 1 12.9, 8 4.2).
 //   Many rows: the exchange of a 128 x 128 part costs about 2 us, so K is split where that saves more (128 rows of
-//   4096 x 5120 13.4 and 12.5, but of 2048 x 6144 8.8 and 10.2), and by 8 and 4 only where the clusters fit beside
-//   each other (1000 columns of 4096: 128 rows by 8 8.2, by 4 9.3; 200 rows by 8 14.1, by 4 9.4).
+//   4096 x 5120 13.0 and 11.7, but of 2048 x 6144 8.5 and 9.0), and by 8 and 4 only where the clusters fit beside
+//   each other (1000 columns of 4096: 128 rows by 8 7.7, by 4 8.4; 200 rows by 8 12.7, by 4 8.4).
 //   Very many: by the times that the two kernels' waves take, which these sizes gave (waves of the many-row kernel
-//   and of pairs, times of both): 512 rows of 7168 x 9216 2, 1, 37.3, 28.0; 600 rows 3, 2, 50.7, 48.3; 8191 rows
-//   31, 16, 477, 382; 900 rows of 4096 x 5120 3, 2, 29.8, 31.1; 2049 rows 5, 3, 48.0, 45.7; 768 rows of 1536 x 7168
-//   3, 2, 14.7, 16.9; 4096 rows 12, 6, 48.0, 43.3.
+//   and of pairs, times of both): 512 rows of 7168 x 9216 2, 1, 37.3, 28.1; 600 rows 3, 2, 50.6, 48.7; 8191 rows
+//   31, 16, 482, 384; 900 rows of 4096 x 5120 3, 2, 29.6, 31.3; 2049 rows 5, 3, 47.6, 45.9; 768 rows of 1536 x 7168
+//   3, 2, 14.9, 16.9; 4096 rows 12, 6, 47.8, 43.5.
 struct Plan {
     int nt;     // rows of x per tile of the few-row kernel; 0: the others
     bool pair;  // the CTA pairs' kernel
