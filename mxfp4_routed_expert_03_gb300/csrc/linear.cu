@@ -350,14 +350,14 @@ __global__ void __launch_bounds__(Wide::THREADS, 1)
     };
     bool ok = true;
     int drained = 0;  // blocks that an adding warp has read
+    if (warp == 0 && tc::elect_one()) {  // the first stages' weights on their way to L2 while the kernel before ends
+        for (int kb = 0; kb < min(C::STAGES, nkb); ++kb) tc::tma_prefetch_2d(&mW, (kb0 + kb) * BK, first / MT * BN);
+    }
+    __syncwarp();
+    grid_dep_wait();  // (every warp: however long the kernel before takes, no wait below runs out meanwhile)
+    grid_dep_launch();
     if (warp < 4) {
         if (warp == 0) {
-            if (tc::elect_one()) {  // the first stages' weights on their way to L2 while the kernel before ends
-                for (int kb = 0; kb < min(C::STAGES, nkb); ++kb) tc::tma_prefetch_2d(&mW, (kb0 + kb) * BK, first / MT * BN);
-            }
-            __syncwarp();
-            grid_dep_wait();
-            grid_dep_launch();
             const uint64_t pol = tc::policy_evict_last();
             int it = 0;
             Ring at;
@@ -399,7 +399,6 @@ __global__ void __launch_bounds__(Wide::THREADS, 1)
             }
             // (the last MMAs have finished when the adding warps are through with the last block)
         } else if (warp == 3) {
-            grid_dep_wait();
             int it = 0;
             for (int tile = first; tile < total && ok; tile += step)
                 for (int g = 0; g < nkb && ok; g += C::G, ++it) {
@@ -593,11 +592,11 @@ __global__ void __launch_bounds__(Pair::THREADS, 1)
         moe_flag(args.status, MOE_ERR_DEVICE_TIMEOUT);
     };
     bool ok = true;
+    grid_dep_wait();  // (every warp, as above)
+    grid_dep_launch();
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_LOW));
         if (warp == 0) {
-            grid_dep_wait();
-            grid_dep_launch();
             const uint64_t pol = tc::policy_evict_last();
             int it = 0;
             Ring at;
@@ -661,7 +660,6 @@ __global__ void __launch_bounds__(Pair::THREADS, 1)
                 }
             }
         } else if (warp == 3) {
-            grid_dep_wait();
             int it = 0;
             for (int tile = first; tile < total && ok; tile += step)
                 for (int g = 0; g < KB && ok; g += C::G, ++it) {

@@ -258,6 +258,30 @@ def test_weights_written_right_before_the_call_count():
         assert torch.equal(s.out, new.out)
 
 
+@pytest.mark.parametrize("T,K,N", [(3, 512, 512), (100, 512, 512), (300, 1536, 7168)])
+def test_the_kernel_before_may_take_long(T, K, N):
+    """A product that starts beside a long one on the SMs that this leaves free, and waits for its end,
+    counts none of that as a wait that ran out (limit: 1e5 cycles, 48 us or more; the long one reads 671 MB on
+    80 SMs, so it takes over 80 us)."""
+    from mxfp4_routed_expert_03_gb300 import MOE_INJECT_NONE, check, moe_linear_set_fault_injection
+    from mxfp4_routed_expert_03_gb300.linear import Fp8Rows, Linear
+    n, k = 10240, 65536
+    codes = torch.randint(0, 0x40, (n + 100, k), device="cuda", dtype=torch.uint8)
+    scales = torch.ones(100, k // 128, device="cuda")
+    long = Linear(k, n, codes[:n], torch.ones(n // 128, k // 128, device="cuda"))
+    long_x, long_out = Fp8Rows(codes[n:], scales), torch.empty(100, n, dtype=torch.bfloat16, device="cuda")
+    s = Setup(T, K, N, seed=14)
+    s.run()
+    want = s.out.clone()
+    check(moe_linear_set_fault_injection(s.linear.h, MOE_INJECT_NONE, 100_000), "limit")
+    for _ in range(3):
+        s.out.fill_(0)
+        check(long.forward(100, long_x, long_out), "moe_linear_forward")
+        s.run()
+        assert long.status() == 0 and s.linear.status() == 0
+        assert torch.equal(s.out, want)
+
+
 def test_no_tokens_and_refusals():
     from mxfp4_routed_expert_03_gb300 import MOE_ERR_INVALID_ARG, moe_linear_forward
     from mxfp4_routed_expert_03_gb300.linear import Fp8Rows, Linear
