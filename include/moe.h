@@ -667,7 +667,8 @@ void moe_norm_destroy(moe_norm *n);
  * multiples of 8; bases 16-byte aligned); for y8 d_model is a multiple of 16.
  * A bf16 output may be an input (same pointer and stride) but must not overlap
  * one otherwise. The squares are summed in fp32: a row whose sum passes its range
- * gives zeros. An infinity or NaN spreads over its row by the norm, and no
+ * gives zeros; one whose squares are below it is normed as if its sum were 0
+ * (with eps 0 that gives no finite values). An infinity or NaN spreads over its row by the norm, and no
  * further. Asynchronous on `stream`, no workspace. */
 int moe_add_norm(moe_norm *n, int32_t T, const uint16_t *x, int64_t x_stride,
                  const uint16_t *residual, int64_t residual_stride, uint16_t *total,

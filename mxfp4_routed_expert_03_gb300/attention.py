@@ -15,7 +15,7 @@ import torch
 from . import (_stream, lib, moe_attn_batch, moe_attn_create, moe_attn_desc, moe_attn_destroy,
                moe_attn_status, moe_attn_workspace_bytes, moe_kv_cache, moe_kv_code_bytes,
                moe_kv_scale_bytes, moe_rope_desc)
-from .checks import flat, on_device, rows
+from .checks import BITS16, bf16_rows, flat, on_device, rows
 from .workspace import Workspace
 
 _i32, _f32 = torch.int32, torch.float32
@@ -134,15 +134,15 @@ class Attention:
 
     def rope_append(self, T, q, k, v, positions, rope: Rope, q_out, slots, stream=None) -> int:
         """norm_rope of q into q_out and of k, which goes with v into the cache (q may be None with q_out)."""
-        if rope.width < self.head_dim:
-            raise ValueError("norm weights: head_dim elements")
+        if rope.width < self.head_dim or any(w is not None and w.dtype not in BITS16 for w in rope.tensors[1:]):
+            raise ValueError("norm weights: head_dim bf16 elements")
         on_device(self.cache["k_q"].get_device(), q, k, v, positions, q_out, slots, *rope.tensors)
         positions = flat(positions, T, _i32, "positions")
         slots = flat(slots, T, _i32, "slots")
-        q, qs = rows(q, T, self.q_width)
-        k, ks = rows(k, T, self.kv_width)
-        v, vs = rows(v, T, self.kv_width)
-        q_out, qos = rows(q_out, T, self.q_width)
+        q, qs = bf16_rows(q, T, self.q_width)
+        k, ks = bf16_rows(k, T, self.kv_width)
+        v, vs = bf16_rows(v, T, self.kv_width)
+        q_out, qos = bf16_rows(q_out, T, self.q_width)
         return lib().moe_rope_append(self.h, T, rope.ref, positions, q, qs, k, ks, v, vs, slots, q_out, qos,
                                      _stream(stream))
 

@@ -3,6 +3,8 @@ from __future__ import annotations
 
 import torch
 
+BITS16 = (torch.bfloat16, torch.int16, torch.uint16)  # bf16, or its bit patterns
+
 
 def rows(t, n: int, width: int):
     """Pointer and row stride of n token rows of `width` 16-bit elements ((None, 0) for None)."""
@@ -17,6 +19,13 @@ def rows(t, n: int, width: int):
     if have < n or cols < width or t.element_size() != 2:
         raise ValueError(f"token rows: {n} rows of {width} bf16 elements")
     return t.data_ptr(), stride
+
+
+def bf16_rows(t, n: int, width: int):
+    """As rows, for elements that are bf16 or its bit patterns."""
+    if t is not None and t.dtype not in BITS16:
+        raise ValueError("token rows: bf16 elements")
+    return rows(t, n, width)
 
 
 def flat(t, n: int, dtype, what: str):

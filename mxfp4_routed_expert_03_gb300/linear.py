@@ -13,19 +13,16 @@ import torch
 
 from . import (MOE_LINEAR_BF16, MOE_LINEAR_F32, _stream, lib, moe_fp8_rows, moe_linear_create, moe_linear_desc,
                moe_linear_destroy, moe_linear_status, moe_norm_create, moe_norm_desc, moe_norm_destroy)
-from .checks import on_device, rows
+from .checks import BITS16, bf16_rows, on_device
 
-_BITS16 = (torch.bfloat16, torch.int16, torch.uint16)  # bf16, or its bit patterns
 _BITS8 = (torch.float8_e4m3fn, torch.uint8, torch.int8)
 
 
 def _bf16(t, n: int, width: int, device: int):
     """Pointer and stride of n bf16 rows on the device ((None, 0) for None)."""
     if t is not None:
-        if t.dtype not in _BITS16:
-            raise ValueError("token rows: bf16 elements")
         on_device(device, t)
-    return rows(t, n, width)
+    return bf16_rows(t, n, width)
 
 
 class Fp8Rows:
@@ -65,7 +62,7 @@ class Norm:
         self.d, self.weight = d, weight
         self.device = torch.cuda.current_device()
         if weight is not None:
-            if weight.dtype not in _BITS16 or weight.numel() < d or not weight.is_contiguous():
+            if weight.dtype not in BITS16 or weight.numel() < d or not weight.is_contiguous():
                 raise ValueError(f"weight: {d} contiguous bf16 elements")
             on_device(self.device, weight)
         self.h = moe_norm_create(moe_norm_desc(d, eps, None if weight is None else weight.data_ptr()))

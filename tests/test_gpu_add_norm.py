@@ -110,6 +110,16 @@ def test_zero_rows_and_small_values(d):
     assert bool((decode(rows.q, rows.s)[1] == 0).all()) and float(rows.s[1, 0]) == 2.0 ** -126
 
 
+@pytest.mark.parametrize("T", [3, 2000])
+def test_a_sum_beyond_its_range_gives_zeros(T):
+    x, r, w = make(T, 1024, seed=12)
+    x[1] = 1e30
+    total, y, rows = run(x, r, w)
+    assert torch.equal(total[1], x[1]) and bool((y[1] == 0).all()) and bool((decode(rows.q, rows.s)[1] == 0).all())
+    others = torch.arange(T, device="cuda") != 1
+    verify(x[others], r[others], w, (total[others], y[others], type(rows)(rows.q.view(torch.uint8)[others].view(rows.q.dtype), rows.s[others])))
+
+
 @pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
 @pytest.mark.parametrize("d", [384, 7168])
 def test_not_finite(bad, d):

@@ -204,10 +204,15 @@ def test_no_tokens_and_refusals():
         assert s.one(q_out, **kw) == MOE_ERR_INVALID_ARG
     assert s.one(None) == MOE_ERR_INVALID_ARG
     for kw in (dict(q=s.q[:19]), dict(k=s.k[:, :64]), dict(v=s.v.float()), dict(slots=s.slots.long()), dict(slots=s.slots[:19]),
-               dict(positions=s.pos[:5]), dict(k=s.k.cpu()), dict(v=s.v.cpu()), dict(slots=s.slots.cpu()), dict(positions=s.pos.cpu())):
+               dict(positions=s.pos[:5]), dict(q=s.q.half()), dict(k=s.k.half()), dict(k=s.k.cpu()), dict(v=s.v.cpu()), dict(slots=s.slots.cpu()), dict(positions=s.pos.cpu())):
         with pytest.raises(ValueError):
             s.one(q_out, **kw)
+    for bad in (q_out.cpu(), q_out.half(), q_out[:19]):
+        with pytest.raises(ValueError):
+            s.one(bad)
+    from mxfp4_routed_expert_03_gb300.attention import Rope
+    half = Rope(s.rope.tensors[0], 64, False, 1e-6, s.rope.tensors[1].half(), s.rope.tensors[2])
     with pytest.raises(ValueError):
-        s.one(q_out.cpu())
+        s.attn.rope_append(20, s.q, s.k, s.v, s.pos, half, q_out, s.slots)
     torch.cuda.synchronize()
     assert bool((q_out == 7.0).all()) and all(bool((s.attn.cache[n] == 0).all()) for n in NAMES)
