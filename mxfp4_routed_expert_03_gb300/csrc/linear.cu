@@ -15,7 +15,7 @@
 //   many: tiles of 128 rows of x (TMEM lanes, so that a thread has one row and one factor per block) x 128 weight
 //   rows;
 //   very many: a pair of CTAs on 256 x 256, which halves what an SM reads per product.
-// Where tiles are few, the first two split K over the CTAs of a cluster, so that every SM reads; the parts are
+// Where tiles are few, the first two split K over the CTAs of a cluster, so that most SMs read; the parts are
 // joined through distributed shared memory in the order of the ranks.
 //
 // In each, one warp copies (TMA), one thread issues the MMAs, 4 or 8 warps add the blocks; one ring of stages,
@@ -111,7 +111,15 @@ __device__ __forceinline__ float4 join(const float *own, const float *recv, int 
     return w[0];
 }
 __device__ __forceinline__ float4 join(const float *own, const float *recv, int step, int rank, int S) {
-    return S == 2 ? join<2>(own, recv, step, rank) : S == 4 ? join<4>(own, recv, step, rank) : join<8>(own, recv, step, rank);
+    switch (S) {
+        case 2: return join<2>(own, recv, step, rank);
+        case 3: return join<3>(own, recv, step, rank);
+        case 4: return join<4>(own, recv, step, rank);
+        case 5: return join<5>(own, recv, step, rank);
+        case 6: return join<6>(own, recv, step, rank);
+        case 7: return join<7>(own, recv, step, rank);
+        default: return join<8>(own, recv, step, rank);
+    }
 }
 
 // After a timeout, by all threads: the copies and MMAs in flight end before the CTA leaves. A stage's last
@@ -141,8 +149,8 @@ struct Wide {
     static constexpr int SROW = 132;                    // row of a scale group: 128 rows of x and a gap (banks)
     static constexpr int SC_BASE = STAGES * STAGE_BYTES;  // scales of x [2][G][SROW], of the weights [2][G][2]
     static constexpr int PITCH = BN + 4;                // row of a part (banks)
-    static constexpr int RECV = SC_BASE + 2 * G * SROW * 4 + 2 * G * 2 * 4;  // parts [split][128 / split][PITCH]
-    static constexpr int BAR = RECV + 128 * PITCH * 4;
+    static constexpr int RECV = SC_BASE + 2 * G * SROW * 4 + 2 * G * 2 * 4;  // parts [split][rows / split][PITCH]
+    static constexpr int BAR = RECV + (128 + 7) * PITCH * 4;
     static constexpr int BYTES = 1024 + BAR + 256;
     static_assert((2 * STAGES + 7) * 8 + 12 <= 256, "barrier area");
     static_assert(STAGE_BYTES % 1024 == 0 && BYTES <= 232448, "shared memory");
@@ -311,6 +319,11 @@ __global__ void __launch_bounds__(Wide::THREADS, 1)
     int *s_issued = abort_flag + 1;        // stages the producer filled
     const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
     const int rank = (int)tc::cluster_rank(), S = (int)tc::cluster_size();
+    const int MT = (args.T + 127) / 128, NT = (args.N + BN - 1) / BN, KB = (args.K + BK - 1) / BK;
+    const int total = MT * NT, first = blockIdx.x / S, step = gridDim.x / S;
+    const int kb0 = KB * rank / S, nkb = KB * (rank + 1) / S - kb0;
+    // split: rows of the (one) tile, how many of them a CTA joins, how many this one does
+    const int rows = min(128, args.T - first % MT * 128), per = (rows + S - 1) / S, own = min(per, rows - rank * per);
     if (tid == 0) {
         *abort_flag = 0;
         *s_issued = 0;
@@ -326,7 +339,7 @@ __global__ void __launch_bounds__(Wide::THREADS, 1)
         tc::mbar_init(drain, 1);
         tc::mbar_init(never, 1);
         tc::fence_mbar_init();
-        if (S > 1) tc::mbar_arrive_expect_tx(recv, (S - 1) * (128 / S) * C::PITCH * 4);
+        if (S > 1 && own > 0) tc::mbar_arrive_expect_tx(recv, (S - 1) * own * C::PITCH * 4);
         tc::prefetch_map(&mW);
         tc::prefetch_map(&mX);
     }
@@ -339,9 +352,6 @@ __global__ void __launch_bounds__(Wide::THREADS, 1)
     tc::tc_fence_after();
     if (S > 1) tc::cluster_arrive();  // (1: this CTA's barriers are ready)
     const uint32_t tmem = *tmem_slot;
-    const int MT = (args.T + 127) / 128, NT = (args.N + BN - 1) / BN, KB = (args.K + BK - 1) / BK;
-    const int total = MT * NT, first = blockIdx.x / S, step = gridDim.x / S;
-    const int kb0 = KB * rank / S, nkb = KB * (rank + 1) / S - kb0;
     const long long LIMIT = args.timeout_cycles;
     volatile int *abort_p = abort_flag;
     auto fail = [&](void) {
@@ -465,20 +475,21 @@ __global__ void __launch_bounds__(Wide::THREADS, 1)
             tc::fence_proxy_async_smem();
             ok = tc::bar_and(1, 256, ok);
             tc::cluster_wait();  // (1)
-            if (ok && warp == 4) send_parts((const float *)smem, parts, recv, S, rank, 128, 128 / S, C::PITCH, lane);
-            ok = ok && tc::mbar_wait_warp(recv, 0, LIMIT, abort_p);
+            if (ok && warp == 4) send_parts((const float *)smem, parts, recv, S, rank, rows, per, C::PITCH, lane);
+            ok = ok && (own <= 0 || tc::mbar_wait_warp(recv, 0, LIMIT, abort_p));
             if (!ok && lane == 0) fail();
         }
     }
     if (S > 1) {
         tc::cluster_arrive();  // (2: this CTA has the parts of its rows)
         if (warp >= 4 && ok) {
-            const int R = 128 / S, t0 = first % MT * 128 + rank * R, n0 = first / MT * BN;
-            for (int u = tid - 128; u < R * BN / 4; u += 256) {
+            const int n0 = first / MT * BN;
+            const int64_t t0 = first % MT * 128 + rank * per;
+            for (int u = tid - 128; u < own * (BN / 4); u += 256) {
                 const int r = u / (BN / 4), c = u % (BN / 4) * 4;
-                if (t0 + r >= args.T || n0 + c >= args.N) continue;
+                if (n0 + c >= args.N) continue;
                 store4(args, (t0 + r) * args.out_stride + n0 + c,
-                       join((const float *)smem + (rank * R + r) * C::PITCH + c, parts + r * C::PITCH + c, R * C::PITCH, rank, S));
+                       join((const float *)smem + (rank * per + r) * C::PITCH + c, parts + r * C::PITCH + c, per * C::PITCH, rank, S));
             }
         }
         __syncwarp();
@@ -753,8 +764,8 @@ struct Narrow {
     static constexpr int G = 32 * EW / NT;                 // blocks whose scales are fetched at a time, one per thread
     static constexpr int PITCH = 132;                      // row of a part: 128 weight rows and a gap (banks)
     static constexpr int SC_BASE = STAGES * STAGE_BYTES;   // scales [2][G][NT]
-    static constexpr int RECV = SC_BASE + 2 * G * NT * 4;  // parts [split][NT / split][PITCH]
-    static constexpr int BAR = RECV + NT * PITCH * 4;
+    static constexpr int RECV = SC_BASE + 2 * G * NT * 4;  // parts [split][rows / split][PITCH]
+    static constexpr int BAR = RECV + (NT + 7) * PITCH * 4;
     static constexpr int BYTES = 1024 + BAR + 256;
     static_assert(NT * G == 32 * EW && STAGES * NT <= TMEM_COLS, "scale loads, accumulators");
     static_assert((2 * STAGES + 3) * 8 + 12 <= 256, "barrier area");
@@ -789,7 +800,7 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, 2)
     const int n0 = tile % NTILES * 128, t0 = tile / NTILES * NT;
     const int kb0 = KB * rank / S, nkb = KB * (rank + 1) / S - kb0;
     const int rows = min(NT, args.T - t0);
-    const int per = NT / S, mine = min(per, rows - rank * per);  // rows of x that a CTA joins, that this one does
+    const int per = (rows + S - 1) / S, mine = min(per, rows - rank * per);  // rows of x that a CTA joins, that this one does
     if (tid == 0) {
         *abort_flag = 0;
         *s_issued = 0;
@@ -963,12 +974,16 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, 2)
 
 namespace {
 
-// Which kernel, and the CTAs that share a tile's K (a power of two up to 8). Times of both sides in us.
-//   Few rows: as many CTAs per tile as fit on the SMs, two each, with two blocks of K at least (1 row of 7168 x
-//   9216: 1 CTA 15.0, 2 12.6, 4 10.8, 8 (which do not all fit) 12.6; of 7168 x 896: 1 12.9, 8 4.2).
+// Which kernel, and the CTAs (up to 8) that share a tile's K. Times of both sides in us.
+//   Few rows: the split of the least cost, of blocks per CTA (0.2 us each), the exchange (0.25, 0.02 a CTA) and two CTAs
+//   on an SM (0.35, where they are on a few SMs only 0.3 more). 1 row of 7168 x 9216 (72 tiles): by 1 15.0, 2 12.6, 3 11.8,
+//   4 10.8; of 7168 x 5632 (44): by 4 8.9, 6 7.5; of 2048 x 4096 (32): by 4 3.7, 8 4.0; of 4096 x 4096: by 4 5.6, 8 5.0;
+//   64 rows of 2048 x 2048 (16): by 6 5.1, 8 5.8; of 256 x 2048: by 1 3.8, 2 4.2. All clusters have to fit
+//   beside each other: 1 row of 7168 x 9600 (75) by 4 15.8, by 3 12.1.
 //   Many rows: the exchange of a 128 x 128 part costs about 2 us, so K is split where that saves more (128 rows of
-//   4096 x 5120 13.0 and 11.7, but of 2048 x 6144 8.5 and 9.0), and by 8 and 4 only where the clusters fit beside
-//   each other (1000 columns of 4096: 128 rows by 8 7.7, by 4 8.4; 200 rows by 8 12.7, by 4 8.4).
+//   4096 x 5120 (40 tiles): by 1 13.2, 2 11.9, 3 10.6, but of 2048 x 6144 (48) by 1 8.5, 2 9.4; of 2048 x 2816 (22) by 4 8.0, by 6
+//   8.1, of 4096 x 2816 9.2 and 9.0), and only by as many as fit (1000 columns of 4096: 128 rows (8 tiles) by 4 8.4, by 8 7.9;
+//   200 rows (16) by 6 8.3, by 8 11.8; 384 rows (24) by 4 8.9, by 6 15.1).
 //   Very many: by the times that the two kernels' waves take, which these sizes gave (waves of the many-row kernel
 //   and of pairs, times of both): 512 rows of 7168 x 9216 2, 1, 37.3, 28.1; 600 rows 3, 2, 50.6, 48.7; 8191 rows
 //   31, 16, 482, 384; 900 rows of 4096 x 5120 3, 2, 29.6, 31.3; 2049 rows 5, 3, 47.6, 45.9; 768 rows of 1536 x 7168
@@ -979,20 +994,34 @@ struct Plan {
     int split;
 };
 
+// Clusters of s CTAs that 152 SMs hold at a time with one CTA an SM (the occupancy query's answers), and with two
+// (found by the few-row kernel's times; 56 clusters of 5 from two rows on: 7168 x 7168 8.9, by 4 9.6; for one row
+// 10.9 and 9.6, so 54).
+constexpr int kClusters1[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
+constexpr int kClusters2[9] = {0, 304, 152, 92, 72, 56, 46, 38, 36};
+
 Plan plan_of(int T, int K, int N, int nsm) {
     const int KB = (K + BK - 1) / BK;
     if (T <= 64) {
         const int nt = T <= 16 ? 16 : T <= 32 ? 32 : 64;
         const int tiles = (N + 127) / 128;
-        int s = 8;
-        while (s > 1 && (tiles * s > 2 * nsm || KB < 2 * s)) s /= 2;
-        return {nt, false, s};
+        int best = 1;
+        for (int s = 1, least = INT32_MAX; s <= 8 && KB >= s; ++s) {
+            const int64_t clusters = (int64_t)tiles * 152;
+            if (s > 1 && clusters > (int64_t)(s == 5 && T == 1 ? 54 : kClusters2[s]) * nsm) continue;
+            const bool two = clusters > (int64_t)kClusters1[s] * nsm, uneven = two && (int64_t)tiles * s * 4 < 5 * nsm;
+            const int cost = 200 * ((KB + s - 1) / s) + 20 * s + 250 * (s > 1) + 350 * two + 300 * uneven;  // ns
+            if (cost < least) least = cost, best = s;
+        }
+        return {nt, false, best};
     }
     const int64_t tiles = (int64_t)((N + 127) / 128) * ((T + 127) / 128);
     const int64_t pairs = (int64_t)((N + 255) / 256) * ((T + 255) / 256);
     int s = 1;
     if (KB >= 16 && tiles * 8 <= nsm * 3 / 4) s = 8;
-    else if (KB >= 16 && tiles * 4 <= nsm * 7 / 8) s = 4;
+    else if (KB >= 32 && tiles * 6 <= nsm * 7 / 8) s = 6;
+    else if (KB >= 16 && tiles * 4 <= nsm * 15 / 16) s = 4;
+    else if (KB >= 20 && tiles * 3 <= nsm * 7 / 8) s = 3;
     else if (KB >= 24 && tiles * 2 <= nsm) s = 2;
     const int64_t waves = (tiles + nsm - 1) / nsm, pair_waves = (pairs + nsm / 2 - 1) / (nsm / 2);
     const bool pair = 5500 + pair_waves * (365 * KB + 1100) < 4000 + waves * (265 * KB + 400);  // ns

@@ -60,6 +60,23 @@ def test_prefill(T, K, N):
     s.verify()
 
 
+# K shared by 2 to 8 CTAs; rows that these do not divide, or fewer of them
+@pytest.mark.parametrize("T", [1, 3, 13, 27, 61])
+@pytest.mark.parametrize("K,N", [(1040, 13000), (2304, 10240), (1536, 7168), (2560, 5120), (4096, 5120), (4096, 4864), (4096, 4096)])
+def test_shared_by_any_number(T, K, N):
+    s = Setup(T, K, N, seed=15)
+    s.run()
+    s.verify()
+
+
+@pytest.mark.parametrize("T,K,N", [(67, 2048, 1000), (129, 4096, 1000), (200, 4096, 1000), (131, 2048, 2000), (100, 4096, 5120),
+                                   (127, 2560, 5000), (70, 4096, 6400)])
+def test_many_rows_shared_by_any_number(T, K, N):
+    s = Setup(T, K, N, seed=16, dtype=torch.float32)
+    s.run()
+    s.verify()
+
+
 @pytest.mark.parametrize("T", [1, 20, 70, 200, 700])
 def test_whole_numbers_are_exact(T):
     """Small whole codes and scales that are powers of two: every sum is a whole number of at most 24
@@ -315,7 +332,7 @@ def test_no_tokens_and_refusals():
     s.verify()
 
 
-@pytest.mark.parametrize("T,N", [(1, 1400), (40, 1400), (100, 1400), (200, 1400), (600, 1400), (500, 5120), (1500, 7000)])
+@pytest.mark.parametrize("T,N", [(1, 1400), (40, 1400), (40, 5120), (100, 1400), (140, 1400), (200, 1400), (600, 1400), (500, 5120), (1500, 7000)])
 def test_stall_times_out_then_recovers(T, N):
     """With the test hook an MMA issuer waits, under a limit of 2e6 SM cycles, on a barrier that
     nothing signals: the status is recorded, copies and products in flight end, tensor memory is
