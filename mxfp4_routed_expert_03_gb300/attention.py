@@ -55,6 +55,7 @@ class Rope:
         if any(w.element_size() != 2 or not w.is_contiguous() for w in weights):
             raise ValueError("norm weights: contiguous bf16 elements")
         self.width = min([w.numel() for w in weights], default=1 << 30)  # that the weights have
+        self.bf16 = all(w.dtype in BITS16 for w in weights)
         self.desc = moe_rope_desc(rope_dim, int(interleaved), n_pos, eps, _ptr(cos_sin),
                                   _ptr(q_weight), _ptr(k_weight))
         self.ref = ctypes.byref(self.desc)
@@ -101,6 +102,7 @@ class Attention:
                 raise ValueError(f"cache {name}: {need} contiguous bytes")
         self.h = moe_attn_create(self.desc, moe_kv_cache(*[cache[n].data_ptr() for n in CACHE_NAMES]))
         self._space = Workspace(cache["k_q"].device)
+        self.device = cache["k_q"].get_device()
         self._need = (None, 0)  # the last batch bounds and their workspace bytes
 
     def close(self):
@@ -134,15 +136,16 @@ class Attention:
 
     def rope_append(self, T, q, k, v, positions, rope: Rope, q_out, slots, stream=None) -> int:
         """norm_rope of q into q_out and of k, which goes with v into the cache (q may be None with q_out)."""
-        if rope.width < self.head_dim or any(w is not None and w.dtype not in BITS16 for w in rope.tensors[1:]):
+        dev = self.device
+        if rope.width < self.head_dim or not rope.bf16:
             raise ValueError("norm weights: head_dim bf16 elements")
-        on_device(self.cache["k_q"].get_device(), q, k, v, positions, q_out, slots, *rope.tensors)
+        on_device(dev, positions, slots, *rope.tensors)
         positions = flat(positions, T, _i32, "positions")
         slots = flat(slots, T, _i32, "slots")
-        q, qs = bf16_rows(q, T, self.q_width)
-        k, ks = bf16_rows(k, T, self.kv_width)
-        v, vs = bf16_rows(v, T, self.kv_width)
-        q_out, qos = bf16_rows(q_out, T, self.q_width)
+        q, qs = bf16_rows(q, T, self.q_width, dev)
+        k, ks = bf16_rows(k, T, self.kv_width, dev)
+        v, vs = bf16_rows(v, T, self.kv_width, dev)
+        q_out, qos = bf16_rows(q_out, T, self.q_width, dev)
         return lib().moe_rope_append(self.h, T, rope.ref, positions, q, qs, k, ks, v, vs, slots, q_out, qos,
                                      _stream(stream))
 

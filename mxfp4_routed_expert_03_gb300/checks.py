@@ -21,11 +21,21 @@ def rows(t, n: int, width: int):
     return t.data_ptr(), stride
 
 
-def bf16_rows(t, n: int, width: int):
-    """As rows, for elements that are bf16 or its bit patterns."""
-    if t is not None and t.dtype not in BITS16:
-        raise ValueError("token rows: bf16 elements")
-    return rows(t, n, width)
+def bf16_rows(t, n: int, width: int, device: int):
+    """As rows, of bf16 elements (or their bit patterns) on CUDA device `device`."""
+    if t is None:
+        return None, 0
+    if t.dtype not in BITS16 or t.get_device() != device:
+        raise ValueError(f"token rows: bf16 elements on the handle's device cuda:{device}")
+    try:
+        (stride, one), (have, cols) = t.stride(), t.shape
+    except ValueError:
+        one = 0  # not 2D
+    if one != 1:
+        raise ValueError("token rows: a 2D tensor with contiguous rows")
+    if have < n or cols < width:
+        raise ValueError(f"token rows: {n} rows of {width} bf16 elements")
+    return t.data_ptr(), stride
 
 
 def flat(t, n: int, dtype, what: str):

@@ -18,13 +18,6 @@ from .checks import BITS16, bf16_rows, on_device
 _BITS8 = (torch.float8_e4m3fn, torch.uint8, torch.int8)
 
 
-def _bf16(t, n: int, width: int, device: int):
-    """Pointer and stride of n bf16 rows on the device ((None, 0) for None)."""
-    if t is not None:
-        on_device(device, t)
-    return bf16_rows(t, n, width)
-
-
 class Fp8Rows:
     """Rows of E4M3 codes with a scale per 128 columns; keeps the tensors. q: [T][d]
     (float8_e4m3fn or bytes), s: fp32 [T][ceil(d / 128)]; rows of either may be strided."""
@@ -81,10 +74,10 @@ class Norm:
     def forward(self, T, x, residual=None, total=None, y=None, y8: Fp8Rows | None = None, stream=None) -> int:
         """total: x + residual; y: the norm of that in bf16; y8: in 8 bits (each may be left out)."""
         dev, d = self.device, self.d
-        x, xs = _bf16(x, T, d, dev)
-        residual, rs = _bf16(residual, T, d, dev)
-        total, ts = _bf16(total, T, d, dev)
-        y, ys = _bf16(y, T, d, dev)
+        x, xs = bf16_rows(x, T, d, dev)
+        residual, rs = bf16_rows(residual, T, d, dev)
+        total, ts = bf16_rows(total, T, d, dev)
+        y, ys = bf16_rows(y, T, d, dev)
         if y8 is not None:
             y8.check(T, d, dev)
             y8 = y8.ref
@@ -130,7 +123,7 @@ class Linear:
             on_device(dev, out)
             kind, ptr, stride = MOE_LINEAR_F32, out.data_ptr(), out.stride(0)
         else:
-            kind, (ptr, stride) = MOE_LINEAR_BF16, _bf16(out, T, self.d_out, dev)
+            kind, (ptr, stride) = MOE_LINEAR_BF16, bf16_rows(out, T, self.d_out, dev)
         return lib().moe_linear_forward(self.h, T, x.ref, ptr, stride, kind, _stream(stream))
 
     def status(self, stream=None) -> int:
