@@ -548,7 +548,7 @@ __device__ __forceinline__ void mma_block_pair(uint32_t d, uint32_t a_s, uint32_
 // accumulator read by both; `free1` in the first CTA, the second half's accumulator read by both; `done` in
 // each CTA, the MMAs of a half.
 // Bound: a block takes 375 ns; its copies alone 306, its additions alone 300, its MMAs alone 274. 8191 rows of 7168 x
-// 9216 374 to 382 us (2.85 PFLOP/s), 432 when it runs for seconds at the power limit.
+// 9216 374 to 384 us (2.85 PFLOP/s), 430 when it runs for seconds at the power limit.
 __global__ void __launch_bounds__(Pair::THREADS, 1)
     moe_linear_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX,
                            const MoeLinearArgs args) {
@@ -776,7 +776,7 @@ struct Narrow {
 }  // namespace
 
 // Bound: the weights, once through HBM; from 32 rows on also what an SM takes in from L2, and the exchange. 1 row of
-// 7168 x 9216 10.6 us (6.2 TB/s), 64 rows of 7168 x 7168 13.1 (3.9 TB/s). Two CTAs an SM: with 16 rows ten
+// 7168 x 9216 10.6 us (6.2 TB/s), 64 rows of 7168 x 7168 12.5 (4.2 TB/s). Two CTAs an SM: with 16 rows ten
 // stages, 180 KB, on their way on each.
 template <int NT>
 __global__ void __launch_bounds__(Narrow<NT>::THREADS, 2)
