@@ -92,11 +92,12 @@ struct Ring {
 // A CTA's part of a tile, [rows][pitch] fp32 in `stage`, goes to the CTAs of the cluster that join `per` of its
 // rows each, rank 0 the first: into their `recv` area [S][per][pitch], counted on their `bar`; its own rows stay.
 // By one warp, once every CTA of the cluster has its barriers ready.
-__device__ __forceinline__ void send_parts(const float *stage, float *recv, uint64_t *bar, int S, int rank, int rows, int per,
-                                           int pitch, int lane) {
+__device__ __forceinline__ void send_parts(const float *stage, float *recv, uint64_t *bar, int S, int rank, int rows,
+                                           int per, int pitch, int lane) {
     const int to = (rank + lane) % S, n = min(per, rows - to * per);
     if (lane > 0 && lane < S && n > 0)
-        tc::bulk_copy_s2peer(tc::peer_addr(recv + rank * per * pitch, to), stage + to * per * pitch, n * pitch * 4, tc::peer_addr(bar, to));
+        tc::bulk_copy_s2peer(tc::peer_addr(recv + rank * per * pitch, to), stage + to * per * pitch, n * pitch * 4,
+                             tc::peer_addr(bar, to));
     __syncwarp();
 }
 
@@ -265,7 +266,8 @@ __device__ __forceinline__ void store_rows(const MoeLinearArgs &args, int64_t t0
 #pragma unroll
             for (int i = 0; i < L; ++i)
                 if (32 / L * i + lane / L < rows)
-                    *(uint4 *)(out + 32 / L * i * args.out_stride * bytes) = *(const uint4 *)(from + 32 / L * i * PITCH);
+                    *(uint4 *)(out + 32 / L * i * args.out_stride * bytes) =
+                        *(const uint4 *)(from + 32 / L * i * PITCH);
         __syncwarp();
     };
     if (args.out_f32) {
@@ -284,7 +286,8 @@ __device__ __forceinline__ void store_rows(const MoeLinearArgs &args, int64_t t0
 #pragma unroll
             for (int j = 0; j < L; ++j) {
                 const float2 *v = sum + SEG / 4 * c + 4 * j;
-                *(uint4 *)(mine + 16 * j) = make_uint4(bf16x2(v[0].x, v[0].y), bf16x2(v[1].x, v[1].y), bf16x2(v[2].x, v[2].y), bf16x2(v[3].x, v[3].y));
+                *(uint4 *)(mine + 16 * j) = make_uint4(bf16x2(v[0].x, v[0].y), bf16x2(v[1].x, v[1].y),
+                                                       bf16x2(v[2].x, v[2].y), bf16x2(v[3].x, v[3].y));
             }
             copy(SEG / 2 * c, 8, 2);
         }
@@ -297,7 +300,8 @@ __device__ __forceinline__ void store_rows(const MoeLinearArgs &args, int64_t t0
 // has been read (an arrival of every adding warp), so the issuer has one wait per block; `done` when its MMAs
 // are finished: its memory is free, its accumulator is full.
 // Bound: an SM takes in about 62 bytes a cycle from L2, 276 ns for the 32 KB of a block (MMAs alone 178 ns, all
-// together 306). 333 rows of 4096 x 5120 12.0 us, 2049 of 4096 x 1000 to fp32 12.1: 32 of these blocks, then start and end.
+// together 306). 333 rows of 4096 x 5120 12.1 us, 2049 of 4096 x 1000 to fp32 12.2: 32 of these blocks, then start
+// and end.
 __global__ void __launch_bounds__(Wide::THREADS, 1)
     moe_linear_wide_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX,
                            const MoeLinearArgs args) {
@@ -413,8 +417,8 @@ __global__ void __launch_bounds__(Wide::THREADS, 1)
             for (int tile = first; tile < total && ok; tile += step)
                 for (int g = 0; g < nkb && ok; g += C::G, ++it) {
                     const int b = it & 1, use = it >> 1;
-                    ok = load_scales<1, C::SROW>(args, xsc + b * C::G * C::SROW, wsc + b * 2 * C::G, tile % MT * 128, tile / MT, kb0, g,
-                                                 nkb, KB, lane, [&] {
+                    ok = load_scales<1, C::SROW>(args, xsc + b * C::G * C::SROW, wsc + b * 2 * C::G, tile % MT * 128,
+                                                 tile / MT, kb0, g, nkb, KB, lane, [&] {
                         return use == 0 || tc::mbar_wait_warp(&sempty[b], (use - 1) & 1, LIMIT, abort_p);
                     });
                     if (ok && lane == 0) tc::mbar_arrive(&sfull[b]);
@@ -468,7 +472,8 @@ __global__ void __launch_bounds__(Wide::THREADS, 1)
                     *(float4 *)(o + 2 * j) = make_float4(sum[j].x, sum[j].y, sum[j + 1].x, sum[j + 1].y);
                 break;  // (one tile per cluster)
             }
-            store_rows<128>(args, (int64_t)(tile % MT) * 128 + q * 32, n0, sum, smem + C::RECV + (warp - 4) * 4608, lane);
+            store_rows<128>(args, (int64_t)(tile % MT) * 128 + q * 32, n0, sum, smem + C::RECV + (warp - 4) * 4608,
+                            lane);
         }
         if (!ok && lane == 0) fail();
         if (S > 1) {
@@ -489,7 +494,8 @@ __global__ void __launch_bounds__(Wide::THREADS, 1)
                 const int r = u / (BN / 4), c = u % (BN / 4) * 4;
                 if (n0 + c >= args.N) continue;
                 store4(args, (t0 + r) * args.out_stride + n0 + c,
-                       join((const float *)smem + (rank * per + r) * C::PITCH + c, parts + r * C::PITCH + c, per * C::PITCH, rank, S));
+                       join((const float *)smem + (rank * per + r) * C::PITCH + c, parts + r * C::PITCH + c,
+                            per * C::PITCH, rank, S));
             }
         }
         __syncwarp();
@@ -675,8 +681,8 @@ __global__ void __launch_bounds__(Pair::THREADS, 1)
             for (int tile = first; tile < total && ok; tile += step)
                 for (int g = 0; g < KB && ok; g += C::G, ++it) {
                     const int b = it & 1, use = it >> 1;
-                    ok = load_scales<2, C::SROW>(args, xsc + b * C::G * C::SROW, wsc + b * 2 * C::G, tile % MT * 256 + rank * 128,
-                                                 tile / MT * 2, 0, g, KB, KB, lane, [&] {
+                    ok = load_scales<2, C::SROW>(args, xsc + b * C::G * C::SROW, wsc + b * 2 * C::G,
+                                                 tile % MT * 256 + rank * 128, tile / MT * 2, 0, g, KB, KB, lane, [&] {
                         return use == 0 || tc::mbar_wait_warp(&sempty[b], (use - 1) & 1, LIMIT, abort_p);
                     });
                     if (ok && lane == 0) tc::mbar_arrive(&sfull[b]);
@@ -800,7 +806,8 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, 2)
     const int n0 = tile % NTILES * 128, t0 = tile / NTILES * NT;
     const int kb0 = KB * rank / S, nkb = KB * (rank + 1) / S - kb0;
     const int rows = min(NT, args.T - t0);
-    const int per = (rows + S - 1) / S, mine = min(per, rows - rank * per);  // rows of x that a CTA joins, that this one does
+    // rows of x that a CTA joins, that this one does
+    const int per = (rows + S - 1) / S, mine = min(per, rows - rank * per);
     if (tid == 0) {
         *abort_flag = 0;
         *s_issued = 0;
@@ -955,8 +962,8 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, 2)
                 const int j = u / 32, n = n0 + u % 32 * 4;
                 if (n < args.N)
                     store4(args, (int64_t)(t0 + rank * per + j) * args.out_stride + n,
-                           join((const float *)smem + (rank * per + j) * C::PITCH + u % 32 * 4, parts + j * C::PITCH + u % 32 * 4,
-                                per * C::PITCH, rank, S));
+                           join((const float *)smem + (rank * per + j) * C::PITCH + u % 32 * 4,
+                                parts + j * C::PITCH + u % 32 * 4, per * C::PITCH, rank, S));
             }
         }
         __syncwarp();
@@ -975,15 +982,15 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, 2)
 namespace {
 
 // Which kernel, and the CTAs (up to 8) that share a tile's K. Times of both sides in us.
-//   Few rows: the split of the least cost, of blocks per CTA (0.2 us each), the exchange (0.25, 0.02 a CTA) and two CTAs
-//   on an SM (0.35, where they are on a few SMs only 0.3 more). 1 row of 7168 x 9216 (72 tiles): by 1 15.0, 2 12.6, 3 11.8,
-//   4 10.8; of 7168 x 5632 (44): by 4 8.9, 6 7.5; of 2048 x 4096 (32): by 4 3.7, 8 4.0; of 4096 x 4096: by 4 5.6, 8 5.0;
-//   64 rows of 2048 x 2048 (16): by 6 5.1, 8 5.8; of 256 x 2048: by 1 3.8, 2 4.2. All clusters have to fit
-//   beside each other: 1 row of 7168 x 9600 (75) by 4 15.8, by 3 12.1.
+//   Few rows: the split of the least cost, of blocks per CTA (0.2 us each), the exchange (0.25, 0.02 a CTA) and two
+//   CTAs on an SM (0.35, where they are on a few SMs only 0.3 more). 1 row of 7168 x 9216 (72 tiles): by 1 15.0, 2
+//   12.6, 3 11.8, 4 10.8; of 7168 x 5632 (44): by 4 8.9, 6 7.5; of 2048 x 4096 (32): by 4 3.7, 8 4.0; of 4096 x 4096:
+//   by 4 5.6, 8 5.0; 64 rows of 2048 x 2048 (16): by 6 5.1, 8 5.8; of 256 x 2048: by 1 3.8, 2 4.2. All clusters have
+//   to fit beside each other: 1 row of 7168 x 9600 (75) by 4 15.8, by 3 12.1.
 //   Many rows: the exchange of a 128 x 128 part costs about 2 us, so K is split where that saves more (128 rows of
-//   4096 x 5120 (40 tiles): by 1 13.2, 2 11.9, 3 10.6, but of 2048 x 6144 (48) by 1 8.5, 2 9.4; of 2048 x 2816 (22) by 4 8.0, by 6
-//   8.1, of 4096 x 2816 9.2 and 9.0), and only by as many as fit (1000 columns of 4096: 128 rows (8 tiles) by 4 8.4, by 8 7.9;
-//   200 rows (16) by 6 8.3, by 8 11.8; 384 rows (24) by 4 8.9, by 6 15.1).
+//   4096 x 5120 (40 tiles): by 1 13.2, 2 11.9, 3 10.6, but of 2048 x 6144 (48) by 1 8.5, 2 9.4; of 2048 x 2816 (22) by
+//   4 8.0, by 6 8.1, of 4096 x 2816 9.2 and 9.0), and only by as many as fit (1000 columns of 4096: 128 rows (8 tiles)
+//   by 4 8.4, by 8 7.9; 200 rows (16) by 6 8.3, by 8 11.8; 384 rows (24) by 4 8.9, by 6 15.1).
 //   Very many: by the times that the two kernels' waves take, which these sizes gave (waves of the many-row kernel
 //   and of pairs, times of both): 512 rows of 7168 x 9216 2, 1, 37.3, 28.1; 600 rows 3, 2, 50.6, 48.7; 8191 rows
 //   31, 16, 482, 384; 900 rows of 4096 x 5120 3, 2, 29.6, 31.3; 2049 rows 5, 3, 47.6, 45.9; 768 rows of 1536 x 7168
@@ -1049,20 +1056,24 @@ cudaError_t launch_split(void (*kern)(KArgs...), int64_t grid, int threads, int 
 }
 
 template <int NT>
-cudaError_t launch_narrow(int split, cudaStream_t st, const CUtensorMap &w, const CUtensorMap &x, const MoeLinearArgs &a) {
+cudaError_t launch_narrow(int split, cudaStream_t st, const CUtensorMap &w, const CUtensorMap &x,
+                          const MoeLinearArgs &a) {
     const int64_t tiles = (int64_t)((a.N + 127) / 128) * ((a.T + NT - 1) / NT);
-    return launch_split(moe_linear_narrow_kernel<NT>, tiles * split, Narrow<NT>::THREADS, Narrow<NT>::BYTES, split, st, w, x, a);
+    return launch_split(moe_linear_narrow_kernel<NT>, tiles * split, Narrow<NT>::THREADS, Narrow<NT>::BYTES, split, st, w,
+                        x, a);
 }
 
-cudaError_t launch_wide(int split, int nsm, cudaStream_t st, const CUtensorMap &w, const CUtensorMap &x, const MoeLinearArgs &a) {
+cudaError_t launch_wide(int split, int nsm, cudaStream_t st, const CUtensorMap &w, const CUtensorMap &x,
+                        const MoeLinearArgs &a) {
     const int64_t tiles = (int64_t)((a.T + 127) / 128) * ((a.N + 127) / 128);
-    return launch_split(moe_linear_wide_kernel, split > 1 ? tiles * split : tiles < nsm ? tiles : nsm, Wide::THREADS, Wide::BYTES,
-                        split, st, w, x, a);
+    return launch_split(moe_linear_wide_kernel, split > 1 ? tiles * split : tiles < nsm ? tiles : nsm, Wide::THREADS,
+                        Wide::BYTES, split, st, w, x, a);
 }
 
 cudaError_t launch_pair(int nsm, cudaStream_t st, const CUtensorMap &w, const CUtensorMap &x, const MoeLinearArgs &a) {
     const int64_t tiles = (int64_t)((a.T + 255) / 256) * ((a.N + 255) / 256), pairs = nsm / 2;
-    return launch_split(moe_linear_pair_kernel, 2 * (tiles < pairs ? tiles : pairs), Pair::THREADS, Pair::BYTES, 2, st, w, x, a);
+    return launch_split(moe_linear_pair_kernel, 2 * (tiles < pairs ? tiles : pairs), Pair::THREADS, Pair::BYTES, 2, st, w,
+                        x, a);
 }
 
 }  // namespace

@@ -43,7 +43,8 @@ __device__ __forceinline__ uint4 add8(const uint4 &x, const uint4 &y) {
     uint32_t r[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&u[i]), *reinterpret_cast<const __nv_bfloat162 *>(&v[i]));
+        const __nv_bfloat162 h = __hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&u[i]),
+                                         *reinterpret_cast<const __nv_bfloat162 *>(&v[i]));
         r[i] = *reinterpret_cast<const uint32_t *>(&h);
     }
     return make_uint4(r[0], r[1], r[2], r[3]);
@@ -64,8 +65,8 @@ struct Place {
 // Row t (of which this thread has the chunks with live[i]) from its loaded chunks to its outputs; `inv_d` = 1 / d.
 // `part`: a word of shared memory per warp.
 template <int CH, bool RES, bool NORM>
-__device__ __forceinline__ void row_out(const MoeNormArgs &a, const Place &p, int64_t t, const bool (&live)[CH], float inv_d,
-                                        uint4 (&x)[CH], const uint4 (&r)[CH], const uint4 (&w)[CH], float *part) {
+__device__ __forceinline__ void row_out(const MoeNormArgs &a, const Place &p, int64_t t, const bool (&live)[CH],
+                                        float inv_d, uint4 (&x)[CH], const uint4 (&r)[CH], const uint4 (&w)[CH], float *part) {
     const int lane = threadIdx.x & 31;
     float v[CH][8];
     float ss = 0.f;
@@ -123,7 +124,8 @@ __device__ __forceinline__ void row_out(const MoeNormArgs &a, const Place &p, in
         uint32_t q[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-            q[k] = to_e4m3x2(v[i][4 * k] * f, v[i][4 * k + 1] * f) | to_e4m3x2(v[i][4 * k + 2] * f, v[i][4 * k + 3] * f) << 16;
+            q[k] = to_e4m3x2(v[i][4 * k] * f, v[i][4 * k + 1] * f) |
+                   to_e4m3x2(v[i][4 * k + 2] * f, v[i][4 * k + 3] * f) << 16;
         if (!live[i]) continue;
         *(uint2 *)(code + 8 * i * p.threads) = make_uint2(q[0], q[1]);
         if ((p.tid & 15) == 0)  // (m is not below infinity: it is that, or NaN)
@@ -225,8 +227,8 @@ int warps_of(int d, int ch) { return (d / 8 + 32 * ch - 1) / (32 * ch); }
 template <int CH, bool RES, bool NORM>
 cudaError_t launch(const MoeNormArgs &a, cudaStream_t st) {
     const int warps = warps_of(a.d, CH), rows = a.T > 1 && warps < 8 ? 8 / warps : 1;
-    return launch_pdl_ready(moe_norm_kernel<CH, RES, NORM>, dim3((unsigned)((a.T + rows - 1) / rows)), dim3(32 * warps * rows), 0,
-                            st, a, warps);
+    return launch_pdl_ready(moe_norm_kernel<CH, RES, NORM>, dim3((unsigned)((a.T + rows - 1) / rows)),
+                            dim3(32 * warps * rows), 0, st, a, warps);
 }
 
 template <bool RES, bool NORM>
@@ -238,9 +240,9 @@ cudaError_t launch(const MoeNormArgs &a, int nsm, cudaStream_t st) {
     const int warps = warps_of(a.d, CH_STREAM), rows = warps < 8 ? 8 / warps : 1, threads = 32 * warps * rows;
     const int smem = 2 * CH_STREAM * (RES ? 2 : 1) * threads * 16;
     // (the registers of 1024 threads on an SM, and at most 128 KB of rows)
-    const int64_t blocks = (a.T + rows - 1) / rows, most = (int64_t)nsm * (1024 / threads);
-    return launch_pdl_ready(moe_norm_stream_kernel<RES, NORM>, dim3((unsigned)(blocks < most ? blocks : most)), dim3(threads), smem,
-                            st, a, warps);
+    const int64_t blocks = ((int64_t)a.T + rows - 1) / rows, most = (int64_t)nsm * (1024 / threads);
+    return launch_pdl_ready(moe_norm_stream_kernel<RES, NORM>, dim3((unsigned)(blocks < most ? blocks : most)),
+                            dim3(threads), smem, st, a, warps);
 }
 
 template <bool RES, bool NORM>

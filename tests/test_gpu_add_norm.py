@@ -183,6 +183,26 @@ def test_many_rows_in_place_on_a_stream_and_in_a_graph():
     assert bool((wide[T] == 7.0).all()) and bool((wide[:, d:d + 8] == 7.0).all())
 
 
+def test_as_many_rows_as_the_count_holds():
+    """2^31 - 1 rows of 8, in place (34 GB)."""
+    from mxfp4_routed_expert_03_gb300 import check
+    from mxfp4_routed_expert_03_gb300.linear import Norm
+    T, d = 2 ** 31 - 1, 8
+    if torch.cuda.mem_get_info()[0] < 40e9:
+        pytest.skip("needs 40 GB")
+    x = torch.zeros(T, d, dtype=torch.bfloat16, device="cuda")
+    some = torch.tensor([0, 2 ** 28 + 1, 2 ** 30, T - 9, T - 1], device="cuda")
+    few, _, w = make(5, d, seed=13, residual=False)
+    x[some] = few
+    check(Norm(d, 1e-6, w).forward(T, x, y=x), "moe_add_norm")
+    got = x[some]
+    x[some] = 0
+    assert int(torch.count_nonzero(x[:1000])) == 0 and int(torch.count_nonzero(x[-1000:])) == 0
+    verify(few, None, w, (None, got, None))
+    del x
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("bad", [float("inf"), float("nan")])
 def test_many_rows_not_finite(bad):
     T, d = 2000, 1024

@@ -275,6 +275,28 @@ def test_weights_written_right_before_the_call_count():
         assert torch.equal(s.out, new.out)
 
 
+def test_as_many_rows_as_are_taken():
+    """2^31 - 513 rows of 16 (77 GB); one more is refused."""
+    from mxfp4_routed_expert_03_gb300 import MOE_ERR_UNSUPPORTED, check, moe_linear_forward
+    from mxfp4_routed_expert_03_gb300.linear import Fp8Rows
+    T = 2 ** 31 - 1 - 512
+    if torch.cuda.mem_get_info()[0] < 90e9:
+        pytest.skip("needs 90 GB")
+    s = Setup(5, 16, 8, seed=17)
+    rows = Fp8Rows(torch.zeros(T, 16, dtype=torch.uint8, device="cuda"), torch.ones(T, 1, device="cuda"))
+    some = torch.tensor([0, 2 ** 27 + 1, 2 ** 30, T - 129, T - 1], device="cuda")
+    rows.q[some], rows.s[some] = s.xq.view(torch.uint8), s.xs
+    out = torch.empty(T, 8, dtype=torch.bfloat16, device="cuda")
+    assert moe_linear_forward(s.linear.h, T + 1, rows.desc, out, 8, 0) == MOE_ERR_UNSUPPORTED
+    check(s.linear.forward(T, rows, out), "moe_linear_forward")
+    s.verify(out[some])
+    out[some] = 0
+    for part in (out[:1000], out[2 ** 30 - 500:2 ** 30 + 500], out[-1000:]):
+        assert bool((part == 0).all())
+    del rows, out, part
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("T,K,N", [(3, 512, 512), (100, 512, 512), (300, 1536, 7168)])
 def test_the_kernel_before_may_take_long(T, K, N):
     """A product that starts beside a long one on the SMs that this leaves free, and waits for its end,
