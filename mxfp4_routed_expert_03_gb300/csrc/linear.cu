@@ -10,8 +10,8 @@
 // tensor core's accumulator truncates.
 //
 // Three kernels:
-//   few rows (up to 64), where reading the weights is what counts: tiles of 128 weight rows (TMEM lanes) x all
-//   rows of x;
+//   few rows (up to 64; more where the weights are few), where reading the weights is what counts: tiles of 128
+//   weight rows (TMEM lanes) x 16, 32 or 64 rows of x;
 //   many: tiles of 128 rows of x (TMEM lanes, so that a thread has one row and one factor per block) x 128 weight
 //   rows;
 //   very many: a pair of CTAs on 256 x 256, which halves what an SM reads per product.
@@ -987,6 +987,10 @@ namespace {
 //   12.6, 3 11.8, 4 10.8; of 7168 x 5632 (44): by 4 8.9, 6 7.5; of 2048 x 4096 (32): by 4 3.7, 8 4.0; of 4096 x 4096:
 //   by 4 5.6, 8 5.0; 64 rows of 2048 x 2048 (16): by 6 5.1, 8 5.8; of 256 x 2048: by 1 3.8, 2 4.2. All clusters have
 //   to fit beside each other: 1 row of 7168 x 9600 (75) by 4 15.8, by 3 12.1.
+//   Rows per tile: all, or fewer where more tiles find SMs to run on, up to 256 rows or so of few weights; both
+//   kernels' times are estimated, and a change has to win 8 or 10 in a hundred. 64 rows of 1040 x 776: tiles of 64 4.7,
+//   of 16 3.4; of 4096 x 5120: 9.0 and 10.6. 128 rows of 4096 x 1000: tiles of 32 5.6, of 128 (the other kernel) 8.0;
+//   of 4096 x 4096 10.0 and 9.7; 256 rows of 7168 x 264: tiles of 64 6.9, of 128 8.4.
 //   Many rows: the exchange of a 128 x 128 part costs about 2 us, so K is split where that saves more (128 rows of
 //   4096 x 5120 (40 tiles): by 1 13.2, 2 11.9, 3 10.6, but of 2048 x 6144 (48) by 1 8.5, 2 9.4; of 2048 x 2816 (22) by
 //   4 8.0, by 6 8.1, of 4096 x 2816 9.2 and 9.0), and only by as many as fit (1000 columns of 4096: 128 rows (8 tiles)
@@ -1007,22 +1011,43 @@ struct Plan {
 constexpr int kClusters1[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
 constexpr int kClusters2[9] = {0, 304, 152, 92, 72, 56, 46, 38, 36};
 
+// Split (0: too many tiles for tiles of less than all rows) and about the time, ns, of the few-row kernel with tiles of
+// nt rows. What a block takes is what it moves through shared memory, so two CTAs on an SM take nearly twice as long.
+struct Few {
+    int split;
+    int64_t ns;
+};
+
+Few few_rows(int nt, int T, int K, int N, int nsm) {
+    const int KB = (K + BK - 1) / BK, i = nt == 16 ? 0 : nt == 32 ? 1 : 2;
+    const int64_t tiles = (int64_t)((N + 127) / 128) * ((T + nt - 1) / nt), clusters = tiles * 152;
+    if (T > nt && clusters > (int64_t)kClusters2[1] * nsm) return {0, 0};
+    Few few = {1, 0};
+    for (int s = 1, least = INT32_MAX; s <= 8 && KB >= s; ++s) {
+        if (s > 1 && clusters > (int64_t)(s == 5 && T == 1 ? 54 : kClusters2[s]) * nsm) continue;
+        const int nb = (KB + s - 1) / s;
+        const bool two = clusters > (int64_t)kClusters1[s] * nsm, uneven = two && tiles * s * 4 < 5 * nsm;
+        const int cost = 200 * nb + 20 * s + 250 * (s > 1) + 350 * two + 300 * uneven;
+        if (cost >= least) continue;
+        constexpr int start[3] = {2300, 2750, 3200}, block[2][3] = {{215, 275, 340}, {225, 320, 510}};
+        least = cost;
+        few = {s, start[i] + 550 * (s > 1) + 800 * two + (int64_t)nb * block[two][i]};
+    }
+    return few;
+}
+
 Plan plan_of(int T, int K, int N, int nsm) {
     const int KB = (K + BK - 1) / BK;
     if (T <= 64) {
-        const int nt = T <= 16 ? 16 : T <= 32 ? 32 : 64;
-        const int tiles = (N + 127) / 128;
-        int best = 1;
-        for (int s = 1, least = INT32_MAX; s <= 8 && KB >= s; ++s) {
-            const int64_t clusters = (int64_t)tiles * 152;
-            if (s > 1 && clusters > (int64_t)(s == 5 && T == 1 ? 54 : kClusters2[s]) * nsm) continue;
-            const bool two = clusters > (int64_t)kClusters1[s] * nsm, uneven = two && (int64_t)tiles * s * 4 < 5 * nsm;
-            const int cost = 200 * ((KB + s - 1) / s) + 20 * s + 250 * (s > 1) + 350 * two + 300 * uneven;  // ns
-            if (cost < least) least = cost, best = s;
+        int nt = T <= 16 ? 16 : T <= 32 ? 32 : 64;
+        Few best = few_rows(nt, T, K, N, nsm);
+        for (int low = 16, all = nt, most = (int)(best.ns * 100 / 108); low < all; low *= 2) {
+            const Few few = few_rows(low, T, K, N, nsm);
+            if (few.split > 0 && few.ns < most) best = few, nt = low, most = (int)few.ns;
         }
-        return {nt, false, best};
+        return {nt, false, best.split};
     }
-    const int64_t tiles = (int64_t)((N + 127) / 128) * ((T + 127) / 128);
+    const int64_t mt = (T + 127) / 128, tiles = (N + 127) / 128 * mt;
     const int64_t pairs = (int64_t)((N + 255) / 256) * ((T + 255) / 256);
     int s = 1;
     if (KB >= 16 && tiles * 8 <= nsm * 3 / 4) s = 8;
@@ -1030,6 +1055,16 @@ Plan plan_of(int T, int K, int N, int nsm) {
     else if (KB >= 16 && tiles * 4 <= nsm * 15 / 16) s = 4;
     else if (KB >= 20 && tiles * 3 <= nsm * 7 / 8) s = 3;
     else if (KB >= 24 && tiles * 2 <= nsm) s = 2;
+    if (tiles <= nsm) {
+        const int64_t rows = T / mt, wide = 1700 + 360 * ((KB + s - 1) / s) + (s > 1) * (1250 + rows * 2100 / 128) + rows * 1700 / 128;
+        Plan plan = {0, false, 0};
+        for (int64_t nt = 16, most = wide * 10 / 11; nt <= 64; nt *= 2) {
+            const Few few = few_rows((int)nt, T, K, N, nsm);
+            const int64_t ns = few.ns + (int64_t)K * N / 27000;  // (and the weights' way from HBM)
+            if (few.split > 0 && ns < most) plan = {(int)nt, false, few.split}, most = ns;
+        }
+        if (plan.nt > 0) return plan;
+    }
     const int64_t waves = (tiles + nsm - 1) / nsm, pair_waves = (pairs + nsm / 2 - 1) / (nsm / 2);
     const bool pair = 5500 + pair_waves * (365 * KB + 1100) < 4000 + waves * (265 * KB + 400);  // ns
     return {0, pair, pair ? 1 : s};

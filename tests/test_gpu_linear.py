@@ -69,8 +69,18 @@ def test_shared_by_any_number(T, K, N):
     s.verify()
 
 
-@pytest.mark.parametrize("T,K,N", [(67, 2048, 1000), (129, 4096, 1000), (200, 4096, 1000), (131, 2048, 2000), (100, 4096, 5120),
-                                   (127, 2560, 5000), (70, 4096, 6400)])
+# tiles of fewer rows than there are, the last one cut
+@pytest.mark.parametrize("T", [18, 33, 47, 64, 67, 95, 97, 128, 131, 200, 257, 350])
+@pytest.mark.parametrize("K,N,dtype", [(1040, 776, torch.bfloat16), (4096, 1000, torch.float32), (7168, 264, torch.bfloat16),
+                                       (512, 4096, torch.bfloat16), (2048, 2048, torch.float32)])
+def test_tiles_of_fewer_rows(T, K, N, dtype):
+    s = Setup(T, K, N, seed=18, dtype=dtype)
+    s.run()
+    s.verify()
+
+
+@pytest.mark.parametrize("T,K,N", [(209, 7168, 896), (257, 7168, 896), (245, 8192, 1408), (385, 4096, 1000), (260, 4096, 2048),
+                                   (129, 4096, 4096), (100, 4096, 5120), (127, 2560, 5000), (70, 4096, 6400)])
 def test_many_rows_shared_by_any_number(T, K, N):
     s = Setup(T, K, N, seed=16, dtype=torch.float32)
     s.run()
@@ -354,14 +364,16 @@ def test_no_tokens_and_refusals():
     s.verify()
 
 
-@pytest.mark.parametrize("T,N", [(1, 1400), (40, 1400), (40, 5120), (100, 1400), (140, 1400), (200, 1400), (600, 1400), (500, 5120), (1500, 7000)])
-def test_stall_times_out_then_recovers(T, N):
+@pytest.mark.parametrize("T,K,N", [(1, 2048, 1400), (40, 2048, 1400), (40, 2048, 5120), (100, 2048, 1400), (140, 2048, 1400),
+                                   (200, 2048, 1400), (245, 8192, 1408), (100, 4096, 5120), (600, 2048, 1400),
+                                   (500, 2048, 5120), (1500, 2048, 7000)])
+def test_stall_times_out_then_recovers(T, K, N):
     """With the test hook an MMA issuer waits, under a limit of 2e6 SM cycles, on a barrier that
     nothing signals: the status is recorded, copies and products in flight end, tensor memory is
     freed, and the next call is right. No GPU fault is involved."""
     from mxfp4_routed_expert_03_gb300 import (MOE_ERR_DEVICE_TIMEOUT, MOE_ERR_INVALID_ARG, MOE_INJECT_ATTN_STALL,
                                               MOE_INJECT_LINEAR_STALL, MOE_INJECT_NONE, check, moe_linear_set_fault_injection)
-    s = Setup(T, 2048, N, seed=13)
+    s = Setup(T, K, N, seed=13)
     s.run()
     clean = s.out.clone()
     for mode, limit in ((7, 0), (MOE_INJECT_ATTN_STALL, 0), (MOE_INJECT_LINEAR_STALL, 1000)):
