@@ -116,15 +116,17 @@ class Linear:
     def forward(self, T, x: Fp8Rows, out, stream=None) -> int:
         """out: [T][d_out] in bf16 or fp32 (rows may be strided)."""
         dev = self.device
-        x.check(T, self.d_in, dev)
-        if out.dtype is torch.float32:
+        if x is not None:
+            x.check(T, self.d_in, dev)
+            x = x.ref
+        if out is not None and out.dtype is torch.float32:
             if out.dim() != 2 or out.stride(1) != 1 or out.shape[0] < T or out.shape[1] < self.d_out:
                 raise ValueError(f"out: {T} contiguous rows of {self.d_out} elements")
             on_device(dev, out)
             kind, ptr, stride = MOE_LINEAR_F32, out.data_ptr(), out.stride(0)
         else:
             kind, (ptr, stride) = MOE_LINEAR_BF16, bf16_rows(out, T, self.d_out, dev)
-        return lib().moe_linear_forward(self.h, T, x.ref, ptr, stride, kind, _stream(stream))
+        return lib().moe_linear_forward(self.h, T, x, ptr, stride, kind, _stream(stream))
 
     def status(self, stream=None) -> int:
         return moe_linear_status(self.h, stream)

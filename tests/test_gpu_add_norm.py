@@ -242,6 +242,7 @@ def test_no_rows_and_refusals():
     norm, y, rows = Norm(256, 1e-6, w), torch.full_like(x, 7.0), Fp8Rows.empty(4, 256)
     assert norm.forward(0, x, r, None, y, rows) == 0 and bool((y == 7.0).all())
     assert norm.forward(4, x, r) == 0  # nothing asked for
+    assert norm.forward(-1, x, r, None, y) == MOE_ERR_INVALID_ARG and norm.forward(4, None, r, None, y) == MOE_ERR_INVALID_ARG
     assert norm.forward(4, x, None, y) == MOE_ERR_INVALID_ARG  # a total without a residual
     for bad in (x[:3], x[:, :128], x.half(), x.float(), x.cpu(), x.t()):
         with pytest.raises(ValueError):

@@ -360,6 +360,8 @@ def test_no_tokens_and_refusals():
     for out in (wide[:, 1:129], wide[:, :128]):  # unaligned base, row stride 300
         assert s.linear.forward(4, s.rows, out) == MOE_ERR_INVALID_ARG
     assert moe_linear_forward(s.linear.h, 4, s.rows.desc, s.out, 128, 2) == MOE_ERR_INVALID_ARG
+    assert s.linear.forward(4, None, s.out) == MOE_ERR_INVALID_ARG and s.linear.forward(4, s.rows, None) == MOE_ERR_INVALID_ARG
+    assert s.linear.forward(-1, s.rows, s.out) == MOE_ERR_INVALID_ARG
     s.run()
     s.verify()
 
