@@ -662,14 +662,17 @@ void moe_norm_destroy(moe_norm *n);
  * and, each where it is not NULL: h into total, y rounded to bf16 into y, y
  * into y8: per 128 columns (the last block may be shorter) the scale
  * s = max(max|y| / 448, 2^-126), codes y / s rounded to the nearest E4M3 value,
- * ties to even. A block holding an infinity or NaN gets a NaN scale: all of it
- * reads as NaN. total needs a residual. bf16 rows may be strided (elements,
- * multiples of 8; bases 16-byte aligned); for y8 d_model is a multiple of 16.
- * A bf16 output may be an input (same pointer and stride) but must not overlap
- * one otherwise. The squares are summed in fp32: a row whose sum passes its range
- * gives zeros; one whose squares are below it is normed as if its sum were 0
- * (with eps 0 that gives no finite values). An infinity or NaN spreads over its row by the norm, and no
- * further. Asynchronous on `stream`, no workspace. */
+ * ties to even. The quotient is taken as h weight / (max|h weight| / 448), where the
+ * row's factor drops out and nothing is rounded before (as y / s where s is 2^-126),
+ * so a code does not depend on how y and s were rounded. A block holding an
+ * infinity or NaN gets a NaN scale: all of it reads as NaN. total needs a
+ * residual. bf16 rows may be strided (elements, multiples of 8; bases 16-byte
+ * aligned); for y8 d_model is a multiple of 16. A bf16 output may be an input
+ * (same pointer and stride) but must not overlap one otherwise. The squares are
+ * summed in fp32: a row whose sum passes its range gives zeros; one whose squares
+ * are below it is normed as if its sum were 0 (with eps 0 that gives no finite
+ * values). An infinity or NaN spreads over its row by the norm, and no further.
+ * Asynchronous on `stream`, no workspace. */
 int moe_add_norm(moe_norm *n, int32_t T, const uint16_t *x, int64_t x_stride,
                  const uint16_t *residual, int64_t residual_stride, uint16_t *total,
                  int64_t total_stride, uint16_t *y, int64_t y_stride, const moe_fp8_rows *y8,

@@ -3,8 +3,10 @@
 //   h = bf16(x + r),  y = h / sqrt(mean(h^2) + eps) * w,
 //   per 128 columns s = max(max|y| / 448, 2^-126), code = e4m3(y / s)
 //
-// h exactly rounded, the rest in fp32. Bound: each of x, r, h, y moves 2 bytes an
-// element, the codes 1; beside that the instructions.
+// h exactly rounded, the rest in fp32. With p = h w, which 16 bits hold exactly, y / s is 448 p / max|p| of the
+// block: the row's factor is not in it, and about one quotient in 8000 is half-way between two codes. Codes are
+// computed from that form, so these go to the even code whatever the roundings of y and s (see row_out).
+// Bound: each of x, r, h, y moves 2 bytes an element, the codes 1; beside that the instructions.
 // Some warps of a block own a row and hold it in registers between the sum and the
 // output: a thread has CH chunks of 8 columns, the row's threads apart, so that 16
 // neighbouring lanes have a scale's 128 columns.
@@ -35,6 +37,30 @@ __device__ __forceinline__ float max_nan(float x, float y) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
     return r;
+}
+
+// 448 / m for m in [2^-119, 2^128), too large by 2^-23.5 to 2^-21.5 of it: an approximate reciprocal (within an
+// ulp), one step of Newton's method (then within 2^-24 of its size), 7 + 3 ulp, a rounding.
+__device__ __forceinline__ float above_448_over(float m) {
+    float r;
+    m *= 0x1p-6f;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(m));
+    r = fmaf(r, fmaf(-m, r, 1.f), r);
+    return r * (7.f + 3 * 0x1p-21f);
+}
+
+// v[j] * w[j], two at a time (each rounded as one product).
+__device__ __forceinline__ void mul8(float (&r)[8], const float (&v)[8], const float (&w)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2)
+        asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 a, a, b;\n\t"
+            "mov.b64 {%0, %1}, a;\n\t}"
+            : "=f"(r[j]), "=f"(r[j + 1])
+            : "f"(v[j]), "f"(v[j + 1]), "f"(w[j]), "f"(w[j + 1]));
+}
+__device__ __forceinline__ void mul8(float (&r)[8], const float (&v)[8], float w) {
+    const float all[8] = {w, w, w, w, w, w, w, w};
+    mul8(r, v, all);
 }
 
 // Sums of eight pairs of bf16 values, each rounded once.
@@ -69,7 +95,7 @@ __device__ __forceinline__ void row_out(const MoeNormArgs &a, const Place &p, in
                                         float inv_d, uint4 (&x)[CH], const uint4 (&r)[CH], const uint4 (&w)[CH], float *part) {
     const int lane = threadIdx.x & 31;
     float v[CH][8];
-    float ss = 0.f;
+    float ss = 0.f, rest = 1.f;
     uint16_t *total = RES && a.total ? a.total + t * a.total_stride + 8 * p.tid : nullptr;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -93,20 +119,29 @@ __device__ __forceinline__ void row_out(const MoeNormArgs &a, const Place &p, in
 #pragma unroll
             for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
         }
+        // inv = unit * rest, unit a power of two (0, infinity and NaN as they are), so that v becomes
+        // h * w exactly, at y's own size, and y = v * rest
         const float inv = rsqrtf(fmaf(ss, inv_d, a.eps));
+        const uint32_t bits = __float_as_uint(inv);
+        const bool split = inv > 0.f && inv < __uint_as_float(0x7F800000u);
+        const float unit = split ? __uint_as_float(bits & 0x7F800000u) : inv;
+        if (split) rest = __uint_as_float((bits & 0x007FFFFFu) | 0x3F800000u);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             float u[8];
             rope::unpack8(w[i], u);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * inv * u[j];
+            mul8(v[i], v[i], unit);
+            mul8(v[i], v[i], u);
         }
     }
     if (a.y) {
         uint16_t *y = a.y + t * a.y_stride + 8 * p.tid;
 #pragma unroll
-        for (int i = 0; i < CH; ++i)
-            if (live[i]) *(uint4 *)(y + 8 * i * p.threads) = rope::pack8(v[i]);
+        for (int i = 0; i < CH; ++i) {
+            float u[8];
+            mul8(u, v[i], rest);
+            if (live[i]) *(uint4 *)(y + 8 * i * p.threads) = rope::pack8(u);
+        }
     }
     if (!a.q) return;
     uint8_t *code = a.q + t * a.q_stride + 8 * p.tid;
@@ -117,19 +152,27 @@ __device__ __forceinline__ void row_out(const MoeNormArgs &a, const Place &p, in
                           max_abs(v[i][6], v[i][7], 0.f));
 #pragma unroll
         for (int o = 8; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        // (a reciprocal within an ulp: of the quotient's rounding to 4 bits that is 2^-19)
-        const float s = fmaxf(m * (1.f / 448.f), 1.17549435e-38f);
-        float f;
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(s));
+        // With the factor slightly above 448 / m a quotient that is half-way comes out on it or up to 6 ulp above
+        // (the product's own rounding included), and the mask takes that back; no other is within 8 ulp of one
+        // (numerator and denominator have 16 bits). Where the scale is the least one, y / s takes no rounding
+        // beyond y's. (Dividing v by a rounded scale instead leaves the side that a half-way quotient falls to
+        // to the roundings: 777 rows of 4096 6.5 us, 6.8 this way; 8191 of 7168 65.2 and 65.4.)
+        const float top = m * rest, s = fmaxf(top * (1.f / 448.f), 1.17549435e-38f);
+        const bool least = s <= 1.17549435e-38f;
+        const float f = least ? rest * 0x1p126f : above_448_over(m);
+        const uint32_t mask = least ? ~0u : ~7u;
+        float u[8];
+        mul8(u, v[i], f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = __uint_as_float(__float_as_uint(u[j]) & mask);
         uint32_t q[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-            q[k] = to_e4m3x2(v[i][4 * k] * f, v[i][4 * k + 1] * f) |
-                   to_e4m3x2(v[i][4 * k + 2] * f, v[i][4 * k + 3] * f) << 16;
+            q[k] = to_e4m3x2(u[4 * k], u[4 * k + 1]) | to_e4m3x2(u[4 * k + 2], u[4 * k + 3]) << 16;
         if (!live[i]) continue;
         *(uint2 *)(code + 8 * i * p.threads) = make_uint2(q[0], q[1]);
-        if ((p.tid & 15) == 0)  // (m is not below infinity: it is that, or NaN)
-            scale[i * p.threads / 16] = m < __uint_as_float(0x7F800000u) ? s : __uint_as_float(0x7FC00000u);
+        if ((p.tid & 15) == 0)  // (top is not below infinity: it is that, or NaN)
+            scale[i * p.threads / 16] = top < __uint_as_float(0x7F800000u) ? s : __uint_as_float(0x7FC00000u);
     }
 }
 

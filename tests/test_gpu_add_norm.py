@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from linear_ref import U, blocks, decode, distance
+from linear_ref import U, blocks, decode, distance, grid
 
 pytestmark = pytest.mark.gpu
 
@@ -263,3 +263,22 @@ def test_no_rows_and_refusals():
     assert norm.forward(4, wide[:, :256], None, None, y) == MOE_ERR_INVALID_ARG  # row stride 300
     odd = Norm(248, 1e-6)
     assert odd.forward(4, x, None, None, None, Fp8Rows.empty(4, 256)) == MOE_ERR_INVALID_ARG  # 8 bits: multiples of 16
+
+
+@pytest.mark.parametrize("T,d", [(1, 7168), (40, 4096), (777, 4096), (9, 144), (3001, 1536), (4099, 8192)])
+@pytest.mark.parametrize("residual,weight", [(True, True), (False, True), (False, False)])
+def test_half_way_codes_go_to_the_even_one(T, d, residual, weight):
+    """Code for code: a block's quotients y / s are h weight / (largest |h weight| / 448), in which the row's
+    factor does not occur. In 64 bits a quotient that is half-way between two codes is exactly that, and any
+    other is at least 2^-21 of its size away from it (16-bit numerators and denominators), so that rounding it
+    to fp32 first changes no code. A code or so in 8000 is half-way."""
+    x, r, w = make(T, d, seed=14, residual=residual, weight=weight)
+    _, _, rows = run(x, r, w, y=False)
+    h, _ = reference(x, r, None, 0.0)
+    p = blocks(h.double() if w is None else h.double() * w.double())
+    u = (448 * p / p.abs().amax(2, keepdim=True)).flatten(1)[:, :d]
+    if T * d > 2 ** 20:
+        g = grid("cuda")
+        at = torch.searchsorted(g, u.contiguous()).clamp(1, g.numel() - 1)
+        assert int((u * 2 == g[at - 1] + g[at]).sum()) > 20
+    assert torch.equal(rows.q.float(), u.float().to(torch.float8_e4m3fn).float())
