@@ -172,7 +172,7 @@ def prepare(case, seed):
         s["rope"] = Rope(s["table"], c["rot"], interleaved=c["pairs"] == "interleaved", eps=1e-6,
                          q_weight=s["wq"], k_weight=s["wk"])
         s["q_out"] = torch.empty(T, H * d, dtype=torch.bfloat16, device=DEV)
-        s["k_out"], s["v_out"] = (torch.zeros(T, KV * d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        s["k_out"], s["v_out"] = (torch.empty(T, KV * d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
     return s
 
 
@@ -271,8 +271,12 @@ def run(state):
         return s["out"]
     a = s["attn"]
     check(a.rope_append(c["T"], s["q"], s["k"], s["v"], s["pos"], s["rope"], s["q_out"], s["slots"], st), "moe_rope_append")
-    # the cache's new tokens as the values that they stand for (4-bit keys fit 8 bits)
-    check(a.read(c["T"], s["slots"], s["k_out"], s["v_out"], st), "moe_kv_read")
+    # the cache's new tokens as the values that they stand for (4-bit keys fit 8 bits); those without a slot are zeros
+    n = c["T"] - c["pad"]
+    check(a.read(n, s["slots"], s["k_out"], s["v_out"], st), "moe_kv_read")
+    if c["pad"]:
+        s["k_out"][n:].zero_()
+        s["v_out"][n:].zero_()
     return {"q": s["q_out"], "k": s["k_out"].to(E5M2), "v": s["v_out"]}
 
 
