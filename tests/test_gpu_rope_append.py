@@ -110,6 +110,47 @@ def test_against_64_bits(d, interleaved):
         assert bool(((got.double() - y).abs() <= tol).all())
 
 
+def cache_values(x):
+    """What the cache holds of x [n][w] (bf16), in 64 bits: per 32 elements the scale 2^(floor(log2 max) - 2), at
+    least 2^-127, and the nearest of E2M1's values, of two equally near ones that with the even code."""
+    b = x.double().unflatten(1, (-1, 32))
+    exponent = torch.frexp(b.abs().amax(2, keepdim=True))[1] - 3  # (frexp's fraction is in [1/2, 1))
+    unit = torch.exp2(exponent.clamp(min=-127).double())
+    levels = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64, device=x.device)
+    off = ((b / unit).abs()[..., None] - levels).abs()
+    near = off == off.amin(-1, keepdim=True)
+    even = near & (torch.arange(8, device=x.device) % 2 == 0)
+    code = torch.where(even.any(-1), even.int().argmax(-1), near.int().argmax(-1))
+    return (torch.copysign(levels[code], b) * unit).flatten(1)
+
+
+@pytest.mark.parametrize("T", [5, 300])
+@pytest.mark.parametrize("H,KV,d,rot,interleaved", [(8, 2, 64, 64, False), (8, 2, 128, 128, False), (3, 1, 128, 48, True)])
+def test_the_cache_holds_the_nearest_values(T, H, KV, d, rot, interleaved):
+    """Element for element, from the key rounded to bf16 and the value. The key is within half a step of bf16
+    (2^-8 of it) and fp32's errors (under 60 roundings of the row's terms) of 64 bits."""
+    from mxfp4_routed_expert_03_gb300 import check
+    s = Setup(T, H, KV, d, 16, rot, interleaved, seed=10 + T)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    # half of the values on a coarse grid: many are half-way between two codes, many block maxima powers of two
+    s.v[:, :KV * d // 2] = (torch.randint(-32, 33, (T, KV * d // 2), device="cuda", generator=g) / 4).bfloat16()
+    q_out, key = torch.empty(T, H * d, dtype=torch.bfloat16, device="cuda"), torch.empty(T, KV * d, dtype=torch.bfloat16, device="cuda")
+    check(s.one(q_out), "moe_rope_append")
+    check(s.other.norm_rope(T, None, s.k, s.pos, s.rope, None, key), "moe_qk_norm_rope")
+    x = s.k.double().reshape(T, KV, d)
+    x = x / torch.sqrt(x.square().mean(-1, keepdim=True) + 1e-6) * s.rope.tensors[2].double()
+    tab = s.rope.tensors[0].double()[s.pos.long()]
+    turn = torch.complex(tab[:, :rot // 2], tab[:, rot // 2:])[:, None]
+    first, second = (slice(0, rot, 2), slice(1, rot, 2)) if interleaved else (slice(0, rot // 2), slice(rot // 2, rot))
+    z, size = torch.complex(x[..., first], x[..., second]) * turn, x.abs()
+    size[..., first] = size[..., second] = z.abs()
+    x[..., first], x[..., second] = z.real, z.imag
+    assert bool(((key.double().view_as(x) - x).abs() <= 2.0 ** -8 * x.abs() + 60 * 2.0 ** -24 * size).all())
+    k, v = (torch.empty(T, KV * d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    check(s.attn.read(T, s.slots, k, v), "moe_kv_read")
+    assert torch.equal(k.double(), cache_values(key)) and torch.equal(v.double(), cache_values(s.v))
+
+
 @pytest.mark.parametrize("T", [200, 1300])
 def test_skipped_tokens(T):
     s = Setup(T, 8, 2, 128, 16, 128, seed=3)
