@@ -696,9 +696,12 @@ __global__ void __launch_bounds__(Pair::THREADS, 1)
         uint64_t *mine = done + half * C::STAGES;
         // where it tells that accumulator `i & 1` has been read: with the stage that uses it next, or by its number
         const uint32_t told = tc::peer_addr(half ? free1 : full, 0);
+        // (only for blocks that come, so that the issuer waits for every arrival: one in flight behind the last
+        // wait could reach a CTA that has left)
+        const int blocks = (total - first + step - 1) / step * KB;
         if (half == 0 && lane == 0) {
             tc::peer_arrive(told);
-            tc::peer_arrive(told + 8);
+            if (blocks > 1) tc::peer_arrive(told + 8);
         }
         int sg = -1, i = 0;  // scale group, block
         Ring at, ahead;      // of block i, of block i + 2
@@ -711,7 +714,7 @@ __global__ void __launch_bounds__(Pair::THREADS, 1)
                 sum, KB, [&] { return acc + (i & 1) * 256; }, [&] { return tc::mbar_test_wait(&mine[at.s], at.par); },
                 [&] { return tc::mbar_wait_warp(&mine[at.s], at.par, LIMIT, abort_p); },
                 [&] {
-                    if (lane == 0) tc::peer_arrive(told + 8 * (half ? i & 1 : ahead.s));
+                    if (lane == 0 && i + 2 < blocks) tc::peer_arrive(told + 8 * (half ? i & 1 : ahead.s));
                     ++i;
                     at.next(C::STAGES);
                     ahead.next(C::STAGES);
@@ -745,7 +748,9 @@ __global__ void __launch_bounds__(Pair::THREADS, 1)
     }
     tc::tc_fence_before();
     __syncthreads();
-    tc::cluster_arrive();
+    // (every arrival at the other CTA has been waited for there, unless a wait ran out: then they end here)
+    if (*abort_p) tc::cluster_arrive_release();
+    else tc::cluster_arrive();
     tc::cluster_wait();
     if (warp == 1) {
         tc::tc_fence_after();

@@ -210,10 +210,14 @@ __device__ __forceinline__ uint32_t cluster_size() {
 }
 
 // The two halves of a barrier over all threads of the cluster. The arrival orders no memory (one that
-// does waits for the CTA's stores): barriers made ready by fence_mbar_init and copies whose completion was
-// waited for need no more.
+// does waits for the CTA's stores): enough behind barriers made ready by fence_mbar_init, and behind copies
+// to and arrivals at other CTAs whose completion was waited for there. What nobody waited for needs the
+// second form before its target may leave.
 __device__ __forceinline__ void cluster_arrive() {
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_arrive_release() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");

@@ -224,6 +224,25 @@ def test_large_whole_numbers_are_exact(T, K, N):
     assert torch.equal(out.double(), product(xq, xs, wq, ws)[0])
 
 
+@pytest.mark.parametrize("T,K,N", [(512, 1408, 9728), (500, 1536, 9704), (1000, 1024, 9728), (8192, 384, 4864), (8000, 512, 4800)])
+def test_pairs_with_few_blocks_end_and_start_again(T, K, N):
+    """11 to 32 blocks of K for a pair of CTAs, odd and even, in one and several tiles. The last blocks of a
+    pair have none behind them that would use their accumulators again, and tell nobody that they have read them;
+    the next call's CTAs come to the same SMs right behind. Whole numbers, so every call is exact."""
+    from mxfp4_routed_expert_03_gb300 import check
+    from mxfp4_routed_expert_03_gb300.linear import Fp8Rows, Linear
+    g = torch.Generator(device="cuda").manual_seed(K)
+    xq = torch.randint(-3, 4, (T, K), device="cuda", generator=g).float().to(E4M3)
+    wq = torch.randint(-3, 4, (N, K), device="cuda", generator=g).float().to(E4M3)
+    xs, ws = torch.ones(T, -(-K // 128), device="cuda"), torch.ones(-(-N // 128), -(-K // 128), device="cuda")
+    out = [torch.empty(T, N, device="cuda") for _ in range(2)]
+    linear, rows = Linear(K, N, wq, ws), Fp8Rows(xq, xs)
+    want = product(xq, xs, wq, ws)[0]
+    for k in range(40):
+        check(linear.forward(T, rows, out[k % 2]), "moe_linear_forward")
+    assert linear.status() == 0 and all(torch.equal(o.double(), want) for o in out)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_large_strided_and_not_finite(dtype):
     from mxfp4_routed_expert_03_gb300 import check
