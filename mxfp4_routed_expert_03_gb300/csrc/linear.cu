@@ -476,6 +476,7 @@ __global__ void __launch_bounds__(Wide::THREADS, 1)
                             lane);
         }
         if (!ok && lane == 0) fail();
+        __syncwarp();  // (the barriers below are for whole warps)
         if (S > 1) {
             tc::fence_proxy_async_smem();
             ok = tc::bar_and(1, 256, ok);
@@ -483,6 +484,7 @@ __global__ void __launch_bounds__(Wide::THREADS, 1)
             if (ok && warp == 4) send_parts((const float *)smem, parts, recv, S, rank, rows, per, C::PITCH, lane);
             ok = ok && (own <= 0 || tc::mbar_wait_warp(recv, 0, LIMIT, abort_p));
             if (!ok && lane == 0) fail();
+            __syncwarp();
         }
     }
     if (S > 1) {
