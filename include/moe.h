@@ -713,6 +713,7 @@ void moe_linear_destroy(moe_linear *l);
  * moe_linear_out). out: rows of d_out elements, 16-byte aligned, out_stride in
  * elements with 16-byte rows; nothing behind the T rows or between them is
  * written. NaN codes and scales reach the rows and columns that they belong to.
+ * After a call that recorded MOE_ERR_DEVICE_TIMEOUT its T rows hold anything.
  * Asynchronous on `stream`, no workspace: calls on any streams may overlap. */
 int moe_linear_forward(moe_linear *l, int32_t T, const moe_fp8_rows *x, void *out,
                        int64_t out_stride, int32_t out_type, void *stream);
@@ -743,7 +744,10 @@ enum moe_inject {
                                   out with operand copies in flight */
     MOE_INJECT_ATTN_STALL = 2, /* moe_attn_forward: the same for the warp that copies the cache
                                   (few query rows) or the first MMA issuer (many) */
-    MOE_INJECT_LINEAR_STALL = 3 /* moe_linear_forward: the same for every MMA issuer */
+    MOE_INJECT_LINEAR_STALL = 3, /* moe_linear_forward: the same for every MMA issuer, */
+    MOE_INJECT_LINEAR_STALL_FIRST = 4, /* for that of the first CTA of each cluster, */
+    MOE_INJECT_LINEAR_STALL_LAST = 5   /* or for that of the last one (a pair of CTAs has its
+                                          issuer in the first) */
 };
 
 /* Host. Sets the handle's injection mode (enum moe_inject) and the limit of
@@ -757,8 +761,8 @@ int moe_set_fault_injection(moe_handle *h, int32_t mode, int64_t timeout_cycles)
  * MOE_INJECT_ATTN_STALL). */
 int moe_attn_set_fault_injection(moe_attn *a, int32_t mode, int64_t timeout_cycles);
 
-/* Host. The same for a linear handle (MOE_INJECT_NONE or
- * MOE_INJECT_LINEAR_STALL). */
+/* Host. The same for a linear handle (MOE_INJECT_NONE or a
+ * MOE_INJECT_LINEAR mode). */
 int moe_linear_set_fault_injection(moe_linear *l, int32_t mode, int64_t timeout_cycles);
 
 /* Host. Synchronises `stream`, returns the first device-side error recorded

@@ -51,6 +51,8 @@ MOE_INJECT_NONE = 0
 MOE_INJECT_GEMM_STALL = 1
 MOE_INJECT_ATTN_STALL = 2
 MOE_INJECT_LINEAR_STALL = 3
+MOE_INJECT_LINEAR_STALL_FIRST = 4
+MOE_INJECT_LINEAR_STALL_LAST = 5
 
 MOE_PROF_NONE = 0
 MOE_PROF_DECODE_GATEUP = 1

@@ -91,7 +91,8 @@ struct Ring {
 
 // A CTA's part of a tile, [rows][pitch] fp32 in `stage`, goes to the CTAs of the cluster that join `per` of its
 // rows each, rank 0 the first: into their `recv` area [S][per][pitch], counted on their `bar`; its own rows stay.
-// By one warp, once every CTA of the cluster has its barriers ready.
+// By one warp, once every CTA of the cluster has its barriers ready, and also where a wait ran out (whatever
+// the part holds then): so the parts that a CTA waits for always come.
 __device__ __forceinline__ void send_parts(const float *stage, float *recv, uint64_t *bar, int S, int rank, int rows,
                                            int per, int pitch, int lane) {
     const int to = (rank + lane) % S, n = min(per, rows - to * per);
@@ -99,6 +100,24 @@ __device__ __forceinline__ void send_parts(const float *stage, float *recv, uint
         tc::bulk_copy_s2peer(tc::peer_addr(recv + rank * per * pitch, to), stage + to * per * pitch, n * pitch * 4,
                              tc::peer_addr(bar, to));
     __syncwarp();
+}
+
+// Waits for the parts of this CTA's rows, by a warp, also in a CTA that has given up: a copy still on its way
+// when the CTAs leave would read or write what is no longer theirs. A CTA of KB blocks at most sends after as many
+// waits as it has blocks and groups of scales, each under `limit`; this limit is longer than all of them.
+__device__ __forceinline__ bool wait_parts(uint64_t *bar, int KB, long long limit) {
+    if (__all_sync(0xFFFFFFFFu, tc::mbar_try_wait(bar, 0))) return true;
+    const long long waits = 2 * KB + 8, most = limit < INT64_MAX / waits ? limit * waits : INT64_MAX, t0 = clock64();
+    do {
+        if (__all_sync(0xFFFFFFFFu, tc::mbar_try_wait(bar, 0))) return true;
+    } while (__all_sync(0xFFFFFFFFu, clock64() - t0 <= most));
+    return false;
+}
+
+// Test hook: whether this CTA's MMA issuer stalls.
+__device__ __forceinline__ bool stalls(int inject, int rank, int S) {
+    return inject == MOE_INJECT_LINEAR_STALL || (inject == MOE_INJECT_LINEAR_STALL_FIRST && rank == 0) ||
+           (inject == MOE_INJECT_LINEAR_STALL_LAST && rank == S - 1);
 }
 
 // Four sums of S parts, this CTA's at `own`, the others' `step` apart at `recv`, in the order of the ranks.
@@ -393,12 +412,13 @@ __global__ void __launch_bounds__(Wide::THREADS, 1)
             }
             if (lane == 0) *s_issued = it;
         } else if (warp == 2) {
+            const bool stall = stalls(args.inject, rank, S);
             int it = 0;
             Ring at;
             for (int tile = first; tile < total && ok; tile += step) {
                 for (int kb = 0; kb < nkb; ++kb, ++it, at.next(C::STAGES)) {
                     if (!tc::mbar_wait_warp(&full[at.s], at.par, LIMIT, abort_p) ||
-                        (args.inject == MOE_INJECT_LINEAR_STALL && !tc::mbar_wait_warp(never, 0, LIMIT, abort_p))) {
+                        (stall && !tc::mbar_wait_warp(never, 0, LIMIT, abort_p))) {
                         ok = false;
                         break;
                     }
@@ -481,8 +501,8 @@ __global__ void __launch_bounds__(Wide::THREADS, 1)
             tc::fence_proxy_async_smem();
             ok = tc::bar_and(1, 256, ok);
             tc::cluster_wait();  // (1)
-            if (ok && warp == 4) send_parts((const float *)smem, parts, recv, S, rank, rows, per, C::PITCH, lane);
-            ok = ok && (own <= 0 || tc::mbar_wait_warp(recv, 0, LIMIT, abort_p));
+            if (warp == 4) send_parts((const float *)smem, parts, recv, S, rank, rows, per, C::PITCH, lane);
+            if (own > 0 && !wait_parts(recv, KB, LIMIT)) ok = false;
             if (!ok && lane == 0) fail();
             __syncwarp();
         }
@@ -501,7 +521,7 @@ __global__ void __launch_bounds__(Wide::THREADS, 1)
             }
         }
         __syncwarp();
-        tc::cluster_wait();  // (2: all parts have arrived, so none is on its way out of this CTA)
+        tc::cluster_wait();  // (2: all parts have arrived, also where a wait ran out: none is on its way to or from here)
     }
     __syncthreads();
     if (*abort_p) wind_down<C::STAGES>(full, drain, warp == 2, warp >= 4 && lane == 0, drained, *s_issued, LIMIT);
@@ -650,12 +670,13 @@ __global__ void __launch_bounds__(Pair::THREADS, 1)
                     __syncwarp();
                 }
         } else if (warp == 2 && rank == 0) {
+            const bool stall = stalls(args.inject, 0, 2);
             int it = 0;
             Ring at;
             for (int tile = first; tile < total && ok; tile += step) {
                 for (int kb = 0; kb < KB; ++kb, ++it, at.next(C::STAGES)) {
                     if (!tc::mbar_wait_warp(&full[at.s], at.par, LIMIT, abort_p) ||
-                        (args.inject == MOE_INJECT_LINEAR_STALL && !tc::mbar_wait_warp(never, 0, LIMIT, abort_p))) {
+                        (stall && !tc::mbar_wait_warp(never, 0, LIMIT, abort_p))) {
                         ok = false;
                         break;
                     }
@@ -871,10 +892,11 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, 2)
         }
         if (lane == 0) *s_issued = it;
     } else if (warp == 1) {
+        const bool stall = stalls(args.inject, rank, S);
         Ring at;
         for (int it = 0; it < nkb; ++it, at.next(C::STAGES)) {
             if (!tc::mbar_wait_warp(&full[at.s], at.par, LIMIT, abort_p) ||
-                (args.inject == MOE_INJECT_LINEAR_STALL && !tc::mbar_wait_warp(never, 0, LIMIT, abort_p))) {
+                (stall && !tc::mbar_wait_warp(never, 0, LIMIT, abort_p))) {
                 ok = false;
                 break;
             }
@@ -958,8 +980,8 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, 2)
     if (S > 1) {
         tc::cluster_wait();  // (1)
         if (warp >= 2) {
-            if (ok && warp == 2) send_parts((const float *)smem, parts, recv, S, rank, rows, per, C::PITCH, lane);
-            ok = ok && (mine <= 0 || tc::mbar_wait_warp(recv, 0, LIMIT, abort_p));
+            if (warp == 2) send_parts((const float *)smem, parts, recv, S, rank, rows, per, C::PITCH, lane);
+            if (mine > 0 && !wait_parts(recv, KB, LIMIT)) ok = false;
             if (!ok && lane == 0) fail();
             __syncwarp();
         }
@@ -974,7 +996,7 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, 2)
             }
         }
         __syncwarp();
-        tc::cluster_wait();  // (2: all parts have arrived, so none is on its way out of this CTA)
+        tc::cluster_wait();  // (2: all parts have arrived, also where a wait ran out: none is on its way to or from here)
     }
     __syncthreads();
     if (*abort_p) wind_down<C::STAGES>(full, drain, warp == 1, warp >= 2 && lane == 0, drained, *s_issued, LIMIT);

@@ -184,7 +184,8 @@ MOE_API int moe_linear_forward(moe_linear *l, int32_t T, const moe_fp8_rows *x, 
 }
 
 MOE_API int moe_linear_set_fault_injection(moe_linear *l, int32_t mode, int64_t timeout_cycles) {
-    if (!l || (mode != MOE_INJECT_NONE && mode != MOE_INJECT_LINEAR_STALL)) return MOE_ERR_INVALID_ARG;
+    if (!l || (mode != MOE_INJECT_NONE && (mode < MOE_INJECT_LINEAR_STALL || mode > MOE_INJECT_LINEAR_STALL_LAST)))
+        return MOE_ERR_INVALID_ARG;
     if (timeout_cycles > 0 && timeout_cycles < 100000) return MOE_ERR_INVALID_ARG;
     l->inject = mode;
     l->timeout = timeout_cycles > 0 ? (long long)timeout_cycles : kTimeoutCycles;

@@ -408,3 +408,26 @@ def test_stall_times_out_then_recovers(T, K, N):
     s.run()
     s.verify()
     assert torch.equal(s.out, clean)
+
+
+@pytest.mark.parametrize("T,K,N", [(1, 7168, 9216), (1, 4096, 4096), (3, 2304, 4096), (40, 2048, 1400), (61, 4096, 5120),
+                                   (200, 2048, 1400), (129, 4096, 4096), (245, 8192, 1408), (100, 4096, 5120), (129, 4096, 1000)])
+@pytest.mark.parametrize("last", [False, True])
+def test_one_cta_of_a_cluster_gives_up(T, K, N, last):
+    """The issuer of one CTA of each cluster stalls: the first, which has rows to join (with one row it is the
+    only one), or the last, whose part the others wait for. The other CTAs send their parts, which have to end
+    before any of them leaves: the call right behind takes their place and is right."""
+    from mxfp4_routed_expert_03_gb300 import (MOE_ERR_DEVICE_TIMEOUT, MOE_INJECT_LINEAR_STALL_FIRST, MOE_INJECT_LINEAR_STALL_LAST,
+                                              MOE_INJECT_NONE, check, moe_linear_set_fault_injection)
+    s = Setup(T, K, N, seed=24)
+    s.run()
+    want, lost = s.out.clone(), torch.empty_like(s.out)
+    mode = MOE_INJECT_LINEAR_STALL_LAST if last else MOE_INJECT_LINEAR_STALL_FIRST
+    for _ in range(3):
+        check(moe_linear_set_fault_injection(s.linear.h, mode, 2_000_000), "inject")
+        check(s.linear.forward(T, s.rows, lost), "moe_linear_forward")
+        check(moe_linear_set_fault_injection(s.linear.h, MOE_INJECT_NONE, 0), "inject off")
+        s.out.fill_(7.0)
+        s.run()
+        assert s.linear.status() == MOE_ERR_DEVICE_TIMEOUT and s.linear.status() == 0
+        assert torch.equal(s.out, want)
