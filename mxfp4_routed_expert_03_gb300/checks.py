@@ -47,6 +47,15 @@ def flat(t, n: int, dtype, what: str):
     return t.data_ptr()
 
 
+def matrix(t, n: int, width: int, dtypes, what: str) -> None:
+    """Refuses what is not a contiguous matrix of n rows of `width` elements by its shape (more rows, rows in
+    several dimensions, dimensions of 1 and all of it in one dimension are fine)."""
+    shape = [s for s in t.shape if s != 1]
+    if (t.dtype not in dtypes or not t.is_contiguous() or t.numel() < n * width
+            or (len(shape) > 1 and shape[-1] != width and width > 1)):
+        raise ValueError(f"{what}: [{n}][{width}] contiguous elements of {dtypes[0]}")
+
+
 def on_device(index: int, *tensors) -> None:
     """Refuses tensors that are not on CUDA device `index` (pointers and None are left alone)."""
     for t in tensors:

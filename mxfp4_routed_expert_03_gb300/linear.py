@@ -13,7 +13,7 @@ import torch
 
 from . import (MOE_LINEAR_BF16, MOE_LINEAR_F32, _stream, lib, moe_fp8_rows, moe_linear_create, moe_linear_desc,
                moe_linear_destroy, moe_linear_status, moe_norm_create, moe_norm_desc, moe_norm_destroy)
-from .checks import BITS16, bf16_rows, on_device
+from .checks import BITS16, bf16_rows, matrix, on_device
 
 _BITS8 = (torch.float8_e4m3fn, torch.uint8, torch.int8)
 
@@ -93,11 +93,8 @@ class Linear:
         self.h = None
         self.d_in, self.d_out = d_in, d_out
         self.device = torch.cuda.current_device()
-        if w_q.dtype not in _BITS8 or w_q.numel() < d_out * d_in or not w_q.is_contiguous():
-            raise ValueError(f"w_q: {d_out} x {d_in} contiguous E4M3 codes")
-        need = -(-d_out // 128) * -(-d_in // 128)
-        if w_s.dtype is not torch.float32 or w_s.numel() < need or not w_s.is_contiguous():
-            raise ValueError(f"w_s: {need} contiguous fp32 scales")
+        matrix(w_q, d_out, d_in, _BITS8, "w_q")
+        matrix(w_s, -(-d_out // 128), -(-d_in // 128), (torch.float32,), "w_s")
         on_device(self.device, w_q, w_s)
         self.w_q, self.w_s = w_q, w_s
         self.h = moe_linear_create(moe_linear_desc(d_in, d_out), w_q, w_s)

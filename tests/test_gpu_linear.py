@@ -431,3 +431,14 @@ def test_one_cta_of_a_cluster_gives_up(T, K, N, last):
         s.run()
         assert s.linear.status() == MOE_ERR_DEVICE_TIMEOUT and s.linear.status() == 0
         assert torch.equal(s.out, want)
+
+
+def test_transposed_weights_are_refused():
+    from mxfp4_routed_expert_03_gb300.linear import Linear
+    s = Setup(4, 256, 640, seed=25)
+    for wq, ws in ((s.wq.t().contiguous(), s.ws), (s.wq, s.ws.t().contiguous()), (s.wq.view(1280, 128), s.ws)):
+        with pytest.raises(ValueError):
+            Linear(256, 640, wq, ws)
+    Linear(256, 640, s.wq.flatten(), s.ws[:, None, :, None])
+    s.run()
+    s.verify()

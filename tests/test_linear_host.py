@@ -60,3 +60,24 @@ def test_rows_of_codes_are_checked():
     for bad in ((q[0], s), (q.float(), s), (q.t(), s), (q, s[0]), (q, s.double()), (q, s[:3]), (q, s[:, :1]), (q, s.t())):
         with pytest.raises(ValueError):
             Fp8Rows(*bad)
+
+
+def test_weights_of_another_layout_are_refused():
+    """A matrix [rows][columns] by its shape: a transposed one has as many elements and would be read as another."""
+    import torch
+    from mxfp4_routed_expert_03_gb300.checks import matrix
+    bits = (torch.uint8, torch.int8)
+    w = torch.zeros(384, 256, dtype=torch.uint8)
+    for ok in (w, w.view(3, 128, 256), w.flatten(), torch.zeros(500, 256, dtype=torch.int8), w.view(3, 1, 128, 256)):
+        matrix(ok, 384, 256, bits, "w_q")
+    for bad in (w.t(), w.t().contiguous(), torch.zeros(256, 384, dtype=torch.uint8), w.view(768, 128), w[:383], w.float(), w[:, ::2], w.flatten()[:-1]):
+        with pytest.raises(ValueError):
+            matrix(bad, 384, 256, bits, "w_q")
+    s = torch.zeros(3, 2)
+    for ok in (s, s[:, None, :, None], s.flatten(), torch.zeros(4, 2)):
+        matrix(ok, 3, 2, (torch.float32,), "w_s")
+    for bad in (s.t(), s.t().contiguous(), s.t().contiguous()[:, None, :, None], s.double(), s[:2]):
+        with pytest.raises(ValueError):
+            matrix(bad, 3, 2, (torch.float32,), "w_s")
+    matrix(torch.zeros(3, 1), 3, 1, (torch.float32,), "w_s")
+    matrix(torch.zeros(1, 5), 1, 5, (torch.float32,), "w_s")
