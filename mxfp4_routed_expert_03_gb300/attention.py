@@ -118,8 +118,8 @@ class Attention:
 
     # (the calls go to the library without the package's wrappers: a step's host time counts)
     def norm_rope(self, T, q, k, positions, rope: Rope, q_out, k_out, stream=None) -> int:
-        if rope.width < self.head_dim:
-            raise ValueError("norm weights: head_dim elements")
+        if rope.width < self.head_dim or not rope.bf16:
+            raise ValueError("norm weights: head_dim bf16 elements")
         positions = flat(positions, T, _i32, "positions")
         q, qs = rows(q, T, self.q_width)
         k, ks = rows(k, T, self.kv_width)

@@ -7,7 +7,7 @@ BITS16 = (torch.bfloat16, torch.int16, torch.uint16)  # bf16, or its bit pattern
 
 
 def rows(t, n: int, width: int):
-    """Pointer and row stride of n token rows of `width` 16-bit elements ((None, 0) for None)."""
+    """Pointer and row stride of n token rows of `width` bf16 elements, or their bit patterns ((None, 0) for None)."""
     if t is None:
         return None, 0
     try:
@@ -16,26 +16,16 @@ def rows(t, n: int, width: int):
         one = 0  # not 2D
     if one != 1:
         raise ValueError("token rows: a 2D tensor with contiguous rows")
-    if have < n or cols < width or t.element_size() != 2:
+    if have < n or cols < width or t.dtype not in BITS16:
         raise ValueError(f"token rows: {n} rows of {width} bf16 elements")
     return t.data_ptr(), stride
 
 
 def bf16_rows(t, n: int, width: int, device: int):
-    """As rows, of bf16 elements (or their bit patterns) on CUDA device `device`."""
-    if t is None:
-        return None, 0
-    if t.dtype not in BITS16 or t.get_device() != device:
-        raise ValueError(f"token rows: bf16 elements on the handle's device cuda:{device}")
-    try:
-        (stride, one), (have, cols) = t.stride(), t.shape
-    except ValueError:
-        one = 0  # not 2D
-    if one != 1:
-        raise ValueError("token rows: a 2D tensor with contiguous rows")
-    if have < n or cols < width:
-        raise ValueError(f"token rows: {n} rows of {width} bf16 elements")
-    return t.data_ptr(), stride
+    """As rows, on CUDA device `device`."""
+    if t is not None and t.get_device() != device:
+        raise ValueError(f"token rows: on the handle's device cuda:{device}")
+    return rows(t, n, width)
 
 
 def flat(t, n: int, dtype, what: str):

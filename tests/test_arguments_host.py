@@ -125,3 +125,35 @@ def test_plan_scored(monkeypatch):
         with pytest.raises(ValueError):
             L.plan_scored(5, None, bad, plan, None)
     assert L.plan_scored(5, None, x, plan, None, bias) == 0 and L.plan_scored(5, None, None, plan, None) == 0
+
+
+def test_other_types_of_two_bytes_are_refused(A):
+    """fp16 rows and weights have as many bytes as bf16 ones and would be read as other numbers."""
+    a = A.make()
+    q, k, slots, pos = torch.zeros(5, H * D, dtype=bf16), torch.zeros(5, KV * D, dtype=bf16), torch.zeros(5, dtype=i32), torch.zeros(5, dtype=i32)
+    _refused(A, a.append, (5, k.half(), k, slots), (5, k, k.half(), slots))
+    _refused(A, a.read, (5, slots, k.half(), k), (5, slots, k, k.half()))
+    table, w = torch.zeros(7, D), torch.zeros(D, dtype=bf16)
+    rope = A.Rope(table, D, q_weight=w, k_weight=w)
+    _refused(A, a.norm_rope, (5, q.half(), k, pos, rope, q, k), (5, q, k.half(), pos, rope, q, k),
+             (5, q, k, pos, rope, q.half(), k), (5, q, k, pos, rope, q, k.half()),
+             (5, q, k, pos, A.Rope(table, D, q_weight=w.half(), k_weight=w), q, k))
+    batch = A.Batch(5, 5, 1, 16, None, torch.ones(5, dtype=i32), torch.zeros(5, 1, dtype=i32), 1.0)
+    _refused(A, lambda *args: a.forward(*args, ws=A.ws), (batch, q.half(), q), (batch, q, q.half()))
+    for good in (bf16, torch.int16, torch.uint16):
+        assert a.append(5, k.view(good), k.view(good), slots) == 0
+        assert a.norm_rope(5, q.view(good), k, pos, rope, q.view(good), k) == 0
+        assert a.forward(batch, q.view(good), q.view(good), ws=A.ws) == 0
+
+
+def test_router_rows_of_another_type_are_refused(monkeypatch):
+    from mxfp4_routed_expert_03_gb300 import MOE_ROUTER_XWR, layer as m
+    calls = []
+    monkeypatch.setattr(m, "moe_plan_scored", lambda *a: calls.append(a) or 0)
+    monkeypatch.setattr(m.Layer, "workspace", lambda self, T, op, stream=None: (torch.empty(1), 1))
+    L = m.Layer.__new__(m.Layer)
+    L.h, L.D, L.E, L.k, L.router_mode, L.atoms = None, 256, 32, 4, MOE_ROUTER_XWR, object()
+    x, plan = torch.zeros(5, 256, dtype=bf16), m.Plan(5, 32, 4, device="cpu")
+    with pytest.raises(ValueError):
+        L.plan_scored(5, None, x.half(), plan, None)
+    assert not calls and L.plan_scored(5, None, x.view(torch.int16), plan, None) == 0
