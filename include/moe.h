@@ -708,8 +708,9 @@ void moe_linear_destroy(moe_linear *l);
 /* out[t][n] = sum_b x_s[t][b] w_s[n/128][b] sum_{k in block b} x_q[t][k] w_q[n][k]
  * for T rows x of d_in codes. The products of the codes are exact; a block's 128
  * are summed by the tensor cores in fp32, the blocks in fp32 with their scales,
- * in an order fixed by the shape (a block's two scales are multiplied first, so
- * their product has to be in fp32's range); rounded once to out_type (enum
+ * in an order fixed by d_in, d_out and T (a row's bits may differ between batches;
+ * up to 16 rows T does not matter). A block's two scales are multiplied first, so
+ * their product has to be in fp32's range. Rounded once to out_type (enum
  * moe_linear_out). out: rows of d_out elements, 16-byte aligned, out_stride in
  * elements with 16-byte rows; nothing behind the T rows or between them is
  * written. NaN codes and scales reach the rows and columns that they belong to.

@@ -985,7 +985,6 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, 2)
             if (!ok && lane == 0) fail();
             __syncwarp();
         }
-        tc::cluster_arrive();  // (2: this CTA has the parts of its rows)
         if (warp >= 2 && ok) {
             for (int u = tid - 64; u < mine * 32; u += 32 * C::EW) {
                 const int j = u / 32, n = n0 + u % 32 * 4;
@@ -996,6 +995,11 @@ __global__ void __launch_bounds__(Narrow<NT>::THREADS, 2)
             }
         }
         __syncwarp();
+        // (2: this CTA has the parts of its rows. Behind the join, so that the CTAs of a cluster leave together: ahead of
+        // it those with few rows or none leave early, and where as many of the next kernel's clusters are wanted as fit,
+        // the last ones find no room until the others have left: 1 row of 7168 x 7168 by 5 10.8 us, 3 rows 10.0, so
+        // 9.0 both; where all find room in any case up to 0.1 us less, 1 row of 7168 x 9216 10.8 and 10.85.)
+        tc::cluster_arrive();
         tc::cluster_wait();  // (2: all parts have arrived, also where a wait ran out: none is on its way to or from here)
     }
     __syncthreads();
@@ -1035,8 +1039,7 @@ struct Plan {
 };
 
 // Clusters of s CTAs that 152 SMs hold at a time with one CTA an SM (the occupancy query's answers), and with two
-// (found by the few-row kernel's times; 56 clusters of 5 from two rows on: 7168 x 7168 8.9, by 4 9.6; for one row
-// 10.9 and 9.6, so 54).
+// (found by the few-row kernel's times: that query counts one of these CTAs an SM).
 constexpr int kClusters1[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
 constexpr int kClusters2[9] = {0, 304, 152, 92, 72, 56, 46, 38, 36};
 
@@ -1053,7 +1056,7 @@ Few few_rows(int nt, int T, int K, int N, int nsm) {
     if (T > nt && clusters > (int64_t)kClusters2[1] * nsm) return {0, 0};
     Few few = {1, 0};
     for (int s = 1, least = INT32_MAX; s <= 8 && KB >= s; ++s) {
-        if (s > 1 && clusters > (int64_t)(s == 5 && T == 1 ? 54 : kClusters2[s]) * nsm) continue;
+        if (s > 1 && clusters > (int64_t)kClusters2[s] * nsm) continue;
         const int nb = (KB + s - 1) / s;
         const bool two = clusters > (int64_t)kClusters1[s] * nsm, uneven = two && tiles * s * 4 < 5 * nsm;
         const int cost = 200 * nb + 20 * s + 250 * (s > 1) + 350 * two + 300 * uneven;

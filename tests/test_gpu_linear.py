@@ -442,3 +442,15 @@ def test_transposed_weights_are_refused():
     Linear(256, 640, s.wq.flatten(), s.ws[:, None, :, None])
     s.run()
     s.verify()
+
+
+@pytest.mark.parametrize("K,N", [(7168, 6912), (7168, 7040), (7168, 7168), (2048, 7168), (7168, 9216), (4096, 4096), (1040, 776)])
+def test_a_row_has_the_same_bits_in_any_batch_of_up_to_16(K, N):
+    from mxfp4_routed_expert_03_gb300 import check
+    from mxfp4_routed_expert_03_gb300.linear import Fp8Rows
+    s = Setup(16, K, N, seed=26, dtype=torch.float32)
+    s.run()
+    for T in (1, 2, 3, 5, 8, 15):
+        out = torch.empty(T, N, device="cuda")
+        check(s.linear.forward(T, Fp8Rows(s.xq[16 - T:], s.xs[16 - T:]), out), "moe_linear_forward")
+        assert torch.equal(out, s.out[16 - T:])
