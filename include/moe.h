@@ -661,10 +661,12 @@ void moe_norm_destroy(moe_norm *n);
  *   y = h / sqrt(mean(h^2) + eps) * weight in fp32 (y = h where weight is NULL)
  * and, each where it is not NULL: h into total, y rounded to bf16 into y, y
  * into y8: per 128 columns (the last block may be shorter) the scale
- * s = max(max|y| / 448, 2^-126), codes y / s rounded to the nearest E4M3 value,
- * ties to even. The quotient is taken as h weight / (max|h weight| / 448), where the
- * row's factor drops out and nothing is rounded before (as y / s where s is 2^-126),
- * so a code does not depend on how y and s were rounded. A block holding an
+ * s = max(max|y| / 448, 2^-126) (max|y| times the fp32 value of 1 / 448), codes
+ * y / s rounded to the nearest E4M3 value, ties to even. Without a norm that is the
+ * quotient of h and the scale, rounded to fp32 first. With one it is
+ * h weight / (max|h weight| / 448), where the row's factor drops out and nothing is
+ * rounded before, so a code does not depend on how y and s were rounded (as y / s
+ * where s is 2^-126). A block holding an
  * infinity or NaN gets a NaN scale: all of it reads as NaN. total needs a
  * residual. bf16 rows may be strided (elements, multiples of 8; bases 16-byte
  * aligned); for y8 d_model is a multiple of 16. A bf16 output may be an input

@@ -3,9 +3,10 @@
 //   h = bf16(x + r),  y = h / sqrt(mean(h^2) + eps) * w,
 //   per 128 columns s = max(max|y| / 448, 2^-126), code = e4m3(y / s)
 //
-// h exactly rounded, the rest in fp32. With p = h w, which 16 bits hold exactly, y / s is 448 p / max|p| of the
-// block: the row's factor is not in it, and about one quotient in 8000 is half-way between two codes. Codes are
-// computed from that form, so these go to the even code whatever the roundings of y and s (see row_out).
+// h exactly rounded, the rest in fp32; y / s is rounded to fp32 and then to a code. With a norm, y / s is
+// 448 p / max|p| of the block for p = h w, which 16 bits hold exactly: the row's factor is not in it, and about one
+// quotient in 8000 is half-way between two codes. Codes are computed from that form, so these go to the even code
+// whatever the roundings of y and s (see row_out).
 // Bound: each of x, r, h, y moves 2 bytes an element, the codes 1; beside that the instructions.
 // Some warps of a block own a row and hold it in registers between the sum and the
 // output: a thread has CH chunks of 8 columns, the row's threads apart, so that 16
@@ -39,17 +40,14 @@ __device__ __forceinline__ float max_nan(float x, float y) {
     return r;
 }
 
-// 448 / m for m in [2^-119, 2^128), too large by 2^-23.5 to 2^-21.5 of it: an approximate reciprocal (within an
-// ulp), one step of Newton's method (then within 2^-24 of its size), 7 + 3 ulp, a rounding.
-__device__ __forceinline__ float above_448_over(float m) {
+// 1 / x within 2^-24 of its size (x, 1 / x normal): an approximate reciprocal and one step of Newton's method.
+__device__ __forceinline__ float reciprocal(float x) {
     float r;
-    m *= 0x1p-6f;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(m));
-    r = fmaf(r, fmaf(-m, r, 1.f), r);
-    return r * (7.f + 3 * 0x1p-21f);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return fmaf(r, fmaf(-x, r, 1.f), r);
 }
 
-// v[j] * w[j], two at a time (each rounded as one product).
+// v[j] * w[j], two at a time (each rounded as one product); v[j] * w[j] + u[j].
 __device__ __forceinline__ void mul8(float (&r)[8], const float (&v)[8], const float (&w)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; j += 2)
@@ -62,6 +60,17 @@ __device__ __forceinline__ void mul8(float (&r)[8], const float (&v)[8], float w
     const float all[8] = {w, w, w, w, w, w, w, w};
     mul8(r, v, all);
 }
+__device__ __forceinline__ void fma8(float (&r)[8], const float (&v)[8], float w, const float (&u)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2)
+        asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%5, %6};\n\t"
+            "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+            : "=f"(r[j]), "=f"(r[j + 1])
+            : "f"(v[j]), "f"(v[j + 1]), "f"(w), "f"(u[j]), "f"(u[j + 1]));
+}
+
+// 448 / m for m in [2^-119, 2^128), too large by 2^-23.5 to 2^-21.5 of it: 7 + 3 ulp, and a rounding.
+__device__ __forceinline__ float above_448_over(float m) { return reciprocal(m * 0x1p-6f) * (7.f + 3 * 0x1p-21f); }
 
 // Sums of eight pairs of bf16 values, each rounded once.
 __device__ __forceinline__ uint4 add8(const uint4 &x, const uint4 &y) {
@@ -75,6 +84,8 @@ __device__ __forceinline__ uint4 add8(const uint4 &x, const uint4 &y) {
     }
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
+
+constexpr float kLeast = 0x1p-126f;  // the least scale
 
 // What a thread has of its row: chunk i is chunk tid + i * threads.
 struct Place {
@@ -152,23 +163,37 @@ __device__ __forceinline__ void row_out(const MoeNormArgs &a, const Place &p, in
                           max_abs(v[i][6], v[i][7], 0.f));
 #pragma unroll
         for (int o = 8; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        // With the factor slightly above 448 / m a quotient that is half-way comes out on it or up to 6 ulp above
-        // (the product's own rounding included), and the mask takes that back; no other is within 8 ulp of one
-        // (numerator and denominator have 16 bits). Where the scale is the least one, y / s takes no rounding
-        // beyond y's. (Dividing v by a rounded scale instead leaves the side that a half-way quotient falls to
-        // to the roundings: 777 rows of 4096 6.5 us, 6.8 this way; 8191 of 7168 65.2 and 65.4.)
-        const float top = m * rest, s = fmaxf(top * (1.f / 448.f), 1.17549435e-38f);
-        const bool least = s <= 1.17549435e-38f;
-        const float f = least ? rest * 0x1p126f : above_448_over(m);
-        const uint32_t mask = least ? ~0u : ~7u;
-        float u[8];
-        mul8(u, v[i], f);
+        float top, s, u[8];
+        if (NORM) {
+            // With the factor slightly above 448 / m a quotient that is half-way comes out on it or up to 6 ulp above
+            // (the product's own rounding included), and the mask takes that back; no other is within 8 ulp of one
+            // (numerator and denominator have 16 bits). Where the scale is the least one, y / s takes no rounding
+            // beyond y's. (Dividing y by its rounded scale leaves the side that a half-way quotient falls to to the
+            // roundings: 777 rows of 4096 6.5 us, 6.8 this way; 8191 of 7168 65.2 and 65.4.)
+            top = m * rest;
+            s = fmaxf(top * (1.f / 448.f), kLeast);
+            const float f = s > kLeast ? above_448_over(m) : rest * 0x1p126f;
+            const uint32_t mask = s > kLeast ? ~7u : ~0u;
+            mul8(u, v[i], f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) u[j] = __uint_as_float(__float_as_uint(u[j]) & mask);
+            for (int j = 0; j < 8; ++j) u[j] = __uint_as_float(__float_as_uint(u[j]) & mask);
+        } else {
+            // h / s correctly rounded: a product with the reciprocal, then with what that leaves of the dividend
+            // (Markstein 1990; checked for all 8-bit significands)
+            top = m;
+            s = fmaxf(m * (1.f / 448.f), kLeast);
+            // (the negated quotient, whose sign is turned below: so a negative zero stays one)
+            const float f = -reciprocal(s);
+            float left[8];
+            mul8(u, v[i], f);
+            fma8(left, u, s, v[i]);
+            fma8(u, left, f, u);
+        }
         uint32_t q[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-            q[k] = to_e4m3x2(u[4 * k], u[4 * k + 1]) | to_e4m3x2(u[4 * k + 2], u[4 * k + 3]) << 16;
+            q[k] = (to_e4m3x2(u[4 * k], u[4 * k + 1]) | to_e4m3x2(u[4 * k + 2], u[4 * k + 3]) << 16) ^
+                   (NORM ? 0u : 0x80808080u);
         if (!live[i]) continue;
         *(uint2 *)(code + 8 * i * p.threads) = make_uint2(q[0], q[1]);
         if ((p.tid & 15) == 0)  // (top is not below infinity: it is that, or NaN)

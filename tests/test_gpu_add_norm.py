@@ -266,19 +266,38 @@ def test_no_rows_and_refusals():
 
 
 @pytest.mark.parametrize("T,d", [(1, 7168), (40, 4096), (777, 4096), (9, 144), (3001, 1536), (4099, 8192)])
-@pytest.mark.parametrize("residual,weight", [(True, True), (False, True), (False, False)])
-def test_half_way_codes_go_to_the_even_one(T, d, residual, weight):
-    """Code for code: a block's quotients y / s are h weight / (largest |h weight| / 448), in which the row's
+@pytest.mark.parametrize("residual", [True, False])
+def test_half_way_codes_go_to_the_even_one(T, d, residual):
+    """Code for code: with a norm a block's quotients y / s are h weight / (largest |h weight| / 448), in which the row's
     factor does not occur. In 64 bits a quotient that is half-way between two codes is exactly that, and any
     other is at least 2^-21 of its size away from it (16-bit numerators and denominators), so that rounding it
     to fp32 first changes no code. A code or so in 8000 is half-way."""
-    x, r, w = make(T, d, seed=14, residual=residual, weight=weight)
+    x, r, w = make(T, d, seed=14, residual=residual)
     _, _, rows = run(x, r, w, y=False)
     h, _ = reference(x, r, None, 0.0)
-    p = blocks(h.double() if w is None else h.double() * w.double())
+    p = blocks(h.double() * w.double())
     u = (448 * p / p.abs().amax(2, keepdim=True)).flatten(1)[:, :d]
     if T * d > 2 ** 20:
         g = grid("cuda")
         at = torch.searchsorted(g, u.contiguous()).clamp(1, g.numel() - 1)
         assert int((u * 2 == g[at - 1] + g[at]).sum()) > 20
     assert torch.equal(rows.q.float(), u.float().to(torch.float8_e4m3fn).float())
+
+
+@pytest.mark.parametrize("few", [False, True])
+def test_codes_without_a_norm_are_those_of_a_division(few):
+    """Bit for bit, signs of zeros too: s = max (1 / 448) and h / s in fp32, then the nearest code. Every significand of
+    a block's largest element with every one of the others, at several sizes."""
+    m = torch.arange(128, 256, dtype=torch.float64)[:, None, None]  # a row for each
+    e = torch.tensor([0, -1, -2, -3, -5, -8, -12, -17]).double()     # two blocks of the row for each
+    h = torch.arange(128, 256, dtype=torch.float64) * torch.exp2(e)[None, :, None] * (1 - 2.0 * (torch.arange(128) % 3 == 1))
+    h = torch.where(h.abs() > m, h / 2, h)
+    ends = torch.cat([m, -m, 0 * m, -0.0 * m], 2).expand(128, 8, 4)
+    x = torch.stack([torch.cat([ends, h[..., :124]], 2), torch.cat([ends, h[..., 4:]], 2)], 2).reshape(128, 2048)
+    x = torch.cat([x * 2.0 ** k for k in ((0,) if few else range(-50, 60, 2))]).bfloat16()
+    b = x.float().unflatten(1, (16, 128))
+    want_s = b.abs().amax(2) * torch.tensor(1 / 448)  # (on the CPU)
+    want = (b / want_s[..., None]).flatten(1).clamp(-448, 448).to(torch.float8_e4m3fn)
+    _, _, got = run(x.cuda(), None, None, y=False)
+    assert torch.equal(got.s.cpu(), want_s)
+    assert torch.equal(got.q.cpu().view(torch.uint8), want.view(torch.uint8))
