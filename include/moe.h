@@ -669,8 +669,9 @@ void moe_norm_destroy(moe_norm *n);
  * where s is 2^-126). A block holding an
  * infinity or NaN gets a NaN scale: all of it reads as NaN. total needs a
  * residual. bf16 rows may be strided (elements, multiples of 8; bases 16-byte
- * aligned); for y8 d_model is a multiple of 16. A bf16 output may be an input
- * (same pointer and stride) but must not overlap one otherwise. The squares are
+ * aligned); y8 is as moe_fp8_rows says, but where d_model is no multiple of 16 its
+ * code rows lie one behind the other (q_stride = d_model). A bf16 output may be an
+ * input (same pointer and stride) but must not overlap one otherwise. The squares are
  * summed in fp32: a row whose sum passes its range gives zeros; one whose squares
  * are below it is normed as if its sum were 0 (with eps 0 that gives no finite
  * values). An infinity or NaN spreads over its row by the norm, and no further.

@@ -45,9 +45,11 @@ static bool rows_ok(const void *p, int64_t stride, int64_t width) {
     return p && aligned16(p) && stride % 8 == 0 && stride >= width;
 }
 
-static bool rows8_ok(const moe_fp8_rows *r, int64_t width) {
-    return r->q && aligned16(r->q) && r->q_stride % 16 == 0 && r->q_stride >= width && r->s &&
-           !((uintptr_t)r->s & 3u) && r->s_stride >= (width + 127) / 128;
+// `packed`: rows of an odd multiple of 8 codes, one behind the other. (With room for a multiple of 16 the product
+// would take the codes behind them, which nobody writes, for part of the row.)
+static bool rows8_ok(const moe_fp8_rows *r, int64_t width, bool packed = false) {
+    return r->q && aligned16(r->q) && (packed ? r->q_stride == width : r->q_stride % 16 == 0 && r->q_stride >= width) &&
+           r->s && !((uintptr_t)r->s & 3u) && r->s_stride >= (width + 127) / 128;
 }
 
 MOE_API int moe_norm_create(const moe_norm_desc *d, moe_norm **out) {
@@ -82,7 +84,7 @@ MOE_API int moe_add_norm(moe_norm *n, int32_t T, const uint16_t *x, int64_t x_st
     const int d = n->desc.d_model;
     if (!rows_ok(x, x_stride, d) || (residual && !rows_ok(residual, residual_stride, d)) ||
         (total && !rows_ok(total, total_stride, d)) || (y && !rows_ok(y, y_stride, d)) ||
-        (y8 && (d % 16 || !rows8_ok(y8, d))) || !current(n->device))
+        (y8 && !rows8_ok(y8, d, d % 16 == 8)) || !current(n->device))
         return MOE_ERR_INVALID_ARG;
     MoeNormArgs g = {};
     g.T = T;

@@ -301,3 +301,20 @@ def test_codes_without_a_norm_are_those_of_a_division(few):
     _, _, got = run(x.cuda(), None, None, y=False)
     assert torch.equal(got.s.cpu(), want_s)
     assert torch.equal(got.q.cpu().view(torch.uint8), want.view(torch.uint8))
+
+
+@pytest.mark.parametrize("d", [8, 24, 136, 248, 1000, 4104, 16376])
+@pytest.mark.parametrize("T,residual,weight", [(1, True, True), (9, False, False), (700, True, True), (1500, False, True)])
+def test_packed_code_rows_of_odd_widths(d, T, residual, weight):
+    """Widths that are multiples of 8 alone: code rows one behind the other; nothing around them is written."""
+    from mxfp4_routed_expert_03_gb300 import MOE_ERR_INVALID_ARG, check
+    from mxfp4_routed_expert_03_gb300.linear import Fp8Rows, Norm
+    x, r, w = make(T, d, seed=d, residual=residual, weight=weight)
+    norm, y, rows = Norm(d, 1e-6, w), torch.empty_like(x), Fp8Rows.empty(T + 1, d)
+    rows.q.view(torch.uint8).fill_(9)
+    rows.s.fill_(9.0)
+    check(norm.forward(T, x, r, None, y, rows), "moe_add_norm")
+    assert bool((rows.q.view(torch.uint8)[T] == 9).all()) and bool((rows.s[T] == 9.0).all())
+    verify(x, r, w, (None, y, Fp8Rows(rows.q[:T], rows.s[:T])))
+    wide = Fp8Rows.empty(T, d + 8)  # (rows that the product would take for whole ones of 16)
+    assert norm.forward(T, x, r, None, y, wide) == MOE_ERR_INVALID_ARG
