@@ -172,7 +172,8 @@ def prepare(case, seed):
         s["rope"] = Rope(s["table"], c["rot"], interleaved=c["pairs"] == "interleaved", eps=1e-6,
                          q_weight=s["wq"], k_weight=s["wk"])
         s["q_out"] = torch.empty(T, H * d, dtype=torch.bfloat16, device=DEV)
-        s["k_out"], s["v_out"] = (torch.empty(T, KV * d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        back = torch.empty(2, T, KV * d, dtype=torch.bfloat16, device=DEV)
+        (s["k_out"], s["v_out"]), s["unread"] = back, back[:, T - c["pad"]:]
     return s
 
 
@@ -275,8 +276,7 @@ def run(state):
     n = c["T"] - c["pad"]
     check(a.read(n, s["slots"], s["k_out"], s["v_out"], st), "moe_kv_read")
     if c["pad"]:
-        s["k_out"][n:].zero_()
-        s["v_out"][n:].zero_()
+        s["unread"].zero_()
     return {"q": s["q_out"], "k": s["k_out"].to(E5M2), "v": s["v_out"]}
 
 
