@@ -207,7 +207,7 @@ __device__ __forceinline__ bool load_scales(const MoeLinearArgs &args, float *xs
 
 // A warp's sums over nkb blocks of 32 rows x 2 N2 columns: sum += accumulator * scale, block by block. TMEM is
 // read 64 columns ahead of the additions, the next block's barrier is tested and its scale read ahead of
-// their use (all of these in turn: 8191 rows of 7168 x 9216 467 us instead of 367; 32 columns ahead: 434).
+// their use (all of these in turn: 8191 rows of 7168 x 9216 467 us, where that build took 367; 32 columns ahead: 434).
 //   acc()           the current block's columns in TMEM
 //   wait(), test()  waits for the current block's MMAs, false: given up; whether they are finished
 //   drained()       its accumulator has been read: on to the next block
@@ -319,7 +319,7 @@ __device__ __forceinline__ void store_rows(const MoeLinearArgs &args, int64_t t0
 // has been read (an arrival of every adding warp), so the issuer has one wait per block; `done` when its MMAs
 // are finished: its memory is free, its accumulator is full.
 // Bound: an SM takes in about 62 bytes a cycle from L2, 276 ns for the 32 KB of a block (MMAs alone 178 ns, all
-// together 306). 333 rows of 4096 x 5120 12.1 us, 2049 of 4096 x 1000 to fp32 12.2: 32 of these blocks, then start
+// together 306). 333 rows of 4096 x 5120 12.2 us, 2049 of 4096 x 1000 to fp32 12.3: 32 of these blocks, then start
 // and end.
 __global__ void __launch_bounds__(Wide::THREADS, 1)
     moe_linear_wide_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX,
@@ -576,7 +576,8 @@ __device__ __forceinline__ void mma_block_pair(uint32_t d, uint32_t a_s, uint32_
 // accumulator read by both; `free1` in the first CTA, the second half's accumulator read by both; `done` in
 // each CTA, the MMAs of a half.
 // Bound: a block takes 375 ns; its copies alone 306, its additions alone 300, its MMAs alone 274. 8191 rows of 7168 x
-// 9216 374 to 384 us (2.85 PFLOP/s), 430 when it runs for seconds at the power limit.
+// 9216 376 to 387 us (2.8 PFLOP/s), 440 when it runs for seconds at the power limit. 60 bytes a thread are spilled; other
+// register splits spill more.
 __global__ void __launch_bounds__(Pair::THREADS, 1)
     moe_linear_pair_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mX,
                            const MoeLinearArgs args) {
@@ -810,7 +811,7 @@ struct Narrow {
 }  // namespace
 
 // Bound: the weights, once through HBM; from 32 rows on also what an SM takes in from L2, and the exchange. 1 row of
-// 7168 x 9216 10.6 us (6.2 TB/s), 64 rows of 7168 x 7168 12.5 (4.2 TB/s). Two CTAs an SM: with 16 rows ten
+// 7168 x 9216 10.8 us (6.1 TB/s), 64 rows of 7168 x 7168 12.2 (4.3 TB/s). Two CTAs an SM: with 16 rows ten
 // stages, 180 KB, on their way on each.
 template <int NT>
 __global__ void __launch_bounds__(Narrow<NT>::THREADS, 2)
@@ -1031,7 +1032,8 @@ namespace {
 //   Very many: by the times that the two kernels' waves take, which these sizes gave (waves of the many-row kernel
 //   and of pairs, times of both): 512 rows of 7168 x 9216 2, 1, 37.3, 28.1; 600 rows 3, 2, 50.6, 48.7; 8191 rows
 //   31, 16, 482, 384; 900 rows of 4096 x 5120 3, 2, 29.6, 31.3; 2049 rows 5, 3, 47.6, 45.9; 768 rows of 1536 x 7168
-//   3, 2, 14.9, 16.9; 4096 rows 12, 6, 47.8, 43.5.
+//   3, 2, 14.9, 16.9; 4096 rows 12, 6, 47.8, 43.5. (The ns a block and a tile in the rules are fitted to whole calls; a
+//   block alone takes 306 ns in the many-row kernel, 375 in the pairs'.)
 struct Plan {
     int nt;     // rows of x per tile of the few-row kernel; 0: the others
     bool pair;  // the CTA pairs' kernel

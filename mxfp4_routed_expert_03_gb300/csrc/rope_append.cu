@@ -6,7 +6,7 @@
 // the two calls, without the keys' way through memory. Bound: 2 bytes read per
 // element, 2 written for queries and 17/32 for keys and values; 8191 tokens of 56
 // query and 8 + 8 key and value heads of 128 49 us (5.7 TB/s of the 277 MB; 56.6
-// with ordinary loads, see cp_async_16).
+// with ordinary loads, see cp_async_16; the two calls take 61.7).
 //
 // A warp has one of three kinds of task: TOK tokens' keys of one head (normed and
 // rotated in two passes of the row layout, exchanged through 2 KB of shared memory
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(32 * kWarps)
                 rope::unpack8(mine[64 * p], x);
                 rope::unpack8(mine[64 * p + 32], y);
                 const float ss = rope::row_squares<D>(x, y);
-                // (rows of a bad position turn by position 0 and are not written below)
+                // (rows of a bad position are not turned, nor written below)
                 const bool ok = pos[p] >= 0 && pos[p] < a.n_pos;
                 rope::Lane turned = l;
                 turned.turn = l.turn && ok;
